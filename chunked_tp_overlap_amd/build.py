@@ -20,7 +20,8 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libub.so")
 
 SOURCES = ["ub_api.cpp", "ub_plan.cpp", "gemm_bf16.hip", "gemm_fp8.hip", "quantize_fp8.hip",
-           "reduce_partials.hip", "static_scratch.hip"]
+           "reduce_partials.hip", "static_scratch.hip", "attn_api.cpp", "kv_append.hip",
+           "attn_prompt.hip", "attn_prompt_bwd.hip", "attn_decode.hip"]
 
 ARCH = "gfx950"
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")

@@ -1,0 +1,226 @@
+// Device helpers shared by the attention kernels: key-value (or query) tiles in LDS, the
+// fragments read from them, cross-lane steps, and the workgroup -> (sequence, tile) map.
+//
+// Fragment layouts (v_mfma_f32_16x16x32_bf16; lane l, g = l / 16, c = l % 16):
+//   A [16 rows x 32 k]  lane holds row c, k 8 g .. 8 g + 7
+//   B [32 k x 16 cols]  lane holds column c, the same k
+//   C [16 x 16]         lane holds column c, rows 4 g .. 4 g + 3
+// The kernels compute score tiles with the tile staged in LDS as the rows and a wave's own
+// rows (in registers) as the columns.  Two such C blocks, of tile rows r .. r + 15 and
+// r + 16 .. r + 31, rounded to bf16, are the B operand of a second product over those 32
+// tile rows with no exchange between lanes, if k index 8 g + j of that product stands for
+// tile row r + 4 g + j (j < 4) or r + 16 + 4 g + j - 4 (j >= 4): a sum over k does not depend
+// on how k is numbered, and the A operand, read transposed from the same tile
+// (ds_read_b64_tr_b16), takes its rows in that numbering.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "attn_internal.h"
+#include "gemm_common.h"
+
+namespace ubx {
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+// A tile of `ROWS` rows of up to 32 DS elements in LDS.  Rows take 128 bytes (DS <= 2) or
+// 256; 16-byte chunk q of row r is kept in slot q ^ swz(r).  swz makes both reads free of
+// bank conflicts: the row reads (16 rows, one chunk: all 16-byte slots of 256 bytes differ)
+// and the transposing reads (8 rows, two neighbouring chunks: all 32-byte slots differ).
+template <int DS>
+struct Tile {
+  static constexpr int CPR = DS <= 2 ? 8 : 16;  // chunks per row
+  static constexpr int RB = 16 * CPR;           // bytes per row
+  static constexpr int DB = 2 * DS;             // 16-wide blocks of a row
+  __device__ static int swz(int r) {
+    return CPR == 16 ? (((r & 7) << 1) | ((r >> 3) & 1)) : ((((r >> 1) & 3) << 1) | ((r >> 3) & 1));
+  }
+};
+
+// A wave's share of the direct-to-LDS loads of a tile of ROWS rows by NW waves: the byte
+// offsets of its lanes' 16-byte pieces from the tile's first row (OOB past head_dim).
+template <int DS, int ROWS, int NW>
+struct TileLoad {
+  using L = Tile<DS>;
+  static constexpr int RPI = 64 / L::CPR;          // rows per wave instruction
+  static constexpr int N = ROWS / RPI / NW;        // instructions per wave
+  static_assert(N >= 1 && N * RPI * NW == ROWS, "rows must divide over the waves");
+  uint32_t off[N];
+
+  __device__ void init(int wave, int lane, int64_t row_stride, int D) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int row = (j * NW + wave) * RPI + lane / L::CPR;
+      const int chunk = (lane % L::CPR) ^ L::swz(row);
+      off[j] = chunk * 8 < D ? (uint32_t)row * (uint32_t)(row_stride * 2) + chunk * 16 : OOB;
+    }
+  }
+  // rows [0, valid) at base; the others read as zeros
+  __device__ void issue(const uint16_t* base, int64_t row_stride, int D, int valid, uint32_t lds,
+                        int wave) const {
+    const uint32_t bytes = valid > 0 ? (uint32_t)(min(valid, ROWS) - 1) * (uint32_t)(row_stride * 2) +
+                                           (uint32_t)D * 2
+                                     : 0u;
+    const i32x4 rsrc = make_rsrc(base, bytes);
+#pragma unroll
+    for (int j = 0; j < N; ++j) dma16(rsrc, lds + (j * NW + wave) * 1024, off[j]);
+  }
+};
+
+// Row fragment: rows 16 b .. 16 b + 15 of the tile, columns 32 s .. 32 s + 31.
+template <int DS>
+struct RowFrag {
+  using L = Tile<DS>;
+  const unsigned char* p[DS];
+  __device__ void init(const unsigned char* tile, int lane) {
+    const int c = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) p[s] = tile + c * L::RB + (((4 * s + g) ^ L::swz(c)) * 16);
+  }
+  __device__ bf16x8 read(int off, int b, int s) const {
+    return *LDS_PTR(const bf16x8, p[s] + off + b * 16 * L::RB);
+  }
+};
+
+// Transposed fragment: columns 16 d .. 16 d + 15 of the tile as the rows of an A operand,
+// over tile rows 32 t .. 32 t + 31 in the numbering described above.
+template <int DS>
+struct ColFrag {
+  using L = Tile<DS>;
+  const unsigned char* p[L::DB];
+  __device__ void init(const unsigned char* tile, int lane) {
+    const int c = lane & 15, g = lane >> 4;
+    const int row = 4 * g + (c >> 2);
+#pragma unroll
+    for (int d = 0; d < L::DB; ++d)
+      p[d] = tile + row * L::RB + (((2 * d + ((c >> 1) & 1)) ^ L::swz(row)) * 16) + 8 * (c & 1);
+  }
+  __device__ bf16x8 read(int off, int t, int d) const {
+    const unsigned char* q = p[d] + off + t * 32 * L::RB;
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, q));
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, q + 16 * L::RB));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+};
+
+// Max (sum) over the four lanes that share a column: lanes c, c + 16, c + 32, c + 48.
+__device__ inline float col_max(float x) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ inline float col_sum(float x) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+__device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// 8 bf16 from two fp32 quads, round to nearest even.
+__device__ inline bf16x8 pack8(f32x4 a, f32x4 b) {
+  bf16x8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[i] = static_cast<__bf16>(a[i]);
+    r[4 + i] = static_cast<__bf16>(b[i]);
+  }
+  return r;
+}
+
+// 16 bytes of a row held in registers as a B operand: zeros past the valid rows or head_dim.
+__device__ inline bf16x8 load_row8(const uint16_t* p, bool valid) {
+  u32x4 v = {0, 0, 0, 0};
+  if (valid) v = *GLOBAL_PTR(const u32x4, p);
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// Sum over the wave's 64 lanes, the same value in all of them.
+__device__ inline int wave_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);  // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);  // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);  // row_shr:8
+  return __builtin_amdgcn_readlane(v, 15) + __builtin_amdgcn_readlane(v, 31) +
+         __builtin_amdgcn_readlane(v, 47) + __builtin_amdgcn_readlane(v, 63);
+}
+
+// Rows of sequence i clamped to [0, T): a bad boundary reads no row outside the matrices.
+__device__ inline int clamp_row(int x, int T) { return min(max(x, 0), T); }
+
+struct SeqTile {
+  int row0, len;  // the sequence's first row and its length; len 0: no tile
+  int tile;       // tile of that sequence
+};
+
+// The tile of `rank` among the tiles of bm rows of all sequences.  Up to 64 sequences (one
+// per lane): in the order of falling tile number, so that the tiles with the most work under
+// a causal mask start first.  A level x holds the tiles number x - 1; C(x) = the tiles of
+// level x and above; the rank's level is the largest x with C(x) > rank, found by
+// bisection, its sequence by the rank's bit in a ballot.  More sequences: in sequence order.
+// `low_first` reverses the levels (tiles whose work falls with their number).
+__device__ inline SeqTile find_tile(const Seqs& s, int bm, int rank, bool low_first) {
+  const int lane = threadIdx.x & 63;
+  SeqTile r{0, 0, 0};
+  if (s.n <= 64) {
+    const int i = min(lane, s.n);
+    const int a = s.n > 0 ? clamp_row(s.cu[i], s.T) : 0;
+    const int b = s.n > 0 ? clamp_row(s.cu[min(lane + 1, s.n)], s.T) : 0;
+    const int len = max(b - a, 0);
+    const int nt = (len + bm - 1) / bm;
+    const int total = wave_sum(nt);
+    if (rank >= total) return r;
+    const int want = low_first ? total - 1 - rank : rank;
+    int lo = 1, hi = (s.T + bm - 1) / bm;  // C(lo) > want always
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (wave_sum(max(nt - mid + 1, 0)) > want) lo = mid;
+      else hi = mid - 1;
+    }
+    int k = want - wave_sum(max(nt - lo, 0));  // index among the level's sequences
+    uint64_t m = __ballot(nt >= lo);
+    while (k-- > 0) m &= m - 1;
+    const int at = __builtin_ctzll(m);
+    r.row0 = __builtin_amdgcn_readlane(a, at);
+    r.len = __builtin_amdgcn_readlane(len, at);
+    r.tile = lo - 1;
+    return r;
+  }
+  int before = 0;
+  for (int c = 0; c < s.n; c += 64) {
+    const int i = min(c + lane, s.n);
+    const int a = clamp_row(s.cu[i], s.T), b = clamp_row(s.cu[min(c + lane + 1, s.n)], s.T);
+    const int len = max(b - a, 0);
+    const int nt = (len + bm - 1) / bm;
+    const int total = wave_sum(nt);
+    if (rank < before + total) {
+      int k = rank - before;
+      for (int j = 0; j < 64; ++j) {
+        const int n = __builtin_amdgcn_readlane(nt, j);
+        if (k < n) {
+          r.row0 = __builtin_amdgcn_readlane(a, j);
+          r.len = __builtin_amdgcn_readlane(len, j);
+          r.tile = low_first ? k : n - 1 - k;
+          return r;
+        }
+        k -= n;
+      }
+    }
+    before += total;
+  }
+  return r;
+}
+
+// Tiles of bm rows that n sequences of T rows together can have.
+inline int64_t max_tiles(int64_t T, int64_t n, int bm) { return T / bm + (n < T ? n : T); }
+
+// Whether row t lies in no sequence: before the first or after the last.
+__device__ inline int first_row(const Seqs& s) { return s.n > 0 ? clamp_row(s.cu[0], s.T) : s.T; }
+__device__ inline int last_row(const Seqs& s) { return s.n > 0 ? clamp_row(s.cu[s.n], s.T) : s.T; }
+
+}  // namespace
+}  // namespace ubx

@@ -1,0 +1,457 @@
+// Gradient of causal attention within packed sequences.
+//
+//   P = exp(s - lse),  delta = dout . out,  dS = P (dout v^T - delta)
+//   dq = scale dS k,   dk = scale dS^T q,   dv = P^T dout
+//
+// Two kernels, each recomputing P from lse, so that every sum runs in one workgroup in a
+// fixed order (no atomics, the same bits on every run):
+//  - attn_bwd_q: a workgroup owns query rows of one head and walks the key tiles, as the
+//    forward pass does; it also leaves delta and lse log2(e) in the workspace.
+//  - attn_bwd_kv: a workgroup owns key rows of one key-value head and walks the query tiles
+//    of its heads.  With few key tiles the heads of a group go to several workgroups, whose
+//    fp32 parts attn_bwd_join adds in order.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "attn_common.h"
+
+namespace ubx {
+namespace {
+
+constexpr int NW = 4;
+constexpr int BN = 64;  // rows of the tiles staged in LDS
+
+struct BwdParams {
+  PromptBwdArgs a;
+  float c;
+  float* lse2;   // [H, T]
+  float* delta;  // [H, T]
+  float* part;   // [parts, 2, G, T, D] when parts > 1
+  int32_t ranks;
+  int32_t parts;
+};
+
+__device__ inline void dma4(i32x4 rsrc, uint32_t lds, uint32_t voffset) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(voffset),
+                   "s"(rsrc)
+                   : "memory");
+}
+
+// Zeros in the rows of no sequence, dealt over the workgroups of a head.
+__device__ inline void fill_pad(const Heads& x, const Seqs& s, int D, int head, int rank, int ranks) {
+  const int lo = first_row(s), hi = last_row(s);
+  const int pad = lo + (s.T - hi);
+  for (int i = rank; i < pad; i += ranks) {
+    const int64_t t = i < lo ? i : hi + (i - lo);
+    if ((int)threadIdx.x < D / 8)
+      *GLOBAL_PTR(u32x4, x.p + t * x.rs + head * x.hs + threadIdx.x * 8) = u32x4{0, 0, 0, 0};
+  }
+}
+
+__device__ inline void store4(uint16_t* p, f32x4 x) {
+  uint2 w = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  *reinterpret_cast<uint2*>(p) = w;
+}
+
+template <int DS, int QF>
+__global__ __launch_bounds__(64 * NW, 1) void attn_bwd_q(BwdParams p) {
+  using L = Tile<DS>;
+  constexpr int BM = 16 * QF * NW;
+  constexpr int TILE = BN * L::RB;
+  extern __shared__ unsigned char smem[];
+  const PromptBwdArgs& a = p.a;
+  const int head = blockIdx.x % a.H, rank = blockIdx.x / a.H;
+  fill_pad(a.dq, a.seqs, a.D, head, rank, p.ranks);
+  const SeqTile st = find_tile(a.seqs, BM, rank, false);
+  if (st.len == 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  const int kvh = head / (a.H / a.G);
+  const int q0 = st.tile * BM;
+  const int wq0 = q0 + wave * 16 * QF;
+  const int n_keys = min(q0 + BM, st.len);
+  const int tiles = (n_keys + BN - 1) / BN;
+  const uint16_t* kbase = a.k.p + (int64_t)st.row0 * a.k.rs + kvh * a.k.hs;
+  const uint16_t* vbase = a.v.p + (int64_t)st.row0 * a.v.rs + kvh * a.v.hs;
+  TileLoad<DS, BN, NW> kl, vl;
+  kl.init(wave, lane, a.k.rs, a.D);
+  vl.init(wave, lane, a.v.rs, a.D);
+  const uint32_t lds = lds_addr(smem);
+  auto load = [&](int j, int stage) {
+    kl.issue(kbase + (int64_t)j * BN * a.k.rs, a.k.rs, a.D, st.len - j * BN, lds + stage * 2 * TILE, wave);
+    vl.issue(vbase + (int64_t)j * BN * a.v.rs, a.v.rs, a.D, st.len - j * BN, lds + stage * 2 * TILE + TILE,
+             wave);
+  };
+  load(0, 0);
+  bf16x8 q[QF][DS], dout[QF][DS];
+  float lse2[QF], delta[QF];
+#pragma unroll
+  for (int f = 0; f < QF; ++f) {
+    const int t = wq0 + f * 16 + col;
+    const bool ok = t < st.len;
+    const int64_t row = st.row0 + t;
+    const uint16_t* qr = a.q.p + row * a.q.rs + head * a.q.hs;
+    const uint16_t* dr = a.dout.p + row * a.dout.rs + head * a.dout.hs;
+    const uint16_t* orow = a.out.p + row * a.out.rs + head * a.out.hs;
+    float x = 0.0f;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      const int e = 32 * s + 8 * g;
+      const bool in = ok && e < a.D;
+      q[f][s] = load_row8(qr + e, in);
+      dout[f][s] = load_row8(dr + e, in);
+      const bf16x8 ov = load_row8(orow + e, in);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x += (float)dout[f][s][i] * (float)ov[i];
+    }
+    delta[f] = col_sum(x);
+    const float l = ok ? a.lse[(int64_t)head * a.seqs.T + row] : 0.0f;
+    lse2[f] = l == -INFINITY ? 0.0f : l * LOG2E;
+    if (ok && g == 0) {
+      p.lse2[(int64_t)head * a.seqs.T + row] = lse2[f];
+      p.delta[(int64_t)head * a.seqs.T + row] = delta[f];
+    }
+  }
+  RowFrag<DS> kf, vf;
+  ColFrag<DS> kt;
+  kf.init(smem, lane);
+  vf.init(smem + TILE, lane);
+  kt.init(smem, lane);
+  f32x4 acc[L::DB][QF];
+#pragma unroll
+  for (int d = 0; d < L::DB; ++d)
+#pragma unroll
+    for (int f = 0; f < QF; ++f) acc[d][f] = f32x4{0, 0, 0, 0};
+  for (int j = 0; j < tiles; ++j) {
+    const int stage = (j & 1) * 2 * TILE;
+    wait_vmcnt_and_barrier<0>();
+    if (j + 1 < tiles) load(j + 1, (j + 1) & 1);
+    const int k0 = j * BN;
+    if (k0 > wq0 + 16 * QF - 1) continue;
+    const bool diag = k0 + BN - 1 > wq0;
+#pragma unroll
+    for (int t = 0; t < BN / 32; ++t) {
+      f32x4 s[2][QF], dp[2][QF];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int f = 0; f < QF; ++f) {
+          s[b][f] = f32x4{0, 0, 0, 0};
+          dp[b][f] = f32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+      for (int d = 0; d < DS; ++d)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const bf16x8 kk = kf.read(stage, 2 * t + b, d);
+          const bf16x8 vv = vf.read(stage, 2 * t + b, d);
+#pragma unroll
+          for (int f = 0; f < QF; ++f) {
+            s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
+            dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, dout[f][d], dp[b][f], 0, 0, 0);
+          }
+        }
+      bf16x8 ds[QF];
+#pragma unroll
+      for (int f = 0; f < QF; ++f) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x = exp2_(s[b][f][i] * p.c - lse2[f]) * (dp[b][f][i] - delta[f]);
+            if (diag && k0 + t * 32 + b * 16 + 4 * g + i > wq0 + f * 16 + col) x = 0.0f;
+            s[b][f][i] = x;
+          }
+        ds[f] = pack8(s[0][f], s[1][f]);
+      }
+#pragma unroll
+      for (int d = 0; d < L::DB; ++d) {
+        const bf16x8 kk = kt.read(stage, t, d);
+#pragma unroll
+        for (int f = 0; f < QF; ++f)
+          acc[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, ds[f], acc[d][f], 0, 0, 0);
+      }
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < QF; ++f) {
+    const int t = wq0 + f * 16 + col;
+    if (t >= st.len) continue;
+    uint16_t* out = a.dq.p + (int64_t)(st.row0 + t) * a.dq.rs + head * a.dq.hs;
+#pragma unroll
+    for (int d = 0; d < L::DB; ++d)
+      if (16 * d + 4 * g < a.D) store4(out + 16 * d + 4 * g, acc[d][f] * a.scale);
+  }
+}
+
+template <int DS, int KF>
+__global__ __launch_bounds__(64 * NW, 1) void attn_bwd_kv(BwdParams p) {
+  using L = Tile<DS>;
+  constexpr int BK = 16 * KF * NW;
+  constexpr int TILE = BN * L::RB;
+  constexpr int STAGE = 2 * TILE + 2 * BN * 4;  // q rows, dout rows, lse2, delta
+  extern __shared__ unsigned char smem[];
+  const PromptBwdArgs& a = p.a;
+  const int GP = a.G * p.parts;
+  const int gp = blockIdx.x % GP, rank = blockIdx.x / GP;
+  const int kvh = gp / p.parts, part = gp - kvh * p.parts;
+  if (part == 0) {
+    fill_pad(a.dk, a.seqs, a.D, kvh, rank, p.ranks);
+    fill_pad(a.dv, a.seqs, a.D, kvh, rank, p.ranks);
+  }
+  const SeqTile st = find_tile(a.seqs, BK, rank, true);
+  if (st.len == 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  const int k0 = st.tile * BK;
+  const int wk0 = k0 + wave * 16 * KF;
+  const int heads = a.H / a.G / p.parts, head0 = kvh * (a.H / a.G) + part * heads;
+  const int qt0 = k0 / BN, qtiles = (st.len + BN - 1) / BN - qt0;
+  const int total = heads * qtiles;
+  const int64_t T = a.seqs.T;
+  TileLoad<DS, BN, NW> ql, dl;
+  ql.init(wave, lane, a.q.rs, a.D);
+  dl.init(wave, lane, a.dout.rs, a.D);
+  const uint32_t lds = lds_addr(smem);
+  int lh = 0, lq = 0;  // head and query tile of the next load
+  auto load = [&](int stage) {
+    const int head = head0 + lh, r = (qt0 + lq) * BN, valid = st.len - r;
+    const uint32_t at = lds + stage * STAGE;
+    const int64_t row = st.row0 + r;
+    ql.issue(a.q.p + row * a.q.rs + head * a.q.hs, a.q.rs, a.D, valid, at, wave);
+    dl.issue(a.dout.p + row * a.dout.rs + head * a.dout.hs, a.dout.rs, a.D, valid, at + TILE, wave);
+    if (wave < 2) {
+      const float* x = (wave == 0 ? p.lse2 : p.delta) + head * T + row;
+      dma4(make_rsrc(x, (uint32_t)min(valid, BN) * 4), at + 2 * TILE + wave * BN * 4, lane * 4);
+    }
+    if (++lq == qtiles) {
+      lq = 0;
+      ++lh;
+    }
+  };
+  load(0);
+  bf16x8 k[KF][DS], v[KF][DS];
+#pragma unroll
+  for (int f = 0; f < KF; ++f) {
+    const int u = wk0 + f * 16 + col;
+    const int64_t row = st.row0 + u;
+    const uint16_t* kr = a.k.p + row * a.k.rs + kvh * a.k.hs;
+    const uint16_t* vr = a.v.p + row * a.v.rs + kvh * a.v.hs;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      const int e = 32 * s + 8 * g;
+      k[f][s] = load_row8(kr + e, u < st.len && e < a.D);
+      v[f][s] = load_row8(vr + e, u < st.len && e < a.D);
+    }
+  }
+  RowFrag<DS> qf, df;
+  ColFrag<DS> qt, dt;
+  qf.init(smem, lane);
+  df.init(smem + TILE, lane);
+  qt.init(smem, lane);
+  dt.init(smem + TILE, lane);
+  f32x4 dk[L::DB][KF], dv[L::DB][KF];
+#pragma unroll
+  for (int d = 0; d < L::DB; ++d)
+#pragma unroll
+    for (int f = 0; f < KF; ++f) dk[d][f] = dv[d][f] = f32x4{0, 0, 0, 0};
+  int cq = 0;  // query tile of the iteration
+  for (int j = 0; j < total; ++j) {
+    const int stage = (j & 1) * STAGE;
+    wait_vmcnt_and_barrier<0>();
+    if (j + 1 < total) load((j + 1) & 1);
+    const int q0 = (qt0 + cq) * BN;
+    if (++cq == qtiles) cq = 0;
+    if (q0 + BN - 1 < wk0) continue;
+    const bool diag = q0 < wk0 + 16 * KF - 1;
+    const float* rows = reinterpret_cast<const float*>(smem + stage + 2 * TILE);
+#pragma unroll
+    for (int t = 0; t < BN / 32; ++t) {
+      f32x4 s[2][KF], dp[2][KF];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const f32x4 nd = -*LDS_PTR(const f32x4, rows + BN + t * 32 + b * 16 + 4 * g);
+#pragma unroll
+        for (int f = 0; f < KF; ++f) {
+          s[b][f] = f32x4{0, 0, 0, 0};
+          dp[b][f] = nd;
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < DS; ++d)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const bf16x8 qq = qf.read(stage, 2 * t + b, d);
+          const bf16x8 dd = df.read(stage, 2 * t + b, d);
+#pragma unroll
+          for (int f = 0; f < KF; ++f) {
+            s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qq, k[f][d], s[b][f], 0, 0, 0);
+            dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dd, v[f][d], dp[b][f], 0, 0, 0);
+          }
+        }
+      bf16x8 pf[KF], ds[KF];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const f32x4 l2 = *LDS_PTR(const f32x4, rows + t * 32 + b * 16 + 4 * g);
+#pragma unroll
+        for (int f = 0; f < KF; ++f)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x = exp2_(s[b][f][i] * p.c - l2[i]);
+            if (diag && wk0 + f * 16 + col > q0 + t * 32 + b * 16 + 4 * g + i) x = dp[b][f][i] = 0.0f;
+            s[b][f][i] = x;
+            dp[b][f][i] *= x;
+          }
+      }
+#pragma unroll
+      for (int f = 0; f < KF; ++f) {
+        pf[f] = pack8(s[0][f], s[1][f]);
+        ds[f] = pack8(dp[0][f], dp[1][f]);
+      }
+#pragma unroll
+      for (int d = 0; d < L::DB; ++d) {
+        const bf16x8 dd = dt.read(stage, t, d);
+        const bf16x8 qq = qt.read(stage, t, d);
+#pragma unroll
+        for (int f = 0; f < KF; ++f) {
+          dv[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dd, pf[f], dv[d][f], 0, 0, 0);
+          dk[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qq, ds[f], dk[d][f], 0, 0, 0);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < KF; ++f) {
+    const int u = wk0 + f * 16 + col;
+    if (u >= st.len) continue;
+    const int64_t row = st.row0 + u;
+    if (p.parts == 1) {
+      uint16_t* ok = a.dk.p + row * a.dk.rs + kvh * a.dk.hs;
+      uint16_t* ov = a.dv.p + row * a.dv.rs + kvh * a.dv.hs;
+#pragma unroll
+      for (int d = 0; d < L::DB; ++d) {
+        const int e = 16 * d + 4 * g;
+        if (e < a.D) {
+          store4(ok + e, dk[d][f] * a.scale);
+          store4(ov + e, dv[d][f]);
+        }
+      }
+    } else {
+      float* ok = p.part + (((int64_t)(part * 2) * a.G + kvh) * T + row) * a.D;
+      float* ov = ok + (int64_t)a.G * T * a.D;
+#pragma unroll
+      for (int d = 0; d < L::DB; ++d) {
+        const int e = 16 * d + 4 * g;
+        if (e < a.D) {
+          *reinterpret_cast<f32x4*>(ok + e) = dk[d][f];
+          *reinterpret_cast<f32x4*>(ov + e) = dv[d][f];
+        }
+      }
+    }
+  }
+}
+
+// dk and dv from their parts, in part order; 8 elements per thread.
+__global__ __launch_bounds__(256) void attn_bwd_join(BwdParams p) {
+  const PromptBwdArgs& a = p.a;
+  const int vec = a.D / 8;
+  const int lo = first_row(a.seqs), hi = last_row(a.seqs);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t per = (int64_t)a.seqs.T * vec;
+  if (i >= per * a.G * 2) return;
+  const int which = (int)(i / (per * a.G));
+  const int64_t r = i - which * per * a.G;
+  const int kvh = (int)(r / per);
+  const int64_t row = (r - kvh * per) / vec;
+  const int e = (int)(r % vec) * 8;
+  if (row < lo || row >= hi) return;
+  const int64_t step = (int64_t)a.G * a.seqs.T * a.D;
+  const float* x = p.part + which * step + ((int64_t)kvh * a.seqs.T + row) * a.D + e;
+  f32x4 s0 = *reinterpret_cast<const f32x4*>(x), s1 = *reinterpret_cast<const f32x4*>(x + 4);
+  for (int k = 1; k < p.parts; ++k) {
+    x += 2 * step;
+    s0 += *reinterpret_cast<const f32x4*>(x);
+    s1 += *reinterpret_cast<const f32x4*>(x + 4);
+  }
+  const Heads& o = which ? a.dv : a.dk;
+  const float scale = which ? 1.0f : a.scale;
+  u32x4 w;
+  w[0] = pack_bf16x2(s0[0] * scale, s0[1] * scale);
+  w[1] = pack_bf16x2(s0[2] * scale, s0[3] * scale);
+  w[2] = pack_bf16x2(s1[0] * scale, s1[1] * scale);
+  w[3] = pack_bf16x2(s1[2] * scale, s1[3] * scale);
+  *GLOBAL_PTR(u32x4, o.p + row * o.rs + kvh * o.hs + e) = w;
+}
+
+constexpr int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+// Parts a group's heads are split into: with fewer than four key tiles per CU the chip would
+// idle behind the longest tiles.
+int bwd_parts(int H, int G, int64_t rows) {
+  const int group = H / G;
+  const int64_t tiles = (rows + 127) / 128 * G;
+  int parts = 1;
+  while (parts < group && tiles * parts < 1024) {
+    ++parts;
+    while (group % parts) ++parts;
+  }
+  return parts;
+}
+
+template <int DS>
+hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
+  constexpr int KF = 2, QF = 2;
+  const int64_t T = a.seqs.T;
+  BwdParams p{};
+  p.a = a;
+  p.c = a.scale * LOG2E;
+  p.parts = bwd_parts(a.H, a.G, T);
+  unsigned char* w = static_cast<unsigned char*>(a.ws);
+  const int64_t stat = align256((int64_t)a.H * T * 4);
+  p.lse2 = reinterpret_cast<float*>(w);
+  p.delta = reinterpret_cast<float*>(w + stat);
+  p.part = reinterpret_cast<float*>(w + 2 * stat);
+  const int64_t ranks = max_tiles(T, a.seqs.n, 16 * QF * NW) + (a.seqs.n == 0);
+  if (ranks * a.H > 0x7FFFFFFF) return hipErrorInvalidValue;
+  p.ranks = (int32_t)ranks;
+  constexpr int lds_q = 4 * BN * Tile<DS>::RB, lds_kv = 2 * (2 * BN * Tile<DS>::RB + 2 * BN * 4);
+  auto kq = &attn_bwd_q<DS, QF>;
+  auto kkv = &attn_bwd_kv<DS, KF>;
+  hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kq), lds_q);
+  if (e == hipSuccess) e = ensure_lds_attr(reinterpret_cast<const void*>(kkv), lds_kv);
+  if (e == hipSuccess) e = launch_k(kq, dim3((unsigned)(ranks * a.H)), dim3(64 * NW), lds_q, s, p);
+  if (e == hipSuccess)
+    e = launch_k(kkv, dim3((unsigned)(ranks * a.G * p.parts)), dim3(64 * NW), lds_kv, s, p);
+  if (e == hipSuccess && p.parts > 1) {
+    const int64_t blocks = (2 * a.G * T * (a.D / 8) + 255) / 256;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    e = launch_k(&attn_bwd_join, dim3((unsigned)blocks), dim3(256), 0, s, p);
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t attn_prompt_bwd_need(int32_t H, int32_t G, int32_t D, int64_t rows) {
+  const int parts = bwd_parts(H, G, rows);
+  return static_cast<size_t>(2 * align256((int64_t)H * rows * 4) +
+                             (parts > 1 ? (int64_t)parts * 2 * G * rows * D * 4 : 0));
+}
+
+size_t attn_prompt_bwd_bytes(int32_t H, int32_t G, int32_t D, int64_t rows) {
+  // the parts fall in steps as rows grow, so fewer rows can need more: each row count up to
+  // `rows` is covered by the last one with the same number of key tiles
+  size_t most = attn_prompt_bwd_need(H, G, D, rows);
+  for (int64_t t = 1; t <= 1024 && t * 128 < rows; ++t)
+    most = std::max(most, attn_prompt_bwd_need(H, G, D, t * 128));
+  return most;
+}
+
+hipError_t launch_attn_prompt_bwd(const PromptBwdArgs& a, hipStream_t s) {
+  if (a.D <= 64) return run<2>(a, s);
+  if (a.D <= 96) return run<3>(a, s);
+  return run<4>(a, s);
+}
+
+}  // namespace ubx

@@ -17,6 +17,7 @@
 // in, 8 out) per vector, four vectors per lane, one short chunk of rows per workgroup.
 #include <hip/hip_runtime.h>
 
+#include "e4m3.h"
 #include "ub_internal.h"
 
 namespace ubx {
@@ -26,22 +27,6 @@ constexpr int THREADS = 256;
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 #define GLOBAL_PTR(T, p) ((__attribute__((address_space(1))) T*)(p))
-
-__device__ inline uint32_t e4m3(float y) {
-  const uint32_t u = __float_as_uint(y);
-  const uint32_t sign = (u >> 24) & 0x80u;
-  const uint32_t a = u & 0x7FFFFFFFu;
-  if (a > 0x7F800000u) return sign | 0x7Fu;                 // NaN
-  if (a >= 0x43E00000u) return sign | 0x7Eu;                // >= 448 (and inf): saturate
-  if (a >= 0x3C800000u) {                                   // >= 2^-6: normal E4M3
-    // round the 23-bit fp32 significand to 3 bits, ties to even (a carry moves the
-    // exponent up), then rebias the exponent from 127 to 7
-    const uint32_t r = (a + 0x7FFFFu + ((a >> 20) & 1u)) >> 20;
-    return sign | (r - (120u << 3));
-  }
-  // subnormal range: multiples of 2^-9 (8 * 2^-9 = 2^-6 is code 0x08, the smallest normal)
-  return sign | (uint32_t)__builtin_rintf(__uint_as_float(a) * 512.0f);
-}
 
 constexpr int V = 4;  // vectors per lane
 

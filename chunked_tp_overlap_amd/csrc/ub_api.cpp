@@ -29,6 +29,7 @@
 
 #include <rocprofiler-sdk-roctx/roctx.h>
 
+#include "attn_internal.h"
 #include "ub_internal.h"
 
 constexpr int kMaxArrivalChunks = 64;
@@ -495,6 +496,15 @@ ubx::ReduceArgs reduce_args(const ub_ctx* h, int64_t row0, int64_t rows, void* o
 }
 
 }  // namespace
+
+// What the attention calls (attn_api.cpp) use of a handle.
+namespace ubx {
+ub_status_t ctx_fail(ub_handle_t h, ub_status_t st, const std::string& message) {
+  return fail(h, st, "%s", message.c_str());
+}
+ub_status_t ctx_bind(ub_handle_t h) { return ensure_device(h, 1); }
+int64_t ctx_rows(ub_handle_t h) { return h->T; }
+}  // namespace ubx
 
 extern "C" {
 

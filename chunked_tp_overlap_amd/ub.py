@@ -37,6 +37,8 @@ UB_MAX_STREAMS = 8
 METHODS = {"ring_exchange": UB_RING_EXCHANGE, "pipeline": UB_PIPELINE, "bulk": UB_BULK}
 UB_REDUCE_ASCENDING, UB_REDUCE_RING = 0, 1
 REDUCE_ORDERS = {"ascending": UB_REDUCE_ASCENDING, "ring": UB_REDUCE_RING}
+UB_ATTN_PROMPT, UB_ATTN_PROMPT_BWD, UB_ATTN_DECODE = 0, 1, 2
+UB_ATTN_MAX_HEAD_DIM = 128
 
 # Every symbol include/ub.h declares.
 EXPORTS = (
@@ -49,6 +51,7 @@ EXPORTS = (
     "ub_quantize_e4m3", "ub_reduce_partials",
     "ub_set_kernel_timing", "ub_get_kernel_timing", "ub_prepare_streams", "ub_debug_set",
     "ub_debug_last_plan", "ub_register_scratch", "ub_destroy", "ub_status_string", "ub_last_error",
+    "ub_attn_required_bytes", "ub_kv_append", "ub_attn_prompt", "ub_attn_prompt_bwd", "ub_attn_decode",
 )
 
 
@@ -79,6 +82,23 @@ class ub_tile_plan_t(ctypes.Structure):
                 ("dispatches", ctypes.c_int32), ("rs_pieces", ctypes.c_int32)]
 
 
+class ub_attn_cfg_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_heads", "n_kv_heads", "head_dim", "rotary_dim",
+                                              "rope_interleaved")] + [("softmax_scale", ctypes.c_float)]
+
+
+class ub_heads_t(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("rows", ctypes.c_int64)]
+
+
+class ub_kv_cache_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
 UB_SCRATCH_COUNTER_BYTES = 256 * 1024
 UB_SCRATCH_MIN_BYTES = UB_SCRATCH_COUNTER_BYTES + 64 * 1024
 
@@ -92,6 +112,8 @@ _H = ctypes.c_void_p
 _P = ctypes.c_void_p
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _CFGP = ctypes.POINTER(ub_overlap_cfg_t)
+
+_ATTNP, _HEADSP, _KVP = (ctypes.POINTER(t) for t in (ub_attn_cfg_t, ub_heads_t, ub_kv_cache_t))
 
 _sig = {
     "ub_overlap_cfg_default": (None, [_CFGP]),
@@ -123,6 +145,12 @@ _sig = {
     "ub_debug_set": (_I32, [_H, ctypes.c_char_p, _I64]),
     "ub_debug_last_plan": (_I32, [_H, ctypes.POINTER(ub_tile_plan_t)]),
     "ub_register_scratch": (_I32, [_H, _P, _SZ]),
+    "ub_attn_required_bytes": (_I32, [_I32, _ATTNP, _I64, _I32, ctypes.POINTER(_SZ)]),
+    "ub_kv_append": (_I32, [_H, _HEADSP, _HEADSP, _HEADSP, _HEADSP, _HEADSP, _P, _P, _P, _I32, _KVP, _P,
+                            _I64, _I32, _ATTNP, _P]),
+    "ub_attn_prompt": (_I32, [_H, _HEADSP, _HEADSP, _HEADSP, _HEADSP, _P, _P, _I32, _ATTNP, _P, _SZ, _P]),
+    "ub_attn_prompt_bwd": (_I32, [_H] + [_HEADSP] * 5 + [_P] + [_HEADSP] * 3 + [_P, _I32, _ATTNP, _P, _SZ, _P]),
+    "ub_attn_decode": (_I32, [_H, _HEADSP, _KVP, _P, _I64, _I32, _P, _I32, _HEADSP, _P, _ATTNP, _P, _SZ, _P]),
     "ub_destroy": (_I32, [_H]),
     "ub_status_string": (ctypes.c_char_p, [_I32]),
     "ub_last_error": (ctypes.c_char_p, [_H]),
@@ -361,6 +389,165 @@ def ub_register_scratch(h, buf, nbytes):
     if buf is not None:
         _fits(buf, nbytes, "scratch")
     _check(_lib.ub_register_scratch(h, _ptr(buf), int(nbytes)), h)
+
+
+# ---- attention ----------------------------------------------------------------------------
+def make_attn_cfg(n_heads, n_kv_heads, head_dim, rotary_dim=None, rope_interleaved=False,
+                  softmax_scale=None):
+    """A ``ub_attn_cfg_t``; rotary_dim defaults to head_dim rounded down to a multiple of 16,
+    softmax_scale to head_dim ** -0.5."""
+    cfg = ub_attn_cfg_t()
+    cfg.n_heads, cfg.n_kv_heads, cfg.head_dim = int(n_heads), int(n_kv_heads), int(head_dim)
+    cfg.rotary_dim = int(head_dim) // 16 * 16 if rotary_dim is None else int(rotary_dim)
+    cfg.rope_interleaved = int(bool(rope_interleaved))
+    cfg.softmax_scale = max(int(head_dim), 1) ** -0.5 if softmax_scale is None else float(softmax_scale)
+    return cfg
+
+
+def heads(x, col=0):
+    """A ``ub_heads_t`` over a device tensor: the heads that start at column ``col`` of a 2-D
+    [rows, columns] matrix, head_dim columns each, or a 3-D [rows, heads, head_dim] view with
+    any row and head strides.  It keeps the tensor alive."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"heads: a 2-D or 3-D tensor, not {x.dim()}-D")
+    if x.element_size() != 2:
+        raise ValueError(f"heads: a bf16 matrix, not {x.dtype}")
+    if x.numel() and x.stride(-1) != 1:
+        raise ValueError("heads: the last dimension must be contiguous")
+    if x.dim() == 3 and col:
+        raise ValueError("heads: col is for 2-D matrices")
+    d = ub_heads_t()
+    d.ptr = x.data_ptr() + 2 * int(col)
+    d.rows = x.shape[0]
+    d.row_stride = x.stride(0)
+    d.head_stride = x.stride(1) if x.dim() == 3 else 0
+    d.tensor, d.col = x, int(col)
+    return d
+
+
+def make_kv_cache(k, v, k_scale=1.0, v_scale=1.0):
+    """A ``ub_kv_cache_t`` over k and v, [n_pages, kv_heads, page_size, head_dim] views of the
+    same strides (any order of heads and tokens), bf16, or float8_e4m3fn with the scales."""
+    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+        raise ValueError("make_kv_cache: k and v must be 4-D, of one shape, dtype and strides")
+    if k.stride(3) != 1:
+        raise ValueError("make_kv_cache: head_dim must be contiguous")
+    dtypes = {torch.bfloat16: UB_DTYPE_BF16, torch.float8_e4m3fn: UB_DTYPE_FP8_E4M3,
+              torch.float16: UB_DTYPE_FP16, torch.float8_e5m2: UB_DTYPE_FP8_E5M2}
+    if k.dtype not in dtypes:
+        raise ValueError(f"make_kv_cache: {k.dtype}")
+    c = ub_kv_cache_t()
+    c.k, c.v = k.data_ptr(), v.data_ptr()
+    c.page_stride, c.head_stride, c.token_stride = k.stride(0), k.stride(1), k.stride(2)
+    c.n_pages, c.page_size = k.shape[0], k.shape[2]
+    c.dtype = dtypes[k.dtype]
+    c.k_scale, c.v_scale = float(k_scale), float(v_scale)
+    c.tensors = (k, v)
+    return c
+
+
+def _heads_arg(x, n, cfg, what):
+    """A pointer to x's struct, once its columns are known to hold n heads."""
+    if x is None:
+        return None
+    t = getattr(x, "tensor", None)
+    if t is not None:
+        if t.dim() == 3 and (t.shape[1] < n or t.shape[2] < cfg.head_dim):
+            raise ValueError(f"{what}: {tuple(t.shape)} does not hold {n} heads of {cfg.head_dim}")
+        if t.dim() == 2 and x.col + n * cfg.head_dim > t.shape[1]:
+            raise ValueError(f"{what}: columns {x.col} to {x.col + n * cfg.head_dim} of {t.shape[1]}")
+    return ctypes.byref(x)
+
+
+def _cache_arg(cache, cfg):
+    if cache is None:
+        return None
+    for t in getattr(cache, "tensors", ()):
+        if t.shape[1] < cfg.n_kv_heads or t.shape[3] < cfg.head_dim:
+            raise ValueError(f"cache: {tuple(t.shape)} does not hold {cfg.n_kv_heads} heads of {cfg.head_dim}")
+    return ctypes.byref(cache)
+
+
+def _int32(x, n, what):
+    """A pointer to at least n contiguous int32 values."""
+    if x is not None and hasattr(x, "data_ptr"):
+        if x.dtype != torch.int32 or not x.is_contiguous() or x.numel() < n:
+            raise ValueError(f"{what}: at least {n} contiguous int32 values")
+    return _ptr(x)
+
+
+def _table(pages, n):
+    """(pointer, row stride, pages per sequence) of a [sequences, pages] int32 tensor."""
+    if pages is None:
+        return None, 0, 0
+    if pages.dim() != 2 or pages.dtype != torch.int32 or (pages.numel() and pages.stride(1) != 1) \
+            or pages.shape[0] < n:
+        raise ValueError(f"pages: an int32 [at least {n}, pages] tensor with contiguous rows")
+    return pages.data_ptr(), max(pages.stride(0), pages.shape[1]), pages.shape[1]
+
+
+def _lse_arg(lse, h, cfg):
+    if lse is not None and hasattr(lse, "data_ptr"):
+        T = ub_get_active_shape(h)[0]
+        if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.numel() < cfg.n_heads * T:
+            raise ValueError(f"lse: a contiguous float32 [{cfg.n_heads}, {T}] tensor")
+    return _ptr(lse)
+
+
+def _ws_arg(ws):
+    if ws is None:
+        return None, 0
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def ub_attn_required_bytes(op, cfg, rows, n_seqs):
+    n = _SZ()
+    _check(_lib.ub_attn_required_bytes(int(op), ctypes.byref(cfg), rows, n_seqs, ctypes.byref(n)))
+    return n.value
+
+
+def ub_kv_append(h, q, k, v, q_out, k_out, inv_freq, cu_seqlens, past_lens, n_seqs, cache, pages, cfg,
+                 stream=None):
+    """q, k, v, q_out, k_out: ``heads(...)`` or None; cache: ``make_kv_cache(...)`` or None; pages:
+    a [sequences, pages] int32 tensor; inv_freq: rotary_dim / 2 floats."""
+    H, G = cfg.n_heads, cfg.n_kv_heads
+    if inv_freq is not None and hasattr(inv_freq, "data_ptr"):
+        if inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous() \
+                or inv_freq.numel() < cfg.rotary_dim // 2:
+            raise ValueError(f"inv_freq: at least {cfg.rotary_dim // 2} contiguous float32 values")
+    table, ld, per_seq = _table(pages, n_seqs)
+    _check(_lib.ub_kv_append(
+        h, _heads_arg(q, H, cfg, "q"), _heads_arg(k, G, cfg, "k"), _heads_arg(v, G, cfg, "v"),
+        _heads_arg(q_out, H, cfg, "q_out"), _heads_arg(k_out, G, cfg, "k_out"), _ptr(inv_freq),
+        _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), _int32(past_lens, n_seqs, "past_lens"), n_seqs,
+        _cache_arg(cache, cfg), table, ld, per_seq, ctypes.byref(cfg), _stream(stream)), h)
+
+
+def ub_attn_prompt(h, q, k, v, out, lse, cu_seqlens, n_seqs, cfg, workspace=None, stream=None):
+    H, G = cfg.n_heads, cfg.n_kv_heads
+    _check(_lib.ub_attn_prompt(
+        h, _heads_arg(q, H, cfg, "q"), _heads_arg(k, G, cfg, "k"), _heads_arg(v, G, cfg, "v"),
+        _heads_arg(out, H, cfg, "out"), _lse_arg(lse, h, cfg), _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"),
+        n_seqs, ctypes.byref(cfg), *_ws_arg(workspace), _stream(stream)), h)
+
+
+def ub_attn_prompt_bwd(h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens, n_seqs, cfg, workspace,
+                       stream=None):
+    H, G = cfg.n_heads, cfg.n_kv_heads
+    _check(_lib.ub_attn_prompt_bwd(
+        h, _heads_arg(dout, H, cfg, "dout"), _heads_arg(q, H, cfg, "q"), _heads_arg(k, G, cfg, "k"),
+        _heads_arg(v, G, cfg, "v"), _heads_arg(out, H, cfg, "out"), _lse_arg(lse, h, cfg),
+        _heads_arg(dq, H, cfg, "dq"), _heads_arg(dk, G, cfg, "dk"), _heads_arg(dv, G, cfg, "dv"),
+        _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), n_seqs, ctypes.byref(cfg), *_ws_arg(workspace),
+        _stream(stream)), h)
+
+
+def ub_attn_decode(h, q, cache, pages, kv_lens, n_seqs, out, lse, cfg, workspace, stream=None):
+    H = cfg.n_heads
+    _check(_lib.ub_attn_decode(
+        h, _heads_arg(q, H, cfg, "q"), _cache_arg(cache, cfg), *_table(pages, n_seqs),
+        _int32(kv_lens, n_seqs, "kv_lens"), n_seqs, _heads_arg(out, H, cfg, "out"), _lse_arg(lse, h, cfg),
+        ctypes.byref(cfg), *_ws_arg(workspace), _stream(stream)), h)
 
 
 def ub_destroy(h):

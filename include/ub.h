@@ -460,6 +460,164 @@ UB_API ub_status_t ub_quantize_e4m3(const void* src, int64_t lds, void* dst, int
 UB_API ub_status_t ub_reduce_partials(ub_handle_t h, void* out, int64_t ldo,
                                       int32_t reduce_order, ub_stream_t stream);
 
+/* ---- Attention of one tensor-parallel rank over packed (THD) tokens ---------------------
+ *
+ * The step between the two GEMM sides of a rank's attention block: the column-parallel QKV
+ * GEMM (ub_gemm_ag_chunked; [MLM#1240] "QKV" diagram) leaves q, k and v of the rank's heads
+ * side by side in C [T, (n_heads + 2 n_kv_heads) head_dim], and the row-parallel output
+ * projection (ub_gemm_rs_chunked) takes the attention's [T, n_heads head_dim].  The calls
+ * read and write those matrices in place, through row strides.
+ *
+ *   ub_kv_append       position rotation of q and k, and the append of k and v to a paged
+ *                      key-value cache
+ *   ub_attn_prompt     causal attention within each packed sequence
+ *   ub_attn_prompt_bwd its gradient
+ *   ub_attn_decode     attention of one new token per sequence over the paged cache
+ *
+ * Rows.  Every call works on the handle's active rows T (ub_set_active_shape): T rows of
+ * every matrix, of which the packed sequences use a prefix.  Sequence i holds rows
+ * [cu_seqlens[i], cu_seqlens[i + 1]) (cu_seqlens: n_seqs + 1 int32 in device memory, from 0,
+ * non-decreasing, the last at most T).  Sequences may be empty.  Rows that belong to no
+ * sequence (the padding that makes T divisible by tp_size) get zeros in every matrix output
+ * and -inf in lse, whatever their inputs hold.  Of a handle the calls use T, the device
+ * binding and the error message; its buffer, hidden size and dtype play no part.
+ *
+ * Lengths, positions and page tables live in device memory and are never read by the host.
+ * The kernels bound what they address by the host's T, n_seqs, pages_per_seq and n_pages,
+ * so that a bad entry cannot reach outside the caller's buffers: see each call for what it
+ * gives instead.  Their kernels are not counted by ub_set_kernel_timing.
+ *
+ * Heads.  Query head h uses key-value head h / (n_heads / n_kv_heads).  bf16 matrices;
+ * head_dim a multiple of 8 up to UB_ATTN_MAX_HEAD_DIM.  Sums, softmax statistics and
+ * gradient accumulators are fp32; softmax weights and score gradients are rounded to bf16 as
+ * operands of their second products (matrix-core operands); each output is rounded once.
+ * Every call gives the same bits for the same inputs on every run: no sum's order depends
+ * on timing.
+ */
+#define UB_ATTN_MAX_HEAD_DIM 128
+
+typedef struct {
+  int32_t n_heads;          /* query heads of this rank, >= 1 */
+  int32_t n_kv_heads;       /* key-value heads of this rank; divides n_heads */
+  int32_t head_dim;         /* multiple of 8, 8 .. UB_ATTN_MAX_HEAD_DIM */
+  int32_t rotary_dim;       /* rotated leading elements of a head: multiple of 16, 0 .. head_dim */
+  int32_t rope_interleaved; /* 0: element i pairs with i + rotary_dim / 2; 1: 2i with 2i + 1 */
+  float softmax_scale;      /* finite and > 0; multiplies q . k */
+} ub_attn_cfg_t;
+
+/* A [rows, heads, head_dim] bf16 matrix in caller memory.  Element (t, h, d) is at
+ * ptr + t row_stride + h head_stride + d.  ptr 16-byte aligned, strides in elements and
+ * multiples of 8; row_stride < 2^22.  rows: the rows the memory holds; a call needs at
+ * least T (else UB_ERR_BUFFER_TOO_SMALL). */
+typedef struct {
+  void* ptr;
+  int64_t row_stride;
+  int64_t head_stride; /* 0: head_dim */
+  int64_t rows;
+} ub_heads_t;
+
+/* A paged key-value cache.  Token `o` of page p for head g starts at element
+ * p page_stride + g head_stride + o token_stride of k (of v), head_dim elements contiguous.
+ * Strides in elements and multiples of 8 (bf16) or 16 (E4M3), the same for k and v; any order
+ * of heads and tokens; 64-bit offsets.  dtype UB_DTYPE_BF16, or UB_DTYPE_FP8_E4M3: codes
+ * sat(RNE_e4m3(x * scale)) (the rule of ub_quantize_e4m3) that stand for code / scale;
+ * k_scale and v_scale finite and > 0, and not used for bf16.  With E4M3 head_dim must be a
+ * multiple of 16. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t page_stride;
+  int64_t head_stride;
+  int64_t token_stride;
+  int64_t n_pages;
+  int32_t page_size;        /* tokens per page, >= 1 */
+  int32_t dtype;            /* ub_dtype_t */
+  float k_scale, v_scale;
+} ub_kv_cache_t;
+
+typedef enum {
+  UB_ATTN_PROMPT = 0,
+  UB_ATTN_PROMPT_BWD = 1,
+  UB_ATTN_DECODE = 2,
+  UB_ATTN_OP_INT32_RANGE_ = 0x7FFFFFFF
+} ub_attn_op_t;
+
+/* Bytes of device workspace a call of `op` needs at up to `rows` active rows and `n_seqs`
+ * sequences (non-decreasing in both; may be 0).  The workspace is the caller's, 16-byte
+ * aligned.  For UB_ATTN_DECODE it must be zero before its first use (e.g. torch.zeros)
+ * and every call leaves the part that has to be zero at zero; the other ops' workspaces need
+ * no preparation.  Calls that overlap on different streams need workspaces of their own, and
+ * different ops must not share a decode workspace.  UB_ERR_INVALID_ARG for a bad cfg (as for
+ * the calls), rows or n_seqs < 0, or another op. */
+UB_API ub_status_t ub_attn_required_bytes(ub_attn_op_t op, const ub_attn_cfg_t* cfg, int64_t rows,
+                                          int32_t n_seqs, size_t* bytes);
+
+/* Position rotation and cache append.  Row t = cu_seqlens[i] + j of sequence i is the token
+ * at position pos = past_lens[i] + j.  With angle_m = pos * inv_freq[m], m < rotary_dim / 2, a
+ * pair (a, b) of q and of k becomes (a cos - b sin, b cos + a sin); the angle is reduced in
+ * 64 bits.  Elements past rotary_dim are copied.
+ *   q, q_out   rotated queries; both NULL: no queries.
+ *   k          needed unless cache and k_out are both NULL.
+ *   k_out      rotated keys as bf16, or NULL.
+ *   v          needed with a cache.
+ *   inv_freq   rotary_dim / 2 floats (ignored if rotary_dim is 0).  Negated frequencies undo
+ *              the rotation: with q = dq, q_out = dq and k = k_out = dk the call turns the
+ *              gradients of rotated queries and keys into those of the projections.
+ *   past_lens  n_seqs int32 (NULL: all 0).
+ *   cache      NULL: no append.  Key and value of the token go to page
+ *              page_table[i pages_ld + pos / page_size], token pos % page_size, rounded once
+ *              from fp32.  A token is not stored if its position is negative or past
+ *              pages_per_seq pages, or its page id is outside [0, n_pages).  Tokens that
+ *              share a slot leave one of their values in each element.
+ * q_out may be q, and k_out may be k, with the same strides (in place). */
+UB_API ub_status_t ub_kv_append(ub_handle_t h, const ub_heads_t* q, const ub_heads_t* k,
+                                const ub_heads_t* v, const ub_heads_t* q_out,
+                                const ub_heads_t* k_out, const float* inv_freq,
+                                const int32_t* cu_seqlens, const int32_t* past_lens,
+                                int32_t n_seqs, const ub_kv_cache_t* cache,
+                                const int32_t* page_table, int64_t pages_ld,
+                                int32_t pages_per_seq, const ub_attn_cfg_t* cfg,
+                                ub_stream_t stream);
+
+/* Causal attention within each sequence: with rows t and u <= t of one sequence and
+ * s = softmax_scale q[t, h] . k[u, g],
+ *   lse[h, t] = log sum_u exp(s),   out[t, h] = sum_u exp(s - lse[h, t]) v[u, g].
+ * lse: [n_heads, T] fp32, head h at lse + h T; NULL: not written.  workspace may be NULL when
+ * ub_attn_required_bytes gives 0. */
+UB_API ub_status_t ub_attn_prompt(ub_handle_t h, const ub_heads_t* q, const ub_heads_t* k,
+                                  const ub_heads_t* v, const ub_heads_t* out, float* lse,
+                                  const int32_t* cu_seqlens, int32_t n_seqs,
+                                  const ub_attn_cfg_t* cfg, void* workspace,
+                                  size_t workspace_bytes, ub_stream_t stream);
+
+/* Gradient of ub_attn_prompt.  out and lse are what ub_attn_prompt gave for q, k, v at the
+ * same T.  With P = exp(s - lse), delta[h, t] = dout[t, h] . out[t, h] and
+ * dS = P (dout v^T - delta):
+ *   dq[t, h] = softmax_scale sum_u dS k[u, g],   dk[u, g] = softmax_scale sum_{t, h of g} dS q[t, h],
+ *   dv[u, g] = sum_{t, h of g} P dout[t, h].
+ * dq, dk, dv are overwritten.  They may share a matrix (its q, k and v columns) but must
+ * not overlap the inputs. */
+UB_API ub_status_t ub_attn_prompt_bwd(ub_handle_t h, const ub_heads_t* dout, const ub_heads_t* q,
+                                      const ub_heads_t* k, const ub_heads_t* v,
+                                      const ub_heads_t* out, const float* lse,
+                                      const ub_heads_t* dq, const ub_heads_t* dk,
+                                      const ub_heads_t* dv, const int32_t* cu_seqlens,
+                                      int32_t n_seqs, const ub_attn_cfg_t* cfg, void* workspace,
+                                      size_t workspace_bytes, ub_stream_t stream);
+
+/* Attention of one new token per sequence.  Row i < n_seqs <= T of q is sequence i's token;
+ * it attends to cache positions u < kv_lens[i] (its own key already appended):
+ *   lse[h, i] = log sum_u exp(s),   out[i, h] = sum_u exp(s - lse[h, i]) v[u, g].
+ * Rows of sequences of length 0 (or less), and rows from n_seqs to T, get out 0 and lse -inf.
+ * A sequence whose length reaches past pages_per_seq pages, or that has a page id outside
+ * [0, n_pages) among the pages its length covers, gets NaN in out and lse.  What the cache
+ * holds past a sequence's length does not matter.  lse: [n_heads, T] fp32 or NULL. */
+UB_API ub_status_t ub_attn_decode(ub_handle_t h, const ub_heads_t* q, const ub_kv_cache_t* cache,
+                                  const int32_t* page_table, int64_t pages_ld,
+                                  int32_t pages_per_seq, const int32_t* kv_lens, int32_t n_seqs,
+                                  const ub_heads_t* out, float* lse, const ub_attn_cfg_t* cfg,
+                                  void* workspace, size_t workspace_bytes, ub_stream_t stream);
+
 /* Per-launch kernel timing.  enable 1: every GEMM and reduction launch is bracketed by HIP
  * events on the stream it is launched on: a start event recorded before it, and an end
  * event that the call's last kernel launch takes (hipExtLaunchKernel's stop event, the
