@@ -446,33 +446,44 @@ def make_kv_cache(k, v, k_scale=1.0, v_scale=1.0):
     return c
 
 
+# A call's own cost is a few microseconds, as much as a small batch's kernel: descriptors are
+# checked against a head layout once, and tensors with as few attribute reads as it takes.
 def _heads_arg(x, n, cfg, what):
-    """A pointer to x's struct, once its columns are known to hold n heads."""
+    """x, once its columns are known to hold n heads."""
     if x is None:
         return None
-    t = getattr(x, "tensor", None)
-    if t is not None:
-        if t.dim() == 3 and (t.shape[1] < n or t.shape[2] < cfg.head_dim):
-            raise ValueError(f"{what}: {tuple(t.shape)} does not hold {n} heads of {cfg.head_dim}")
-        if t.dim() == 2 and x.col + n * cfg.head_dim > t.shape[1]:
-            raise ValueError(f"{what}: columns {x.col} to {x.col + n * cfg.head_dim} of {t.shape[1]}")
-    return ctypes.byref(x)
+    D = cfg.head_dim
+    if getattr(x, "held", None) != (n, D):
+        t = getattr(x, "tensor", None)
+        if t is not None:
+            if t.dim() == 3 and (t.shape[1] < n or t.shape[2] < D):
+                raise ValueError(f"{what}: {tuple(t.shape)} does not hold {n} heads of {D}")
+            if t.dim() == 2 and x.col + n * D > t.shape[1]:
+                raise ValueError(f"{what}: columns {x.col} to {x.col + n * D} of {t.shape[1]}")
+            x.held = (n, D)
+    return x
 
 
 def _cache_arg(cache, cfg):
     if cache is None:
         return None
-    for t in getattr(cache, "tensors", ()):
-        if t.shape[1] < cfg.n_kv_heads or t.shape[3] < cfg.head_dim:
-            raise ValueError(f"cache: {tuple(t.shape)} does not hold {cfg.n_kv_heads} heads of {cfg.head_dim}")
-    return ctypes.byref(cache)
+    n, D = cfg.n_kv_heads, cfg.head_dim
+    if getattr(cache, "held", None) != (n, D):
+        tensors = getattr(cache, "tensors", ())
+        for t in tensors:
+            if t.shape[1] < n or t.shape[3] < D:
+                raise ValueError(f"cache: {tuple(t.shape)} does not hold {n} heads of {D}")
+        if tensors:
+            cache.held = (n, D)
+    return cache
 
 
 def _int32(x, n, what):
     """A pointer to at least n contiguous int32 values."""
-    if x is not None and hasattr(x, "data_ptr"):
-        if x.dtype != torch.int32 or not x.is_contiguous() or x.numel() < n:
+    if isinstance(x, torch.Tensor):
+        if x.dtype is not torch.int32 or not x.is_contiguous() or x.numel() < n:
             raise ValueError(f"{what}: at least {n} contiguous int32 values")
+        return x.data_ptr()
     return _ptr(x)
 
 
@@ -480,24 +491,31 @@ def _table(pages, n):
     """(pointer, row stride, pages per sequence) of a [sequences, pages] int32 tensor."""
     if pages is None:
         return None, 0, 0
-    if pages.dim() != 2 or pages.dtype != torch.int32 or (pages.numel() and pages.stride(1) != 1) \
-            or pages.shape[0] < n:
-        raise ValueError(f"pages: an int32 [at least {n}, pages] tensor with contiguous rows")
-    return pages.data_ptr(), max(pages.stride(0), pages.shape[1]), pages.shape[1]
+    shape = pages.shape
+    if len(shape) == 2 and pages.dtype is torch.int32:
+        rows, per = shape
+        ld, one = pages.stride()
+        if rows >= n and (one == 1 or rows * per == 0):
+            return pages.data_ptr(), ld if ld > per else per, per
+    raise ValueError(f"pages: an int32 [at least {n}, pages] tensor with contiguous rows")
 
 
-def _lse_arg(lse, h, cfg):
-    if lse is not None and hasattr(lse, "data_ptr"):
-        T = ub_get_active_shape(h)[0]
-        if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.numel() < cfg.n_heads * T:
-            raise ValueError(f"lse: a contiguous float32 [{cfg.n_heads}, {T}] tensor")
+def _lse_arg(lse, h, cfg, out):
+    """A call needs n_heads T values.  It refuses an `out` of fewer than T rows, so as many per
+    row of `out` are enough; asking the handle for T costs a call of its own."""
+    if isinstance(lse, torch.Tensor):
+        n, H = lse.numel(), cfg.n_heads
+        if lse.dtype is not torch.float32 or not lse.is_contiguous() or \
+                ((out is None or n < H * out.rows) and n < H * ub_get_active_shape(h)[0]):
+            raise ValueError(f"lse: a contiguous float32 [{H}, {ub_get_active_shape(h)[0]}] tensor")
+        return lse.data_ptr()
     return _ptr(lse)
 
 
 def _ws_arg(ws):
     if ws is None:
         return None, 0
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def ub_attn_required_bytes(op, cfg, rows, n_seqs):
@@ -511,24 +529,27 @@ def ub_kv_append(h, q, k, v, q_out, k_out, inv_freq, cu_seqlens, past_lens, n_se
     """q, k, v, q_out, k_out: ``heads(...)`` or None; cache: ``make_kv_cache(...)`` or None; pages:
     a [sequences, pages] int32 tensor; inv_freq: rotary_dim / 2 floats."""
     H, G = cfg.n_heads, cfg.n_kv_heads
-    if inv_freq is not None and hasattr(inv_freq, "data_ptr"):
-        if inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous() \
+    if isinstance(inv_freq, torch.Tensor):
+        if inv_freq.dtype is not torch.float32 or not inv_freq.is_contiguous() \
                 or inv_freq.numel() < cfg.rotary_dim // 2:
             raise ValueError(f"inv_freq: at least {cfg.rotary_dim // 2} contiguous float32 values")
+        inv_freq = inv_freq.data_ptr()
+    else:
+        inv_freq = _ptr(inv_freq)
     table, ld, per_seq = _table(pages, n_seqs)
     _check(_lib.ub_kv_append(
         h, _heads_arg(q, H, cfg, "q"), _heads_arg(k, G, cfg, "k"), _heads_arg(v, G, cfg, "v"),
-        _heads_arg(q_out, H, cfg, "q_out"), _heads_arg(k_out, G, cfg, "k_out"), _ptr(inv_freq),
+        _heads_arg(q_out, H, cfg, "q_out"), _heads_arg(k_out, G, cfg, "k_out"), inv_freq,
         _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), _int32(past_lens, n_seqs, "past_lens"), n_seqs,
-        _cache_arg(cache, cfg), table, ld, per_seq, ctypes.byref(cfg), _stream(stream)), h)
+        _cache_arg(cache, cfg), table, ld, per_seq, cfg, _stream(stream)), h)
 
 
 def ub_attn_prompt(h, q, k, v, out, lse, cu_seqlens, n_seqs, cfg, workspace=None, stream=None):
     H, G = cfg.n_heads, cfg.n_kv_heads
     _check(_lib.ub_attn_prompt(
         h, _heads_arg(q, H, cfg, "q"), _heads_arg(k, G, cfg, "k"), _heads_arg(v, G, cfg, "v"),
-        _heads_arg(out, H, cfg, "out"), _lse_arg(lse, h, cfg), _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"),
-        n_seqs, ctypes.byref(cfg), *_ws_arg(workspace), _stream(stream)), h)
+        _heads_arg(out, H, cfg, "out"), _lse_arg(lse, h, cfg, out),
+        _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), n_seqs, cfg, *_ws_arg(workspace), _stream(stream)), h)
 
 
 def ub_attn_prompt_bwd(h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens, n_seqs, cfg, workspace,
@@ -536,18 +557,17 @@ def ub_attn_prompt_bwd(h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens, n_seq
     H, G = cfg.n_heads, cfg.n_kv_heads
     _check(_lib.ub_attn_prompt_bwd(
         h, _heads_arg(dout, H, cfg, "dout"), _heads_arg(q, H, cfg, "q"), _heads_arg(k, G, cfg, "k"),
-        _heads_arg(v, G, cfg, "v"), _heads_arg(out, H, cfg, "out"), _lse_arg(lse, h, cfg),
+        _heads_arg(v, G, cfg, "v"), _heads_arg(out, H, cfg, "out"), _lse_arg(lse, h, cfg, out),
         _heads_arg(dq, H, cfg, "dq"), _heads_arg(dk, G, cfg, "dk"), _heads_arg(dv, G, cfg, "dv"),
-        _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), n_seqs, ctypes.byref(cfg), *_ws_arg(workspace),
-        _stream(stream)), h)
+        _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), n_seqs, cfg, *_ws_arg(workspace), _stream(stream)), h)
 
 
 def ub_attn_decode(h, q, cache, pages, kv_lens, n_seqs, out, lse, cfg, workspace, stream=None):
     H = cfg.n_heads
     _check(_lib.ub_attn_decode(
         h, _heads_arg(q, H, cfg, "q"), _cache_arg(cache, cfg), *_table(pages, n_seqs),
-        _int32(kv_lens, n_seqs, "kv_lens"), n_seqs, _heads_arg(out, H, cfg, "out"), _lse_arg(lse, h, cfg),
-        ctypes.byref(cfg), *_ws_arg(workspace), _stream(stream)), h)
+        _int32(kv_lens, n_seqs, "kv_lens"), n_seqs, _heads_arg(out, H, cfg, "out"),
+        _lse_arg(lse, h, cfg, out), cfg, *_ws_arg(workspace), _stream(stream)), h)
 
 
 def ub_destroy(h):
