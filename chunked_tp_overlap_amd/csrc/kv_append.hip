@@ -8,15 +8,17 @@
 // and a precise sine and cosine.  A workgroup therefore computes the (cos, sin) pairs of its
 // tokens once into LDS, where all their heads read them.  The same pass looks up each
 // token's sequence (a ballot over 64 boundaries at a time: one load's latency instead of a
-// binary search's chain) and its cache slot.
+// binary search's chain) and its cache slot, a token to a lane.
 //
 // Items: a rotary item is 8 pairs (two 16-byte vectors of one head), a copy item is one
-// 16-byte vector (elements past rotary_dim, and v).  Items of one token are numbered head by
-// head, so that neighbouring threads take neighbouring addresses.
+// 16-byte vector (elements past rotary_dim, and v).  Items come in five sections (rotated q,
+// rotated k, the rest of q, the rest of k, v), each numbered token by token and head by
+// head; a wave takes 64 items of one section at a time, so that its lanes do the same work:
+// with sections mixed in a wave every wave ran the E4M3 conversion's instructions.  The next
+// items are loaded before the present ones are finished, the first ones before the lookup.
 #include <hip/hip_runtime.h>
 
 #include "attn_internal.h"
-#include "e4m3.h"
 #include "gemm_common.h"
 #include "kv_pages.h"
 
@@ -24,15 +26,23 @@ namespace ubx {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int MAX_TOKENS = 8;  // tokens of a workgroup
+constexpr int WAVES = THREADS / 64;
+constexpr int MAX_TOKENS = 8;   // tokens of a workgroup
 constexpr int MAX_HALF = UB_ATTN_MAX_HEAD_DIM / 2;
+enum { ROT_Q, ROT_K, REST_Q, REST_K, VALUES, SECTIONS };
+
+struct Section {
+  int32_t n;         // items per token
+  int32_t per;       // items per head
+  float inv_n;       // 1 / n
+  uint32_t per_inv;  // ceil(2^32 / per)
+  int32_t task_end;  // waves' tasks of this section and the ones before
+};
 
 struct AppendParams {
   AppendArgs a;
-  int32_t tokens;      // tokens of a workgroup
-  int32_t rot_per_head, copy_per_head, v_per_head;  // items
-  int32_t n_rot, n_copy, n_items;                   // per token
-  int32_t qh;                                       // query heads handled (0 without q)
+  int32_t tokens;  // tokens of a workgroup
+  Section s[SECTIONS];
 };
 
 struct Token {
@@ -44,14 +54,29 @@ struct Token {
 __device__ inline float lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ inline float hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
+// E4M3 codes of 4 values: the rule of e4m3.h by the hardware's conversion, which rounds to
+// nearest even but neither saturates (so values past 448 are cut first; NaN passes) nor keeps
+// a NaN's sign (so the signs are put in from the values).
+__device__ inline uint32_t e4m3x4(const float* x, float scale) {
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[i] = x[i] * scale;
+    if (fabsf(y[i]) > 448.0f) y[i] = copysignf(448.0f, y[i]);
+  }
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+  // top bytes of the four values
+  const uint32_t tops = __builtin_amdgcn_perm(__float_as_uint(y[1]), __float_as_uint(y[0]), 0x0C0C0703u) |
+                        __builtin_amdgcn_perm(__float_as_uint(y[3]), __float_as_uint(y[2]), 0x07030C0Cu);
+  return ((uint32_t)w & 0x7F7F7F7Fu) | (tops & 0x80808080u);
+}
+
 // 8 values to a cache slot: bf16, or E4M3 codes of x * scale.
 __device__ inline void store_cache(const KvCache& c, void* base, int64_t off, const float* x,
                                    float scale) {
   if (c.e4m3) {
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i / 4] |= e4m3(x[i] * scale) << (8 * (i % 4));
-    uint2 o = make_uint2(w[0], w[1]);
+    uint2 o = make_uint2(e4m3x4(x, scale), e4m3x4(x + 4, scale));
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + off) = o;
   } else {
     u32x4 o;
@@ -76,29 +101,87 @@ __device__ inline void unpack(u32x4 v, float* x) {
   }
 }
 
+// A lane's item of a wave's task, loaded.
+struct Item {
+  int sec;     // the wave's section
+  bool valid;
+  int j, head, e0, e1;  // token of the workgroup, head, first elements of its vectors
+  u32x4 x, y;
+};
+
+__device__ inline Item load_item(const AppendParams& p, int task, int t0, int nt, int lane) {
+  const AppendArgs& a = p.a;
+  Item w;
+  w.sec = 0;
+  int base = 0;
+#pragma unroll
+  for (int i = 0; i + 1 < SECTIONS; ++i)
+    if (task >= p.s[i].task_end) {
+      w.sec = i + 1;
+      base = p.s[i].task_end;
+    }
+  const Section s = p.s[w.sec];
+  const int i = (task - base) * 64 + lane;
+  // i / n: both under 2^24, so the product is off by less than one
+  w.j = (int)((float)i * s.inv_n);
+  int it = i - w.j * s.n;
+  if (it < 0) {
+    --w.j;
+    it += s.n;
+  } else if (it >= s.n) {
+    ++w.j;
+    it -= s.n;
+  }
+  w.valid = task < p.s[SECTIONS - 1].task_end && w.j < nt;
+  w.head = s.per == 1 ? it : (int)__umulhi((uint32_t)it, s.per_inv);
+  const int c = (it - w.head * s.per) * 8;
+  const bool rot = w.sec <= ROT_K, inter = a.interleaved != 0;
+  w.e0 = rot ? (inter ? 2 * c : c) : (w.sec == VALUES ? c : a.rotary + c);
+  w.e1 = inter ? w.e0 + 8 : w.e0 + a.rotary / 2;
+  w.x = w.y = u32x4{0, 0, 0, 0};
+  if (w.valid) {
+    const Heads& src = w.sec == VALUES ? a.v : (w.sec == ROT_Q || w.sec == REST_Q) ? a.q : a.k;
+    const uint16_t* in = src.p + (int64_t)(t0 + w.j) * src.rs + w.head * src.hs;
+    w.x = *GLOBAL_PTR(const u32x4, in + w.e0);
+    if (rot) w.y = *GLOBAL_PTR(const u32x4, in + w.e1);
+  }
+  return w;
+}
+
 __global__ __launch_bounds__(THREADS) void kv_append(AppendParams p) {
   __shared__ Token tok[MAX_TOKENS];
   __shared__ float2 rot[MAX_TOKENS][MAX_HALF];
   const AppendArgs& a = p.a;
   const int t0 = blockIdx.x * p.tokens;
   const int nt = min(p.tokens, a.seqs.T - t0);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int j = wave; j < nt; j += THREADS / 64) {
-    const int t = t0 + j;
-    // sequences that end at or before row t come first: their number is t's sequence
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tasks = p.s[SECTIONS - 1].task_end;
+  Item w = load_item(p, wave, t0, nt, lane);
+  const int half = a.rotary / 2;
+  const float freq = lane < half ? a.inv_freq[lane] : 0.0f;
+  if (wave == 0) {
+    // lane j: token j of the workgroup.  Sequences that end at or before its row come first:
+    // their number is its sequence
     int seq = 0;
     for (int c = 0; c < a.seqs.n; c += 64) {
       const int i = c + lane;
-      const int m = __popcll(__ballot(i < a.seqs.n && a.seqs.cu[min(i + 1, a.seqs.n)] <= t));
-      seq += m;
-      if (m < 64) break;
+      const int end = i < a.seqs.n ? a.seqs.cu[i + 1] : 0x7FFFFFFF;
+      int more = 0;
+      for (int j = 0; j < nt; ++j) {
+        const int m = __popcll(__ballot(end <= t0 + j));
+        seq += lane == j ? m : 0;
+        more |= m == 64;
+      }
+      if (!more) break;
     }
-    if (lane == 0) {
+    if (lane < nt) {
+      const int t = t0 + lane;
       Token k{-1, 0, 0};
       if (seq < a.seqs.n) {
         const int start = a.seqs.cu[seq];
+        const int past = a.past ? a.past[seq] : 0;
         if (start >= 0 && start <= t) {
-          const int64_t pos = (int64_t)(a.past ? a.past[seq] : 0) + (t - start);
+          const int64_t pos = (int64_t)past + (t - start);
           k.live = 1;
           k.pos = pos;
           const int e = a.cache.k ? page_entry(pos, a.cache.page_size, a.pages_per_seq) : -1;
@@ -107,42 +190,40 @@ __global__ __launch_bounds__(THREADS) void kv_append(AppendParams p) {
                                   a.cache.page_size, a.cache.ps, a.cache.ts);
         }
       }
-      tok[j] = k;
+      tok[lane] = k;
     }
   }
   __syncthreads();
-  const int half = a.rotary / 2;
-  for (int i = threadIdx.x; i < nt * half; i += THREADS) {
-    const int j = i / half, m = i - j * half;
+  for (int j = wave; j < nt; j += WAVES) {
+    if (lane >= half) break;
     // revolutions, reduced in 64 bits; the product pos * inv_freq is exact there
-    double r = (double)tok[j].pos * (double)a.inv_freq[m] * 0.15915494309189533577;
+    double r = (double)tok[j].pos * (double)freq * 0.15915494309189533577;
     r -= rint(r);
     float s, c;
     sincospif(2.0f * (float)r, &s, &c);
-    rot[j][m] = make_float2(c, s);
+    rot[j][lane] = make_float2(c, s);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < nt * p.n_items; i += THREADS) {
-    const int j = i / p.n_items;
-    int it = i - j * p.n_items;
-    const int64_t t = t0 + j;
-    const Token k = tok[j];
-    float x[8], y[8];
-    if (it < p.n_rot) {
-      const int head = it / p.rot_per_head, m = (it - head * p.rot_per_head) * 8;
-      const bool is_q = head < p.qh;
-      const int hh = is_q ? head : head - p.qh;
-      const Heads& src = is_q ? a.q : a.k;
+  for (int task = wave; task < tasks; task += WAVES) {
+    const Item next = load_item(p, task + WAVES, t0, nt, lane);
+    if (w.valid) {
+      const Token k = tok[w.j];
+      const int64_t t = t0 + w.j;
+      float x[8], y[8];
+      unpack(k.live ? w.x : u32x4{0, 0, 0, 0}, x);
+      const bool is_q = w.sec == ROT_Q || w.sec == REST_Q;
       const Heads& dst = is_q ? a.q_out : a.k_out;
-      const int e0 = a.interleaved ? 2 * m : m, e1 = a.interleaved ? 2 * m + 8 : m + half;
-      const uint16_t* in = src.p + t * src.rs + hh * src.hs;
-      if (k.live) {
-        unpack(*reinterpret_cast<const u32x4*>(in + e0), x);
-        unpack(*reinterpret_cast<const u32x4*>(in + e1), y);
+      const bool slot = !is_q && k.slot >= 0;
+      const int64_t off = k.slot + w.head * a.cache.hs;
+      void* const cache = w.sec == VALUES ? a.cache.v : a.cache.k;
+      const float scale = w.sec == VALUES ? a.cache.v_scale : a.cache.k_scale;
+      if (w.sec <= ROT_K) {
+        unpack(k.live ? w.y : u32x4{0, 0, 0, 0}, y);
         if (a.interleaved) {
+          const float2* r = rot[w.j] + w.e0 / 2;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const float2 c0 = rot[j][m + u], c1 = rot[j][m + 4 + u];
+            const float2 c0 = r[u], c1 = r[4 + u];
             const float p0 = x[2 * u], p1 = x[2 * u + 1], r0 = y[2 * u], r1 = y[2 * u + 1];
             x[2 * u] = p0 * c0.x - p1 * c0.y;
             x[2 * u + 1] = p1 * c0.x + p0 * c0.y;
@@ -150,49 +231,22 @@ __global__ __launch_bounds__(THREADS) void kv_append(AppendParams p) {
             y[2 * u + 1] = r1 * c1.x + r0 * c1.y;
           }
         } else {
+          const float2* r = rot[w.j] + w.e0;
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const float2 c = rot[j][m + u];
+            const float2 c = r[u];
             const float p0 = x[u], p1 = y[u];
             x[u] = p0 * c.x - p1 * c.y;
             y[u] = p1 * c.x + p0 * c.y;
           }
         }
-      } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = y[u] = 0.0f;
+        if (dst.p) store_bf16(dst.p + t * dst.rs + w.head * dst.hs + w.e1, y);
+        if (slot) store_cache(a.cache, cache, off + w.e1, y, scale);
       }
-      if (dst.p) {
-        uint16_t* o = dst.p + t * dst.rs + hh * dst.hs;
-        store_bf16(o + e0, x);
-        store_bf16(o + e1, y);
-      }
-      if (!is_q && k.slot >= 0) {
-        const int64_t off = k.slot + hh * a.cache.hs;
-        store_cache(a.cache, a.cache.k, off + e0, x, a.cache.k_scale);
-        store_cache(a.cache, a.cache.k, off + e1, y, a.cache.k_scale);
-      }
-      continue;
+      if (dst.p && w.sec != VALUES) store_bf16(dst.p + t * dst.rs + w.head * dst.hs + w.e0, x);
+      if (slot) store_cache(a.cache, cache, off + w.e0, x, scale);
     }
-    it -= p.n_rot;
-    const bool is_v = it >= p.n_copy;
-    if (is_v) it -= p.n_copy;
-    const int per = is_v ? p.v_per_head : p.copy_per_head;
-    const int head = it / per, e = (is_v ? 0 : a.rotary) + (it - head * per) * 8;
-    const bool is_q = !is_v && head < p.qh;
-    const int hh = is_v || is_q ? head : head - p.qh;
-    const Heads& src = is_v ? a.v : is_q ? a.q : a.k;
-    const Heads& dst = is_q ? a.q_out : a.k_out;
-    if (k.live) {
-      unpack(*reinterpret_cast<const u32x4*>(src.p + t * src.rs + hh * src.hs + e), x);
-    } else {
-#pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = 0.0f;
-    }
-    if (!is_v && dst.p) store_bf16(dst.p + t * dst.rs + hh * dst.hs + e, x);
-    if (!is_q && k.slot >= 0)
-      store_cache(a.cache, is_v ? a.cache.v : a.cache.k, k.slot + hh * a.cache.hs + e, x,
-                  is_v ? a.cache.v_scale : a.cache.k_scale);
+    w = next;
   }
 }
 
@@ -201,19 +255,35 @@ __global__ __launch_bounds__(THREADS) void kv_append(AppendParams p) {
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s) {
   AppendParams p{};
   p.a = a;
-  p.qh = a.q.p ? a.H : 0;
-  const int kh = a.k.p ? a.G : 0;
-  p.rot_per_head = a.rotary / 16;
-  p.copy_per_head = (a.D - a.rotary) / 8;
-  p.v_per_head = a.D / 8;
-  p.n_rot = (p.qh + kh) * p.rot_per_head;
-  p.n_copy = (p.qh + kh) * p.copy_per_head;
-  p.n_items = p.n_rot + p.n_copy + (a.cache.k ? a.G * p.v_per_head : 0);
-  if (a.seqs.T <= 0 || p.n_items == 0) return hipSuccess;
-  // Few tokens: one per workgroup, for latency.  Many: 8, so that the angles' cost is shared
-  // by more threads and fewer workgroups start.
-  p.tokens = a.seqs.T <= 1024 ? 1 : MAX_TOKENS;
-  const int blocks = (a.seqs.T + p.tokens - 1) / p.tokens;
+  const int qh = a.q.p ? a.H : 0, kh = a.k.p ? a.G : 0, vh = a.cache.k ? a.G : 0;
+  const int pairs = a.rotary / 16, rest = (a.D - a.rotary) / 8;
+  const int heads[SECTIONS] = {qh, kh, qh, kh, vh};
+  const int per[SECTIONS] = {pairs, pairs, rest, rest, a.D / 8};
+  int most = 0;
+  for (int i = 0; i < SECTIONS; ++i) {
+    Section& x = p.s[i];
+    x.n = heads[i] * per[i];
+    x.per = per[i] > 0 ? per[i] : 1;
+    x.inv_n = x.n > 0 ? 1.0f / (float)x.n : 0.0f;
+    x.per_inv = x.per > 1 ? (uint32_t)(((uint64_t(1) << 32) + x.per - 1) / x.per) : 0;
+    if (x.n > most) most = x.n;
+  }
+  if (a.seqs.T <= 0 || most == 0) return hipSuccess;
+  // One token per workgroup of a small call starts soonest; 8 share the angles' and the
+  // lookup's time and leave enough workgroups to even out the CUs' load.  Measured at 8184
+  // tokens (4 + 4 heads, bf16 cache) with 2, 4, 8, 16 tokens: 15.9, 14.9, 13.5, 16.9 us; at
+  // 32520 (8 + 1 heads, E4M3): 53.6, 42.7, 39.7, 45.0 us, 4.0 TB/s.  An item's number stays
+  // under 2^24.
+  int tokens = (a.seqs.T + 1023) / 1024;
+  if (tokens > MAX_TOKENS) tokens = MAX_TOKENS;
+  if (tokens * (int64_t)most + 64 * (WAVES + 1) >= (1 << 24)) tokens = 1;
+  p.tokens = tokens;
+  int end = 0;
+  for (int i = 0; i < SECTIONS; ++i) {
+    end += (int)(((int64_t)p.s[i].n * tokens + 63) / 64);
+    p.s[i].task_end = end;
+  }
+  const int blocks = (a.seqs.T + tokens - 1) / tokens;
   return launch_k(&kv_append, dim3(blocks), dim3(THREADS), 0, s, p);
 }
 

@@ -323,6 +323,59 @@ def test_append_in_place_and_back(ub):
     assert torch.equal(got[:, (H + G) * D:], want[:, (H + G) * D:])
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.37, 6e4])
+def test_append_every_code(ub, scale):
+    """Every bf16 value through an E4M3 cache: the codes ub_quantize_e4m3 gives, NaN's among them."""
+    D, T = 64, 1024
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF16).reshape(T, D).cuda()
+    kc, vc = make_cache(1, D, 16, T // 16, True, False, 5)
+    want = torch.empty((T, D), dtype=torch.uint8, device="cuda")
+    table = torch.arange(T // 16, dtype=torch.int32, device="cuda")[None]
+    with Rank(ub, T) as h:
+        ub.ub_kv_append(h, None, ub.heads(x), ub.heads(x), None, None, None, i32([0, T]), None, 1,
+                        ub.make_kv_cache(kc, vc, scale, scale), table, ub.make_attn_cfg(1, 1, D, rotary_dim=0))
+        ub.ub_quantize_e4m3(x, D, want, D, T, D, scale)
+        torch.cuda.synchronize()
+    for c in (kc, vc):
+        got = raw(c).reshape(T, D)
+        bad = (got != want).flatten().nonzero().flatten()
+        assert not len(bad), [(hex(i), int(got.flatten()[i]), int(want.flatten()[i])) for i in bad[:20].tolist()] + [len(bad)]
+
+
+@pytest.mark.parametrize("T,H,G,D,rotary,inter,f8", [(2500, 6, 3, 80, 48, False, True), (5001, 5, 5, 64, 64, True, False),
+                                                    (34001, 9, 1, 128, 112, True, True)])
+def test_append_many_tokens(ub, T, H, G, D, rotary, inter, f8):
+    """Several tokens to a workgroup, items of every section."""
+    page, past = 64, 100
+    x = normal(7, (T, (H + 2 * G) * D)).cuda()
+    n_pages = -(-(T - 1 + past) // page)
+    table = torch.randperm(n_pages, generator=torch.Generator().manual_seed(2)).to(torch.int32).cuda()[None]
+    kc, vc = make_cache(G, D, page, n_pages, f8, True, 20)
+    inv = (500000.0 ** (-torch.arange(0, rotary, 2, dtype=torch.float64) / rotary)).float().cuda()
+    q_out, k_out = torch.empty((T, H * D), dtype=BF16, device="cuda"), torch.empty((T, G * D), dtype=BF16, device="cuda")
+    with Rank(ub, T) as h:
+        ub.ub_kv_append(h, ub.heads(x), ub.heads(x, H * D), ub.heads(x, (H + G) * D), ub.heads(q_out), ub.heads(k_out),
+                        inv, i32([0, T - 1]), i32([past]), 1, ub.make_kv_cache(kc, vc, 40.0, 60.0), table,
+                        ub.make_attn_cfg(H, G, D, rotary_dim=rotary, rope_interleaved=inter))
+        torch.cuda.synchronize()
+    pos = past + torch.arange(T - 1, device="cuda")
+    y, e = ref.rotate(x[:-1, : (H + G) * D].double().reshape(T - 1, H + G, D), pos, inv, inter, rotary)
+    v = x[:-1, (H + G) * D:].double().reshape(T - 1, G, D)
+    check = lambda got, w, e, what: ref.check(got, w.cpu(), (e * (1 + ref.U16) + ref.U16 * w.abs()).cpu(), what)
+    check(q_out[:-1].reshape(T - 1, H, D), y[:, :H], e[:, :H], "q_out")
+    check(k_out[:-1].reshape(T - 1, G, D), y[:, H:], e[:, H:], "k_out")
+    assert bool((q_out[-1] == 0).all()) and bool((k_out[-1] == 0).all())
+    at = table[0].long()[pos // page], pos % page
+    for c, w, e, sc, what in ((kc, y[:, H:], e[:, H:], 40.0, "k"), (vc, v, torch.zeros_like(v), 60.0, "v")):
+        got = (c.view(torch.uint8) if f8 else c)[at[0], :, at[1]]
+        if f8:
+            w = (w * sc).clamp(-448, 448)
+            tol = (e * sc + 2 * ref.U32 * w.abs()) * (1 + ref.U8) + torch.maximum(ref.U8 * w.abs(), torch.full_like(w, 2.0 ** -10))
+            ref.check(got.cpu().view(F8), w.cpu(), tol.cpu(), what)
+        else:
+            check(got, w, e, what)
+
+
 def test_append_bad_pages(ub):
     """Tokens whose page is missing (negative position, past the table, a bad id) are not
     stored; the others are."""
