@@ -544,11 +544,9 @@ typedef enum {
 
 /* Bytes of device workspace a call of `op` needs at up to `rows` active rows and `n_seqs`
  * sequences (non-decreasing in both; may be 0).  The workspace is the caller's, 16-byte
- * aligned.  For UB_ATTN_DECODE it must be zero before its first use (e.g. torch.zeros)
- * and every call leaves the part that has to be zero at zero; the other ops' workspaces need
- * no preparation.  Calls that overlap on different streams need workspaces of their own, and
- * different ops must not share a decode workspace.  UB_ERR_INVALID_ARG for a bad cfg (as for
- * the calls), rows or n_seqs < 0, or another op. */
+ * aligned, and needs no preparation.  Calls that overlap on different streams need workspaces
+ * of their own.  UB_ERR_INVALID_ARG for a bad cfg (as for the calls), rows or n_seqs < 0, or
+ * another op. */
 UB_API ub_status_t ub_attn_required_bytes(ub_attn_op_t op, const ub_attn_cfg_t* cfg, int64_t rows,
                                           int32_t n_seqs, size_t* bytes);
 

@@ -470,6 +470,19 @@ def test_decode(ub, H, G, D, lens, page, f8, token_major, pad):
     assert bool((out[n:] == 0).all()) and bool((lse[:, n:] == -math.inf).all())
 
 
+
+@pytest.mark.parametrize("H,G,D,lens,page,f8,token_major,pad", [
+    (4, 2, 128, [0, 1, 31, 32, 33, 500, 2000] * 30, 16, True, True, 1),   # parts within and across ranges
+    (4, 2, 128, [700, 0, 64, 5000] * 20, 48, False, False, 0),
+    (3, 3, 72, [0, 257, 4100] * 25, 24, False, True, 0),                   # pages that a block of tokens leaves
+    (2, 2, 48, [9000, 40, 17000], 32, True, False, 0),                    # over 32 steps of a wave
+    (1, 1, 128, [70000], 16, False, False, 0),
+    (600, 600, 16, [40, 90], 16, False, False, 0),                        # more heads than workgroups at once
+])
+def test_decode_ranges(ub, H, G, D, lens, page, f8, token_major, pad):
+    test_decode(ub, H, G, D, lens, page, f8, token_major, pad)
+
+
 def test_decode_bad_tables(ub):
     """A length past the table, a bad page id: NaN for that sequence, the others as ever."""
     H, G, D, page = 4, 2, 64, 16
