@@ -40,22 +40,26 @@ struct Tile {
 };
 
 // A wave's share of the direct-to-LDS loads of a tile of ROWS rows by NW waves: the byte
-// offsets of its lanes' 16-byte pieces from the tile's first row (OOB past head_dim).
+// offset of its lanes' 16-byte pieces from the tile's first row (OOB past head_dim).  The
+// instructions' rows lie RPI NW apart; the swizzle repeats every 16 rows, so only the first
+// P offsets are kept.
 template <int DS, int ROWS, int NW>
 struct TileLoad {
   using L = Tile<DS>;
   static constexpr int RPI = 64 / L::CPR;          // rows per wave instruction
   static constexpr int N = ROWS / RPI / NW;        // instructions per wave
+  static constexpr int P = RPI * NW >= 16 ? 1 : 16 / (RPI * NW);
   static_assert(N >= 1 && N * RPI * NW == ROWS, "rows must divide over the waves");
-  uint32_t off[N];
+  uint32_t off[P], step;
 
   __device__ void init(int wave, int lane, int64_t row_stride, int D) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
+    for (int j = 0; j < P; ++j) {
       const int row = (j * NW + wave) * RPI + lane / L::CPR;
       const int chunk = (lane % L::CPR) ^ L::swz(row);
       off[j] = chunk * 8 < D ? (uint32_t)row * (uint32_t)(row_stride * 2) + chunk * 16 : OOB;
     }
+    step = P * RPI * NW * (uint32_t)(row_stride * 2);  // N steps from OOB stay under 2^32
   }
   // rows [0, valid) at base; the others read as zeros
   __device__ void issue(const uint16_t* base, int64_t row_stride, int D, int valid, uint32_t lds,
@@ -65,22 +69,24 @@ struct TileLoad {
                                      : 0u;
     const i32x4 rsrc = make_rsrc(base, bytes);
 #pragma unroll
-    for (int j = 0; j < N; ++j) dma16(rsrc, lds + (j * NW + wave) * 1024, off[j]);
+    for (int j = 0; j < N; ++j) dma16(rsrc, lds + (j * NW + wave) * 1024, off[j % P] + j / P * step);
   }
 };
 
-// Row fragment: rows 16 b .. 16 b + 15 of the tile, columns 32 s .. 32 s + 31.
+// Row fragment: rows 16 b .. 16 b + 15 of the tile, columns 32 s .. 32 s + 31.  The lane's
+// chunk (4 s + g) ^ swz is that of s = 0 with bits changed by 4 s, so one address (of a tile on
+// a 256-byte boundary) serves all.
 template <int DS>
 struct RowFrag {
   using L = Tile<DS>;
-  const unsigned char* p[DS];
+  const unsigned char* p;
   __device__ void init(const unsigned char* tile, int lane) {
     const int c = lane & 15, g = lane >> 4;
-#pragma unroll
-    for (int s = 0; s < DS; ++s) p[s] = tile + c * L::RB + (((4 * s + g) ^ L::swz(c)) * 16);
+    p = tile + c * L::RB + ((g ^ L::swz(c)) * 16);
   }
   __device__ bf16x8 read(int off, int b, int s) const {
-    return *LDS_PTR(const bf16x8, p[s] + off + b * 16 * L::RB);
+    const uint32_t at = ((uint32_t)(size_t)LDS_PTR(const unsigned char, p) + off) ^ (64 * s);
+    return *LDS_PTR(const bf16x8, at + b * 16 * L::RB);
   }
 };
 
@@ -89,16 +95,15 @@ struct RowFrag {
 template <int DS>
 struct ColFrag {
   using L = Tile<DS>;
-  const unsigned char* p[L::DB];
+  const unsigned char* p;
   __device__ void init(const unsigned char* tile, int lane) {
     const int c = lane & 15, g = lane >> 4;
     const int row = 4 * g + (c >> 2);
-#pragma unroll
-    for (int d = 0; d < L::DB; ++d)
-      p[d] = tile + row * L::RB + (((2 * d + ((c >> 1) & 1)) ^ L::swz(row)) * 16) + 8 * (c & 1);
+    p = tile + row * L::RB + ((((c >> 1) & 1) ^ L::swz(row)) * 16) + 8 * (c & 1);
   }
   __device__ bf16x8 read(int off, int t, int d) const {
-    const unsigned char* q = p[d] + off + t * 32 * L::RB;
+    const uint32_t at = ((uint32_t)(size_t)LDS_PTR(const unsigned char, p) + off) ^ (32 * d);
+    const uint32_t q = at + t * 32 * L::RB;
     const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, q));
     const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, q + 16 * L::RB));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -138,6 +143,11 @@ __device__ inline bf16x8 load_row8(const uint16_t* p, bool valid) {
   if (valid) v = *GLOBAL_PTR(const u32x4, p);
   return __builtin_bit_cast(bf16x8, v);
 }
+
+// Makes the compiler wait here for a value it loads.  It does not count the direct-to-LDS
+// loads, so a wait that it left to a value's first use, inside a loop, would be one for all
+// loads in flight there: the next tile's among them, in every iteration.
+__device__ inline void arrived(bf16x8& x) { __asm__ volatile("" : "+v"(x)); }
 
 // Sum over the wave's 64 lanes, the same value in all of them.
 __device__ inline int wave_sum(int v) {

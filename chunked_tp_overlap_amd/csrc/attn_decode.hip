@@ -162,7 +162,7 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
   constexpr int SMEM = NW * TILE > MERGE ? NW * TILE : MERGE;
   constexpr int EB = Y::EB, KV = Y::KV, VPR = Y::VPR, VI = Y::VI;
   constexpr int RPI = 64 / VPR;  // value rows of a load
-  __shared__ __align__(16) unsigned char smem[SMEM];
+  __shared__ __align__(256) unsigned char smem[SMEM];
   const DecodeArgs& a = p.a;
   const int GQ = a.G * p.qb;
   const int gq = blockIdx.x % GQ, rank = blockIdx.x / GQ;

@@ -19,8 +19,7 @@
 namespace ubx {
 namespace {
 
-constexpr int NW = 4;
-constexpr int BN = 64;
+constexpr float SLACK = 8.0f;  // powers of two a score may pass its row's reference by
 
 struct PromptParams {
   PromptArgs a;
@@ -41,36 +40,48 @@ __device__ inline void fill_pad(const PromptArgs& a, int head, int rank, int ran
   }
 }
 
-template <int DS, int QF>
-__global__ __launch_bounds__(64 * NW, 2) void attn_prompt(PromptParams p) {
+// RW waves of 16 QF rows each, KG times: group kg of RW waves takes the key tiles (BN rows)
+// kg, kg + KG, ...
+template <int DS_, int QF_, int RW_, int KG_, int BN_>
+struct Shape {
+  static constexpr int DS = DS_, QF = QF_, RW = RW_, KG = KG_, BN = BN_;
   using L = Tile<DS>;
-  constexpr int BM = 16 * QF * NW;
+  static constexpr int NW = RW * KG, BM = 16 * QF * RW, TILE = BN * L::RB;
+  static constexpr int STAGE = KG * 2 * TILE;                 // the groups' key and value tiles
+  static constexpr int PART = L::DB * QF * 64 * 16;           // a wave's output, for the join
+  static constexpr int STAT = NW * QF * 16 * 8;
+  static constexpr int LDS = KG == 1 || 2 * STAGE > NW * PART + STAT ? 2 * STAGE : NW * PART + STAT;
+};
+
+template <class S>
+__global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
+  constexpr int DS = S::DS, QF = S::QF, KG = S::KG, BN = S::BN, BM = S::BM, TILE = S::TILE;
+  using L = Tile<DS>;
   constexpr int KB = BN / 16;
-  constexpr int TILE = BN * L::RB;
-  extern __shared__ unsigned char smem[];
+  extern __shared__ __align__(256) unsigned char smem[];
   const PromptArgs& a = p.a;
   const int head = blockIdx.x % a.H, rank = blockIdx.x / a.H;
   fill_pad(a, head, rank, p.ranks);
   const SeqTile st = find_tile(a.seqs, BM, rank, false);
   if (st.len == 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rw = wave % S::RW, kg = wave / S::RW;
   const int col = lane & 15, g = lane >> 4;
   const int kvh = head / (a.H / a.G);
   const int q0 = st.tile * BM;
-  const int wq0 = q0 + wave * 16 * QF;  // the wave's first query
+  const int wq0 = q0 + rw * 16 * QF;  // the wave's first query
   const int n_keys = min(q0 + BM, st.len);
   const int tiles = (n_keys + BN - 1) / BN;
   const uint16_t* kbase = a.k.p + (int64_t)st.row0 * a.k.rs + kvh * a.k.hs;
   const uint16_t* vbase = a.v.p + (int64_t)st.row0 * a.v.rs + kvh * a.v.hs;
 
-  TileLoad<DS, BN, NW> kl, vl;
-  kl.init(wave, lane, a.k.rs, a.D);
-  vl.init(wave, lane, a.v.rs, a.D);
-  const uint32_t lds = lds_addr(smem);
-  auto load = [&](int j, int stage) {
-    kl.issue(kbase + (int64_t)j * BN * a.k.rs, a.k.rs, a.D, st.len - j * BN, lds + stage * 2 * TILE, wave);
-    vl.issue(vbase + (int64_t)j * BN * a.v.rs, a.v.rs, a.D, st.len - j * BN, lds + stage * 2 * TILE + TILE,
-             wave);
+  TileLoad<DS, BN, S::RW> kl, vl;
+  kl.init(rw, lane, a.k.rs, a.D);
+  vl.init(rw, lane, a.v.rs, a.D);
+  const uint32_t lds = lds_addr(smem) + kg * 2 * TILE;
+  auto load = [&](int j, int stage) {  // rows past the sequence's end read as zeros
+    kl.issue(kbase + (int64_t)j * BN * a.k.rs, a.k.rs, a.D, st.len - j * BN, lds + stage * S::STAGE, rw);
+    vl.issue(vbase + (int64_t)j * BN * a.v.rs, a.v.rs, a.D, st.len - j * BN, lds + stage * S::STAGE + TILE, rw);
   };
   bf16x8 q[QF][DS];
 #pragma unroll
@@ -80,14 +91,18 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt(PromptParams p) {
 #pragma unroll
     for (int s = 0; s < DS; ++s) q[f][s] = load_row8(row + 32 * s + 8 * g, t < st.len && 32 * s + 8 * g < a.D);
   }
-  load(0, 0);
+#pragma unroll
+  for (int f = 0; f < QF; ++f)
+#pragma unroll
+    for (int s = 0; s < DS; ++s) arrived(q[f][s]);
+  if (kg < tiles) load(kg, 0);
 
   RowFrag<DS> kf;
   ColFrag<DS> vf;
-  kf.init(smem, lane);
-  vf.init(smem + TILE, lane);
+  kf.init(smem + kg * 2 * TILE, lane);
+  vf.init(smem + kg * 2 * TILE + TILE, lane);
   f32x4 o[L::DB][QF];
-  float m[QF], l[QF];
+  float m[QF], l[QF];  // m: the row's reference, at most SLACK / c under its maximum so far
 #pragma unroll
   for (int f = 0; f < QF; ++f) {
     m[f] = -INFINITY;
@@ -95,12 +110,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt(PromptParams p) {
 #pragma unroll
     for (int d = 0; d < L::DB; ++d) o[d][f] = f32x4{0, 0, 0, 0};
   }
-  for (int j = 0; j < tiles; ++j) {
-    const int stage = (j & 1) * 2 * TILE;
+  const int steps = (tiles + KG - 1) / KG;
+  for (int i = 0; i < steps; ++i) {
+    const int j = i * KG + kg;
+    const int stage = (i & 1) * S::STAGE;
     wait_vmcnt_and_barrier<0>();
-    if (j + 1 < tiles) load(j + 1, (j + 1) & 1);
+    if (j + KG < tiles) load(j + KG, (i + 1) & 1);
     const int k0 = j * BN;
-    if (k0 > wq0 + 16 * QF - 1) continue;  // all keys after the wave's queries
+    if (KG > 1 && j >= tiles) continue;
     f32x4 s[KB][QF];
 #pragma unroll
     for (int b = 0; b < KB; ++b)
@@ -124,6 +141,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt(PromptParams p) {
           for (int i = 0; i < 4; ++i)
             if (k0 + b * 16 + 4 * g + i > wq0 + f * 16 + col) s[b][f][i] = -INFINITY;
     }
+    float top[QF];
+    bool above = false;
 #pragma unroll
     for (int f = 0; f < QF; ++f) {
       float x = s[0][f][0];
@@ -131,20 +150,33 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt(PromptParams p) {
       for (int b = 0; b < KB; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x = fmaxf(x, s[b][f][i]);
-      x = fmaxf(col_max(x), m[f]);
-      const float base = x == -INFINITY ? 0.0f : x * p.c;
-      const float r = exp2_(m[f] * p.c - base);  // 0 the first time
-      m[f] = x;
-      l[f] *= r;
+      top[f] = col_max(x);
+      above = above || (top[f] - m[f]) * p.c > SLACK;
+    }
+    if (__ballot(above)) {
+      // the reference moves to the maximum, here and for what was summed so far
 #pragma unroll
-      for (int d = 0; d < L::DB; ++d) o[d][f] *= r;
+      for (int f = 0; f < QF; ++f) {
+        const float x = fmaxf(top[f], m[f]);
+        const float r = exp2_(m[f] * p.c - (x == -INFINITY ? 0.0f : x * p.c));  // 0 the first time
+        m[f] = x;
+        l[f] *= r;
+#pragma unroll
+        for (int d = 0; d < L::DB; ++d) o[d][f] *= r;
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < QF; ++f) {
+      const float base = m[f] == -INFINITY ? 0.0f : m[f] * p.c;
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // short sums, so that a long row's l loses little
 #pragma unroll
       for (int b = 0; b < KB; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           s[b][f][i] = exp2_(s[b][f][i] * p.c - base);
-          l[f] += s[b][f][i];
+          sum[i] += s[b][f][i];
         }
+      l[f] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
 #pragma unroll
     for (int t = 0; t < KB / 2; ++t) {
@@ -160,46 +192,97 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt(PromptParams p) {
       }
     }
   }
+  float base[QF], sum[QF];
+#pragma unroll
+  for (int f = 0; f < QF; ++f) {
+    base[f] = m[f] == -INFINITY ? -INFINITY : m[f] * p.c;
+    sum[f] = col_sum(l[f]);
+  }
+  if (KG > 1) {
+    // Join of the groups: all outputs and statistics through LDS; group kg joins blocks kg,
+    // kg + KG, ... of the columns.
+    __syncthreads();
+    f32x4* parts = reinterpret_cast<f32x4*>(smem);  // [NW][DB][QF][64]
+    float2* stats = reinterpret_cast<float2*>(smem + S::NW * S::PART);  // [NW][QF][16]
+#pragma unroll
+    for (int f = 0; f < QF; ++f) {
+#pragma unroll
+      for (int d = 0; d < L::DB; ++d) parts[((wave * L::DB + d) * QF + f) * 64 + lane] = o[d][f];
+      if (g == 0) stats[(wave * QF + f) * 16 + col] = make_float2(base[f], sum[f]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int f = 0; f < QF; ++f) {
+      float2 x[KG];
+      float top = -INFINITY, total = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KG; ++k) {
+        x[k] = stats[((k * S::RW + rw) * QF + f) * 16 + col];
+        top = fmaxf(top, x[k].x);
+      }
+      const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int k = 0; k < KG; ++k) {
+        x[k].x = exp2_(x[k].x - ref);
+        total += x[k].x * x[k].y;
+      }
+      base[f] = top;
+      sum[f] = total;
+#pragma unroll
+      for (int d = 0; d < L::DB; ++d) {
+        if (d % KG != kg) continue;
+        f32x4 y = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < KG; ++k) y += parts[(((k * S::RW + rw) * L::DB + d) * QF + f) * 64 + lane] * x[k].x;
+        o[d][f] = y;
+      }
+    }
+  }
 #pragma unroll
   for (int f = 0; f < QF; ++f) {
     const int t = wq0 + f * 16 + col;
-    const float sum = col_sum(l[f]);
-    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+    const float inv = sum[f] > 0.0f ? 1.0f / sum[f] : (sum[f] == 0.0f ? 0.0f : sum[f]);
     if (t >= st.len) continue;
     const int64_t row = st.row0 + t;
     uint16_t* out = a.out.p + row * a.out.rs + head * a.out.hs;
 #pragma unroll
     for (int d = 0; d < L::DB; ++d) {
       const int e = 16 * d + 4 * g;
-      if (e < a.D) {
+      if (e < a.D && (KG == 1 || d % KG == kg)) {
         const f32x4 x = o[d][f] * inv;
         uint2 w = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
         *reinterpret_cast<uint2*>(out + e) = w;
       }
     }
-    if (g == 0 && a.lse)
-      a.lse[(int64_t)head * a.seqs.T + row] = sum == 0.0f ? -INFINITY : m[f] * p.c * LN2 + logf(sum);
+    if (g == 0 && kg == 0 && a.lse)
+      a.lse[(int64_t)head * a.seqs.T + row] = sum[f] == 0.0f ? -INFINITY : base[f] * LN2 + logf(sum[f]);
   }
 }
 
-template <int DS, int QF>
+template <class S>
 hipError_t run(const PromptArgs& a, hipStream_t s) {
-  constexpr int lds = 4 * BN * Tile<DS>::RB;
-  const int64_t ranks = max_tiles(a.seqs.T, a.seqs.n, 16 * QF * NW) + (a.seqs.n == 0);
+  const int64_t ranks = max_tiles(a.seqs.T, a.seqs.n, S::BM) + (a.seqs.n == 0);
   if (ranks * a.H > 0x7FFFFFFF) return hipErrorInvalidValue;
   PromptParams p{a, a.scale * LOG2E, (int32_t)ranks};
-  auto kernel = &attn_prompt<DS, QF>;
-  hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kernel), lds);
+  auto kernel = &attn_prompt<S>;
+  hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kernel), S::LDS);
   if (e != hipSuccess) return e;
-  return launch_k(kernel, dim3((unsigned)(ranks * a.H)), dim3(64 * NW), lds, s, p);
+  return launch_k(kernel, dim3((unsigned)(ranks * a.H)), dim3(64 * S::NW), S::LDS, s, p);
+}
+
+template <int DS>
+hipError_t choose(const PromptArgs& a, hipStream_t s) {
+  // RULE
+  if ((int64_t)a.seqs.T * a.H < 64 * 1024) return run<Shape<DS, 2, 2, 4, 32>>(a, s);
+  return run<Shape<DS, 2, 4, 1, 64>>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_attn_prompt(const PromptArgs& a, hipStream_t s) {
-  if (a.D <= 64) return run<2, 2>(a, s);
-  if (a.D <= 96) return run<3, 2>(a, s);
-  return run<4, 2>(a, s);
+  if (a.D <= 64) return choose<2>(a, s);
+  if (a.D <= 96) return choose<3>(a, s);
+  return choose<4>(a, s);
 }
 
 }  // namespace ubx

@@ -55,11 +55,11 @@ __device__ inline void store4(uint16_t* p, f32x4 x) {
 }
 
 template <int DS, int QF>
-__global__ __launch_bounds__(64 * NW, 1) void attn_bwd_q(BwdParams p) {
+__global__ __launch_bounds__(64 * NW, 2) void attn_bwd_q(BwdParams p) {
   using L = Tile<DS>;
   constexpr int BM = 16 * QF * NW;
   constexpr int TILE = BN * L::RB;
-  extern __shared__ unsigned char smem[];
+  extern __shared__ __align__(256) unsigned char smem[];
   const PromptBwdArgs& a = p.a;
   const int head = blockIdx.x % a.H, rank = blockIdx.x / a.H;
   fill_pad(a.dq, a.seqs, a.D, head, rank, p.ranks);
@@ -113,11 +113,17 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_bwd_q(BwdParams p) {
       p.delta[(int64_t)head * a.seqs.T + row] = delta[f];
     }
   }
-  RowFrag<DS> kf, vf;
-  ColFrag<DS> kt;
-  kf.init(smem, lane);
-  vf.init(smem + TILE, lane);
-  kt.init(smem, lane);
+#pragma unroll
+  for (int f = 0; f < QF; ++f)
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      arrived(q[f][s]);
+      arrived(dout[f][s]);
+    }
+  RowFrag<DS> rf;  // of k; v's lie TILE bytes on
+  ColFrag<DS> cf;
+  rf.init(smem, lane);
+  cf.init(smem, lane);
   f32x4 acc[L::DB][QF];
 #pragma unroll
   for (int d = 0; d < L::DB; ++d)
@@ -128,7 +134,6 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_bwd_q(BwdParams p) {
     wait_vmcnt_and_barrier<0>();
     if (j + 1 < tiles) load(j + 1, (j + 1) & 1);
     const int k0 = j * BN;
-    if (k0 > wq0 + 16 * QF - 1) continue;
     const bool diag = k0 + BN - 1 > wq0;
 #pragma unroll
     for (int t = 0; t < BN / 32; ++t) {
@@ -144,8 +149,8 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_bwd_q(BwdParams p) {
       for (int d = 0; d < DS; ++d)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const bf16x8 kk = kf.read(stage, 2 * t + b, d);
-          const bf16x8 vv = vf.read(stage, 2 * t + b, d);
+          const bf16x8 kk = rf.read(stage, 2 * t + b, d);
+          const bf16x8 vv = rf.read(stage + TILE, 2 * t + b, d);
 #pragma unroll
           for (int f = 0; f < QF; ++f) {
             s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
@@ -167,7 +172,7 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_bwd_q(BwdParams p) {
       }
 #pragma unroll
       for (int d = 0; d < L::DB; ++d) {
-        const bf16x8 kk = kt.read(stage, t, d);
+        const bf16x8 kk = cf.read(stage, t, d);
 #pragma unroll
         for (int f = 0; f < QF; ++f)
           acc[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, ds[f], acc[d][f], 0, 0, 0);
@@ -185,13 +190,17 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_bwd_q(BwdParams p) {
   }
 }
 
+// The values stay in LDS beside the query tiles: with them in registers too, the 128
+// accumulators of 32 keys left too few for the rest.
 template <int DS, int KF>
-__global__ __launch_bounds__(64 * NW, 1) void attn_bwd_kv(BwdParams p) {
+__global__ __launch_bounds__(64 * NW, 2) void attn_bwd_kv(BwdParams p) {
   using L = Tile<DS>;
+  constexpr int BQ = 32;  // query rows of a tile
   constexpr int BK = 16 * KF * NW;
-  constexpr int TILE = BN * L::RB;
-  constexpr int STAGE = 2 * TILE + 2 * BN * 4;  // q rows, dout rows, lse2, delta
-  extern __shared__ unsigned char smem[];
+  constexpr int TILE = BQ * L::RB;
+  constexpr int STAGE = 2 * TILE + 2 * BQ * 4;  // q rows, dout rows, lse2, delta
+  constexpr int V = 2 * STAGE;                  // the values' place
+  extern __shared__ __align__(256) unsigned char smem[];
   const PromptBwdArgs& a = p.a;
   const int GP = a.G * p.parts;
   const int gp = blockIdx.x % GP, rank = blockIdx.x / GP;
@@ -207,50 +216,51 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_bwd_kv(BwdParams p) {
   const int k0 = st.tile * BK;
   const int wk0 = k0 + wave * 16 * KF;
   const int heads = a.H / a.G / p.parts, head0 = kvh * (a.H / a.G) + part * heads;
-  const int qt0 = k0 / BN, qtiles = (st.len + BN - 1) / BN - qt0;
+  const int qt0 = k0 / BQ, qtiles = (st.len + BQ - 1) / BQ - qt0;
   const int total = heads * qtiles;
   const int64_t T = a.seqs.T;
-  TileLoad<DS, BN, NW> ql, dl;
+  const uint32_t lds = lds_addr(smem);
+  TileLoad<DS, BQ, NW> ql, dl;
   ql.init(wave, lane, a.q.rs, a.D);
   dl.init(wave, lane, a.dout.rs, a.D);
-  const uint32_t lds = lds_addr(smem);
   int lh = 0, lq = 0;  // head and query tile of the next load
   auto load = [&](int stage) {
-    const int head = head0 + lh, r = (qt0 + lq) * BN, valid = st.len - r;
+    const int head = head0 + lh, r = (qt0 + lq) * BQ, valid = st.len - r;
     const uint32_t at = lds + stage * STAGE;
     const int64_t row = st.row0 + r;
     ql.issue(a.q.p + row * a.q.rs + head * a.q.hs, a.q.rs, a.D, valid, at, wave);
     dl.issue(a.dout.p + row * a.dout.rs + head * a.dout.hs, a.dout.rs, a.D, valid, at + TILE, wave);
-    if (wave < 2) {
+    if (wave < 2 && lane < BQ) {
       const float* x = (wave == 0 ? p.lse2 : p.delta) + head * T + row;
-      dma4(make_rsrc(x, (uint32_t)min(valid, BN) * 4), at + 2 * TILE + wave * BN * 4, lane * 4);
+      dma4(make_rsrc(x, (uint32_t)min(valid, BQ) * 4), at + 2 * TILE + wave * BQ * 4, lane * 4);
     }
     if (++lq == qtiles) {
       lq = 0;
       ++lh;
     }
   };
-  load(0);
-  bf16x8 k[KF][DS], v[KF][DS];
+  bf16x8 k[KF][DS];
 #pragma unroll
   for (int f = 0; f < KF; ++f) {
     const int u = wk0 + f * 16 + col;
-    const int64_t row = st.row0 + u;
-    const uint16_t* kr = a.k.p + row * a.k.rs + kvh * a.k.hs;
-    const uint16_t* vr = a.v.p + row * a.v.rs + kvh * a.v.hs;
+    const uint16_t* kr = a.k.p + (st.row0 + u) * a.k.rs + kvh * a.k.hs;
 #pragma unroll
-    for (int s = 0; s < DS; ++s) {
-      const int e = 32 * s + 8 * g;
-      k[f][s] = load_row8(kr + e, u < st.len && e < a.D);
-      v[f][s] = load_row8(vr + e, u < st.len && e < a.D);
-    }
+    for (int s = 0; s < DS; ++s) k[f][s] = load_row8(kr + 32 * s + 8 * g, u < st.len && 32 * s + 8 * g < a.D);
   }
-  RowFrag<DS> qf, df;
-  ColFrag<DS> qt, dt;
-  qf.init(smem, lane);
-  df.init(smem + TILE, lane);
-  qt.init(smem, lane);
-  dt.init(smem + TILE, lane);
+#pragma unroll
+  for (int f = 0; f < KF; ++f)
+#pragma unroll
+    for (int s = 0; s < DS; ++s) arrived(k[f][s]);
+  {
+    TileLoad<DS, BK, NW> vl;
+    vl.init(wave, lane, a.v.rs, a.D);
+    vl.issue(a.v.p + (int64_t)(st.row0 + k0) * a.v.rs + kvh * a.v.hs, a.v.rs, a.D, st.len - k0, lds + V, wave);
+  }
+  load(0);
+  RowFrag<DS> rf;  // of q; dout's lie TILE bytes on, v's V bytes
+  ColFrag<DS> cf;
+  rf.init(smem, lane);
+  cf.init(smem, lane);
   f32x4 dk[L::DB][KF], dv[L::DB][KF];
 #pragma unroll
   for (int d = 0; d < L::DB; ++d)
@@ -261,63 +271,63 @@ __global__ __launch_bounds__(64 * NW, 1) void attn_bwd_kv(BwdParams p) {
     const int stage = (j & 1) * STAGE;
     wait_vmcnt_and_barrier<0>();
     if (j + 1 < total) load((j + 1) & 1);
-    const int q0 = (qt0 + cq) * BN;
+    const int q0 = (qt0 + cq) * BQ;
     if (++cq == qtiles) cq = 0;
-    if (q0 + BN - 1 < wk0) continue;
     const bool diag = q0 < wk0 + 16 * KF - 1;
     const float* rows = reinterpret_cast<const float*>(smem + stage + 2 * TILE);
+    f32x4 s[2][KF], dp[2][KF];
 #pragma unroll
-    for (int t = 0; t < BN / 32; ++t) {
-      f32x4 s[2][KF], dp[2][KF];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const f32x4 nd = -*LDS_PTR(const f32x4, rows + BN + t * 32 + b * 16 + 4 * g);
-#pragma unroll
-        for (int f = 0; f < KF; ++f) {
-          s[b][f] = f32x4{0, 0, 0, 0};
-          dp[b][f] = nd;
-        }
-      }
-#pragma unroll
-      for (int d = 0; d < DS; ++d)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const bf16x8 qq = qf.read(stage, 2 * t + b, d);
-          const bf16x8 dd = df.read(stage, 2 * t + b, d);
-#pragma unroll
-          for (int f = 0; f < KF; ++f) {
-            s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qq, k[f][d], s[b][f], 0, 0, 0);
-            dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dd, v[f][d], dp[b][f], 0, 0, 0);
-          }
-        }
-      bf16x8 pf[KF], ds[KF];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const f32x4 l2 = *LDS_PTR(const f32x4, rows + t * 32 + b * 16 + 4 * g);
-#pragma unroll
-        for (int f = 0; f < KF; ++f)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x = exp2_(s[b][f][i] * p.c - l2[i]);
-            if (diag && wk0 + f * 16 + col > q0 + t * 32 + b * 16 + 4 * g + i) x = dp[b][f][i] = 0.0f;
-            s[b][f][i] = x;
-            dp[b][f][i] *= x;
-          }
-      }
+    for (int b = 0; b < 2; ++b) {
+      const f32x4 nd = -*LDS_PTR(const f32x4, rows + BQ + b * 16 + 4 * g);
 #pragma unroll
       for (int f = 0; f < KF; ++f) {
-        pf[f] = pack8(s[0][f], s[1][f]);
-        ds[f] = pack8(dp[0][f], dp[1][f]);
+        s[b][f] = f32x4{0, 0, 0, 0};
+        dp[b][f] = nd;
       }
+    }
 #pragma unroll
-      for (int d = 0; d < L::DB; ++d) {
-        const bf16x8 dd = dt.read(stage, t, d);
-        const bf16x8 qq = qt.read(stage, t, d);
+    for (int d = 0; d < DS; ++d) {
+      bf16x8 v[KF];
+#pragma unroll
+      for (int f = 0; f < KF; ++f) v[f] = rf.read(V, wave * KF + f, d);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const bf16x8 qq = rf.read(stage, b, d);
+        const bf16x8 dd = rf.read(stage + TILE, b, d);
 #pragma unroll
         for (int f = 0; f < KF; ++f) {
-          dv[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dd, pf[f], dv[d][f], 0, 0, 0);
-          dk[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qq, ds[f], dk[d][f], 0, 0, 0);
+          s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qq, k[f][d], s[b][f], 0, 0, 0);
+          dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dd, v[f], dp[b][f], 0, 0, 0);
         }
+      }
+    }
+    bf16x8 pf[KF], ds[KF];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const f32x4 l2 = *LDS_PTR(const f32x4, rows + b * 16 + 4 * g);
+#pragma unroll
+      for (int f = 0; f < KF; ++f)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x = exp2_(s[b][f][i] * p.c - l2[i]);
+          if (diag && wk0 + f * 16 + col > q0 + b * 16 + 4 * g + i) x = dp[b][f][i] = 0.0f;
+          s[b][f][i] = x;
+          dp[b][f][i] *= x;
+        }
+    }
+#pragma unroll
+    for (int f = 0; f < KF; ++f) {
+      pf[f] = pack8(s[0][f], s[1][f]);
+      ds[f] = pack8(dp[0][f], dp[1][f]);
+    }
+#pragma unroll
+    for (int d = 0; d < L::DB; ++d) {
+      const bf16x8 dd = cf.read(stage + TILE, 0, d);
+      const bf16x8 qq = cf.read(stage, 0, d);
+#pragma unroll
+      for (int f = 0; f < KF; ++f) {
+        dv[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dd, pf[f], dv[d][f], 0, 0, 0);
+        dk[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qq, ds[f], dk[d][f], 0, 0, 0);
       }
     }
   }
@@ -415,7 +425,7 @@ hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
   const int64_t ranks = max_tiles(T, a.seqs.n, 16 * QF * NW) + (a.seqs.n == 0);
   if (ranks * a.H > 0x7FFFFFFF) return hipErrorInvalidValue;
   p.ranks = (int32_t)ranks;
-  constexpr int lds_q = 4 * BN * Tile<DS>::RB, lds_kv = 2 * (2 * BN * Tile<DS>::RB + 2 * BN * 4);
+  constexpr int lds_q = 4 * BN * Tile<DS>::RB, lds_kv = 2 * (2 * 32 * Tile<DS>::RB + 2 * 32 * 4) + 16 * KF * NW * Tile<DS>::RB;
   auto kq = &attn_bwd_q<DS, QF>;
   auto kkv = &attn_bwd_kv<DS, KF>;
   hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kq), lds_q);
