@@ -149,6 +149,30 @@ __device__ inline bf16x8 load_row8(const uint16_t* p, bool valid) {
 // loads in flight there: the next tile's among them, in every iteration.
 __device__ inline void arrived(bf16x8& x) { __asm__ volatile("" : "+v"(x)); }
 
+// Sum over NG groups of W waves each of the accumulators that wave w of every group holds,
+// in group order, through NW B F KB of LDS; group grp gets blocks grp, grp + NG, ...
+template <int NG, int W, int B, int F>
+__device__ inline void join_groups(f32x4 (&x)[B][F], unsigned char* smem, int grp, int w, int lane) {
+  f32x4* parts = reinterpret_cast<f32x4*>(smem);
+  __syncthreads();
+#pragma unroll
+  for (int d = 0; d < B; ++d)
+#pragma unroll
+    for (int f = 0; f < F; ++f) parts[(((grp * W + w) * B + d) * F + f) * 64 + lane] = x[d][f];
+  __syncthreads();
+#pragma unroll
+  for (int d = 0; d < B; ++d) {
+    if (d % NG != grp) continue;
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      f32x4 y = parts[((w * B + d) * F + f) * 64 + lane];
+#pragma unroll
+      for (int k = 1; k < NG; ++k) y += parts[(((k * W + w) * B + d) * F + f) * 64 + lane];
+      x[d][f] = y;
+    }
+  }
+}
+
 // Sum over the wave's 64 lanes, the same value in all of them.
 __device__ inline int wave_sum(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);  // row_shr:1

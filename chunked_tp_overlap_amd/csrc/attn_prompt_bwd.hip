@@ -19,8 +19,15 @@
 namespace ubx {
 namespace {
 
-constexpr int NW = 4;
-constexpr int BN = 64;  // rows of the tiles staged in LDS
+// NR waves of 32 rows each (of queries or keys), NG times: group grp takes the tiles (of keys
+// or queries, ROWS rows in LDS) grp, grp + NG, ... of what the rows meet.
+template <int DS_, int NR_, int NG_, int ROWS_>
+struct Shape {
+  static constexpr int DS = DS_, NR = NR_, NG = NG_, ROWS = ROWS_, F = 2;
+  using L = Tile<DS>;
+  static constexpr int NW = NR * NG, BM = 16 * F * NR, TILE = ROWS * L::RB;
+  static constexpr int JOIN = NG > 1 ? NW * L::DB * F * 1024 : 0;
+};
 
 struct BwdParams {
   PromptBwdArgs a;
@@ -54,11 +61,11 @@ __device__ inline void store4(uint16_t* p, f32x4 x) {
   *reinterpret_cast<uint2*>(p) = w;
 }
 
-template <int DS, int QF>
-__global__ __launch_bounds__(64 * NW, 2) void attn_bwd_q(BwdParams p) {
+template <class S>
+__global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_q(BwdParams p) {
+  constexpr int DS = S::DS, QF = S::F, NG = S::NG, BN = S::ROWS, BM = S::BM, TILE = S::TILE;
   using L = Tile<DS>;
-  constexpr int BM = 16 * QF * NW;
-  constexpr int TILE = BN * L::RB;
+  constexpr int STAGE = NG * 2 * TILE;
   extern __shared__ __align__(256) unsigned char smem[];
   const PromptBwdArgs& a = p.a;
   const int head = blockIdx.x % a.H, rank = blockIdx.x / a.H;
@@ -66,24 +73,24 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_bwd_q(BwdParams p) {
   const SeqTile st = find_tile(a.seqs, BM, rank, false);
   if (st.len == 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = wave % S::NR, grp = wave / S::NR;
   const int col = lane & 15, g = lane >> 4;
   const int kvh = head / (a.H / a.G);
   const int q0 = st.tile * BM;
-  const int wq0 = q0 + wave * 16 * QF;
+  const int wq0 = q0 + w * 16 * QF;
   const int n_keys = min(q0 + BM, st.len);
   const int tiles = (n_keys + BN - 1) / BN;
   const uint16_t* kbase = a.k.p + (int64_t)st.row0 * a.k.rs + kvh * a.k.hs;
   const uint16_t* vbase = a.v.p + (int64_t)st.row0 * a.v.rs + kvh * a.v.hs;
-  TileLoad<DS, BN, NW> kl, vl;
-  kl.init(wave, lane, a.k.rs, a.D);
-  vl.init(wave, lane, a.v.rs, a.D);
-  const uint32_t lds = lds_addr(smem);
+  TileLoad<DS, BN, S::NR> kl, vl;
+  kl.init(w, lane, a.k.rs, a.D);
+  vl.init(w, lane, a.v.rs, a.D);
+  const uint32_t lds = lds_addr(smem) + grp * 2 * TILE;
   auto load = [&](int j, int stage) {
-    kl.issue(kbase + (int64_t)j * BN * a.k.rs, a.k.rs, a.D, st.len - j * BN, lds + stage * 2 * TILE, wave);
-    vl.issue(vbase + (int64_t)j * BN * a.v.rs, a.v.rs, a.D, st.len - j * BN, lds + stage * 2 * TILE + TILE,
-             wave);
+    kl.issue(kbase + (int64_t)j * BN * a.k.rs, a.k.rs, a.D, st.len - j * BN, lds + stage * STAGE, w);
+    vl.issue(vbase + (int64_t)j * BN * a.v.rs, a.v.rs, a.D, st.len - j * BN, lds + stage * STAGE + TILE, w);
   };
-  load(0, 0);
+  if (grp < tiles) load(grp, 0);
   bf16x8 q[QF][DS], dout[QF][DS];
   float lse2[QF], delta[QF];
 #pragma unroll
@@ -108,7 +115,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_bwd_q(BwdParams p) {
     delta[f] = col_sum(x);
     const float l = ok ? a.lse[(int64_t)head * a.seqs.T + row] : 0.0f;
     lse2[f] = l == -INFINITY ? 0.0f : l * LOG2E;
-    if (ok && g == 0) {
+    if (ok && g == 0 && grp == 0) {
       p.lse2[(int64_t)head * a.seqs.T + row] = lse2[f];
       p.delta[(int64_t)head * a.seqs.T + row] = delta[f];
     }
@@ -122,17 +129,20 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_bwd_q(BwdParams p) {
     }
   RowFrag<DS> rf;  // of k; v's lie TILE bytes on
   ColFrag<DS> cf;
-  rf.init(smem, lane);
-  cf.init(smem, lane);
+  rf.init(smem + grp * 2 * TILE, lane);
+  cf.init(smem + grp * 2 * TILE, lane);
   f32x4 acc[L::DB][QF];
 #pragma unroll
   for (int d = 0; d < L::DB; ++d)
 #pragma unroll
     for (int f = 0; f < QF; ++f) acc[d][f] = f32x4{0, 0, 0, 0};
-  for (int j = 0; j < tiles; ++j) {
-    const int stage = (j & 1) * 2 * TILE;
+  const int steps = (tiles + NG - 1) / NG;
+  for (int i = 0; i < steps; ++i) {
+    const int j = i * NG + grp;
+    const int stage = (i & 1) * STAGE;
     wait_vmcnt_and_barrier<0>();
-    if (j + 1 < tiles) load(j + 1, (j + 1) & 1);
+    if (j + NG < tiles) load(j + NG, (i + 1) & 1);
+    if (NG > 1 && j >= tiles) continue;
     const int k0 = j * BN;
     const bool diag = k0 + BN - 1 > wq0;
 #pragma unroll
@@ -179,6 +189,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_bwd_q(BwdParams p) {
       }
     }
   }
+  if (NG > 1) join_groups<NG, S::NR>(acc, smem, grp, w, lane);
 #pragma unroll
   for (int f = 0; f < QF; ++f) {
     const int t = wq0 + f * 16 + col;
@@ -186,20 +197,20 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_bwd_q(BwdParams p) {
     uint16_t* out = a.dq.p + (int64_t)(st.row0 + t) * a.dq.rs + head * a.dq.hs;
 #pragma unroll
     for (int d = 0; d < L::DB; ++d)
-      if (16 * d + 4 * g < a.D) store4(out + 16 * d + 4 * g, acc[d][f] * a.scale);
+      if (16 * d + 4 * g < a.D && (NG == 1 || d % NG == grp)) store4(out + 16 * d + 4 * g, acc[d][f] * a.scale);
   }
 }
 
 // The values stay in LDS beside the query tiles: with them in registers too, the 128
 // accumulators of 32 keys left too few for the rest.
-template <int DS, int KF>
-__global__ __launch_bounds__(64 * NW, 2) void attn_bwd_kv(BwdParams p) {
+template <class S>
+__global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
+  constexpr int DS = S::DS, KF = S::F, NG = S::NG, BQ = S::ROWS, BK = S::BM, TILE = S::TILE;
   using L = Tile<DS>;
-  constexpr int BQ = 32;  // query rows of a tile
-  constexpr int BK = 16 * KF * NW;
-  constexpr int TILE = BQ * L::RB;
-  constexpr int STAGE = 2 * TILE + 2 * BQ * 4;  // q rows, dout rows, lse2, delta
-  constexpr int V = 2 * STAGE;                  // the values' place
+  constexpr int SET = 2 * TILE + 2 * BQ * 4;  // q rows, dout rows, lse2, delta
+  constexpr int STAGE = NG * SET;
+  constexpr int V = 2 * STAGE;  // the values' place
+  static_assert(BQ == 32, "one step of the second products");
   extern __shared__ __align__(256) unsigned char smem[];
   const PromptBwdArgs& a = p.a;
   const int GP = a.G * p.parts;
@@ -212,32 +223,38 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_bwd_kv(BwdParams p) {
   const SeqTile st = find_tile(a.seqs, BK, rank, true);
   if (st.len == 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = wave % S::NR, grp = wave / S::NR;
   const int col = lane & 15, g = lane >> 4;
   const int k0 = st.tile * BK;
-  const int wk0 = k0 + wave * 16 * KF;
+  const int wk0 = k0 + w * 16 * KF;
   const int heads = a.H / a.G / p.parts, head0 = kvh * (a.H / a.G) + part * heads;
   const int qt0 = k0 / BQ, qtiles = (st.len + BQ - 1) / BQ - qt0;
   const int total = heads * qtiles;
   const int64_t T = a.seqs.T;
   const uint32_t lds = lds_addr(smem);
-  TileLoad<DS, BQ, NW> ql, dl;
-  ql.init(wave, lane, a.q.rs, a.D);
-  dl.init(wave, lane, a.dout.rs, a.D);
-  int lh = 0, lq = 0;  // head and query tile of the next load
+  TileLoad<DS, BQ, S::NR> ql, dl;
+  ql.init(w, lane, a.q.rs, a.D);
+  dl.init(w, lane, a.dout.rs, a.D);
+  int lh = 0, lq = grp;  // head and query tile of the group's next load
+  auto wrap = [&](int& q, int& h) {
+    while (q >= qtiles) {
+      q -= qtiles;
+      ++h;
+    }
+  };
+  wrap(lq, lh);
   auto load = [&](int stage) {
     const int head = head0 + lh, r = (qt0 + lq) * BQ, valid = st.len - r;
-    const uint32_t at = lds + stage * STAGE;
+    const uint32_t at = lds + stage * STAGE + grp * SET;
     const int64_t row = st.row0 + r;
-    ql.issue(a.q.p + row * a.q.rs + head * a.q.hs, a.q.rs, a.D, valid, at, wave);
-    dl.issue(a.dout.p + row * a.dout.rs + head * a.dout.hs, a.dout.rs, a.D, valid, at + TILE, wave);
-    if (wave < 2 && lane < BQ) {
-      const float* x = (wave == 0 ? p.lse2 : p.delta) + head * T + row;
-      dma4(make_rsrc(x, (uint32_t)min(valid, BQ) * 4), at + 2 * TILE + wave * BQ * 4, lane * 4);
+    ql.issue(a.q.p + row * a.q.rs + head * a.q.hs, a.q.rs, a.D, valid, at, w);
+    dl.issue(a.dout.p + row * a.dout.rs + head * a.dout.hs, a.dout.rs, a.D, valid, at + TILE, w);
+    if (w < 2 && lane < BQ) {
+      const float* x = (w == 0 ? p.lse2 : p.delta) + head * T + row;
+      dma4(make_rsrc(x, (uint32_t)min(valid, BQ) * 4), at + 2 * TILE + w * BQ * 4, lane * 4);
     }
-    if (++lq == qtiles) {
-      lq = 0;
-      ++lh;
-    }
+    lq += NG;
+    wrap(lq, lh);
   };
   bf16x8 k[KF][DS];
 #pragma unroll
@@ -252,12 +269,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_bwd_kv(BwdParams p) {
 #pragma unroll
     for (int s = 0; s < DS; ++s) arrived(k[f][s]);
   {
-    TileLoad<DS, BK, NW> vl;
+    TileLoad<DS, BK, S::NW> vl;
     vl.init(wave, lane, a.v.rs, a.D);
     vl.issue(a.v.p + (int64_t)(st.row0 + k0) * a.v.rs + kvh * a.v.hs, a.v.rs, a.D, st.len - k0, lds + V, wave);
   }
-  load(0);
-  RowFrag<DS> rf;  // of q; dout's lie TILE bytes on, v's V bytes
+  if (grp < total) load(0);
+  RowFrag<DS> rf;  // from the stage; the group's q lie grp SET bytes on, dout TILE further
   ColFrag<DS> cf;
   rf.init(smem, lane);
   cf.init(smem, lane);
@@ -266,13 +283,18 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_bwd_kv(BwdParams p) {
   for (int d = 0; d < L::DB; ++d)
 #pragma unroll
     for (int f = 0; f < KF; ++f) dk[d][f] = dv[d][f] = f32x4{0, 0, 0, 0};
-  int cq = 0;  // query tile of the iteration
-  for (int j = 0; j < total; ++j) {
-    const int stage = (j & 1) * STAGE;
+  int cq = grp, ch = 0;  // query tile (and head) of the step
+  wrap(cq, ch);
+  const int steps = (total + NG - 1) / NG;
+  for (int i = 0; i < steps; ++i) {
+    const int j = i * NG + grp;
+    const int stage = (i & 1) * STAGE + grp * SET;
     wait_vmcnt_and_barrier<0>();
-    if (j + 1 < total) load((j + 1) & 1);
+    if (j + NG < total) load((i + 1) & 1);
+    if (NG > 1 && j >= total) continue;
     const int q0 = (qt0 + cq) * BQ;
-    if (++cq == qtiles) cq = 0;
+    cq += NG;
+    wrap(cq, ch);
     const bool diag = q0 < wk0 + 16 * KF - 1;
     const float* rows = reinterpret_cast<const float*>(smem + stage + 2 * TILE);
     f32x4 s[2][KF], dp[2][KF];
@@ -289,7 +311,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_bwd_kv(BwdParams p) {
     for (int d = 0; d < DS; ++d) {
       bf16x8 v[KF];
 #pragma unroll
-      for (int f = 0; f < KF; ++f) v[f] = rf.read(V, wave * KF + f, d);
+      for (int f = 0; f < KF; ++f) v[f] = rf.read(V, w * KF + f, d);
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const bf16x8 qq = rf.read(stage, b, d);
@@ -331,6 +353,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_bwd_kv(BwdParams p) {
       }
     }
   }
+  if (NG > 1) {
+    join_groups<NG, S::NR>(dk, smem, grp, w, lane);
+    join_groups<NG, S::NR>(dv, smem, grp, w, lane);
+  }
 #pragma unroll
   for (int f = 0; f < KF; ++f) {
     const int u = wk0 + f * 16 + col;
@@ -342,7 +368,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_bwd_kv(BwdParams p) {
 #pragma unroll
       for (int d = 0; d < L::DB; ++d) {
         const int e = 16 * d + 4 * g;
-        if (e < a.D) {
+        if (e < a.D && (NG == 1 || d % NG == grp)) {
           store4(ok + e, dk[d][f] * a.scale);
           store4(ov + e, dv[d][f]);
         }
@@ -353,7 +379,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_bwd_kv(BwdParams p) {
 #pragma unroll
       for (int d = 0; d < L::DB; ++d) {
         const int e = 16 * d + 4 * g;
-        if (e < a.D) {
+        if (e < a.D && (NG == 1 || d % NG == grp)) {
           *reinterpret_cast<f32x4*>(ok + e) = dk[d][f];
           *reinterpret_cast<f32x4*>(ov + e) = dv[d][f];
         }
@@ -396,22 +422,28 @@ __global__ __launch_bounds__(256) void attn_bwd_join(BwdParams p) {
 
 constexpr int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
-// Parts a group's heads are split into: with fewer than four key tiles per CU the chip would
-// idle behind the longest tiles.
+// Calls that cannot fill the card with workgroups of 128 rows (one of four waves per SIMD pair
+// for each) take 64 rows and four groups of waves: see attn_prompt.hip.
+bool grouped(int H, int64_t rows) { return rows * H < 64 * 1024; }
+
+// Parts a group's heads are split into: with fewer than two (four of the smaller) workgroups
+// per CU the chip would idle behind the longest tiles.
 int bwd_parts(int H, int G, int64_t rows) {
   const int group = H / G;
-  const int64_t tiles = (rows + 127) / 128 * G;
+  const bool small = grouped(H, rows);
+  const int64_t tiles = small ? (rows + 63) / 64 * G : (rows + 127) / 128 * G;
   int parts = 1;
-  while (parts < group && tiles * parts < 1024) {
+  while (parts < group && tiles * parts < (small ? 512 : 1024)) {
     ++parts;
     while (group % parts) ++parts;
   }
   return parts;
 }
 
-template <int DS>
+template <class SQ, class SK>
 hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
-  constexpr int KF = 2, QF = 2;
+  static_assert(SQ::BM == SK::BM, "one count of tiles");
+  constexpr int DS = SQ::DS;
   const int64_t T = a.seqs.T;
   BwdParams p{};
   p.a = a;
@@ -422,23 +454,30 @@ hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
   p.lse2 = reinterpret_cast<float*>(w);
   p.delta = reinterpret_cast<float*>(w + stat);
   p.part = reinterpret_cast<float*>(w + 2 * stat);
-  const int64_t ranks = max_tiles(T, a.seqs.n, 16 * QF * NW) + (a.seqs.n == 0);
+  const int64_t ranks = max_tiles(T, a.seqs.n, SQ::BM) + (a.seqs.n == 0);
   if (ranks * a.H > 0x7FFFFFFF) return hipErrorInvalidValue;
   p.ranks = (int32_t)ranks;
-  constexpr int lds_q = 4 * BN * Tile<DS>::RB, lds_kv = 2 * (2 * 32 * Tile<DS>::RB + 2 * 32 * 4) + 16 * KF * NW * Tile<DS>::RB;
-  auto kq = &attn_bwd_q<DS, QF>;
-  auto kkv = &attn_bwd_kv<DS, KF>;
+  constexpr int lds_q = std::max(2 * SQ::NG * 2 * SQ::TILE, SQ::JOIN);
+  constexpr int lds_kv = std::max(2 * SK::NG * (2 * SK::TILE + 2 * SK::ROWS * 4) + SK::BM * Tile<DS>::RB, SK::JOIN);
+  auto kq = &attn_bwd_q<SQ>;
+  auto kkv = &attn_bwd_kv<SK>;
   hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kq), lds_q);
   if (e == hipSuccess) e = ensure_lds_attr(reinterpret_cast<const void*>(kkv), lds_kv);
-  if (e == hipSuccess) e = launch_k(kq, dim3((unsigned)(ranks * a.H)), dim3(64 * NW), lds_q, s, p);
+  if (e == hipSuccess) e = launch_k(kq, dim3((unsigned)(ranks * a.H)), dim3(64 * SQ::NW), lds_q, s, p);
   if (e == hipSuccess)
-    e = launch_k(kkv, dim3((unsigned)(ranks * a.G * p.parts)), dim3(64 * NW), lds_kv, s, p);
+    e = launch_k(kkv, dim3((unsigned)(ranks * a.G * p.parts)), dim3(64 * SK::NW), lds_kv, s, p);
   if (e == hipSuccess && p.parts > 1) {
     const int64_t blocks = (2 * a.G * T * (a.D / 8) + 255) / 256;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     e = launch_k(&attn_bwd_join, dim3((unsigned)blocks), dim3(256), 0, s, p);
   }
   return e;
+}
+
+template <int DS>
+hipError_t choose(const PromptBwdArgs& a, hipStream_t s) {
+  if (grouped(a.H, a.seqs.T)) return run<Shape<DS, 2, 4, 32>, Shape<DS, 2, 4, 32>>(a, s);
+  return run<Shape<DS, 4, 1, 64>, Shape<DS, 4, 1, 32>>(a, s);
 }
 
 }  // namespace
@@ -453,15 +492,17 @@ size_t attn_prompt_bwd_bytes(int32_t H, int32_t G, int32_t D, int64_t rows) {
   // the parts fall in steps as rows grow, so fewer rows can need more: each row count up to
   // `rows` is covered by the last one with the same number of key tiles
   size_t most = attn_prompt_bwd_need(H, G, D, rows);
-  for (int64_t t = 1; t <= 1024 && t * 128 < rows; ++t)
-    most = std::max(most, attn_prompt_bwd_need(H, G, D, t * 128));
+  for (int64_t t = 1; t <= 2048 && t * 64 < rows; ++t)
+    most = std::max(most, attn_prompt_bwd_need(H, G, D, t * 64));
+  const int64_t last = (64 * 1024 - 1) / H;  // the last that is grouped
+  if (last < rows) most = std::max(most, attn_prompt_bwd_need(H, G, D, last));
   return most;
 }
 
 hipError_t launch_attn_prompt_bwd(const PromptBwdArgs& a, hipStream_t s) {
-  if (a.D <= 64) return run<2>(a, s);
-  if (a.D <= 96) return run<3>(a, s);
-  return run<4>(a, s);
+  if (a.D <= 64) return choose<2>(a, s);
+  if (a.D <= 96) return choose<3>(a, s);
+  return choose<4>(a, s);
 }
 
 }  // namespace ubx
