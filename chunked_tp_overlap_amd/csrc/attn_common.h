@@ -26,16 +26,21 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
 // A tile of `ROWS` rows of up to 32 DS elements in LDS.  Rows take 128 bytes (DS <= 2) or
-// 256; 16-byte chunk q of row r is kept in slot q ^ swz(r).  swz makes both reads free of
-// bank conflicts: the row reads (16 rows, one chunk: all 16-byte slots of 256 bytes differ)
-// and the transposing reads (8 rows, two neighbouring chunks: all 32-byte slots differ).
+// 256; 16-byte chunk q of row r is kept in slot q ^ swz(r).  swz makes both reads free of bank
+// conflicts.  A 16-byte read is served 16 lanes at a time, lanes 0-3, 12-15 and 20-27 first
+// (measured, by which pairs of lanes conflict), then 4-11, 16-19 and 28-31: of the rows that a
+// row fragment reads, those with bits 2 and 3 alike at one chunk and the others at the next.
+// Their 16 slots differ if rows whose swz differ in bit 0 alone are of the same kind: r and
+// r ^ 12.  A transposing read serves 8 rows, two neighbouring chunks each: their swz differ
+// above bit 0.
 template <int DS>
 struct Tile {
   static constexpr int CPR = DS <= 2 ? 8 : 16;  // chunks per row
   static constexpr int RB = 16 * CPR;           // bytes per row
   static constexpr int DB = 2 * DS;             // 16-wide blocks of a row
   __device__ static int swz(int r) {
-    return CPR == 16 ? (((r & 7) << 1) | ((r >> 3) & 1)) : ((((r >> 1) & 3) << 1) | ((r >> 3) & 1));
+    return CPR == 16 ? ((((r & 7) ^ ((r >> 1) & 4)) << 1) | ((r >> 3) & 1))
+                     : (((((r >> 1) & 3) ^ ((r >> 2) & 2)) << 1) | ((r >> 3) & 1));
   }
 };
 

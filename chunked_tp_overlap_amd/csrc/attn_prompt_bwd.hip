@@ -144,7 +144,6 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_q(BwdParams p) {
     if (j + NG < tiles) load(j + NG, (i + 1) & 1);
     if (NG > 1 && j >= tiles) continue;
     const int k0 = j * BN;
-    const bool diag = k0 + BN - 1 > wq0;
 #pragma unroll
     for (int t = 0; t < BN / 32; ++t) {
       f32x4 s[2][QF], dp[2][QF];
@@ -167,19 +166,25 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_q(BwdParams p) {
             dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, dout[f][d], dp[b][f], 0, 0, 0);
           }
         }
-      bf16x8 ds[QF];
 #pragma unroll
-      for (int f = 0; f < QF; ++f) {
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int f = 0; f < QF; ++f)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            s[b][f][i] = exp2_(s[b][f][i] * p.c - lse2[f]) * (dp[b][f][i] - delta[f]);
+      if (k0 + BN - 1 > wq0) {  // the diagonal: keys after the query
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x = exp2_(s[b][f][i] * p.c - lse2[f]) * (dp[b][f][i] - delta[f]);
-            if (diag && k0 + t * 32 + b * 16 + 4 * g + i > wq0 + f * 16 + col) x = 0.0f;
-            s[b][f][i] = x;
-          }
-        ds[f] = pack8(s[0][f], s[1][f]);
+          for (int f = 0; f < QF; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (k0 + t * 32 + b * 16 + 4 * g + i > wq0 + f * 16 + col) s[b][f][i] = 0.0f;
       }
+      bf16x8 ds[QF];
+#pragma unroll
+      for (int f = 0; f < QF; ++f) ds[f] = pack8(s[0][f], s[1][f]);
 #pragma unroll
       for (int d = 0; d < L::DB; ++d) {
         const bf16x8 kk = cf.read(stage, t, d);
@@ -295,7 +300,6 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
     const int q0 = (qt0 + cq) * BQ;
     cq += NG;
     wrap(cq, ch);
-    const bool diag = q0 < wk0 + 16 * KF - 1;
     const float* rows = reinterpret_cast<const float*>(smem + stage + 2 * TILE);
     f32x4 s[2][KF], dp[2][KF];
 #pragma unroll
@@ -323,7 +327,6 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
         }
       }
     }
-    bf16x8 pf[KF], ds[KF];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const f32x4 l2 = *LDS_PTR(const f32x4, rows + b * 16 + 4 * g);
@@ -331,12 +334,20 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
       for (int f = 0; f < KF; ++f)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float x = exp2_(s[b][f][i] * p.c - l2[i]);
-          if (diag && wk0 + f * 16 + col > q0 + b * 16 + 4 * g + i) x = dp[b][f][i] = 0.0f;
-          s[b][f][i] = x;
-          dp[b][f][i] *= x;
+          s[b][f][i] = exp2_(s[b][f][i] * p.c - l2[i]);
+          dp[b][f][i] *= s[b][f][i];
         }
     }
+    if (q0 < wk0 + 16 * KF - 1) {  // the diagonal: queries before the key
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int f = 0; f < KF; ++f)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (wk0 + f * 16 + col > q0 + b * 16 + 4 * g + i) s[b][f][i] = dp[b][f][i] = 0.0f;
+    }
+    bf16x8 pf[KF], ds[KF];
 #pragma unroll
     for (int f = 0; f < KF; ++f) {
       pf[f] = pack8(s[0][f], s[1][f]);
