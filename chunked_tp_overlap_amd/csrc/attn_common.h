@@ -154,26 +154,38 @@ __device__ inline bf16x8 load_row8(const uint16_t* p, bool valid) {
 // loads in flight there: the next tile's among them, in every iteration.
 __device__ inline void arrived(bf16x8& x) { __asm__ volatile("" : "+v"(x)); }
 
+// The barrier between the two phases of a step of kernels whose groups of waves work in turns:
+// the later half of the groups starts one barrier late, so that while one half multiplies
+// score tiles the other does its exponentials; all at once, each unit would idle in turn.
+__device__ inline void phase_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Sum over NG groups of W waves each of the accumulators that wave w of every group holds,
-// in group order, through NW B F KB of LDS; group grp gets blocks grp, grp + NG, ...
+// in group order, through NG W B F KB of LDS.  Group grp's x[0], x[1], ... become the sums of
+// blocks grp, grp + NG, ... (of no block past B).
 template <int NG, int W, int B, int F>
 __device__ inline void join_groups(f32x4 (&x)[B][F], unsigned char* smem, int grp, int w, int lane) {
-  f32x4* parts = reinterpret_cast<f32x4*>(smem);
+  f32x4* parts = reinterpret_cast<f32x4*>(smem);  // [NG][W][B][F][64]
   __syncthreads();
+  f32x4* mine = parts + (grp * W + w) * B * F * 64 + lane;
 #pragma unroll
   for (int d = 0; d < B; ++d)
 #pragma unroll
-    for (int f = 0; f < F; ++f) parts[(((grp * W + w) * B + d) * F + f) * 64 + lane] = x[d][f];
+    for (int f = 0; f < F; ++f) mine[(d * F + f) * 64] = x[d][f];
   __syncthreads();
+  const f32x4* all = parts + (w * B + grp) * F * 64 + lane;
 #pragma unroll
-  for (int d = 0; d < B; ++d) {
-    if (d % NG != grp) continue;
+  for (int i = 0; i < (B + NG - 1) / NG; ++i) {
+    if (i * NG + grp >= B) break;
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-      f32x4 y = parts[((w * B + d) * F + f) * 64 + lane];
+      f32x4 y = all[(i * NG * F + f) * 64];
 #pragma unroll
-      for (int k = 1; k < NG; ++k) y += parts[(((k * W + w) * B + d) * F + f) * 64 + lane];
-      x[d][f] = y;
+      for (int k = 1; k < NG; ++k) y += all[((k * W * B + i * NG) * F + f) * 64];
+      x[i][f] = y;
     }
   }
 }
@@ -188,6 +200,18 @@ __device__ inline int wave_sum(int v) {
          __builtin_amdgcn_readlane(v, 47) + __builtin_amdgcn_readlane(v, 63);
 }
 
+// Inclusive prefix sum over the wave.
+__device__ inline int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  const int a = __builtin_amdgcn_readlane(v, 15), b = __builtin_amdgcn_readlane(v, 31),
+            c = __builtin_amdgcn_readlane(v, 47);
+  const int row = (threadIdx.x & 63) >> 4;
+  return v + (row > 0 ? a : 0) + (row > 1 ? b : 0) + (row > 2 ? c : 0);
+}
+
 // Rows of sequence i clamped to [0, T): a bad boundary reads no row outside the matrices.
 __device__ inline int clamp_row(int x, int T) { return min(max(x, 0), T); }
 
@@ -200,8 +224,9 @@ struct SeqTile {
 // per lane): in the order of falling tile number, so that the tiles with the most work under
 // a causal mask start first.  A level x holds the tiles number x - 1; C(x) = the tiles of
 // level x and above; the rank's level is the largest x with C(x) > rank, found by
-// bisection, its sequence by the rank's bit in a ballot.  More sequences: in sequence order.
-// `low_first` reverses the levels (tiles whose work falls with their number).
+// bisection, its sequence by the rank's bit in a ballot.  A grid that runs at once needs no
+// order, and more sequences do without: in sequence order.  `low_first` reverses the levels
+// (tiles whose work falls with their number).
 __device__ inline SeqTile find_tile(const Seqs& s, int bm, int rank, bool low_first) {
   const int lane = threadIdx.x & 63;
   SeqTile r{0, 0, 0};
@@ -211,6 +236,16 @@ __device__ inline SeqTile find_tile(const Seqs& s, int bm, int rank, bool low_fi
     const int b = s.n > 0 ? clamp_row(s.cu[min(lane + 1, s.n)], s.T) : 0;
     const int len = max(b - a, 0);
     const int nt = (len + bm - 1) / bm;
+    if (gridDim.x <= 256) {
+      const int incl = wave_scan(nt);
+      const uint64_t m = __ballot(incl > rank);
+      if (m == 0) return r;
+      const int at = __builtin_ctzll(m);
+      r.row0 = __builtin_amdgcn_readlane(a, at);
+      r.len = __builtin_amdgcn_readlane(len, at);
+      r.tile = rank - __builtin_amdgcn_readlane(incl - nt, at);
+      return r;
+    }
     const int total = wave_sum(nt);
     if (rank >= total) return r;
     const int want = low_first ? total - 1 - rank : rank;

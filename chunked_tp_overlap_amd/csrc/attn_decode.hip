@@ -48,18 +48,6 @@ struct DecodeParams {
   float2* stat;     // [2 ranges, G qb, COLS]: maximum (base 2, scaled), sum
 };
 
-// Inclusive prefix sum over the wave.
-__device__ inline int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
-  const int a = __builtin_amdgcn_readlane(v, 15), b = __builtin_amdgcn_readlane(v, 31),
-            c = __builtin_amdgcn_readlane(v, 47);
-  const int row = (threadIdx.x & 63) >> 4;
-  return v + (row > 0 ? a : 0) + (row > 1 ? b : 0) + (row > 2 ? c : 0);
-}
-
 // Cached tokens of sequence i, as far as the page table reaches.
 __device__ inline int kv_len(const DecodeParams& p, int i) { return clamp_len(p.a.lens[i], p.cap); }
 

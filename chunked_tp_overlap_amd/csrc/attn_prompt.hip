@@ -83,6 +83,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
     kl.issue(kbase + (int64_t)j * BN * a.k.rs, a.k.rs, a.D, st.len - j * BN, lds + stage * S::STAGE, rw);
     vl.issue(vbase + (int64_t)j * BN * a.v.rs, a.v.rs, a.D, st.len - j * BN, lds + stage * S::STAGE + TILE, rw);
   };
+  if (kg < tiles) load(kg, 0);
   bf16x8 q[QF][DS];
 #pragma unroll
   for (int f = 0; f < QF; ++f) {
@@ -95,7 +96,6 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
   for (int f = 0; f < QF; ++f)
 #pragma unroll
     for (int s = 0; s < DS; ++s) arrived(q[f][s]);
-  if (kg < tiles) load(kg, 0);
 
   RowFrag<DS> kf;
   ColFrag<DS> vf;
@@ -111,48 +111,54 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
     for (int d = 0; d < L::DB; ++d) o[d][f] = f32x4{0, 0, 0, 0};
   }
   const int steps = (tiles + KG - 1) / KG;
+  const bool late = kg >= (KG + 1) / 2;
+  if (late) phase_barrier();
   for (int i = 0; i < steps; ++i) {
     const int j = i * KG + kg;
     const int stage = (i & 1) * S::STAGE;
     wait_vmcnt_and_barrier<0>();
     if (j + KG < tiles) load(j + KG, (i + 1) & 1);
     const int k0 = j * BN;
-    if (KG > 1 && j >= tiles) continue;
+    const bool live = KG == 1 || j < tiles;
     f32x4 s[KB][QF];
-#pragma unroll
-    for (int b = 0; b < KB; ++b)
-#pragma unroll
-      for (int f = 0; f < QF; ++f) s[b][f] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int d = 0; d < DS; ++d)
-#pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        const bf16x8 kk = kf.read(stage, b, d);
-#pragma unroll
-        for (int f = 0; f < QF; ++f)
-          s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
-      }
-    if (k0 + BN - 1 > wq0) {  // the diagonal: keys after the query
-#pragma unroll
-      for (int b = 0; b < KB; ++b)
-#pragma unroll
-        for (int f = 0; f < QF; ++f)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (k0 + b * 16 + 4 * g + i > wq0 + f * 16 + col) s[b][f][i] = -INFINITY;
-    }
     float top[QF];
     bool above = false;
-#pragma unroll
-    for (int f = 0; f < QF; ++f) {
-      float x = s[0][f][0];
+    if (live) {
 #pragma unroll
       for (int b = 0; b < KB; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x = fmaxf(x, s[b][f][i]);
-      top[f] = col_max(x);
-      above = above || (top[f] - m[f]) * p.c > SLACK;
+        for (int f = 0; f < QF; ++f) s[b][f] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int d = 0; d < DS; ++d)
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+          const bf16x8 kk = kf.read(stage, b, d);
+#pragma unroll
+          for (int f = 0; f < QF; ++f)
+            s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
+        }
+      if (k0 + BN - 1 > wq0) {  // the diagonal: keys after the query
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+          for (int f = 0; f < QF; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (k0 + b * 16 + 4 * g + i > wq0 + f * 16 + col) s[b][f][i] = -INFINITY;
+      }
+#pragma unroll
+      for (int f = 0; f < QF; ++f) {
+        float x = s[0][f][0];
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x = fmaxf(x, s[b][f][i]);
+        top[f] = col_max(x);
+        above = above || (top[f] - m[f]) * p.c > SLACK;
+      }
     }
+    if (KG > 1) phase_barrier();
+    if (!live) continue;
     if (__ballot(above)) {
       // the reference moves to the maximum, here and for what was summed so far
 #pragma unroll
@@ -192,6 +198,8 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
       }
     }
   }
+  if (KG > 1 && !late) phase_barrier();
+  constexpr int MINE = (L::DB + KG - 1) / KG;  // blocks of the output that a wave writes
   float base[QF], sum[QF];
 #pragma unroll
   for (int f = 0; f < QF; ++f) {
@@ -202,15 +210,17 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
     // Join of the groups: all outputs and statistics through LDS; group kg joins blocks kg,
     // kg + KG, ... of the columns.
     __syncthreads();
-    f32x4* parts = reinterpret_cast<f32x4*>(smem);  // [NW][DB][QF][64]
-    float2* stats = reinterpret_cast<float2*>(smem + S::NW * S::PART);  // [NW][QF][16]
+    f32x4* parts = reinterpret_cast<f32x4*>(smem);  // [KG][RW][DB][QF][64]
+    float2* stats = reinterpret_cast<float2*>(smem + S::NW * S::PART);  // [KG][RW][QF][16]
+    f32x4* mine = parts + wave * L::DB * QF * 64 + lane;
 #pragma unroll
     for (int f = 0; f < QF; ++f) {
 #pragma unroll
-      for (int d = 0; d < L::DB; ++d) parts[((wave * L::DB + d) * QF + f) * 64 + lane] = o[d][f];
+      for (int d = 0; d < L::DB; ++d) mine[(d * QF + f) * 64] = o[d][f];
       if (g == 0) stats[(wave * QF + f) * 16 + col] = make_float2(base[f], sum[f]);
     }
     __syncthreads();
+    const f32x4* all = parts + (rw * L::DB + kg) * QF * 64 + lane;
 #pragma unroll
     for (int f = 0; f < QF; ++f) {
       float2 x[KG];
@@ -229,12 +239,12 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
       base[f] = top;
       sum[f] = total;
 #pragma unroll
-      for (int d = 0; d < L::DB; ++d) {
-        if (d % KG != kg) continue;
+      for (int i = 0; i < MINE; ++i) {
+        if (i * KG + kg >= L::DB) break;
         f32x4 y = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < KG; ++k) y += parts[(((k * S::RW + rw) * L::DB + d) * QF + f) * 64 + lane] * x[k].x;
-        o[d][f] = y;
+        for (int k = 0; k < KG; ++k) y += all[((k * S::RW * L::DB + i * KG) * QF + f) * 64] * x[k].x;
+        o[i][f] = y;
       }
     }
   }
@@ -246,10 +256,10 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
     const int64_t row = st.row0 + t;
     uint16_t* out = a.out.p + row * a.out.rs + head * a.out.hs;
 #pragma unroll
-    for (int d = 0; d < L::DB; ++d) {
-      const int e = 16 * d + 4 * g;
-      if (e < a.D && (KG == 1 || d % KG == kg)) {
-        const f32x4 x = o[d][f] * inv;
+    for (int i = 0; i < MINE; ++i) {
+      const int e = 16 * (i * KG + kg) + 4 * g;
+      if (e < a.D) {
+        const f32x4 x = o[i][f] * inv;
         uint2 w = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
         *reinterpret_cast<uint2*>(out + e) = w;
       }

@@ -137,35 +137,41 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_q(BwdParams p) {
 #pragma unroll
     for (int f = 0; f < QF; ++f) acc[d][f] = f32x4{0, 0, 0, 0};
   const int steps = (tiles + NG - 1) / NG;
+  const bool late = grp >= (NG + 1) / 2;
+  if (late) phase_barrier();
   for (int i = 0; i < steps; ++i) {
     const int j = i * NG + grp;
     const int stage = (i & 1) * STAGE;
     wait_vmcnt_and_barrier<0>();
     if (j + NG < tiles) load(j + NG, (i + 1) & 1);
-    if (NG > 1 && j >= tiles) continue;
+    const bool live = NG == 1 || j < tiles;
     const int k0 = j * BN;
 #pragma unroll
     for (int t = 0; t < BN / 32; ++t) {
       f32x4 s[2][QF], dp[2][QF];
+      if (live) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int f = 0; f < QF; ++f) {
-          s[b][f] = f32x4{0, 0, 0, 0};
-          dp[b][f] = f32x4{0, 0, 0, 0};
-        }
-#pragma unroll
-      for (int d = 0; d < DS; ++d)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const bf16x8 kk = rf.read(stage, 2 * t + b, d);
-          const bf16x8 vv = rf.read(stage + TILE, 2 * t + b, d);
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int f = 0; f < QF; ++f) {
-            s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
-            dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, dout[f][d], dp[b][f], 0, 0, 0);
+            s[b][f] = f32x4{0, 0, 0, 0};
+            dp[b][f] = f32x4{0, 0, 0, 0};
           }
-        }
+#pragma unroll
+        for (int d = 0; d < DS; ++d)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const bf16x8 kk = rf.read(stage, 2 * t + b, d);
+            const bf16x8 vv = rf.read(stage + TILE, 2 * t + b, d);
+#pragma unroll
+            for (int f = 0; f < QF; ++f) {
+              s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
+              dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, dout[f][d], dp[b][f], 0, 0, 0);
+            }
+          }
+      }
+      if (NG > 1) phase_barrier();
+      if (!live) continue;
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -194,6 +200,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_q(BwdParams p) {
       }
     }
   }
+  if (NG > 1 && !late) phase_barrier();
   if (NG > 1) join_groups<NG, S::NR>(acc, smem, grp, w, lane);
 #pragma unroll
   for (int f = 0; f < QF; ++f) {
@@ -201,8 +208,10 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_q(BwdParams p) {
     if (t >= st.len) continue;
     uint16_t* out = a.dq.p + (int64_t)(st.row0 + t) * a.dq.rs + head * a.dq.hs;
 #pragma unroll
-    for (int d = 0; d < L::DB; ++d)
-      if (16 * d + 4 * g < a.D && (NG == 1 || d % NG == grp)) store4(out + 16 * d + 4 * g, acc[d][f] * a.scale);
+    for (int i = 0; i < (L::DB + NG - 1) / NG; ++i) {
+      const int e = 16 * (i * NG + grp) + 4 * g;
+      if (e < a.D) store4(out + e, acc[i][f] * a.scale);
+    }
   }
 }
 
@@ -261,6 +270,12 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
     lq += NG;
     wrap(lq, lh);
   };
+  {
+    TileLoad<DS, BK, S::NW> vl;
+    vl.init(wave, lane, a.v.rs, a.D);
+    vl.issue(a.v.p + (int64_t)(st.row0 + k0) * a.v.rs + kvh * a.v.hs, a.v.rs, a.D, st.len - k0, lds + V, wave);
+  }
+  if (grp < total) load(0);
   bf16x8 k[KF][DS];
 #pragma unroll
   for (int f = 0; f < KF; ++f) {
@@ -273,12 +288,6 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
   for (int f = 0; f < KF; ++f)
 #pragma unroll
     for (int s = 0; s < DS; ++s) arrived(k[f][s]);
-  {
-    TileLoad<DS, BK, S::NW> vl;
-    vl.init(wave, lane, a.v.rs, a.D);
-    vl.issue(a.v.p + (int64_t)(st.row0 + k0) * a.v.rs + kvh * a.v.hs, a.v.rs, a.D, st.len - k0, lds + V, wave);
-  }
-  if (grp < total) load(0);
   RowFrag<DS> rf;  // from the stage; the group's q lie grp SET bytes on, dout TILE further
   ColFrag<DS> cf;
   rf.init(smem, lane);
@@ -291,42 +300,48 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
   int cq = grp, ch = 0;  // query tile (and head) of the step
   wrap(cq, ch);
   const int steps = (total + NG - 1) / NG;
+  const bool late = grp >= (NG + 1) / 2;
+  if (late) phase_barrier();
   for (int i = 0; i < steps; ++i) {
     const int j = i * NG + grp;
     const int stage = (i & 1) * STAGE + grp * SET;
     wait_vmcnt_and_barrier<0>();
     if (j + NG < total) load((i + 1) & 1);
-    if (NG > 1 && j >= total) continue;
+    const bool live = NG == 1 || j < total;
     const int q0 = (qt0 + cq) * BQ;
     cq += NG;
     wrap(cq, ch);
     const float* rows = reinterpret_cast<const float*>(smem + stage + 2 * TILE);
     f32x4 s[2][KF], dp[2][KF];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const f32x4 nd = -*LDS_PTR(const f32x4, rows + BQ + b * 16 + 4 * g);
-#pragma unroll
-      for (int f = 0; f < KF; ++f) {
-        s[b][f] = f32x4{0, 0, 0, 0};
-        dp[b][f] = nd;
-      }
-    }
-#pragma unroll
-    for (int d = 0; d < DS; ++d) {
-      bf16x8 v[KF];
-#pragma unroll
-      for (int f = 0; f < KF; ++f) v[f] = rf.read(V, w * KF + f, d);
+    if (live) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const bf16x8 qq = rf.read(stage, b, d);
-        const bf16x8 dd = rf.read(stage + TILE, b, d);
+        const f32x4 nd = -*LDS_PTR(const f32x4, rows + BQ + b * 16 + 4 * g);
 #pragma unroll
         for (int f = 0; f < KF; ++f) {
-          s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qq, k[f][d], s[b][f], 0, 0, 0);
-          dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dd, v[f], dp[b][f], 0, 0, 0);
+          s[b][f] = f32x4{0, 0, 0, 0};
+          dp[b][f] = nd;
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < DS; ++d) {
+        bf16x8 v[KF];
+#pragma unroll
+        for (int f = 0; f < KF; ++f) v[f] = rf.read(V, w * KF + f, d);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const bf16x8 qq = rf.read(stage, b, d);
+          const bf16x8 dd = rf.read(stage + TILE, b, d);
+#pragma unroll
+          for (int f = 0; f < KF; ++f) {
+            s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qq, k[f][d], s[b][f], 0, 0, 0);
+            dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dd, v[f], dp[b][f], 0, 0, 0);
+          }
         }
       }
     }
+    if (NG > 1) phase_barrier();
+    if (!live) continue;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const f32x4 l2 = *LDS_PTR(const f32x4, rows + b * 16 + 4 * g);
@@ -365,6 +380,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
     }
   }
   if (NG > 1) {
+    if (!late) phase_barrier();
     join_groups<NG, S::NR>(dk, smem, grp, w, lane);
     join_groups<NG, S::NR>(dv, smem, grp, w, lane);
   }
@@ -377,22 +393,22 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
       uint16_t* ok = a.dk.p + row * a.dk.rs + kvh * a.dk.hs;
       uint16_t* ov = a.dv.p + row * a.dv.rs + kvh * a.dv.hs;
 #pragma unroll
-      for (int d = 0; d < L::DB; ++d) {
-        const int e = 16 * d + 4 * g;
-        if (e < a.D && (NG == 1 || d % NG == grp)) {
-          store4(ok + e, dk[d][f] * a.scale);
-          store4(ov + e, dv[d][f]);
+      for (int i = 0; i < (L::DB + NG - 1) / NG; ++i) {
+        const int e = 16 * (i * NG + grp) + 4 * g;
+        if (e < a.D) {
+          store4(ok + e, dk[i][f] * a.scale);
+          store4(ov + e, dv[i][f]);
         }
       }
     } else {
       float* ok = p.part + (((int64_t)(part * 2) * a.G + kvh) * T + row) * a.D;
       float* ov = ok + (int64_t)a.G * T * a.D;
 #pragma unroll
-      for (int d = 0; d < L::DB; ++d) {
-        const int e = 16 * d + 4 * g;
-        if (e < a.D && (NG == 1 || d % NG == grp)) {
-          *reinterpret_cast<f32x4*>(ok + e) = dk[d][f];
-          *reinterpret_cast<f32x4*>(ov + e) = dv[d][f];
+      for (int i = 0; i < (L::DB + NG - 1) / NG; ++i) {
+        const int e = 16 * (i * NG + grp) + 4 * g;
+        if (e < a.D) {
+          *reinterpret_cast<f32x4*>(ok + e) = dk[i][f];
+          *reinterpret_cast<f32x4*>(ov + e) = dv[i][f];
         }
       }
     }
@@ -469,7 +485,8 @@ hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
   if (ranks * a.H > 0x7FFFFFFF) return hipErrorInvalidValue;
   p.ranks = (int32_t)ranks;
   constexpr int lds_q = std::max(2 * SQ::NG * 2 * SQ::TILE, SQ::JOIN);
-  constexpr int lds_kv = std::max(2 * SK::NG * (2 * SK::TILE + 2 * SK::ROWS * 4) + SK::BM * Tile<DS>::RB, SK::JOIN);
+  constexpr int lds_kv = std::max(2 * SK::NG * (2 * SK::TILE + 2 * SK::ROWS * 4) + SK::BM * Tile<DS>::RB,
+                                  SK::JOIN);
   auto kq = &attn_bwd_q<SQ>;
   auto kkv = &attn_bwd_kv<SK>;
   hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kq), lds_q);
