@@ -2,24 +2,31 @@
 //
 //   s = scale q k^T (u <= t),  lse = log sum_u exp(s),  out = sum_u exp(s - lse) v
 //
-// One pass over the keys with the running maximum m and sum l of the softmax, in base 2:
-// with c = scale log2(e), p = exp2(c s - c m).  A workgroup owns BM query rows of one head;
-// each of its 4 waves keeps its rows (as columns of the score tiles, see attn_common.h),
-// their fp32 output [head_dim x rows] and statistics in registers, and all waves share the
-// 64-row key and value tiles that direct-to-LDS loads bring in, double-buffered.  A score
-// column lives in four lanes, so its maximum costs two lane swaps and its rescaling factor
-// is a per-lane scalar.
+// One pass over the keys in base 2: with c = scale log2(e), p = exp2(c s - c m).  The reference
+// m is the maximum of the row's first tile, not a running one: p then can exceed 1, which costs
+// fp32 and bf16 nothing up to very large ratios, and no tile needs maxima, a rescaling of the
+// output or an exchange between lanes.  Where a sum passes 2^60, or an output is not finite, the
+// workgroup repeats its pass with the running maximum, which has no such limit: for scores that
+// pass the first tile's by 41 and more.
+//
+// A workgroup owns BM query rows of one head; each of its 4 waves keeps its rows (as columns of
+// the score tiles, see attn_common.h), their fp32 output [head_dim x rows] and sums in
+// registers, and all waves share the 64-row key and value tiles that direct-to-LDS loads bring
+// in, double-buffered.
 //
 // Rows past a sequence's end (of any input) are never read: their loads fall outside the
 // buffer resource and give zeros.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "attn_common.h"
 
 namespace ubx {
 namespace {
 
-constexpr float SLACK = 8.0f;  // powers of two a score may pass its row's reference by
+// A lane's sum with the first tile's reference beyond which the pass is done again.
+constexpr float MOST = 0x1p60f;
 
 struct PromptParams {
   PromptArgs a;
@@ -102,109 +109,140 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
   kf.init(smem + kg * 2 * TILE, lane);
   vf.init(smem + kg * 2 * TILE + TILE, lane);
   f32x4 o[L::DB][QF];
-  float m[QF], l[QF];  // m: the row's reference, at most SLACK / c under its maximum so far
-#pragma unroll
-  for (int f = 0; f < QF; ++f) {
-    m[f] = -INFINITY;
-    l[f] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < L::DB; ++d) o[d][f] = f32x4{0, 0, 0, 0};
-  }
+  float m[QF], l[QF];  // a row's reference and sum
   const int steps = (tiles + KG - 1) / KG;
   const bool late = kg >= (KG + 1) / 2;
-  if (late) phase_barrier();
-  for (int i = 0; i < steps; ++i) {
-    const int j = i * KG + kg;
-    const int stage = (i & 1) * S::STAGE;
-    wait_vmcnt_and_barrier<0>();
-    if (j + KG < tiles) load(j + KG, (i + 1) & 1);
-    const int k0 = j * BN;
-    const bool live = KG == 1 || j < tiles;
-    f32x4 s[KB][QF];
-    float top[QF];
-    bool above = false;
-    if (live) {
-#pragma unroll
-      for (int b = 0; b < KB; ++b)
-#pragma unroll
-        for (int f = 0; f < QF; ++f) s[b][f] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int d = 0; d < DS; ++d)
-#pragma unroll
-        for (int b = 0; b < KB; ++b) {
-          const bf16x8 kk = kf.read(stage, b, d);
-#pragma unroll
-          for (int f = 0; f < QF; ++f)
-            s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
-        }
-      if (k0 + BN - 1 > wq0) {  // the diagonal: keys after the query
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-          for (int f = 0; f < QF; ++f)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (k0 + b * 16 + 4 * g + i > wq0 + f * 16 + col) s[b][f][i] = -INFINITY;
-      }
-#pragma unroll
-      for (int f = 0; f < QF; ++f) {
-        float x = s[0][f][0];
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x = fmaxf(x, s[b][f][i]);
-        top[f] = col_max(x);
-        above = above || (top[f] - m[f]) * p.c > SLACK;
-      }
-    }
-    if (KG > 1) phase_barrier();
-    if (!live) continue;
-    if (__ballot(above)) {
-      // the reference moves to the maximum, here and for what was summed so far
-#pragma unroll
-      for (int f = 0; f < QF; ++f) {
-        const float x = fmaxf(top[f], m[f]);
-        const float r = exp2_(m[f] * p.c - (x == -INFINITY ? 0.0f : x * p.c));  // 0 the first time
-        m[f] = x;
-        l[f] *= r;
-#pragma unroll
-        for (int d = 0; d < L::DB; ++d) o[d][f] *= r;
-      }
-    }
+  // All key tiles, the first of which is being loaded.  FIXED: the reference is the first
+  // tile's maximum; true where that will not do.
+  auto pass = [&](auto fixed) __attribute__((always_inline)) {
+    constexpr bool FIXED = decltype(fixed)::value;
+    bool bad = false;
 #pragma unroll
     for (int f = 0; f < QF; ++f) {
-      const float base = m[f] == -INFINITY ? 0.0f : m[f] * p.c;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // short sums, so that a long row's l loses little
+      m[f] = -INFINITY;
+      l[f] = 0.0f;
 #pragma unroll
-      for (int b = 0; b < KB; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[b][f][i] = exp2_(s[b][f][i] * p.c - base);
-          sum[i] += s[b][f][i];
-        }
-      l[f] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      for (int d = 0; d < L::DB; ++d) o[d][f] = f32x4{0, 0, 0, 0};
     }
+    if (late) phase_barrier();
+    for (int i = 0; i < steps; ++i) {
+      const int j = i * KG + kg;
+      const int stage = (i & 1) * S::STAGE;
+      wait_vmcnt_and_barrier<0>();
+      if (j + KG < tiles) load(j + KG, (i + 1) & 1);
+      const int k0 = j * BN;
+      const bool live = KG == 1 || j < tiles;
+      f32x4 s[KB][QF];
+      if (live) {
 #pragma unroll
-    for (int t = 0; t < KB / 2; ++t) {
-      bf16x8 pf[QF];
+        for (int b = 0; b < KB; ++b)
 #pragma unroll
-      for (int f = 0; f < QF; ++f) pf[f] = pack8(s[2 * t][f], s[2 * t + 1][f]);
+          for (int f = 0; f < QF; ++f) s[b][f] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int d = 0; d < L::DB; ++d) {
-        const bf16x8 vv = vf.read(stage, t, d);
+        for (int d = 0; d < DS; ++d)
 #pragma unroll
-        for (int f = 0; f < QF; ++f)
-          o[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[f], o[d][f], 0, 0, 0);
+          for (int b = 0; b < KB; ++b) {
+            const bf16x8 kk = kf.read(stage, b, d);
+#pragma unroll
+            for (int f = 0; f < QF; ++f)
+              s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
+          }
+        if (k0 + BN - 1 > wq0) {  // the diagonal: keys after the query
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int f = 0; f < QF; ++f)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (k0 + b * 16 + 4 * g + i > wq0 + f * 16 + col) s[b][f][i] = -INFINITY;
+        }
+        if (!FIXED || i == 0) {
+#pragma unroll
+          for (int f = 0; f < QF; ++f) {
+            float x = s[0][f][0];
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x = fmaxf(x, s[b][f][i]);
+            x = col_max(x);
+            if (FIXED) {
+              // no score, though a key of the tile is not after the query
+              bad = bad || (x == -INFINITY && wq0 + f * 16 + col >= k0);
+              m[f] = x == -INFINITY ? 0.0f : x;
+            } else {
+              x = fmaxf(x, m[f]);
+              const float r = exp2_(m[f] * p.c - (x == -INFINITY ? 0.0f : x * p.c));  // 0 the first time
+              m[f] = x;
+              l[f] *= r;
+#pragma unroll
+              for (int d = 0; d < L::DB; ++d) o[d][f] *= r;
+            }
+          }
+        }
+      }
+      if (KG > 1) phase_barrier();
+      if (!live) continue;
+#pragma unroll
+      for (int f = 0; f < QF; ++f) {
+        const float base = !FIXED && m[f] == -INFINITY ? 0.0f : m[f] * p.c;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // short sums, so that a long row's l loses little
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[b][f][i] = exp2_(s[b][f][i] * p.c - base);
+            sum[i] += s[b][f][i];
+          }
+        l[f] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      }
+#pragma unroll
+      for (int t = 0; t < KB / 2; ++t) {
+        bf16x8 pf[QF];
+#pragma unroll
+        for (int f = 0; f < QF; ++f) pf[f] = pack8(s[2 * t][f], s[2 * t + 1][f]);
+#pragma unroll
+        for (int d = 0; d < L::DB; ++d) {
+          const bf16x8 vv = vf.read(stage, t, d);
+#pragma unroll
+          for (int f = 0; f < QF; ++f)
+            o[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[f], o[d][f], 0, 0, 0);
+        }
       }
     }
+    if (KG > 1 && !late) phase_barrier();
+    if (FIXED) {
+      float z = 0.0f;  // NaN if an output is not finite
+#pragma unroll
+      for (int f = 0; f < QF; ++f) {
+        bad = bad || !(l[f] < MOST);
+#pragma unroll
+        for (int d = 0; d < L::DB; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z += o[d][f][i] * 0.0f;
+      }
+      bad = bad || z != 0.0f;
+    }
+    return bad;
+  };
+  const bool bad = __ballot(pass(std::true_type{})) != 0;
+  int* flags = reinterpret_cast<int*>(smem);
+  __syncthreads();
+  if (lane == 0) flags[wave] = bad;
+  __syncthreads();
+  int again = 0;
+#pragma unroll
+  for (int w = 0; w < S::NW; ++w) again |= flags[w];
+  if (again) {
+    __syncthreads();
+    if (kg < tiles) load(kg, 0);
+    pass(std::false_type{});
   }
-  if (KG > 1 && !late) phase_barrier();
   constexpr int MINE = (L::DB + KG - 1) / KG;  // blocks of the output that a wave writes
   float base[QF], sum[QF];
 #pragma unroll
   for (int f = 0; f < QF; ++f) {
-    base[f] = m[f] == -INFINITY ? -INFINITY : m[f] * p.c;
     sum[f] = col_sum(l[f]);
+    base[f] = sum[f] == 0.0f ? -INFINITY : m[f] * p.c;
   }
   if (KG > 1) {
     // Join of the groups: all outputs and statistics through LDS; group kg joins blocks kg,

@@ -135,6 +135,72 @@ def test_prompt_and_gradient(ub, shape, lens, pad):
     assert bool(torch.isnan(dx[:, (H + 2 * G) * D:]).all())
 
 
+
+@pytest.mark.parametrize("shape,lens,pad", [
+    ((64, 64, 24), [700, 0, 330], 2),
+    ((72, 8, 128), [1, 300, 613], 0),
+    ((66, 22, 80), [1000], 1),
+    ((70, 70, 64), [129, 500, 64, 63, 255], 7),
+])
+def test_prompt_and_gradient_many_heads(ub, shape, lens, pad):
+    """Enough rows times heads for the kernels of one group of waves per workgroup."""
+    assert (sum(lens) + pad) * shape[0] >= 64 * 1024
+    test_prompt_and_gradient(ub, shape, lens, pad)
+
+
+@pytest.mark.parametrize("H,T", [(2, 700), (128, 530)])
+@pytest.mark.parametrize("low,high", [(0.0, 60.0), (-300.0, 300.0), (100.0, -100.0)])
+def test_prompt_scores_that_leave_the_first_tile(ub, H, T, low, high):
+    """Scores that rise (fall) along the keys by up to 600: beyond what the first tile's maximum
+    can stand for, so that the pass is repeated with the running one."""
+    D = 16
+    x = torch.zeros((T, 3, H, D), dtype=BF16)
+    x[:, 0, :, 0] = 4.0
+    x[:, 0, :, 1:] = normal(1, (T, H, D - 1))
+    x[:, 1, :, 0] = (torch.linspace(low, high, T) / 4)[:, None].to(BF16)
+    x[:, 1, :, 1:] = normal(2, (T, H, D - 1))
+    x[:, 2] = normal(3, (T, H, D))
+    x = x.reshape(T, -1)
+    cu = [0, 65, 66, T]
+    out = torch.full((T, H * D), math.nan, dtype=BF16, device="cuda")
+    lse = torch.full((H, T), math.nan, device="cuda")
+    xd = x.cuda()
+    with Rank(ub, T) as h:
+        ub.ub_attn_prompt(h, ub.heads(xd), ub.heads(xd, H * D), ub.heads(xd, 2 * H * D), ub.heads(out), lse, i32(cu), 3,
+                          ub.make_attn_cfg(H, H, D, softmax_scale=1.0))
+        torch.cuda.synchronize()
+    q, k, v = (t.double() for t in split(x, (H, H, D)))
+    w, l, tw, tl = ref.prompt(q, k, v, cu, 1.0)
+    ref.check(out.reshape(T, H, D), w, tw, "out")
+    ref.check(lse, l, tl, "lse")
+
+
+def test_prompt_first_tile_without_scores(ub):
+    """Scores of -inf at all keys of the first tiles, and finite ones after them."""
+    H, D, T = 2, 64, 400
+    x = normal(5, (T, 3, H, D))
+    x[:, 0, :, 0] = -3e38
+    x[:, 1, :, 0] = 0.0
+    x[:140, 1, :, 0] = 3e38
+    x = x.reshape(T, -1)
+    out = torch.empty((T, H * D), dtype=BF16, device="cuda")
+    lse = torch.empty((H, T), device="cuda")
+    xd = x.cuda()
+    with Rank(ub, T) as h:
+        ub.ub_attn_prompt(h, ub.heads(xd), ub.heads(xd, H * D), ub.heads(xd, 2 * H * D), ub.heads(out), lse,
+                          i32([0, T]), 1, ub.make_attn_cfg(H, H, D))
+        torch.cuda.synchronize()
+    assert bool((out[:140] == 0).all()) and bool((lse[:, :140] == -math.inf).all())
+    q, k, v = (t.double() for t in split(x, (H, H, D)))
+    q[..., 0] = 0.0
+    for g in range(H):
+        mask = torch.ones(T, T, dtype=torch.bool).tril()
+        mask[:, :140] = False
+        o, l, t, tl = ref.one(q[140:, g], k[:, g], v[:, g], D ** -0.5, mask[140:])
+        ref.check(out[140:].reshape(-1, H, D)[:, g], o, t, "out")
+        ref.check(lse[g, 140:], l, tl, "lse")
+
+
 @pytest.mark.parametrize("scale,std", [(1.0, 2.0), (0.01, 1.0), (0.125, 8.0)])
 def test_prompt_large_and_small_scores(ub, scale, std):
     """Scores far apart (one key takes the whole row) and nearly equal."""
