@@ -32,10 +32,9 @@ COMMON = [
 # Device code is compiled without packed-fp32 instructions.
 DEVICE = ["--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 # Instruction scheduling for parallelism within a wave rather than for registers, of which the
-# prompt kernels' two waves per SIMD have enough: forward 1239 -> 1212 us (24392 tokens, 8 heads
-# on 1), gradient 386 + 591 -> 376 + 579 us (16264 tokens).  Decode does not gain.
-MAX_ILP = ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]
-FLAGS = {"attn_prompt.hip": MAX_ILP, "attn_prompt_bwd.hip": MAX_ILP}
+# forward kernel's two waves per SIMD have enough: 1239 -> 1212 us (24392 tokens, 8 heads on 1).
+# The gradient's kernels and decode do not gain.
+FLAGS = {"attn_prompt.hip": ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]}
 
 
 def hipcc():

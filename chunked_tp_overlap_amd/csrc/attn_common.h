@@ -149,6 +149,50 @@ __device__ inline bf16x8 load_row8(const uint16_t* p, bool valid) {
   return __builtin_bit_cast(bf16x8, v);
 }
 
+// Diagonal tiles: a pair that the mask leaves out has weight 0, but the product over a tile's
+// 32 rows would take 0 times its value, NaN for one that is not finite.  A workgroup whose
+// diagonal tiles hold such values does its pass again with seen_product, every column computed
+// by itself from the rows that the mask lets it see.  (As a branch in the one pass it would make
+// the compiler copy or spill the accumulators.)
+// Whether wave w of the W that share a tile of BYTES finds such a value in its share of it.
+template <int BYTES, int W>
+__device__ inline bool not_finite(const unsigned char* tile, int w, int lane) {
+  static_assert(BYTES % (1024 * W) == 0, "a tile divides over the waves");
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < BYTES / (1024 * W); ++i) {
+    const u32x4 x = *LDS_PTR(const u32x4, tile + (i * W + w) * 1024 + lane * 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) any |= (x[k] & 0x7F807F80u) + 0x00800080u;  // exponents of all ones carry
+  }
+  return (any & 0x80008000u) != 0;
+}
+// Bits of the lane's 8 elements whose tile rows (the first at `row`, in the numbering at the
+// top) come no later than `at` (UP_TO) or no earlier.
+template <bool UP_TO>
+__device__ inline u32x4 keep_rows(int row, int at, int g) {
+  u32x4 m;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row + 4 * g + (i & 1) * 2 + (i >> 1) * 16;
+    const bool lo = UP_TO ? r <= at : r >= at, hi = UP_TO ? r + 1 <= at : r + 1 >= at;
+    m[i] = (lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+  }
+  return m;
+}
+// acc + A B, column c of the 16 (the tile row at + c) from the rows that it sees.
+template <bool UP_TO>
+__device__ inline f32x4 seen_product(bf16x8 a, bf16x8 b, f32x4 acc, int row, int at, int lane) {
+  f32x4 r = acc;
+#pragma unroll 1
+  for (int c = 0; c < 16; ++c) {
+    const u32x4 x = __builtin_bit_cast(u32x4, a) & keep_rows<UP_TO>(row, at + c, lane >> 4);
+    const f32x4 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), b, acc, 0, 0, 0);
+    if ((lane & 15) == c) r = y;
+  }
+  return r;
+}
+
 // Makes the compiler wait here for a value it loads.  It does not count the direct-to-LDS
 // loads, so a wait that it left to a value's first use, inside a loop, would be one for all
 // loads in flight there: the next tile's among them, in every iteration.
@@ -161,6 +205,21 @@ __device__ inline void phase_barrier() {
   __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
+}
+
+// Whether any wave of the workgroup says so; through LDS that nothing is being loaded into.
+template <int NW>
+__device__ inline bool any_wave(bool x, unsigned char* smem, int wave, int lane) {
+  int* flags = reinterpret_cast<int*>(smem);
+  const bool mine = __ballot(x) != 0;
+  __syncthreads();
+  if (lane == 0) flags[wave] = mine;
+  __syncthreads();
+  int any = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) any |= flags[w];
+  __syncthreads();
+  return any != 0;
 }
 
 // Sum over NG groups of W waves each of the accumulators that wave w of every group holds,

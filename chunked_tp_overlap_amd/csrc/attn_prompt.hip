@@ -113,7 +113,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
   const int steps = (tiles + KG - 1) / KG;
   const bool late = kg >= (KG + 1) / 2;
   // All key tiles, the first of which is being loaded.  FIXED: the reference is the first
-  // tile's maximum; true where that will not do.
+  // tile's maximum, and values are finite; true where that will not do.
   auto pass = [&](auto fixed) __attribute__((always_inline)) {
     constexpr bool FIXED = decltype(fixed)::value;
     bool bad = false;
@@ -125,7 +125,9 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
       for (int d = 0; d < L::DB; ++d) o[d][f] = f32x4{0, 0, 0, 0};
     }
     if (late) phase_barrier();
-    for (int i = 0; i < steps; ++i) {
+    // DIAGONAL: tiles that may hold keys after one of the workgroup's queries
+    auto step = [&](int i, auto diagonal) __attribute__((always_inline)) {
+      constexpr bool DIAGONAL = decltype(diagonal)::value;
       const int j = i * KG + kg;
       const int stage = (i & 1) * S::STAGE;
       wait_vmcnt_and_barrier<0>();
@@ -147,7 +149,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
             for (int f = 0; f < QF; ++f)
               s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
           }
-        if (k0 + BN - 1 > wq0) {  // the diagonal: keys after the query
+        if (DIAGONAL && k0 + BN - 1 > wq0) {
 #pragma unroll
           for (int b = 0; b < KB; ++b)
 #pragma unroll
@@ -181,7 +183,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
         }
       }
       if (KG > 1) phase_barrier();
-      if (!live) continue;
+      if (!live) return;
 #pragma unroll
       for (int f = 0; f < QF; ++f) {
         const float base = !FIXED && m[f] == -INFINITY ? 0.0f : m[f] * p.c;
@@ -195,20 +197,37 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
           }
         l[f] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
+      bf16x8 pf[KB / 2][QF];
 #pragma unroll
-      for (int t = 0; t < KB / 2; ++t) {
-        bf16x8 pf[QF];
+      for (int t = 0; t < KB / 2; ++t)
 #pragma unroll
-        for (int f = 0; f < QF; ++f) pf[f] = pack8(s[2 * t][f], s[2 * t + 1][f]);
+        for (int f = 0; f < QF; ++f) pf[t][f] = pack8(s[2 * t][f], s[2 * t + 1][f]);
+      if (FIXED && DIAGONAL)
+        bad = bad || not_finite<TILE, S::RW>(smem + stage + kg * 2 * TILE + TILE, rw, lane);
+      if (!FIXED && DIAGONAL) {
+#pragma unroll
+        for (int t = 0; t < KB / 2; ++t)
+#pragma unroll
+          for (int d = 0; d < L::DB; ++d)
+#pragma unroll
+            for (int f = 0; f < QF; ++f)
+              o[d][f] = seen_product<true>(vf.read(stage, t, d), pf[t][f], o[d][f], k0 + 32 * t, wq0 + f * 16, lane);
+        return;
+      }
+#pragma unroll
+      for (int t = 0; t < KB / 2; ++t)
 #pragma unroll
         for (int d = 0; d < L::DB; ++d) {
           const bf16x8 vv = vf.read(stage, t, d);
 #pragma unroll
           for (int f = 0; f < QF; ++f)
-            o[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[f], o[d][f], 0, 0, 0);
+            o[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[t][f], o[d][f], 0, 0, 0);
         }
-      }
-    }
+    };
+    const int full = min(q0 / (BN * KG), steps);  // steps of tiles before every query
+    int i = 0;
+    for (; i < full; ++i) step(i, std::false_type{});
+    for (; i < steps; ++i) step(i, std::true_type{});
     if (KG > 1 && !late) phase_barrier();
     if (FIXED) {
       float z = 0.0f;  // NaN if an output is not finite
@@ -224,16 +243,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
     }
     return bad;
   };
-  const bool bad = __ballot(pass(std::true_type{})) != 0;
-  int* flags = reinterpret_cast<int*>(smem);
-  __syncthreads();
-  if (lane == 0) flags[wave] = bad;
-  __syncthreads();
-  int again = 0;
-#pragma unroll
-  for (int w = 0; w < S::NW; ++w) again |= flags[w];
-  if (again) {
-    __syncthreads();
+  if (any_wave<S::NW>(pass(std::true_type{}), smem, wave, lane)) {
     if (kg < tiles) load(kg, 0);
     pass(std::false_type{});
   }

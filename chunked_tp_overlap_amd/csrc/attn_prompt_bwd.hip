@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_common.h"
 
@@ -132,75 +133,102 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_q(BwdParams p) {
   rf.init(smem + grp * 2 * TILE, lane);
   cf.init(smem + grp * 2 * TILE, lane);
   f32x4 acc[L::DB][QF];
-#pragma unroll
-  for (int d = 0; d < L::DB; ++d)
-#pragma unroll
-    for (int f = 0; f < QF; ++f) acc[d][f] = f32x4{0, 0, 0, 0};
   const int steps = (tiles + NG - 1) / NG;
   const bool late = grp >= (NG + 1) / 2;
-  if (late) phase_barrier();
-  for (int i = 0; i < steps; ++i) {
-    const int j = i * NG + grp;
-    const int stage = (i & 1) * STAGE;
-    wait_vmcnt_and_barrier<0>();
-    if (j + NG < tiles) load(j + NG, (i + 1) & 1);
-    const bool live = NG == 1 || j < tiles;
-    const int k0 = j * BN;
+  // All key tiles, the first of which is being loaded; true if a diagonal one holds values that
+  // are not finite, unless it is CAREFUL of them.
+  auto pass = [&](auto careful) __attribute__((always_inline)) {
+    constexpr bool CAREFUL = decltype(careful)::value;
+    bool bad = false;
 #pragma unroll
-    for (int t = 0; t < BN / 32; ++t) {
-      f32x4 s[2][QF], dp[2][QF];
-      if (live) {
+    for (int d = 0; d < L::DB; ++d)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+      for (int f = 0; f < QF; ++f) acc[d][f] = f32x4{0, 0, 0, 0};
+    if (late) phase_barrier();
+    // DIAGONAL: tiles that may hold keys after one of the workgroup's queries
+    auto step = [&](int i, auto diagonal) __attribute__((always_inline)) {
+      constexpr bool DIAGONAL = decltype(diagonal)::value;
+      const int j = i * NG + grp;
+      const int stage = (i & 1) * STAGE;
+      wait_vmcnt_and_barrier<0>();
+      if (j + NG < tiles) load(j + NG, (i + 1) & 1);
+      const bool live = NG == 1 || j < tiles;
+      const int k0 = j * BN;
+      if (!CAREFUL && DIAGONAL && live)
+        bad = bad || not_finite<TILE, S::NR>(smem + grp * 2 * TILE + stage, w, lane);
 #pragma unroll
-          for (int f = 0; f < QF; ++f) {
-            s[b][f] = f32x4{0, 0, 0, 0};
-            dp[b][f] = f32x4{0, 0, 0, 0};
-          }
+      for (int t = 0; t < BN / 32; ++t) {
+        f32x4 s[2][QF], dp[2][QF];
+        if (live) {
 #pragma unroll
-        for (int d = 0; d < DS; ++d)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const bf16x8 kk = rf.read(stage, 2 * t + b, d);
-            const bf16x8 vv = rf.read(stage + TILE, 2 * t + b, d);
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int f = 0; f < QF; ++f) {
-              s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
-              dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, dout[f][d], dp[b][f], 0, 0, 0);
+              s[b][f] = f32x4{0, 0, 0, 0};
+              dp[b][f] = f32x4{0, 0, 0, 0};
             }
-          }
-      }
-      if (NG > 1) phase_barrier();
-      if (!live) continue;
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+          for (int d = 0; d < DS; ++d)
 #pragma unroll
-        for (int f = 0; f < QF; ++f)
+            for (int b = 0; b < 2; ++b) {
+              const bf16x8 kk = rf.read(stage, 2 * t + b, d);
+              const bf16x8 vv = rf.read(stage + TILE, 2 * t + b, d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            s[b][f][i] = exp2_(s[b][f][i] * p.c - lse2[f]) * (dp[b][f][i] - delta[f]);
-      if (k0 + BN - 1 > wq0) {  // the diagonal: keys after the query
+              for (int f = 0; f < QF; ++f) {
+                s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
+                dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, dout[f][d], dp[b][f], 0, 0, 0);
+              }
+            }
+        }
+        if (NG > 1) phase_barrier();
+        if (!live) continue;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int f = 0; f < QF; ++f)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (k0 + t * 32 + b * 16 + 4 * g + i > wq0 + f * 16 + col) s[b][f][i] = 0.0f;
+              s[b][f][i] = exp2_(s[b][f][i] * p.c - lse2[f]) * (dp[b][f][i] - delta[f]);
+        if (DIAGONAL && k0 + BN - 1 > wq0) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int f = 0; f < QF; ++f)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (k0 + t * 32 + b * 16 + 4 * g + i > wq0 + f * 16 + col) s[b][f][i] = 0.0f;
+        }
+        bf16x8 ds[QF];
+#pragma unroll
+        for (int f = 0; f < QF; ++f) ds[f] = pack8(s[0][f], s[1][f]);
+        if (CAREFUL && DIAGONAL) {
+#pragma unroll
+          for (int d = 0; d < L::DB; ++d)
+#pragma unroll
+            for (int f = 0; f < QF; ++f)
+              acc[d][f] = seen_product<true>(cf.read(stage, t, d), ds[f], acc[d][f], k0 + t * 32, wq0 + f * 16, lane);
+          continue;
+        }
+#pragma unroll
+        for (int d = 0; d < L::DB; ++d) {
+          const bf16x8 kk = cf.read(stage, t, d);
+#pragma unroll
+          for (int f = 0; f < QF; ++f)
+            acc[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, ds[f], acc[d][f], 0, 0, 0);
+        }
       }
-      bf16x8 ds[QF];
-#pragma unroll
-      for (int f = 0; f < QF; ++f) ds[f] = pack8(s[0][f], s[1][f]);
-#pragma unroll
-      for (int d = 0; d < L::DB; ++d) {
-        const bf16x8 kk = cf.read(stage, t, d);
-#pragma unroll
-        for (int f = 0; f < QF; ++f)
-          acc[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, ds[f], acc[d][f], 0, 0, 0);
-      }
-    }
+    };
+    const int full = min(q0 / (BN * NG), steps);  // steps of tiles before every query
+    int i = 0;
+    for (; i < full; ++i) step(i, std::false_type{});
+    for (; i < steps; ++i) step(i, std::true_type{});
+    if (NG > 1 && !late) phase_barrier();
+    return bad;
+  };
+  if (any_wave<S::NW>(pass(std::false_type{}), smem, wave, lane)) {
+    if (grp < tiles) load(grp, 0);
+    pass(std::true_type{});
   }
-  if (NG > 1 && !late) phase_barrier();
   if (NG > 1) join_groups<NG, S::NR>(acc, smem, grp, w, lane);
 #pragma unroll
   for (int f = 0; f < QF; ++f) {
@@ -249,16 +277,30 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
   TileLoad<DS, BQ, S::NR> ql, dl;
   ql.init(w, lane, a.q.rs, a.D);
   dl.init(w, lane, a.dout.rs, a.D);
-  int lh = 0, lq = grp;  // head and query tile of the group's next load
-  auto wrap = [&](int& q, int& h) {
-    while (q >= qtiles) {
-      q -= qtiles;
-      ++h;
-    }
+  // The query tiles that may hold rows before one of the workgroup's keys come first, head by
+  // head, then the others: item j of the group's j = grp, grp + NG, ...
+  const int edge = min(BK / BQ, qtiles);
+  struct Item {
+    int h, q, end;  // head, query tile, and where the head's tiles of this kind end
   };
-  wrap(lq, lh);
+  auto advance = [&](Item& x, int n) {
+    for (; n > 0; --n)
+      if (++x.q == x.end) {
+        if (++x.h == heads) {
+          x.h = 0;
+          x.end = qtiles;
+        }
+        x.q = x.end == edge ? 0 : edge;
+      }
+  };
+  Item next;  // the group's next load
+  auto start = [&] {
+    next = Item{0, 0, edge};
+    advance(next, grp);
+  };
+  start();
   auto load = [&](int stage) {
-    const int head = head0 + lh, r = (qt0 + lq) * BQ, valid = st.len - r;
+    const int head = head0 + next.h, r = (qt0 + next.q) * BQ, valid = st.len - r;
     const uint32_t at = lds + stage * STAGE + grp * SET;
     const int64_t row = st.row0 + r;
     ql.issue(a.q.p + row * a.q.rs + head * a.q.hs, a.q.rs, a.D, valid, at, w);
@@ -267,8 +309,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
       const float* x = (w == 0 ? p.lse2 : p.delta) + head * T + row;
       dma4(make_rsrc(x, (uint32_t)min(valid, BQ) * 4), at + 2 * TILE + w * BQ * 4, lane * 4);
     }
-    lq += NG;
-    wrap(lq, lh);
+    advance(next, NG);
   };
   {
     TileLoad<DS, BK, S::NW> vl;
@@ -293,94 +334,121 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
   rf.init(smem, lane);
   cf.init(smem, lane);
   f32x4 dk[L::DB][KF], dv[L::DB][KF];
-#pragma unroll
-  for (int d = 0; d < L::DB; ++d)
-#pragma unroll
-    for (int f = 0; f < KF; ++f) dk[d][f] = dv[d][f] = f32x4{0, 0, 0, 0};
-  int cq = grp, ch = 0;  // query tile (and head) of the step
-  wrap(cq, ch);
   const int steps = (total + NG - 1) / NG;
   const bool late = grp >= (NG + 1) / 2;
-  if (late) phase_barrier();
-  for (int i = 0; i < steps; ++i) {
-    const int j = i * NG + grp;
-    const int stage = (i & 1) * STAGE + grp * SET;
-    wait_vmcnt_and_barrier<0>();
-    if (j + NG < total) load((i + 1) & 1);
-    const bool live = NG == 1 || j < total;
-    const int q0 = (qt0 + cq) * BQ;
-    cq += NG;
-    wrap(cq, ch);
-    const float* rows = reinterpret_cast<const float*>(smem + stage + 2 * TILE);
-    f32x4 s[2][KF], dp[2][KF];
-    if (live) {
+  // As in attn_bwd_q.
+  auto pass = [&](auto careful) __attribute__((always_inline)) {
+    constexpr bool CAREFUL = decltype(careful)::value;
+    bool bad = false;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const f32x4 nd = -*LDS_PTR(const f32x4, rows + BQ + b * 16 + 4 * g);
+    for (int d = 0; d < L::DB; ++d)
 #pragma unroll
-        for (int f = 0; f < KF; ++f) {
-          s[b][f] = f32x4{0, 0, 0, 0};
-          dp[b][f] = nd;
-        }
-      }
-#pragma unroll
-      for (int d = 0; d < DS; ++d) {
-        bf16x8 v[KF];
-#pragma unroll
-        for (int f = 0; f < KF; ++f) v[f] = rf.read(V, w * KF + f, d);
+      for (int f = 0; f < KF; ++f) dk[d][f] = dv[d][f] = f32x4{0, 0, 0, 0};
+    Item now{0, 0, edge};
+    advance(now, grp);
+    if (late) phase_barrier();
+    auto step = [&](int i, auto diagonal) __attribute__((always_inline)) {
+      constexpr bool DIAGONAL = decltype(diagonal)::value;
+      const int j = i * NG + grp;
+      const int stage = (i & 1) * STAGE + grp * SET;
+      wait_vmcnt_and_barrier<0>();
+      if (j + NG < total) load((i + 1) & 1);
+      const bool live = NG == 1 || j < total;
+      const int q0 = (qt0 + now.q) * BQ;
+      advance(now, NG);
+      const float* rows = reinterpret_cast<const float*>(smem + stage + 2 * TILE);
+      f32x4 s[2][KF], dp[2][KF];
+      if (live) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const bf16x8 qq = rf.read(stage, b, d);
-          const bf16x8 dd = rf.read(stage + TILE, b, d);
+          const f32x4 nd = -*LDS_PTR(const f32x4, rows + BQ + b * 16 + 4 * g);
 #pragma unroll
           for (int f = 0; f < KF; ++f) {
-            s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qq, k[f][d], s[b][f], 0, 0, 0);
-            dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dd, v[f], dp[b][f], 0, 0, 0);
+            s[b][f] = f32x4{0, 0, 0, 0};
+            dp[b][f] = nd;
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < DS; ++d) {
+          bf16x8 v[KF];
+#pragma unroll
+          for (int f = 0; f < KF; ++f) v[f] = rf.read(V, w * KF + f, d);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const bf16x8 qq = rf.read(stage, b, d);
+            const bf16x8 dd = rf.read(stage + TILE, b, d);
+#pragma unroll
+            for (int f = 0; f < KF; ++f) {
+              s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qq, k[f][d], s[b][f], 0, 0, 0);
+              dp[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dd, v[f], dp[b][f], 0, 0, 0);
+            }
           }
         }
       }
-    }
-    if (NG > 1) phase_barrier();
-    if (!live) continue;
+      if (NG > 1) phase_barrier();
+      if (!live) return;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const f32x4 l2 = *LDS_PTR(const f32x4, rows + b * 16 + 4 * g);
-#pragma unroll
-      for (int f = 0; f < KF; ++f)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[b][f][i] = exp2_(s[b][f][i] * p.c - l2[i]);
-          dp[b][f][i] *= s[b][f][i];
-        }
-    }
-    if (q0 < wk0 + 16 * KF - 1) {  // the diagonal: queries before the key
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < 2; ++b) {
+        const f32x4 l2 = *LDS_PTR(const f32x4, rows + b * 16 + 4 * g);
 #pragma unroll
         for (int f = 0; f < KF; ++f)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (wk0 + f * 16 + col > q0 + b * 16 + 4 * g + i) s[b][f][i] = dp[b][f][i] = 0.0f;
-    }
-    bf16x8 pf[KF], ds[KF];
+          for (int i = 0; i < 4; ++i) {
+            s[b][f][i] = exp2_(s[b][f][i] * p.c - l2[i]);
+            dp[b][f][i] *= s[b][f][i];
+          }
+      }
+      if (DIAGONAL && q0 < wk0 + 16 * KF - 1) {
 #pragma unroll
-    for (int f = 0; f < KF; ++f) {
-      pf[f] = pack8(s[0][f], s[1][f]);
-      ds[f] = pack8(dp[0][f], dp[1][f]);
-    }
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int d = 0; d < L::DB; ++d) {
-      const bf16x8 dd = cf.read(stage + TILE, 0, d);
-      const bf16x8 qq = cf.read(stage, 0, d);
+          for (int f = 0; f < KF; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (wk0 + f * 16 + col > q0 + b * 16 + 4 * g + i) s[b][f][i] = dp[b][f][i] = 0.0f;
+      }
+      bf16x8 pf[KF], ds[KF];
 #pragma unroll
       for (int f = 0; f < KF; ++f) {
-        dv[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dd, pf[f], dv[d][f], 0, 0, 0);
-        dk[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qq, ds[f], dk[d][f], 0, 0, 0);
+        pf[f] = pack8(s[0][f], s[1][f]);
+        ds[f] = pack8(dp[0][f], dp[1][f]);
       }
-    }
+      if (!CAREFUL && DIAGONAL)
+        bad = bad || not_finite<2 * TILE, S::NR>(smem + stage, w, lane);
+      if (CAREFUL && DIAGONAL) {
+#pragma unroll
+        for (int d = 0; d < L::DB; ++d)
+#pragma unroll
+          for (int f = 0; f < KF; ++f) {
+            dv[d][f] = seen_product<false>(cf.read(stage + TILE, 0, d), pf[f], dv[d][f], q0, wk0 + f * 16, lane);
+            dk[d][f] = seen_product<false>(cf.read(stage, 0, d), ds[f], dk[d][f], q0, wk0 + f * 16, lane);
+          }
+        return;
+      }
+#pragma unroll
+      for (int d = 0; d < L::DB; ++d) {
+        const bf16x8 dd = cf.read(stage + TILE, 0, d);
+        const bf16x8 qq = cf.read(stage, 0, d);
+#pragma unroll
+        for (int f = 0; f < KF; ++f) {
+          dv[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dd, pf[f], dv[d][f], 0, 0, 0);
+          dk[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qq, ds[f], dk[d][f], 0, 0, 0);
+        }
+      }
+    };
+    const int first = min((heads * edge + NG - 1) / NG, steps);  // steps with tiles of the first kind
+    int i = 0;
+    for (; i < first; ++i) step(i, std::true_type{});
+    for (; i < steps; ++i) step(i, std::false_type{});
+    if (NG > 1 && !late) phase_barrier();
+    return bad;
+  };
+  if (any_wave<S::NW>(pass(std::false_type{}), smem, wave, lane)) {
+    start();
+    if (grp < total) load(0);
+    pass(std::true_type{});
   }
   if (NG > 1) {
-    if (!late) phase_barrier();
     join_groups<NG, S::NR>(dk, smem, grp, w, lane);
     join_groups<NG, S::NR>(dv, smem, grp, w, lane);
   }

@@ -201,6 +201,60 @@ def test_prompt_first_tile_without_scores(ub):
         ref.check(lse[g, 140:], l, tl, "lse")
 
 
+
+@pytest.mark.parametrize("H,G,D,lens", [(2, 1, 64, [30, 333, 70]), (4, 2, 128, [500]), (96, 48, 40, [100, 590]),
+                                        (72, 72, 128, [940])])
+@pytest.mark.parametrize("r", [1, 17, 63, 64, 200])
+def test_prompt_values_that_the_mask_leaves_out(ub, H, G, D, lens, r):
+    """NaN and inf in row r of a sequence: no row before it sees its key and value, and no key
+    after it its query."""
+    x, T = make((H, G, D), lens, 0, 11)
+    cu, scale = cu_of(lens), D ** -0.5
+    cfg = ub.make_attn_cfg(H, G, D)
+    long = max(range(len(lens)), key=lambda i: lens[i])
+    at = cu[long] + r  # other sequences and the rows named below are as without it
+    do = normal(12, (T, H * D))
+    q, k, v = (t.double() for t in split(x, (H, G, D)))
+    o, l, to, tl = ref.prompt(q, k, v, cu, scale)
+    grads, tols = ref.prompt_bwd(do.double().reshape(T, H, D), q, k, v, cu, scale)
+    for which in ("keys", "queries"):
+        y, dy = x.clone(), do.clone()
+        if which == "keys":
+            y[at, H * D:(H + G) * D: 2] = math.inf
+            y[at, (H + G) * D:] = math.nan
+            y[at, -1] = -math.inf
+        else:
+            y[at, : H * D] = math.nan
+            dy[at] = math.nan
+            dy[at, ::3] = math.inf
+        yd, dyd = y.cuda(), dy.cuda()
+        out, lse = torch.empty((T, H * D), dtype=BF16, device="cuda"), torch.empty((H, T), device="cuda")
+        dx = torch.empty_like(yd)
+        ws = workspace(ub, ub.UB_ATTN_PROMPT_BWD, cfg, T, len(lens))
+        hs = [ub.heads(yd, c) for c in (0, H * D, (H + G) * D)]
+        with Rank(ub, T) as h:
+            ub.ub_attn_prompt(h, *hs, ub.heads(out), lse, i32(cu), len(lens), cfg)
+            ub.ub_attn_prompt_bwd(h, ub.heads(dyd), *hs, ub.heads(out), lse,
+                                  *[ub.heads(dx, c) for c in (0, H * D, (H + G) * D)], i32(cu), len(lens), cfg, ws)
+            torch.cuda.synchronize()
+        dq, dk, dv = split(dx, (H, G, D))
+        others = torch.ones(T, dtype=torch.bool)
+        others[cu[long]: cu[long + 1]] = False
+        before, after, not_it = others.clone(), others.clone(), torch.ones(T, dtype=torch.bool)
+        before[cu[long]: at] = True
+        after[at + 1: cu[long + 1]] = True
+        not_it[at] = False
+        if which == "keys":
+            checks = [(out.reshape(T, H, D), o, to, before), (dq, grads[0], tols[0], before)]
+        else:
+            checks = [(out.reshape(T, H, D), o, to, not_it), (dq, grads[0], tols[0], not_it),
+                      (dk, grads[1], tols[1], after), (dv, grads[2], tols[2], after)]
+        for n, (got, want, tol, rows) in enumerate(checks):
+            ref.check(got.cpu()[rows], want[rows], tol[rows], f"{which} {n}")
+        rows = before if which == "keys" else not_it
+        ref.check(lse.cpu()[:, rows], l[:, rows], tl[:, rows], f"{which} lse")
+
+
 @pytest.mark.parametrize("scale,std", [(1.0, 2.0), (0.01, 1.0), (0.125, 8.0)])
 def test_prompt_large_and_small_scores(ub, scale, std):
     """Scores far apart (one key takes the whole row) and nearly equal."""
