@@ -88,11 +88,13 @@ class ub_attn_cfg_t(ctypes.Structure):
 
 
 class ub_heads_t(ctypes.Structure):
+    tensor = held = None  # what heads() describes; the (heads, dim) it was last checked against
     _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("rows", ctypes.c_int64)]
 
 
 class ub_kv_cache_t(ctypes.Structure):
+    tensors, held = (), None
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
                 ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32),
@@ -448,40 +450,31 @@ def make_kv_cache(k, v, k_scale=1.0, v_scale=1.0):
 
 # A call's own cost is a few microseconds, as much as a small batch's kernel: descriptors are
 # checked against a head layout once, and tensors with as few attribute reads as it takes.
-def _heads_arg(x, n, cfg, what):
-    """x, once its columns are known to hold n heads."""
-    if x is None:
-        return None
-    D = cfg.head_dim
-    if getattr(x, "held", None) != (n, D):
-        t = getattr(x, "tensor", None)
-        if t is not None:
-            if t.dim() == 3 and (t.shape[1] < n or t.shape[2] < D):
-                raise ValueError(f"{what}: {tuple(t.shape)} does not hold {n} heads of {D}")
-            if t.dim() == 2 and x.col + n * D > t.shape[1]:
-                raise ValueError(f"{what}: columns {x.col} to {x.col + n * D} of {t.shape[1]}")
-            x.held = (n, D)
-    return x
+def _hold_heads(x, layout, what):
+    """Checks that x's columns hold the (heads, dim) of layout."""
+    n, D = layout
+    t = x.tensor
+    if t is not None:
+        if t.dim() == 3 and (t.shape[1] < n or t.shape[2] < D):
+            raise ValueError(f"{what}: {tuple(t.shape)} does not hold {n} heads of {D}")
+        if t.dim() == 2 and x.col + n * D > t.shape[1]:
+            raise ValueError(f"{what}: columns {x.col} to {x.col + n * D} of {t.shape[1]}")
+        x.held = layout
 
 
-def _cache_arg(cache, cfg):
-    if cache is None:
-        return None
-    n, D = cfg.n_kv_heads, cfg.head_dim
-    if getattr(cache, "held", None) != (n, D):
-        tensors = getattr(cache, "tensors", ())
-        for t in tensors:
-            if t.shape[1] < n or t.shape[3] < D:
-                raise ValueError(f"cache: {tuple(t.shape)} does not hold {n} heads of {D}")
-        if tensors:
-            cache.held = (n, D)
-    return cache
+def _hold_cache(cache, layout):
+    n, D = layout
+    for t in cache.tensors:
+        if t.shape[1] < n or t.shape[3] < D:
+            raise ValueError(f"cache: {tuple(t.shape)} does not hold {n} heads of {D}")
+    if cache.tensors:
+        cache.held = layout
 
 
 def _int32(x, n, what):
     """A pointer to at least n contiguous int32 values."""
-    if isinstance(x, torch.Tensor):
-        if x.dtype is not torch.int32 or not x.is_contiguous() or x.numel() < n:
+    if type(x) is torch.Tensor or isinstance(x, torch.Tensor):
+        if x.dtype is not torch.int32 or x.numel() < n or not x.is_contiguous():
             raise ValueError(f"{what}: at least {n} contiguous int32 values")
         return x.data_ptr()
     return _ptr(x)
@@ -503,7 +496,7 @@ def _table(pages, n):
 def _lse_arg(lse, h, cfg, out):
     """A call needs n_heads T values.  It refuses an `out` of fewer than T rows, so as many per
     row of `out` are enough; asking the handle for T costs a call of its own."""
-    if isinstance(lse, torch.Tensor):
+    if type(lse) is torch.Tensor or isinstance(lse, torch.Tensor):
         n, H = lse.numel(), cfg.n_heads
         if lse.dtype is not torch.float32 or not lse.is_contiguous() or \
                 ((out is None or n < H * out.rows) and n < H * ub_get_active_shape(h)[0]):
@@ -528,8 +521,21 @@ def ub_kv_append(h, q, k, v, q_out, k_out, inv_freq, cu_seqlens, past_lens, n_se
                  stream=None):
     """q, k, v, q_out, k_out: ``heads(...)`` or None; cache: ``make_kv_cache(...)`` or None; pages:
     a [sequences, pages] int32 tensor; inv_freq: rotary_dim / 2 floats."""
-    H, G = cfg.n_heads, cfg.n_kv_heads
-    if isinstance(inv_freq, torch.Tensor):
+    D = cfg.head_dim
+    H, G = (cfg.n_heads, D), (cfg.n_kv_heads, D)
+    if q is not None and q.held != H:
+        _hold_heads(q, H, "q")
+    if k is not None and k.held != G:
+        _hold_heads(k, G, "k")
+    if v is not None and v.held != G:
+        _hold_heads(v, G, "v")
+    if q_out is not None and q_out.held != H:
+        _hold_heads(q_out, H, "q_out")
+    if k_out is not None and k_out.held != G:
+        _hold_heads(k_out, G, "k_out")
+    if cache is not None and cache.held != G:
+        _hold_cache(cache, G)
+    if type(inv_freq) is torch.Tensor or isinstance(inv_freq, torch.Tensor):
         if inv_freq.dtype is not torch.float32 or not inv_freq.is_contiguous() \
                 or inv_freq.numel() < cfg.rotary_dim // 2:
             raise ValueError(f"inv_freq: at least {cfg.rotary_dim // 2} contiguous float32 values")
@@ -537,37 +543,57 @@ def ub_kv_append(h, q, k, v, q_out, k_out, inv_freq, cu_seqlens, past_lens, n_se
     else:
         inv_freq = _ptr(inv_freq)
     table, ld, per_seq = _table(pages, n_seqs)
-    _check(_lib.ub_kv_append(
-        h, _heads_arg(q, H, cfg, "q"), _heads_arg(k, G, cfg, "k"), _heads_arg(v, G, cfg, "v"),
-        _heads_arg(q_out, H, cfg, "q_out"), _heads_arg(k_out, G, cfg, "k_out"), inv_freq,
-        _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), _int32(past_lens, n_seqs, "past_lens"), n_seqs,
-        _cache_arg(cache, cfg), table, ld, per_seq, cfg, _stream(stream)), h)
+    st = _lib.ub_kv_append(h, q, k, v, q_out, k_out, inv_freq, _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"),
+                           _int32(past_lens, n_seqs, "past_lens"), n_seqs, cache, table, ld, per_seq, cfg,
+                           _stream(stream))
+    if st:
+        _check(st, h)
 
 
 def ub_attn_prompt(h, q, k, v, out, lse, cu_seqlens, n_seqs, cfg, workspace=None, stream=None):
-    H, G = cfg.n_heads, cfg.n_kv_heads
-    _check(_lib.ub_attn_prompt(
-        h, _heads_arg(q, H, cfg, "q"), _heads_arg(k, G, cfg, "k"), _heads_arg(v, G, cfg, "v"),
-        _heads_arg(out, H, cfg, "out"), _lse_arg(lse, h, cfg, out),
-        _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), n_seqs, cfg, *_ws_arg(workspace), _stream(stream)), h)
+    D = cfg.head_dim
+    H, G = (cfg.n_heads, D), (cfg.n_kv_heads, D)
+    for x, layout, what in ((q, H, "q"), (k, G, "k"), (v, G, "v"), (out, H, "out")):
+        if x is not None and x.held != layout:
+            _hold_heads(x, layout, what)
+    ws, ws_bytes = _ws_arg(workspace)
+    st = _lib.ub_attn_prompt(h, q, k, v, out, _lse_arg(lse, h, cfg, out), _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"),
+                             n_seqs, cfg, ws, ws_bytes, _stream(stream))
+    if st:
+        _check(st, h)
 
 
 def ub_attn_prompt_bwd(h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens, n_seqs, cfg, workspace,
                        stream=None):
-    H, G = cfg.n_heads, cfg.n_kv_heads
-    _check(_lib.ub_attn_prompt_bwd(
-        h, _heads_arg(dout, H, cfg, "dout"), _heads_arg(q, H, cfg, "q"), _heads_arg(k, G, cfg, "k"),
-        _heads_arg(v, G, cfg, "v"), _heads_arg(out, H, cfg, "out"), _lse_arg(lse, h, cfg, out),
-        _heads_arg(dq, H, cfg, "dq"), _heads_arg(dk, G, cfg, "dk"), _heads_arg(dv, G, cfg, "dv"),
-        _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), n_seqs, cfg, *_ws_arg(workspace), _stream(stream)), h)
+    D = cfg.head_dim
+    H, G = (cfg.n_heads, D), (cfg.n_kv_heads, D)
+    for x, layout, what in ((dout, H, "dout"), (q, H, "q"), (k, G, "k"), (v, G, "v"), (out, H, "out"), (dq, H, "dq"),
+                            (dk, G, "dk"), (dv, G, "dv")):
+        if x is not None and x.held != layout:
+            _hold_heads(x, layout, what)
+    ws, ws_bytes = _ws_arg(workspace)
+    st = _lib.ub_attn_prompt_bwd(h, dout, q, k, v, out, _lse_arg(lse, h, cfg, out), dq, dk, dv,
+                                 _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), n_seqs, cfg, ws, ws_bytes,
+                                 _stream(stream))
+    if st:
+        _check(st, h)
 
 
 def ub_attn_decode(h, q, cache, pages, kv_lens, n_seqs, out, lse, cfg, workspace, stream=None):
-    H = cfg.n_heads
-    _check(_lib.ub_attn_decode(
-        h, _heads_arg(q, H, cfg, "q"), _cache_arg(cache, cfg), *_table(pages, n_seqs),
-        _int32(kv_lens, n_seqs, "kv_lens"), n_seqs, _heads_arg(out, H, cfg, "out"),
-        _lse_arg(lse, h, cfg, out), cfg, *_ws_arg(workspace), _stream(stream)), h)
+    D = cfg.head_dim
+    H, G = (cfg.n_heads, D), (cfg.n_kv_heads, D)
+    if q is not None and q.held != H:
+        _hold_heads(q, H, "q")
+    if out is not None and out.held != H:
+        _hold_heads(out, H, "out")
+    if cache is not None and cache.held != G:
+        _hold_cache(cache, G)
+    table, ld, per_seq = _table(pages, n_seqs)
+    ws, ws_bytes = _ws_arg(workspace)
+    st = _lib.ub_attn_decode(h, q, cache, table, ld, per_seq, _int32(kv_lens, n_seqs, "kv_lens"), n_seqs, out,
+                             _lse_arg(lse, h, cfg, out), cfg, ws, ws_bytes, _stream(stream))
+    if st:
+        _check(st, h)
 
 
 def ub_destroy(h):
