@@ -517,12 +517,15 @@ __global__ __launch_bounds__(256) void attn_bwd_join(BwdParams p) {
 
 constexpr int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
-// Calls that cannot fill the card with workgroups of 128 rows (one of four waves per SIMD pair
-// for each) take 64 rows and four groups of waves: see attn_prompt.hip.
-bool grouped(int H, int64_t rows) { return rows * H < 64 * 1024; }
+// Calls of few rows times heads take 64 rows and four groups of waves per workgroup, for the
+// reason given in attn_prompt.hip.  Measured, the gradient alone, groups against one: 8184 rows
+// of 4 heads on 4 (2 sequences) 160 and 264 us, 5120 of 8 on 1 (2) 179 and 195, of 8 on 8 (8)
+// 123 and 147; 7168 of 8 on 1 276 and 268, on 8 186 and 193.
+constexpr int64_t GROUPED_BELOW = 56 * 1024;
+bool grouped(int H, int64_t rows) { return rows * H < GROUPED_BELOW; }
 
-// Parts a group's heads are split into: with fewer than two (four of the smaller) workgroups
-// per CU the chip would idle behind the longest tiles.
+// Parts a group's heads are split into: with fewer workgroups than two rounds (of 512, or 256
+// of four groups, at once) the chip would idle behind the longest tiles.
 int bwd_parts(int H, int G, int64_t rows) {
   const int group = H / G;
   const bool small = grouped(H, rows);
@@ -590,7 +593,7 @@ size_t attn_prompt_bwd_bytes(int32_t H, int32_t G, int32_t D, int64_t rows) {
   size_t most = attn_prompt_bwd_need(H, G, D, rows);
   for (int64_t t = 1; t <= 2048 && t * 64 < rows; ++t)
     most = std::max(most, attn_prompt_bwd_need(H, G, D, t * 64));
-  const int64_t last = (64 * 1024 - 1) / H;  // the last that is grouped
+  const int64_t last = (GROUPED_BELOW - 1) / H;  // the last that is grouped
   if (last < rows) most = std::max(most, attn_prompt_bwd_need(H, G, D, last));
   return most;
 }
