@@ -3,13 +3,13 @@
 //   P = exp(s - lse),  delta = dout . out,  dS = P (dout v^T - delta)
 //   dq = scale dS k,   dk = scale dS^T q,   dv = P^T dout
 //
-// Two kernels, each recomputing P from lse, so that every sum runs in one workgroup in a
-// fixed order (no atomics, the same bits on every run):
-//  - attn_bwd_q: a workgroup owns query rows of one head and walks the key tiles, as the
-//    forward pass does; it also leaves delta and lse log2(e) in the workspace.
-//  - attn_bwd_kv: a workgroup owns key rows of one key-value head and walks the query tiles
-//    of its heads.  With few key tiles the heads of a group go to several workgroups, whose
-//    fp32 parts attn_bwd_join adds in order.
+// attn_bwd_rows leaves delta and lse log2(e) of each row in the workspace.  In attn_bwd two
+// kinds of workgroups, each recomputing P from lse, take the three products' sums, so that
+// every sum runs in one workgroup in a fixed order (no atomics, the same bits on every run):
+//  - bwd_q owns query rows of one head and walks the key tiles, as the forward pass does.
+//  - bwd_kv owns key rows of one key-value head and walks the query tiles of its heads.  With
+//    few key tiles the heads of a group go to several workgroups, whose fp32 parts
+//    attn_bwd_join adds in order.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -62,14 +62,60 @@ __device__ inline void store4(uint16_t* p, f32x4 x) {
   *reinterpret_cast<uint2*>(p) = w;
 }
 
+// Sum over the LPR lanes (8 or 16) that share a row.
+template <int LPR>
+__device__ inline float row_sum(float x) {
+  auto add = [&](float y) { x += y; };
+  add(__int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0xB1, 0xf, 0xf, true)));   // lane ^ 1
+  add(__int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x4E, 0xf, 0xf, true)));   // lane ^ 2
+  add(__int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x141, 0xf, 0xf, true)));  // 7 - lane
+  if (LPR == 16)
+    add(__int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x140, 0xf, 0xf, true)));  // 15 - lane
+  return x;
+}
+
+// delta and lse log2(e) of all rows, 32 of one head to a wave; what they are in rows of no
+// sequence is not read.
+template <int LPR>
+__global__ __launch_bounds__(256) void attn_bwd_rows(BwdParams p) {
+  constexpr int AT_ONCE = 64 / LPR, N = 32 / AT_ONCE;
+  const PromptBwdArgs& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t T = a.seqs.T, task = (int64_t)blockIdx.x * 4 + wave;
+  const int head = (int)(task % a.H);
+  const int64_t row0 = task / a.H * 32;
+  if (row0 >= T) return;
+  const int e = lane % LPR * 8;
+  bf16x8 d[N], o[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t row = row0 + i * AT_ONCE + lane / LPR;
+    const bool in = row < T && e < a.D;
+    d[i] = load_row8(a.dout.p + row * a.dout.rs + head * a.dout.hs + e, in);
+    o[i] = load_row8(a.out.p + row * a.out.rs + head * a.out.hs + e, in);
+  }
+  if (lane < 32 && row0 + lane < T) {
+    const int64_t at = head * T + row0 + lane;
+    const float l = a.lse[at];
+    p.lse2[at] = l == -INFINITY ? 0.0f : l * LOG2E;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float x = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x += (float)d[i][k] * (float)o[i][k];
+    x = row_sum<LPR>(x);
+    const int64_t row = row0 + i * AT_ONCE + lane / LPR;
+    if (lane % LPR == 0 && row < T) p.delta[head * T + row] = x;
+  }
+}
+
 template <class S>
-__global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_q(BwdParams p) {
+__device__ __forceinline__ void bwd_q(const BwdParams& p, int head, int rank, unsigned char* smem) {
   constexpr int DS = S::DS, QF = S::F, NG = S::NG, BN = S::ROWS, BM = S::BM, TILE = S::TILE;
   using L = Tile<DS>;
   constexpr int STAGE = NG * 2 * TILE;
-  extern __shared__ __align__(256) unsigned char smem[];
   const PromptBwdArgs& a = p.a;
-  const int head = blockIdx.x % a.H, rank = blockIdx.x / a.H;
   fill_pad(a.dq, a.seqs, a.D, head, rank, p.ranks);
   const SeqTile st = find_tile(a.seqs, BM, rank, false);
   if (st.len == 0) return;
@@ -101,25 +147,14 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_q(BwdParams p) {
     const int64_t row = st.row0 + t;
     const uint16_t* qr = a.q.p + row * a.q.rs + head * a.q.hs;
     const uint16_t* dr = a.dout.p + row * a.dout.rs + head * a.dout.hs;
-    const uint16_t* orow = a.out.p + row * a.out.rs + head * a.out.hs;
-    float x = 0.0f;
 #pragma unroll
     for (int s = 0; s < DS; ++s) {
       const int e = 32 * s + 8 * g;
-      const bool in = ok && e < a.D;
-      q[f][s] = load_row8(qr + e, in);
-      dout[f][s] = load_row8(dr + e, in);
-      const bf16x8 ov = load_row8(orow + e, in);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x += (float)dout[f][s][i] * (float)ov[i];
+      q[f][s] = load_row8(qr + e, ok && e < a.D);
+      dout[f][s] = load_row8(dr + e, ok && e < a.D);
     }
-    delta[f] = col_sum(x);
-    const float l = ok ? a.lse[(int64_t)head * a.seqs.T + row] : 0.0f;
-    lse2[f] = l == -INFINITY ? 0.0f : l * LOG2E;
-    if (ok && g == 0 && grp == 0) {
-      p.lse2[(int64_t)head * a.seqs.T + row] = lse2[f];
-      p.delta[(int64_t)head * a.seqs.T + row] = delta[f];
-    }
+    lse2[f] = ok ? p.lse2[(int64_t)head * a.seqs.T + row] : 0.0f;
+    delta[f] = ok ? p.delta[(int64_t)head * a.seqs.T + row] : 0.0f;
   }
 #pragma unroll
   for (int f = 0; f < QF; ++f)
@@ -246,17 +281,14 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_q(BwdParams p) {
 // The values stay in LDS beside the query tiles: with them in registers too, the 128
 // accumulators of 32 keys left too few for the rest.
 template <class S>
-__global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
+__device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, unsigned char* smem) {
   constexpr int DS = S::DS, KF = S::F, NG = S::NG, BQ = S::ROWS, BK = S::BM, TILE = S::TILE;
   using L = Tile<DS>;
   constexpr int SET = 2 * TILE + 2 * BQ * 4;  // q rows, dout rows, lse2, delta
   constexpr int STAGE = NG * SET;
   constexpr int V = 2 * STAGE;  // the values' place
   static_assert(BQ == 32, "one step of the second products");
-  extern __shared__ __align__(256) unsigned char smem[];
   const PromptBwdArgs& a = p.a;
-  const int GP = a.G * p.parts;
-  const int gp = blockIdx.x % GP, rank = blockIdx.x / GP;
   const int kvh = gp / p.parts, part = gp - kvh * p.parts;
   if (part == 0) {
     fill_pad(a.dk, a.seqs, a.D, kvh, rank, p.ranks);
@@ -336,7 +368,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
   f32x4 dk[L::DB][KF], dv[L::DB][KF];
   const int steps = (total + NG - 1) / NG;
   const bool late = grp >= (NG + 1) / 2;
-  // As in attn_bwd_q.
+  // As in bwd_q.
   auto pass = [&](auto careful) __attribute__((always_inline)) {
     constexpr bool CAREFUL = decltype(careful)::value;
     bool bad = false;
@@ -483,6 +515,17 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_bwd_kv(BwdParams p) {
   }
 }
 
+// Both kinds in one launch, each by falling work, so that the second starts where the last and
+// longest of the first still run: on 8184 rows of 4 heads on 4 in 5 sequences 190 us, where a
+// launch for each takes 84 and 125.  Rank by rank in turns it takes 230.
+template <class SQ, class SK>
+__global__ __launch_bounds__(64 * SQ::NW, 2) void attn_bwd(BwdParams p) {
+  extern __shared__ __align__(256) unsigned char smem[];
+  const int H = p.a.H, GP = p.a.G * p.parts, b = blockIdx.x, kv = p.ranks * GP;
+  if (b < kv) bwd_kv<SK>(p, b % GP, b / GP, smem);
+  else bwd_q<SQ>(p, (b - kv) % H, (b - kv) / H, smem);
+}
+
 // dk and dv from their parts, in part order; 8 elements per thread.
 __global__ __launch_bounds__(256) void attn_bwd_join(BwdParams p) {
   const PromptBwdArgs& a = p.a;
@@ -519,19 +562,21 @@ constexpr int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
 // Calls of few rows times heads take 64 rows and four groups of waves per workgroup, for the
 // reason given in attn_prompt.hip.  Measured, the gradient alone, groups against one: 8184 rows
-// of 4 heads on 4 (2 sequences) 160 and 264 us, 5120 of 8 on 1 (2) 179 and 195, of 8 on 8 (8)
-// 123 and 147; 7168 of 8 on 1 276 and 268, on 8 186 and 193.
-constexpr int64_t GROUPED_BELOW = 56 * 1024;
+// of 4 heads on 4, 2 sequences 187 and 195 us, 5 sequences 161 and 196; 5120 of 8 on 1 (2) 151
+// and 134, of 8 on 8 (8) 115 and 99.
+constexpr int64_t GROUPED_BELOW = 36 * 1024;
 bool grouped(int H, int64_t rows) { return rows * H < GROUPED_BELOW; }
 
-// Parts a group's heads are split into: with fewer workgroups than two rounds (of 512, or 256
-// of four groups, at once) the chip would idle behind the longest tiles.
+// Parts a group's heads are split into, until the key-value workgroups make one round (of 512,
+// or of 256 of four groups): fewer leave much of the chip idle (half a round: 306 us against 252
+// for 8184 rows of 8 heads on 1), more only write more parts (4096 rows: 105 us with two rounds
+// against 92).
 int bwd_parts(int H, int G, int64_t rows) {
   const int group = H / G;
   const bool small = grouped(H, rows);
   const int64_t tiles = small ? (rows + 63) / 64 * G : (rows + 127) / 128 * G;
   int parts = 1;
-  while (parts < group && tiles * parts < (small ? 512 : 1024)) {
+  while (parts < group && tiles * parts < (small ? 256 : 512)) {
     ++parts;
     while (group % parts) ++parts;
   }
@@ -540,7 +585,7 @@ int bwd_parts(int H, int G, int64_t rows) {
 
 template <class SQ, class SK>
 hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
-  static_assert(SQ::BM == SK::BM, "one count of tiles");
+  static_assert(SQ::BM == SK::BM && SQ::NW == SK::NW, "one count of tiles, one of waves");
   constexpr int DS = SQ::DS;
   const int64_t T = a.seqs.T;
   BwdParams p{};
@@ -553,18 +598,20 @@ hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
   p.delta = reinterpret_cast<float*>(w + stat);
   p.part = reinterpret_cast<float*>(w + 2 * stat);
   const int64_t ranks = max_tiles(T, a.seqs.n, SQ::BM) + (a.seqs.n == 0);
-  if (ranks * a.H > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const int64_t blocks = ranks * (a.H + a.G * p.parts);
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   p.ranks = (int32_t)ranks;
   constexpr int lds_q = std::max(2 * SQ::NG * 2 * SQ::TILE, SQ::JOIN);
   constexpr int lds_kv = std::max(2 * SK::NG * (2 * SK::TILE + 2 * SK::ROWS * 4) + SK::BM * Tile<DS>::RB,
                                   SK::JOIN);
-  auto kq = &attn_bwd_q<SQ>;
-  auto kkv = &attn_bwd_kv<SK>;
-  hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kq), lds_q);
-  if (e == hipSuccess) e = ensure_lds_attr(reinterpret_cast<const void*>(kkv), lds_kv);
-  if (e == hipSuccess) e = launch_k(kq, dim3((unsigned)(ranks * a.H)), dim3(64 * SQ::NW), lds_q, s, p);
-  if (e == hipSuccess)
-    e = launch_k(kkv, dim3((unsigned)(ranks * a.G * p.parts)), dim3(64 * SK::NW), lds_kv, s, p);
+  constexpr int lds = std::max(lds_q, lds_kv);
+  auto kernel = &attn_bwd<SQ, SK>;
+  hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kernel), lds);
+  if (e == hipSuccess && T > 0) {
+    auto rows = DS <= 2 ? &attn_bwd_rows<8> : &attn_bwd_rows<16>;
+    e = launch_k(rows, dim3((unsigned)(((T + 31) / 32 * a.H + 3) / 4)), dim3(256), 0, s, p);
+  }
+  if (e == hipSuccess) e = launch_k(kernel, dim3((unsigned)blocks), dim3(64 * SQ::NW), lds, s, p);
   if (e == hipSuccess && p.parts > 1) {
     const int64_t blocks = (2 * a.G * T * (a.D / 8) + 255) / 256;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
