@@ -282,9 +282,10 @@ struct SeqTile {
 // The tile of `rank` among the tiles of bm rows of all sequences.  Up to 64 sequences (one
 // per lane): in the order of falling tile number, so that the tiles with the most work under
 // a causal mask start first.  A level x holds the tiles number x - 1; C(x) = the tiles of
-// level x and above; the rank's level is the largest x with C(x) > rank, its sequence by the rank's bit in a ballot.  A grid that runs at once needs no
-// order, and more sequences do without: in sequence order.  `low_first` reverses the levels
-// (tiles whose work falls with their number).
+// level x and above; the rank's level is the largest x with C(x) > rank, its sequence by the
+// rank's bit in a ballot.  A grid that runs at once needs no order, and more sequences do
+// without: in sequence order.  `low_first` reverses the levels (tiles whose work falls with
+// their number).
 __device__ inline SeqTile find_tile(const Seqs& s, int bm, int rank, bool low_first) {
   const int lane = threadIdx.x & 63;
   SeqTile r{0, 0, 0};

@@ -10,6 +10,11 @@
 //  - bwd_kv owns key rows of one key-value head and walks the query tiles of its heads.  With
 //    few key tiles the heads of a group go to several workgroups, whose fp32 parts
 //    attn_bwd_join adds in order.
+//
+// Measured on MI355X, all launches.  16264 tokens in 2 sequences, 8 heads of 128 on 1: 0.88 ms, 1.08
+// PFLOP/s of the seven products done (five are counted); the matrix cores are busy 52% of the
+// time at the 2.1 GHz that the power limit leaves.  8184 tokens in 5 sequences, 4 heads of 128 on
+// 4: 171 us, bounded by the steps of the longest rows, as the forward pass.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -490,7 +490,8 @@ UB_API ub_status_t ub_reduce_partials(ub_handle_t h, void* out, int64_t ldo,
  * Heads.  Query head h uses key-value head h / (n_heads / n_kv_heads).  bf16 matrices;
  * head_dim a multiple of 8 up to UB_ATTN_MAX_HEAD_DIM.  Sums, softmax statistics and
  * gradient accumulators are fp32; softmax weights and score gradients are rounded to bf16 as
- * operands of their second products (matrix-core operands); each output is rounded once.
+ * operands of their second products (matrix-core operands; score gradients next to the
+ * diagonal to the sum of two bf16 numbers); each output is rounded once.
  * What the mask leaves out does not matter, whatever it holds: infinities and NaN of later
  * rows' keys and values (of earlier rows' queries, in dk and dv), or of other sequences.
  * Every call gives the same bits for the same inputs on every run: no sum's order depends
