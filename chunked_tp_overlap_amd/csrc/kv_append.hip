@@ -16,6 +16,13 @@
 // head; a wave takes 64 items of one section at a time, so that its lanes do the same work:
 // with sections mixed in a wave every wave ran the E4M3 conversion's instructions.  The next
 // items are loaded before the present ones are finished, the first ones before the lookup.
+//
+// Stores to the cache do not pass through the L2 (it is read by later calls, the decode steps
+// above all), nor do q_out and k_out where they are larger than it: with inputs that no cache
+// holds, 32520 tokens of 8 + 1 heads to an E4M3 cache take 29.0 us (5.4 TB/s, a copy's rate)
+// instead of 37.2, and with ub_attn_prompt after it 612 instead of 610.  Smaller outputs the next
+// call finds there: 8184 tokens of 4 + 4 heads took 12.9 us, with ub_attn_prompt 73, where past the
+// L2 they took 12.5 and 74.5.
 #include <hip/hip_runtime.h>
 
 #include "attn_internal.h"
@@ -29,6 +36,7 @@ constexpr int THREADS = 256;
 constexpr int WAVES = THREADS / 64;
 constexpr int MAX_TOKENS = 8;   // tokens of a workgroup
 constexpr int MAX_HALF = UB_ATTN_MAX_HEAD_DIM / 2;
+constexpr int64_t L2_BYTES = 32 << 20;  // the XCDs' together
 enum { ROT_Q, ROT_K, REST_Q, REST_K, VALUES, SECTIONS };
 
 struct Section {
@@ -77,20 +85,23 @@ __device__ inline void store_cache(const KvCache& c, void* base, int64_t off, co
                                    float scale) {
   if (c.e4m3) {
     uint2 o = make_uint2(e4m3x4(x, scale), e4m3x4(x + 4, scale));
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + off) = o;
+    __builtin_nontemporal_store(__builtin_bit_cast(uint64_t, o),
+                                GLOBAL_PTR(uint64_t, static_cast<uint8_t*>(base) + off));
   } else {
     u32x4 o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + off) = o;
+    __builtin_nontemporal_store(o, GLOBAL_PTR(u32x4, static_cast<uint16_t*>(base) + off));
   }
 }
 
+template <bool PAST_L2>
 __device__ inline void store_bf16(uint16_t* p, const float* x) {
   u32x4 o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-  *reinterpret_cast<u32x4*>(p) = o;
+  if (PAST_L2) __builtin_nontemporal_store(o, GLOBAL_PTR(u32x4, p));
+  else *GLOBAL_PTR(u32x4, p) = o;
 }
 
 __device__ inline void unpack(u32x4 v, float* x) {
@@ -100,6 +111,10 @@ __device__ inline void unpack(u32x4 v, float* x) {
     x[2 * i + 1] = hi(v[i]);
   }
 }
+
+// Place of pair 8 k + u among a token's: two pairs in 16 bytes, those that lanes read together
+// (of the items k of a head) side by side.
+__device__ inline int at_pair(int k, int u) { return ((u >> 1) * (MAX_HALF / 8) + k) * 2 + (u & 1); }
 
 // A lane's item of a wave's task, loaded.
 struct Item {
@@ -148,7 +163,9 @@ __device__ inline Item load_item(const AppendParams& p, int task, int t0, int nt
   return w;
 }
 
-__global__ __launch_bounds__(THREADS) void kv_append(AppendParams p) {
+// 64 registers, for 8 waves per SIMD: 37.2 us in the second case above, 39.4 with 66 and 7.
+template <bool PAST_L2>
+__global__ __launch_bounds__(THREADS, 8) void kv_append(AppendParams p) {
   __shared__ Token tok[MAX_TOKENS];
   __shared__ float2 rot[MAX_TOKENS][MAX_HALF];
   const AppendArgs& a = p.a;
@@ -201,7 +218,7 @@ __global__ __launch_bounds__(THREADS) void kv_append(AppendParams p) {
     r -= rint(r);
     float s, c;
     sincospif(2.0f * (float)r, &s, &c);
-    rot[j][lane] = make_float2(c, s);
+    rot[j][at_pair(lane >> 3, lane & 7)] = make_float2(c, s);
   }
   __syncthreads();
   for (int task = wave; task < tasks; task += WAVES) {
@@ -220,10 +237,11 @@ __global__ __launch_bounds__(THREADS) void kv_append(AppendParams p) {
       if (w.sec <= ROT_K) {
         unpack(k.live ? w.y : u32x4{0, 0, 0, 0}, y);
         if (a.interleaved) {
-          const float2* r = rot[w.j] + w.e0 / 2;
+          const float2* r = rot[w.j];
+          const int k = w.e0 >> 4;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const float2 c0 = r[u], c1 = r[4 + u];
+            const float2 c0 = r[at_pair(k, u)], c1 = r[at_pair(k, 4 + u)];
             const float p0 = x[2 * u], p1 = x[2 * u + 1], r0 = y[2 * u], r1 = y[2 * u + 1];
             x[2 * u] = p0 * c0.x - p1 * c0.y;
             x[2 * u + 1] = p1 * c0.x + p0 * c0.y;
@@ -231,19 +249,20 @@ __global__ __launch_bounds__(THREADS) void kv_append(AppendParams p) {
             y[2 * u + 1] = r1 * c1.x + r0 * c1.y;
           }
         } else {
-          const float2* r = rot[w.j] + w.e0;
+          const float2* r = rot[w.j];
+          const int k = w.e0 >> 3;
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const float2 c = r[u];
+            const float2 c = r[at_pair(k, u)];
             const float p0 = x[u], p1 = y[u];
             x[u] = p0 * c.x - p1 * c.y;
             y[u] = p1 * c.x + p0 * c.y;
           }
         }
-        if (dst.p) store_bf16(dst.p + t * dst.rs + w.head * dst.hs + w.e1, y);
+        if (dst.p) store_bf16<PAST_L2>(dst.p + t * dst.rs + w.head * dst.hs + w.e1, y);
         if (slot) store_cache(a.cache, cache, off + w.e1, y, scale);
       }
-      if (dst.p && w.sec != VALUES) store_bf16(dst.p + t * dst.rs + w.head * dst.hs + w.e0, x);
+      if (dst.p && w.sec != VALUES) store_bf16<PAST_L2>(dst.p + t * dst.rs + w.head * dst.hs + w.e0, x);
       if (slot) store_cache(a.cache, cache, off + w.e0, x, scale);
     }
     w = next;
@@ -269,12 +288,12 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s) {
     if (x.n > most) most = x.n;
   }
   if (a.seqs.T <= 0 || most == 0) return hipSuccess;
-  // One token per workgroup of a small call starts soonest; 8 share the angles' and the
-  // lookup's time and leave enough workgroups to even out the CUs' load.  Measured at 8184
-  // tokens (4 + 4 heads, bf16 cache) with 2, 4, 8, 16 tokens: 15.9, 14.9, 13.5, 16.9 us; at
-  // 32520 (8 + 1 heads, E4M3): 53.6, 42.7, 39.7, 45.0 us, 4.0 TB/s.  An item's number stays
+  // One token per workgroup of a small call starts soonest; more share the angles' and the
+  // lookup's time.  2048 workgroups run at once, and past that 8 tokens serve best.  Measured with
+  // 4 and 8 tokens: 8184 tokens (4 + 4 heads, bf16 cache) 11.9 and 12.9 us, 4096 11.8 with
+  // 2 and 13.2 with 4; 32520 (8 + 1 heads, E4M3) 32.9 and 29.0, with 16 30.4.  An item's number stays
   // under 2^24.
-  int tokens = (a.seqs.T + 1023) / 1024;
+  int tokens = (a.seqs.T + 2047) / 2048;
   if (tokens > MAX_TOKENS) tokens = MAX_TOKENS;
   if (tokens * (int64_t)most + 64 * (WAVES + 1) >= (1 << 24)) tokens = 1;
   p.tokens = tokens;
@@ -284,7 +303,8 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s) {
     p.s[i].task_end = end;
   }
   const int blocks = (a.seqs.T + tokens - 1) / tokens;
-  return launch_k(&kv_append, dim3(blocks), dim3(THREADS), 0, s, p);
+  const int64_t out = (int64_t)a.seqs.T * ((a.q_out.p ? a.H : 0) + (a.k_out.p ? a.G : 0)) * a.D * 2;
+  return launch_k(out > L2_BYTES ? &kv_append<true> : &kv_append<false>, dim3(blocks), dim3(THREADS), 0, s, p);
 }
 
 }  // namespace ubx
