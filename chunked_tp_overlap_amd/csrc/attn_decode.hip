@@ -21,7 +21,7 @@
 //
 // Measured on MI355X, both kernels, where a plain read of as many bytes takes 84 us: 64
 // sequences of 1 to 8192 tokens, 4 + 4 heads of 128, bf16, pages of 16: 104 us (4.9 TB/s); 128
-// of 100 to 32520, 8 heads on 1, E4M3, pages of 64: 105 us (5.0 TB/s).
+// of 100 to 32520, 8 heads on 1, E4M3, pages of 64: 95 us (5.6 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "attn_common.h"
@@ -214,6 +214,15 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
       bad = bad || place < 0;
       place = max(place, (int64_t)0) * EB;
     };
+    // E4M3 rows pass by the caches.  Measured, passing by and not: the second case above 95 and
+    // 105 us, 64 sequences of 100 to 8192 tokens, 2 heads of 64 on 2 26 and 39.  Of bf16, where
+    // a row takes two lines, only some calls gain: with its values alone passing by, the first
+    // case takes 99 instead of 104, but 32 sequences of 4000 to 8192, 32 heads on 1 (two
+    // workgroups read each row) 59 instead of 53, 64 of 100 to 8192, 2 heads of 64 on 2 54
+    // instead of 51.
+    auto load = [](const unsigned char* at) {
+      return F8 ? __builtin_nontemporal_load(GLOBAL_PTR(const u32x4, at)) : *GLOBAL_PTR(const u32x4, at);
+    };
     auto fetch = [&](int j, S& x) {
       const int t = t0 + j * (NW * STEP);
       if (WHOLE) {
@@ -224,10 +233,10 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int s = 0; s < KV; ++s) x.k[b][s] = *GLOBAL_PTR(const u32x4, kb + at[b] + kofs[s]);
+          for (int s = 0; s < KV; ++s) x.k[b][s] = load(kb + at[b] + kofs[s]);
 #pragma unroll
         for (int i = 0; i < VI; ++i)
-          x.v[i] = *GLOBAL_PTR(const u32x4, vb + at[i * RPI / 16] + (int64_t)(i * RPI % 16) * row_bytes + vofs);
+          x.v[i] = load(vb + at[i * RPI / 16] + (int64_t)(i * RPI % 16) * row_bytes + vofs);
       } else {
         look_up(min(t + (lane & 31), end - 1));  // past the end: the last token again
         const int lo = (int)(uint32_t)place, hi = (int)(place >> 32);
@@ -238,11 +247,11 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
         for (int b = 0; b < 2; ++b) {
           const unsigned char* at = kb + row(16 * b + col);
 #pragma unroll
-          for (int s = 0; s < KV; ++s) x.k[b][s] = *GLOBAL_PTR(const u32x4, at + kofs[s]);
+          for (int s = 0; s < KV; ++s) x.k[b][s] = load(at + kofs[s]);
         }
 #pragma unroll
         for (int i = 0; i < VI; ++i)
-          x.v[i] = *GLOBAL_PTR(const u32x4, vb + row(i * RPI + lane / VPR) + vofs);
+          x.v[i] = load(vb + row(i * RPI + lane / VPR) + vofs);
       }
     };
     auto use = [&](int j, S& x) {
