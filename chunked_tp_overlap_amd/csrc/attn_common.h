@@ -360,6 +360,13 @@ __device__ inline SeqTile find_tile(const Seqs& s, int bm, int rank, bool low_fi
   return r;
 }
 
+// Four groups of waves on the keys shorten a call's longest rows.  Many sequences make many
+// workgroups of few steps each, and then those of one group, two to a CU, are faster whatever
+// the rows.  Measured, groups against one (forward; gradient, us): 4200 rows, 30 sequences, 8 heads
+// on 8 29 and 20, 71 and 42; 2048 rows, 16 sequences 18 and 15, 40 and 34; 4264 rows, 12 sequences
+// 32 and 29, 82 and 60; 2096 rows, 4 sequences, 8 on 1 23 and 32, 64 and 77.
+inline bool few_sequences(int64_t n, int H) { return n * H < 96; }
+
 // Tiles of bm rows that n sequences of T rows together can have.
 inline int64_t max_tiles(int64_t T, int64_t n, int bm) { return T / bm + (n < T ? n : T); }
 

@@ -345,7 +345,7 @@ hipError_t choose(const PromptArgs& a, hipStream_t s) {
   // against one: 4096 rows of 8 heads on 8 (8 sequences) 33 and 37 us, 8184 of 4 on 4 (2) 55 and
   // 76; 5120 of 8 on 1 (2) 57 and 55, of 8 on 8 (8) 41 and 43; 6144 of 8 on 1 70 and 65, on 8
   // 53 and 49.
-  if ((int64_t)a.seqs.T * a.H < 44 * 1024) return run<Shape<DS, 2, 2, 4, 32>>(a, s);
+  if ((int64_t)a.seqs.T * a.H < 44 * 1024 && few_sequences(a.seqs.n, a.H)) return run<Shape<DS, 2, 2, 4, 32>>(a, s);
   return run<Shape<DS, 2, 4, 1, 64>>(a, s);
 }
 

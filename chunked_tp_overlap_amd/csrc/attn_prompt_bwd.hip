@@ -598,15 +598,14 @@ constexpr int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 // of 4 heads on 4, 2 sequences 187 and 195 us, 5 sequences 161 and 196; 5120 of 8 on 1 (2) 151
 // and 134, of 8 on 8 (8) 115 and 99.
 constexpr int64_t GROUPED_BELOW = 36 * 1024;
-bool grouped(int H, int64_t rows) { return rows * H < GROUPED_BELOW; }
+bool grouped(int H, int64_t rows, int64_t n) { return rows * H < GROUPED_BELOW && few_sequences(n, H); }
 
 // Parts a group's heads are split into, until the key-value workgroups make one round (of 512,
 // or of 256 of four groups): fewer leave much of the chip idle (half a round: 306 us against 252
 // for 8184 rows of 8 heads on 1), more only write more parts (4096 rows: 105 us with two rounds
 // against 92).
-int bwd_parts(int H, int G, int64_t rows) {
+int bwd_parts(int H, int G, int64_t rows, bool small) {
   const int group = H / G;
-  const bool small = grouped(H, rows);
   const int64_t tiles = small ? (rows + 63) / 64 * G : (rows + 127) / 128 * G;
   int parts = 1;
   while (parts < group && tiles * parts < (small ? 256 : 512)) {
@@ -624,7 +623,7 @@ hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
   BwdParams p{};
   p.a = a;
   p.c = a.scale * LOG2E;
-  p.parts = bwd_parts(a.H, a.G, T);
+  p.parts = bwd_parts(a.H, a.G, T, SK::NG > 1);
   unsigned char* w = static_cast<unsigned char*>(a.ws);
   const int64_t stat = align256((int64_t)a.H * T * 4);
   p.lse2 = reinterpret_cast<float*>(w);
@@ -655,14 +654,14 @@ hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
 
 template <int DS>
 hipError_t choose(const PromptBwdArgs& a, hipStream_t s) {
-  if (grouped(a.H, a.seqs.T)) return run<Shape<DS, 2, 4, 32>, Shape<DS, 2, 4, 32>>(a, s);
+  if (grouped(a.H, a.seqs.T, a.seqs.n)) return run<Shape<DS, 2, 4, 32>, Shape<DS, 2, 4, 32>>(a, s);
   return run<Shape<DS, 4, 1, 64>, Shape<DS, 4, 1, 32>>(a, s);
 }
 
 }  // namespace
 
 size_t attn_prompt_bwd_need(int32_t H, int32_t G, int32_t D, int64_t rows) {
-  const int parts = bwd_parts(H, G, rows);
+  const int parts = bwd_parts(H, G, rows, false);  // groups take no more
   return static_cast<size_t>(2 * align256((int64_t)H * rows * 4) +
                              (parts > 1 ? (int64_t)parts * 2 * G * rows * D * 4 : 0));
 }
@@ -673,8 +672,6 @@ size_t attn_prompt_bwd_bytes(int32_t H, int32_t G, int32_t D, int64_t rows) {
   size_t most = attn_prompt_bwd_need(H, G, D, rows);
   for (int64_t t = 1; t <= 2048 && t * 64 < rows; ++t)
     most = std::max(most, attn_prompt_bwd_need(H, G, D, t * 64));
-  const int64_t last = (GROUPED_BELOW - 1) / H;  // the last that is grouped
-  if (last < rows) most = std::max(most, attn_prompt_bwd_need(H, G, D, last));
   return most;
 }
 
