@@ -488,9 +488,11 @@ def _table(pages, n):
     if len(shape) == 2 and pages.dtype is torch.int32:
         rows, per = shape
         ld, one = pages.stride()
-        if rows >= n and (one == 1 or rows * per == 0):
+        # the stride of a single row means nothing; rows that overlap (an expanded one among them)
+        # are not what the calls read
+        if rows >= n and (one == 1 or rows * per == 0) and (ld >= per or n <= 1):
             return pages.data_ptr(), ld if ld > per else per, per
-    raise ValueError(f"pages: an int32 [at least {n}, pages] tensor with contiguous rows")
+    raise ValueError(f"pages: an int32 [at least {n}, pages] tensor with contiguous rows that do not overlap")
 
 
 def _lse_arg(lse, h, cfg, out):

@@ -1,0 +1,39 @@
+"""Host-side tests of what the attention calls' binding refuses before any address reaches a
+kernel (no GPU): tensors that do not hold what a call would read or write."""
+
+import pytest
+import torch
+
+ub = pytest.importorskip("chunked_tp_overlap_amd.ub", reason="libub.so not built")
+FAKE = 0x7F0000000000
+T = 64
+
+
+@pytest.fixture
+def h():
+    x = ub.ub_init(T, 64, 1, ub.UB_DTYPE_BF16, FAKE, T * 64 * 2)
+    yield x
+    ub.ub_destroy(x)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def test_page_table_strides():
+    """A table is described by its own row stride; rows that overlap, or one row expanded to
+    several sequences, are no layout that the calls take (they would be read `pages` entries
+    apart, past the tensor's end)."""
+    t = i32(3, 8)
+    assert ub._table(t, 3) == (t.data_ptr(), 8, 8)
+    wide = t[:, :5]
+    assert ub._table(wide, 3) == (t.data_ptr(), 8, 5)
+    for bad in (i32(1, 5).expand(3, 5), i32(40).as_strided((3, 8), (4, 1)), i32(2, 8).t()):
+        with pytest.raises(ValueError, match="pages"):
+            ub._table(bad, 2)
+    one = i32(40).as_strided((1, 8), (3, 1))  # the stride of a single row means nothing
+    assert ub._table(one, 1) == (one.data_ptr(), 8, 8)
+    assert ub._table(i32(1, 5).expand(1, 5), 1)[1:] == (5, 5)
+    # rows beyond the sequences are not read
+    many = i32(1, 5).expand(3, 5)
+    assert ub._table(many, 1)[1:] == (5, 5)
