@@ -37,3 +37,14 @@ def test_page_table_strides():
     # rows beyond the sequences are not read
     many = i32(1, 5).expand(3, 5)
     assert ub._table(many, 1)[1:] == (5, 5)
+
+
+def test_heads_expanded_over_heads():
+    """One head expanded to several has head stride 0, which a descriptor reads as head_dim."""
+    x = torch.zeros((T, 1, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="head"):
+        ub.heads(x.expand(T, 8, 64))
+    d = ub.heads(x.expand(T, 1, 64))
+    assert (d.ptr, d.row_stride, d.rows) == (x.data_ptr(), 64, T)
+    y = torch.zeros((4, T, 64), dtype=torch.bfloat16).transpose(0, 1)
+    assert ub.heads(y).head_stride == T * 64
