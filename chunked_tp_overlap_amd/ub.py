@@ -412,7 +412,7 @@ def heads(x, col=0):
     any row and head strides.  It keeps the tensor alive."""
     if x.dim() not in (2, 3):
         raise ValueError(f"heads: a 2-D or 3-D tensor, not {x.dim()}-D")
-    if x.element_size() != 2:
+    if x.dtype is not torch.bfloat16:
         raise ValueError(f"heads: a bf16 matrix, not {x.dtype}")
     if x.numel() and x.stride(-1) != 1:
         raise ValueError("heads: the last dimension must be contiguous")

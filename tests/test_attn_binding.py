@@ -48,3 +48,12 @@ def test_heads_expanded_over_heads():
     assert (d.ptr, d.row_stride, d.rows) == (x.data_ptr(), 64, T)
     y = torch.zeros((4, T, 64), dtype=torch.bfloat16).transpose(0, 1)
     assert ub.heads(y).head_stride == T * 64
+
+
+@pytest.mark.parametrize("dtype", (torch.float16, torch.int16, torch.uint16, torch.float32, torch.float8_e4m3fn))
+def test_heads_dtype(dtype):
+    """Matrices are bf16: other 2-byte values would have their bits read as bf16."""
+    with pytest.raises(ValueError, match="bf16"):
+        ub.heads(torch.zeros((T, 256), dtype=dtype))
+    with pytest.raises(ValueError, match="bf16"):
+        ub.heads(torch.zeros((T, 4, 64), dtype=dtype))
