@@ -418,6 +418,8 @@ def heads(x, col=0):
         raise ValueError("heads: the last dimension must be contiguous")
     if x.dim() == 3 and col:
         raise ValueError("heads: col is for 2-D matrices")
+    if col < 0:
+        raise ValueError(f"heads: col {col} lies before the matrix")
     if x.dim() == 3 and x.shape[1] > 1 and x.stride(1) == 0:
         raise ValueError("heads: one head expanded to several; a head stride of 0 stands for head_dim")
     d = ub_heads_t()

@@ -57,3 +57,12 @@ def test_heads_dtype(dtype):
         ub.heads(torch.zeros((T, 256), dtype=dtype))
     with pytest.raises(ValueError, match="bf16"):
         ub.heads(torch.zeros((T, 4, 64), dtype=dtype))
+
+
+def test_heads_column():
+    """A column before the matrix is an address before the tensor."""
+    x = torch.zeros((T, 256), dtype=torch.bfloat16)
+    for col in (-1, -8, -64):
+        with pytest.raises(ValueError, match="col"):
+            ub.heads(x, col)
+    assert ub.heads(x, 64).ptr == x.data_ptr() + 128
