@@ -514,6 +514,8 @@ def _lse_arg(lse, h, cfg, out):
 def _ws_arg(ws):
     if ws is None:
         return None, 0
+    if not ws.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor")
     return ws.data_ptr(), ws.nbytes
 
 

@@ -66,3 +66,12 @@ def test_heads_column():
         with pytest.raises(ValueError, match="col"):
             ub.heads(x, col)
     assert ub.heads(x, 64).ptr == x.data_ptr() + 128
+
+
+def test_workspace_is_contiguous():
+    """A workspace has the bytes that its tensor counts only if they lie side by side."""
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros((64, 64), dtype=torch.uint8)[:, :8]):
+        with pytest.raises(ValueError, match="workspace"):
+            ub._ws_arg(bad)
+    assert ub._ws_arg(None) == (None, 0)
+    assert ub._ws_arg(torch.zeros(48, dtype=torch.float32))[1] == 192
