@@ -454,6 +454,12 @@ def make_kv_cache(k, v, k_scale=1.0, v_scale=1.0):
 
 # A call's own cost is a few microseconds, as much as a small batch's kernel: descriptors are
 # checked against a head layout once, and tensors with as few attribute reads as it takes.
+def _host(x, what):
+    """Refuses a tensor of pageable host memory, which no kernel can address."""
+    if not x.is_pinned():
+        raise ValueError(f"{what}: a device tensor, not one in host memory")
+
+
 def _hold_heads(x, layout, what):
     """Checks that x's columns hold the (heads, dim) of layout."""
     n, D = layout
@@ -463,6 +469,8 @@ def _hold_heads(x, layout, what):
             raise ValueError(f"{what}: {tuple(t.shape)} does not hold {n} heads of {D}")
         if t.dim() == 2 and x.col + n * D > t.shape[1]:
             raise ValueError(f"{what}: columns {x.col} to {x.col + n * D} of {t.shape[1]}")
+        if not t.is_cuda:
+            _host(t, what)
         x.held = layout
 
 
@@ -471,6 +479,8 @@ def _hold_cache(cache, layout):
     for t in cache.tensors:
         if t.shape[1] < n or t.shape[3] < D:
             raise ValueError(f"cache: {tuple(t.shape)} does not hold {n} heads of {D}")
+        if not t.is_cuda:
+            _host(t, "cache")
     if cache.tensors:
         cache.held = layout
 
@@ -480,6 +490,8 @@ def _int32(x, n, what):
     if type(x) is torch.Tensor or isinstance(x, torch.Tensor):
         if x.dtype is not torch.int32 or x.numel() < n or not x.is_contiguous():
             raise ValueError(f"{what}: at least {n} contiguous int32 values")
+        if not x.is_cuda:
+            _host(x, what)
         return x.data_ptr()
     return _ptr(x)
 
@@ -495,6 +507,8 @@ def _table(pages, n):
         # the stride of a single row means nothing; rows that overlap (an expanded one among them)
         # are not what the calls read
         if rows >= n and (one == 1 or rows * per == 0) and (ld >= per or n <= 1):
+            if not pages.is_cuda:
+                _host(pages, "pages")
             return pages.data_ptr(), ld if ld > per else per, per
     raise ValueError(f"pages: an int32 [at least {n}, pages] tensor with contiguous rows that do not overlap")
 
@@ -507,6 +521,8 @@ def _lse_arg(lse, h, cfg, out):
         if lse.dtype is not torch.float32 or not lse.is_contiguous() or \
                 ((out is None or n < H * out.rows) and n < H * ub_get_active_shape(h)[0]):
             raise ValueError(f"lse: a contiguous float32 [{H}, {ub_get_active_shape(h)[0]}] tensor")
+        if not lse.is_cuda:
+            _host(lse, "lse")
         return lse.data_ptr()
     return _ptr(lse)
 
@@ -516,6 +532,8 @@ def _ws_arg(ws):
         return None, 0
     if not ws.is_contiguous():
         raise ValueError("workspace: a contiguous tensor")
+    if not ws.is_cuda:
+        _host(ws, "workspace")
     return ws.data_ptr(), ws.nbytes
 
 
@@ -547,6 +565,8 @@ def ub_kv_append(h, q, k, v, q_out, k_out, inv_freq, cu_seqlens, past_lens, n_se
         if inv_freq.dtype is not torch.float32 or not inv_freq.is_contiguous() \
                 or inv_freq.numel() < cfg.rotary_dim // 2:
             raise ValueError(f"inv_freq: at least {cfg.rotary_dim // 2} contiguous float32 values")
+        if not inv_freq.is_cuda:
+            _host(inv_freq, "inv_freq")
         inv_freq = inv_freq.data_ptr()
     else:
         inv_freq = _ptr(inv_freq)
