@@ -10,7 +10,8 @@ microbatch of packed tokens:
       -> ub_attn_prompt or ub_attn_decode -> ub_gemm_rs_chunked (output projection) -> y
 
 Rows of a microbatch beyond its tokens (T is a multiple of tp_size) are padding.  Only device
-memory comes from torch.
+memory comes from torch.  A call's work runs on torch's current stream, in order with the torch
+operations around it; a decode step can be captured into a graph.
 """
 
 import torch
@@ -61,19 +62,21 @@ class AttentionBlock:
         """QKV of x's rows; the active shape becomes their number, rounded up to tp."""
         rows = x.shape[0]
         T = -(-rows // self.tp) * self.tp
+        stream = torch.cuda.current_stream()
         ub.ub_set_active_shape(self.h, (T, self.hidden))
-        ub.ub_copy_in(self.h, x, rows, 0)
+        ub.ub_copy_in(self.h, x, rows, 0, stream)
         n = self.qkv.shape[1]
-        ub.ub_gemm_ag_chunked(self.h, self.wqkv, n, n, self.qkv, n, self.gemm)
+        ub.ub_gemm_ag_chunked(self.h, self.wqkv, n, n, self.qkv, n, self.gemm, stream)
         return T
 
     def _append(self, cu, past, n, cache):
         ub.ub_kv_append(self.h, *self.hqkv, self.hq, self.hk, self.inv_freq, cu, past, n, cache,
-                        None if cache is None else self.pages, self.cfg)
+                        None if cache is None else self.pages, self.cfg, torch.cuda.current_stream())
 
     def _project_out(self, rows):
         k = self.heads * self.dim
-        ub.ub_gemm_rs_chunked(self.h, self.attn, k, k, self.wo, self.hidden, self.y, self.hidden, self.gemm)
+        ub.ub_gemm_rs_chunked(self.h, self.attn, k, k, self.wo, self.hidden, self.y, self.hidden, self.gemm,
+                              torch.cuda.current_stream())
         return self.y[:rows]
 
     def prefill(self, x, lens):
@@ -83,7 +86,8 @@ class AttentionBlock:
         n = len(lens)
         self._project_in(x)
         self._append(cu, None, n, self.cache)
-        ub.ub_attn_prompt(self.h, self.hq, self.hk, self.hqkv[2], self.hattn, None, cu, n, self.cfg, self.ws)
+        ub.ub_attn_prompt(self.h, self.hq, self.hk, self.hqkv[2], self.hattn, None, cu, n, self.cfg, self.ws,
+                          torch.cuda.current_stream())
         self.lens[:n] = cu[1:] - cu[:-1]
         self.step = torch.arange(n + 1, dtype=torch.int32, device="cuda")
         return self._project_out(x.shape[0])
@@ -94,26 +98,27 @@ class AttentionBlock:
         self._project_in(x)
         self._append(self.step, self.lens, n, self.cache)
         self.lens[:n] += 1
-        ub.ub_attn_decode(self.h, self.hq, self.cache, self.pages, self.lens, n, self.hattn, None, self.cfg, self.ws)
+        ub.ub_attn_decode(self.h, self.hq, self.cache, self.pages, self.lens, n, self.hattn, None, self.cfg, self.ws,
+                          torch.cuda.current_stream())
         return self._project_out(n)
 
     def train(self, x, lens, dattn):
         """A training step's attention: the block's output for documents x, and the gradient of
         the projected q, k and v for the gradient dattn [rows, heads dim] of the attention."""
         cu = torch.tensor([0] + list(lens), dtype=torch.int32).cumsum(0, dtype=torch.int32).cuda()
-        n, rows = len(lens), x.shape[0]
+        n, rows, stream = len(lens), x.shape[0], torch.cuda.current_stream()
         T = self._project_in(x)
         self._append(cu, None, n, None)
         lse = torch.empty((self.heads, T), dtype=torch.float32, device="cuda")
         d = torch.zeros((T, self.heads * self.dim), dtype=BF16, device="cuda")
         d[:rows] = dattn
-        ub.ub_attn_prompt(self.h, self.hq, self.hk, self.hqkv[2], self.hattn, lse, cu, n, self.cfg, self.ws)
+        ub.ub_attn_prompt(self.h, self.hq, self.hk, self.hqkv[2], self.hattn, lse, cu, n, self.cfg, self.ws, stream)
         y = self._project_out(rows)
         ub.ub_attn_prompt_bwd(self.h, ub.heads(d), self.hq, self.hk, self.hqkv[2], self.hattn, lse, *self.hdqkv, cu, n,
-                              self.cfg, self.ws)
+                              self.cfg, self.ws, stream)
         # back through the rotation: the negated frequencies, in place
         dq, dk, _ = self.hdqkv
-        ub.ub_kv_append(self.h, dq, dk, None, dq, dk, -self.inv_freq, cu, None, n, None, None, self.cfg)
+        ub.ub_kv_append(self.h, dq, dk, None, dq, dk, -self.inv_freq, cu, None, n, None, None, self.cfg, stream)
         return y, self.dqkv[:rows]
 
     def close(self):

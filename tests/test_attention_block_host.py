@@ -1,0 +1,65 @@
+"""Host-side test of the attention block's streams (no GPU): every call that issues work gets
+torch's current stream, on which the block's own tensor operations run."""
+
+import contextlib
+import inspect
+
+import pytest
+import torch
+
+ub = pytest.importorskip("chunked_tp_overlap_amd.ub", reason="libub.so not built")
+
+
+class Stream:
+    cuda_stream = 0x1234
+
+
+def on_host(f):
+    def g(*a, **kw):
+        kw.pop("device", None)
+        return f(*a, **kw)
+    return g
+
+
+@contextlib.contextmanager
+def recorded(monkeypatch):
+    """The block on host tensors, with the calls that issue work recorded in place of made:
+    (name, stream)."""
+    from chunked_tp_overlap_amd import attention_block as m
+
+    calls = []
+    with monkeypatch.context() as p:
+        for name in ("zeros", "empty", "arange", "full"):
+            p.setattr(torch, name, on_host(getattr(torch, name)))
+        p.setattr(torch.Tensor, "cuda", lambda self, *a, **kw: self)
+        p.setattr(torch.cuda, "current_stream", lambda *a: Stream)
+        for name in ub.EXPORTS:
+            f = getattr(ub, name, None)
+            if f is None or "stream" not in inspect.signature(f).parameters:
+                continue
+
+            def call(*a, f=f, name=name, **kw):
+                calls.append((name, inspect.signature(f).bind(*a, **kw).arguments.get("stream")))
+            p.setattr(ub, name, call)
+        yield m, calls
+
+
+def test_every_call_runs_on_the_current_stream(monkeypatch):
+    H, G, D, hidden, lens = 4, 2, 64, 128, [5, 1]
+    with recorded(monkeypatch) as (m, calls):
+        w = torch.zeros(hidden, (H + 2 * G) * D, dtype=torch.bfloat16), torch.zeros(H * D, hidden, dtype=torch.bfloat16)
+        b = m.AttentionBlock(*w, H, G, D, capacity=16, max_seqs=2, max_len=32, tp=2)
+        x = torch.zeros(6, hidden, dtype=torch.bfloat16)
+        made = {}
+        for name, f in (("prefill", lambda: b.prefill(x, lens)), ("decode", lambda: b.decode(x[:2])),
+                        ("train", lambda: b.train(x, lens, torch.zeros(6, H * D, dtype=torch.bfloat16)))):
+            calls.clear()
+            f()
+            made[name] = list(calls)
+        b.close()
+    ends = ["ub_copy_in", "ub_gemm_ag_chunked", "ub_kv_append"], ["ub_gemm_rs_chunked"]
+    for name, middle in (("prefill", ["ub_attn_prompt"]), ("decode", ["ub_attn_decode"])):
+        assert [c for c, _ in made[name]] == ends[0] + middle + ends[1]
+    assert [c for c, _ in made["train"]] == ends[0] + ["ub_attn_prompt"] + ends[1] + ["ub_attn_prompt_bwd", "ub_kv_append"]
+    for name, cs in made.items():
+        assert [c for c, s in cs if s is not Stream] == [], name
