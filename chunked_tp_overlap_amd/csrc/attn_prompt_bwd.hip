@@ -398,7 +398,9 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
   f32x4 dk[L::DB][KF], dv[L::DB][KF];
   const int steps = (total + NG - 1) / NG;
   const bool late = grp >= (NG + 1) / 2;
-  // As in bwd_q.
+  // As in bwd_q.  A tile's rows past the sequence's end are zeros, and so are their products, but
+  // not with a key or value that is not finite: then a sum is NaN, and the CAREFUL pass leaves
+  // those rows out.
   auto pass = [&](auto careful) __attribute__((always_inline)) {
     constexpr bool CAREFUL = decltype(careful)::value;
     bool bad = false;
@@ -469,6 +471,15 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
             for (int i = 0; i < 4; ++i)
               if (wk0 + f * 16 + col > q0 + b * 16 + 4 * g + i) s[b][f][i] = dp[b][f][i] = 0.0f;
       }
+      if (CAREFUL && q0 + BQ > st.len) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int f = 0; f < KF; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (q0 + b * 16 + 4 * g + i >= st.len) s[b][f][i] = dp[b][f][i] = 0.0f;
+      }
       bf16x8 pf[KF], ds[KF], rest[KF];
 #pragma unroll
       for (int f = 0; f < KF; ++f) {
@@ -506,6 +517,16 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
     for (; i < first; ++i) step(i, std::true_type{});
     for (; i < steps; ++i) step(i, std::false_type{});
     if (NG > 1 && !late) phase_barrier();
+    if (!CAREFUL && st.len % BQ != 0) {
+      float z = 0.0f;  // NaN if a sum is not finite
+#pragma unroll
+      for (int d = 0; d < L::DB; ++d)
+#pragma unroll
+        for (int f = 0; f < KF; ++f)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z += dk[d][f][i] * 0.0f + dv[d][f][i] * 0.0f;
+      bad = bad || z != 0.0f;
+    }
     return bad;
   };
   if (any_wave<S::NW>(pass(std::false_type{}), smem, wave, lane)) {
