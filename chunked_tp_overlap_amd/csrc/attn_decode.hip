@@ -178,6 +178,14 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
   const int vpiece = lane % VPR < pieces ? lane % VPR : 0;
 #pragma unroll
   for (int s = 0; s < KV; ++s) kofs[s] = (WHOLE ? col * row_bytes : 0) + (4 * s + g < pieces ? 4 * s + g : 0) * 16;
+  // Lanes whose last keys' piece lies past head_dim read piece 0, which their zero queries turn
+  // into NaN if it is infinite (E4M3 has no infinity): those pieces count as zeros.
+  u32x4 in_key[KV];
+#pragma unroll
+  for (int s = 0; s < KV; ++s) {
+    const uint32_t in = 4 * s + g < pieces ? 0xFFFFFFFFu : 0u;
+    in_key[s] = u32x4{in, in, in, in};
+  }
   const uint32_t vofs = (WHOLE ? lane / VPR * row_bytes : 0) + vpiece * 16;
 
   int64_t first = 0;  // units before the sequence
@@ -267,7 +275,8 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const u32x4 y = x.k[b][F8 ? d / 2 : d];
-          const u32x4 w = !F8 ? y : d & 1 ? cvt8(y[2], y[3]) : cvt8(y[0], y[1]);
+          // above a head_dim of 64 only the last piece can lie past it
+          const u32x4 w = F8 ? (d & 1 ? cvt8(y[2], y[3]) : cvt8(y[0], y[1])) : DS == 2 || d == DS - 1 ? y & in_key[d] : y;
           s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), q[d], s[b], 0, 0, 0);
         }
       if (t + STEP > end) {

@@ -59,3 +59,38 @@ def test_gradient_of_keys_without_weight(ub, H, G, D, lens):
         want[at] = 0.0  # weight 0, where the finite element's is not quite
         ref.check(got, want, tol, name)
         assert bool((got[at] == 0).all()), name
+
+
+@pytest.mark.parametrize("page", [16, 24])  # a block of tokens in one page, and token by token
+@pytest.mark.parametrize("H,G,D", [(2, 1, 8), (4, 2, 40), (6, 3, 80), (2, 2, 72), (3, 1, 104), (4, 2, 64), (2, 1, 128)])
+def test_decode_of_keys_without_weight(ub, H, G, D, page):
+    lens = [1 + page, 300]
+    n, per = len(lens), -(-max(lens) // page)
+    scale = 0.125
+    q = normal(31, (n, H, D))
+    q[..., 0] = 4.0
+    k, v = normal(32, (n * per, G, page, D)), normal(33, (n * per, G, page, D))
+    k[..., 0] = 0.0
+    table = torch.arange(n * per, dtype=torch.int32).view(n, per)
+    where = [(i, u) for i, m in enumerate(lens) for u in (0, m // 2, m - 1)]
+    for i, u in where:
+        k[i * per + u // page, :, u % page, 0] = FAR
+    y = k.clone()
+    for i, u in where:
+        y[i * per + u // page, :, u % page, 0] = -math.inf
+    cfg = ub.make_attn_cfg(H, G, D, softmax_scale=scale)
+    qd, kd, vd = q.reshape(n, -1).cuda(), y.cuda(), v.cuda()
+    out, lse = torch.empty((n, H * D), dtype=BF16, device="cuda"), torch.empty((H, n), device="cuda")
+    ws = workspace(ub, ub.UB_ATTN_DECODE, cfg, n, n)
+    with Rank(ub, n) as h:
+        ub.ub_attn_decode(h, ub.heads(qd), ub.make_kv_cache(kd, vd), table.cuda(), i32(lens), n, ub.heads(out), lse, cfg, ws)
+        torch.cuda.synchronize()
+    for i, m in enumerate(lens):
+        u = torch.arange(m)
+        pg, off = i * per + u // page, u % page
+        for g in range(G):
+            hs = slice(g * (H // G), (g + 1) * (H // G))
+            o, l, to, tl = ref.one(q[i, hs].double(), k[pg, g, off].double(), v[pg, g, off].double(), scale,
+                                   torch.ones(H // G, m, dtype=torch.bool))
+            ref.check(out[i].reshape(H, D)[hs], o, to, f"out {i} {g}")
+            ref.check(lse[hs, i], l, tl, f"lse {i} {g}")
