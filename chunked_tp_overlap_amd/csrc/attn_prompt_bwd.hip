@@ -391,6 +391,9 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
   for (int f = 0; f < KF; ++f)
 #pragma unroll
     for (int s = 0; s < DS; ++s) arrived(k[f][s]);
+  // This wave's share of the values is in LDS: all waves read them after the first barrier, which
+  // the later groups reach without a step's wait.
+  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
   RowFrag<DS> rf;  // from the stage; the group's q lie grp SET bytes on, dout TILE further
   ColFrag<DS> cf;
   rf.init(smem, lane);
