@@ -60,11 +60,13 @@ class AttentionBlock:
 
     def _project_in(self, x):
         """QKV of x's rows; the active shape becomes their number, rounded up to tp."""
+        if x.dim() != 2 or x.shape[1] != self.hidden or x.dtype is not BF16:
+            raise ValueError(f"x: a bf16 matrix of hidden size {self.hidden}, not {x.dtype} {tuple(x.shape)}")
         rows = x.shape[0]
         T = -(-rows // self.tp) * self.tp
         stream = torch.cuda.current_stream()
         ub.ub_set_active_shape(self.h, (T, self.hidden))
-        ub.ub_copy_in(self.h, x, rows, 0, stream)
+        ub.ub_copy_in(self.h, x.contiguous(), rows, 0, stream)
         n = self.qkv.shape[1]
         ub.ub_gemm_ag_chunked(self.h, self.wqkv, n, n, self.qkv, n, self.gemm, stream)
         return T
