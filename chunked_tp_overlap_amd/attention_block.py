@@ -23,11 +23,15 @@ BF16 = torch.bfloat16
 
 class AttentionBlock:
     """Heads of one rank: wqkv [hidden, (heads + 2 kv_heads) dim] and wo [heads dim, hidden], both
-    bf16.  The cache has room for `max_len` tokens of each of `max_seqs` sequences, as bf16 or
-    (with scales k_scale and v_scale) E4M3."""
+    contiguous bf16 matrices, which are kept and not copied.  The cache has room for `max_len` tokens
+    of each of `max_seqs` sequences, as bf16 or (with scales k_scale and v_scale) E4M3."""
 
     def __init__(self, wqkv, wo, heads, kv_heads, dim, capacity, max_seqs, max_len, page=64, tp=1, cache=BF16,
                  k_scale=1.0, v_scale=1.0, rope_base=10000.0):
+        for name, w, shape in (("wqkv", wqkv, (wqkv.shape[0], (heads + 2 * kv_heads) * dim)),
+                               ("wo", wo, (heads * dim, wqkv.shape[0]))):
+            if tuple(w.shape) != shape or w.dtype is not BF16 or not w.is_contiguous():
+                raise ValueError(f"{name}: a contiguous bf16 {list(shape)} matrix")
         self.wqkv, self.wo, self.tp, self.hidden = wqkv, wo, tp, wqkv.shape[0]
         self.heads, self.kv_heads, self.dim, self.max_seqs = heads, kv_heads, dim, max_seqs
         bf16 = dict(dtype=BF16, device="cuda")

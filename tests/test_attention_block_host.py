@@ -88,3 +88,20 @@ def test_rows_of_any_layout(monkeypatch):
                     f()
             assert len(copied) == n
         b.close()
+
+
+def test_weights(monkeypatch):
+    """The weights are kept, not copied, and read row by row: others than contiguous bf16 matrices
+    of the block's sizes are refused."""
+    with recorded(monkeypatch) as (m, _, _):
+        wqkv, wo = torch.randn(128, 512).bfloat16(), torch.randn(256, 128).bfloat16()
+        make = lambda a, b: m.AttentionBlock(a, b, 4, 2, 64, capacity=16, max_seqs=2, max_len=32)
+        b = make(wqkv, wo)
+        assert b.wqkv is wqkv and b.wo is wo
+        b.close()
+        for bad in ((wqkv.t().contiguous(), wo), (wqkv.t().contiguous().t(), wo), (wqkv.float(), wo), (wqkv[:, :504], wo)):
+            with pytest.raises(ValueError, match="wqkv"):
+                make(*bad)
+        for bad in (wo.t().contiguous(), wo.t().contiguous().t(), wo.half(), wo[:, :120].contiguous(), wo[:255]):
+            with pytest.raises(ValueError, match="wo:"):
+                make(wqkv, bad)
