@@ -362,9 +362,13 @@ __device__ inline SeqTile find_tile(const Seqs& s, int bm, int rank, bool low_fi
 
 // Four groups of waves on the keys shorten a call's longest rows.  Many sequences make many
 // workgroups of few steps each, and then those of one group, two to a CU, are faster whatever
-// the rows.  Measured, groups against one (forward; gradient, us): 4200 rows, 30 sequences, 8 heads
-// on 8 29 and 20, 71 and 42; 2048 rows, 16 sequences 18 and 15, 40 and 34; 4264 rows, 12 sequences
-// 32 and 29, 82 and 60; 2096 rows, 4 sequences, 8 on 1 23 and 32, 64 and 77.
+// the rows.  Measured, lengths within a factor of 5 but for an empty sequence and one of a single
+// token, groups against one (forward; gradient, us): 4200 rows, 30 sequences, 8 heads on 8 29 and 20,
+// 71 and 42; 2048 rows, 16 sequences 18 and 15, 40 and 34; 4264 rows, 12 sequences 32 and 29, 82 and
+// 60; 2096 rows, 4 sequences, 8 on 1 23 and 32, 64 and 77.  n counts the call's sequences, empty ones
+// too, as their lengths are on the device: where a table of many entries holds a few long sequences
+// the rule is wrong (8184 rows of 4 heads on 4 in 5 sequences, one of 4677: 51 and 170 us with 5 to
+// 23 entries, 81 and 196 with 24 and more).
 inline bool few_sequences(int64_t n, int H) { return n * H < 96; }
 
 // Tiles of bm rows that n sequences of T rows together can have.

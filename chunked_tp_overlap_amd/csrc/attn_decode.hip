@@ -19,9 +19,10 @@
 // more waves without that (12, or 16 with fewer registers) were slower (110, 137 us against
 // 104 in the first case below).
 //
-// Measured on MI355X, both kernels, where a plain read of as many bytes takes 84 us: 64
-// sequences of 1 to 8192 tokens, 4 + 4 heads of 128, bf16, pages of 16: 104 us (4.9 TB/s); 128
-// of 100 to 32520, 8 heads on 1, E4M3, pages of 64: 95 us (5.6 TB/s).
+// Measured on MI355X, both kernels, where a plain read reaches 5.3 to 6.4 TB/s (1 GiB, by the number
+// of workgroups and the cache policy): 64 sequences of 1 to 8192 tokens, 4 + 4 heads of 128, bf16,
+// pages of 16: 104 us (4.9 TB/s); 128 of 100 to 32520, 8 heads on 1, E4M3, pages of 64: 94 us (5.6
+// TB/s).
 #include <hip/hip_runtime.h>
 
 #include "attn_common.h"

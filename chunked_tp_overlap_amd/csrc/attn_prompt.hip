@@ -19,9 +19,12 @@
 // a bf16 library product of 8192^3 reaches 1.27.  The matrix cores are busy 59% of the time at
 // the 1.9 GHz that the power limit leaves.  8184 tokens, the longest sequence 4677, 4 heads of 128
 // on 4: 50 us.  The last rows of that sequence alone take 44: 37 steps of 128 keys, 0.95 us each,
-// for which LDS is read or written 80% of the time, and 6 us before and after them.  More waves
-// of 16 rows each (57.3 us against 57.4 in one trace), two such workgroups to a CU (62) and the
-// product with the values one step late, beside the next scores (68), were no faster.
+// and 6 us before and after them.  A step is some 1900 cycles; by count, its matrix instructions
+// take 1024 of each SIMD and its 128 KB of fragment reads and 64 KB of loads pass through LDS.  What
+// is left is the chain of a step: barrier, scores, exponentials, products, with two waves to a
+// SIMD to cover it.  Measured, the kernel in one trace 57.4 us: without loads after the first 55;
+// more waves of 16 rows each 57.3; two such workgroups to a CU 62; the product with the values one
+// step late, beside the next scores, 68.
 //
 // Rows past a sequence's end (of any input) are never read: their loads fall outside the
 // buffer resource and give zeros.

@@ -11,10 +11,11 @@
 //    few key tiles the heads of a group go to several workgroups, whose fp32 parts
 //    attn_bwd_join adds in order.
 //
-// Measured on MI355X, all launches.  16264 tokens in 2 sequences, 8 heads of 128 on 1: 0.88 ms, 1.08
-// PFLOP/s of the seven products done (five are counted); the matrix cores are busy 52% of the
-// time at the 2.1 GHz that the power limit leaves.  8184 tokens in 5 sequences, 4 heads of 128 on
-// 4: 171 us, bounded by the steps of the longest rows, as the forward pass.
+// Measured on MI355X, all launches, calls one after another.  16264 tokens in 2 sequences, 8 heads of
+// 128 on 1: 883 us, 1.08 PFLOP/s of the seven products done (five are counted); the matrix cores
+// are busy 52% of the time at the 2.1 GHz that the power limit leaves.  8184 tokens in 5 sequences,
+// 4 heads of 128 on 4: 170-174 us, bounded by the steps of the longest rows, as the forward pass.
+// (One call at a time, under a profiler, its kernels take 191.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -116,7 +117,7 @@ __global__ __launch_bounds__(256) void attn_bwd_rows(BwdParams p) {
 }
 
 // What pack8 leaves of 8 values, as bf16.  P and dS are rounded to bf16 for the matrix cores, by
-// up to 2^-9 of each.  The rows of few keys, in the diagonal tiles, have the largest dS, and
+// up to 2^-8 of each.  The rows of few keys, in the diagonal tiles, have the largest dS, and
 // those that suffer most from delta's error (out is bf16): their dS is used as two bf16 numbers,
 // which takes the gradients' error from 1.53 of that of their own rounding to 1.32 (sequences of 1
 // to 521 tokens; 1.47 to 1.37 with 817 to 5038) for 13.4 us instead of 12.6.
@@ -573,8 +574,8 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
 }
 
 // Both kinds in one launch, each by falling work, so that the second starts where the last and
-// longest of the first still run: on 8184 rows of 4 heads on 4 in 5 sequences 190 us, where a
-// launch for each takes 84 and 125.  Rank by rank in turns it takes 230.
+// longest of the first still run.  Measured on an earlier version of the two, 8184 rows of 4 heads on
+// 4 in 5 sequences: 190 us, where a launch for each took 84 and 125; rank by rank in turns 230.
 template <class SQ, class SK>
 __global__ __launch_bounds__(64 * SQ::NW, 2) void attn_bwd(BwdParams p) {
   extern __shared__ __align__(256) unsigned char smem[];
@@ -618,9 +619,9 @@ __global__ __launch_bounds__(256) void attn_bwd_join(BwdParams p) {
 constexpr int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
 // Calls of few rows times heads take 64 rows and four groups of waves per workgroup, for the
-// reason given in attn_prompt.hip.  Measured, the gradient alone, groups against one: 8184 rows
-// of 4 heads on 4, 2 sequences 187 and 195 us, 5 sequences 161 and 196; 5120 of 8 on 1 (2) 151
-// and 134, of 8 on 8 (8) 115 and 99.
+// reason given in attn_prompt.hip.  Measured on an earlier version of both (the second case takes
+// 170-174 now), the gradient alone, groups against one: 8184 rows of 4 heads on 4, 2 sequences 187 and
+// 195 us, 5 sequences 161 and 196; 5120 of 8 on 1 (2) 151 and 134, of 8 on 8 (8) 115 and 99.
 constexpr int64_t GROUPED_BELOW = 36 * 1024;
 bool grouped(int H, int64_t rows, int64_t n) { return rows * H < GROUPED_BELOW && few_sequences(n, H); }
 

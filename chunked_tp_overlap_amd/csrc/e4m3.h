@@ -1,4 +1,5 @@
-// fp32 -> OCP E4M3 with saturation, shared by the kernels that write E4M3 codes.
+// fp32 -> OCP E4M3 with saturation, as quantize_fp8.hip uses it.  kv_append.hip gives the same codes
+// by the hardware's conversion, which the tests compare with this one for every bf16 value.
 //
 //   e4m3(y) = sat(RNE_e4m3(y)): the nearest OCP E4M3 value (bias 7, 3 significand bits,
 //   subnormal spacing 2^-9), ties to even; magnitudes beyond 448 (and infinities) saturate

@@ -213,7 +213,8 @@ __global__ __launch_bounds__(THREADS, 8) void kv_append(AppendParams p) {
   __syncthreads();
   for (int j = wave; j < nt; j += WAVES) {
     if (lane >= half) break;
-    // revolutions, reduced in 64 bits; the product pos * inv_freq is exact there
+    // revolutions, reduced in 64 bits; the product pos * inv_freq, of a position below 2^29 and a
+    // 24-bit significand, is exact there
     double r = (double)tok[j].pos * (double)freq * 0.15915494309189533577;
     r -= rint(r);
     float s, c;
