@@ -110,7 +110,8 @@ class AttentionBlock:
 
     def train(self, x, lens, dattn):
         """A training step's attention: the block's output for documents x, and the gradient of
-        the projected q, k and v for the gradient dattn [rows, heads dim] of the attention."""
+        the projected q, k and v for the gradient dattn [rows, heads dim] of the attention's output.
+        (The gradients of the projections, before and after it, are the caller's.)"""
         cu = torch.tensor([0] + list(lens), dtype=torch.int32).cumsum(0, dtype=torch.int32).cuda()
         n, rows, stream = len(lens), x.shape[0], torch.cuda.current_stream()
         T = self._project_in(x)

@@ -15,7 +15,7 @@
 // 128 on 1: 883 us, 1.08 PFLOP/s of the seven products done (five are counted); the matrix cores
 // are busy 52% of the time at the 2.1 GHz that the power limit leaves.  8184 tokens in 5 sequences,
 // 4 heads of 128 on 4: 170-174 us, bounded by the steps of the longest rows, as the forward pass.
-// (One call at a time, under a profiler, its kernels take 191.)
+// (One call at a time, under a profiler, its kernels take 187.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
