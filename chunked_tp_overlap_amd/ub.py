@@ -407,9 +407,9 @@ def make_attn_cfg(n_heads, n_kv_heads, head_dim, rotary_dim=None, rope_interleav
 
 
 def heads(x, col=0):
-    """A ``ub_heads_t`` over a device tensor: the heads that start at column ``col`` of a 2-D
+    """A ``ub_heads_t`` over a bf16 device tensor: the heads that start at column ``col`` of a 2-D
     [rows, columns] matrix, head_dim columns each, or a 3-D [rows, heads, head_dim] view with
-    any row and head strides.  It keeps the tensor alive."""
+    any row and head strides of head_dim and more.  It keeps the tensor alive."""
     if x.dim() not in (2, 3):
         raise ValueError(f"heads: a 2-D or 3-D tensor, not {x.dim()}-D")
     if x.dtype is not torch.bfloat16:
