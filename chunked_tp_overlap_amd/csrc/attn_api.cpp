@@ -115,6 +115,14 @@ ubx::KvCache cache(Checks& c, const ub_kv_cache_t* x, const int32_t* table, int6
                       f8 ? x->k_scale : 1.0f, f8 ? x->v_scale : 1.0f};
 }
 
+ubx::Window window(Checks& c, const ub_attn_window_t* x) {
+  c.need(x != nullptr, "window is NULL");
+  if (c.st != UB_OK) return ubx::Window{};
+  c.need(x->window >= 1, "window must be >= 1");
+  c.need(x->sinks >= 0 && x->sinks <= UB_ATTN_MAX_SINKS, "sinks must be in [0, UB_ATTN_MAX_SINKS]");
+  return ubx::Window{x->window < ubx::kMaxWindow ? x->window : ubx::kMaxWindow, x->sinks};
+}
+
 void workspace(Checks& c, const void* ws, size_t have, size_t need) {
   if (need == 0 || c.st != UB_OK) return;
   c.need(ws != nullptr && aligned16(ws), "workspace must be non-NULL and 16-byte aligned");
@@ -140,6 +148,118 @@ ub_status_t guarded(F&& f) {
   }
 }
 
+// The three calls without and with a window (`windowed`), by the name that messages carry.
+ub_status_t prompt(const char* name, ub_handle_t h, const ub_heads_t* q, const ub_heads_t* k,
+                   const ub_heads_t* v, const ub_heads_t* out, float* lse, const int32_t* cu_seqlens,
+                   int32_t n_seqs, bool windowed, const ub_attn_window_t* win, const ub_attn_cfg_t* cfg,
+                   ub_stream_t stream) {
+  const TraceRange range(name);
+  if (!h) return UB_ERR_NOT_INITIALIZED;
+  return guarded([&] {
+    Checks c{h};
+    check_cfg(c, cfg);
+    if (c.st != UB_OK) return c.st;
+    const int64_t T = ubx::ctx_rows(h);
+    ubx::PromptArgs a{};
+    a.H = cfg->n_heads;
+    a.G = cfg->n_kv_heads;
+    a.D = cfg->head_dim;
+    a.scale = cfg->softmax_scale;
+    a.q = heads(c, "q", q, a.H, T, cfg);
+    a.k = heads(c, "k", k, a.G, T, cfg);
+    a.v = heads(c, "v", v, a.G, T, cfg);
+    a.out = heads(c, "out", out, a.H, T, cfg);
+    a.lse = lse;
+    a.seqs = seqs(c, cu_seqlens, n_seqs, T);
+    if (windowed) a.win = window(c, win);
+    if (c.st != UB_OK) return c.st;
+    ub_status_t st = ubx::ctx_bind(h);
+    if (st != UB_OK) return st;
+    return launched(h, ubx::launch_attn_prompt(a, static_cast<hipStream_t>(stream)), name);
+  });
+}
+
+ub_status_t prompt_bwd(const char* name, ub_handle_t h, const ub_heads_t* dout, const ub_heads_t* q,
+                       const ub_heads_t* k, const ub_heads_t* v, const ub_heads_t* out,
+                       const float* lse, const ub_heads_t* dq, const ub_heads_t* dk,
+                       const ub_heads_t* dv, const int32_t* cu_seqlens, int32_t n_seqs, bool windowed,
+                       const ub_attn_window_t* win, const ub_attn_cfg_t* cfg, void* ws,
+                       size_t ws_bytes, ub_stream_t stream) {
+  const TraceRange range(name);
+  if (!h) return UB_ERR_NOT_INITIALIZED;
+  return guarded([&] {
+    Checks c{h};
+    check_cfg(c, cfg);
+    if (c.st != UB_OK) return c.st;
+    const int64_t T = ubx::ctx_rows(h);
+    ubx::PromptBwdArgs a{};
+    a.H = cfg->n_heads;
+    a.G = cfg->n_kv_heads;
+    a.D = cfg->head_dim;
+    a.scale = cfg->softmax_scale;
+    a.dout = heads(c, "dout", dout, a.H, T, cfg);
+    a.q = heads(c, "q", q, a.H, T, cfg);
+    a.k = heads(c, "k", k, a.G, T, cfg);
+    a.v = heads(c, "v", v, a.G, T, cfg);
+    a.out = heads(c, "out", out, a.H, T, cfg);
+    a.dq = heads(c, "dq", dq, a.H, T, cfg);
+    a.dk = heads(c, "dk", dk, a.G, T, cfg);
+    a.dv = heads(c, "dv", dv, a.G, T, cfg);
+    c.need(lse != nullptr, "lse is NULL");
+    a.lse = lse;
+    a.seqs = seqs(c, cu_seqlens, n_seqs, T);
+    if (windowed) a.win = window(c, win);
+    if (c.st == UB_OK)
+      workspace(c, ws, ws_bytes, ubx::attn_prompt_bwd_need(a.H, a.G, a.D, T) +
+                                     (a.win.sinks ? ubx::attn_prompt_bwd_sink_bytes(a.H, a.G, a.D, T) : 0));
+    a.ws = ws;
+    if (c.st != UB_OK) return c.st;
+    ub_status_t st = ubx::ctx_bind(h);
+    if (st != UB_OK) return st;
+    return launched(h, ubx::launch_attn_prompt_bwd(a, static_cast<hipStream_t>(stream)), name);
+  });
+}
+
+ub_status_t decode(const char* name, ub_handle_t h, const ub_heads_t* q, const ub_kv_cache_t* kv,
+                   const int32_t* page_table, int64_t pages_ld, int32_t pages_per_seq,
+                   const int32_t* kv_lens, int32_t n_seqs, bool windowed, const ub_attn_window_t* win,
+                   const ub_heads_t* out, float* lse, const ub_attn_cfg_t* cfg, void* ws,
+                   size_t ws_bytes, ub_stream_t stream) {
+  const TraceRange range(name);
+  if (!h) return UB_ERR_NOT_INITIALIZED;
+  return guarded([&] {
+    Checks c{h};
+    check_cfg(c, cfg);
+    if (c.st != UB_OK) return c.st;
+    const int64_t T = ubx::ctx_rows(h);
+    ubx::DecodeArgs a{};
+    a.H = cfg->n_heads;
+    a.G = cfg->n_kv_heads;
+    a.D = cfg->head_dim;
+    a.scale = cfg->softmax_scale;
+    a.q = heads(c, "q", q, a.H, T, cfg);
+    a.out = heads(c, "out", out, a.H, T, cfg);
+    a.lse = lse;
+    c.need(n_seqs >= 0 && n_seqs <= T, "n_seqs must be in [0, T]: one row of q per sequence");
+    c.need(n_seqs == 0 || kv_lens != nullptr, "kv_lens is NULL");
+    if (c.st == UB_OK && T > kMaxRows) c.bad(UB_ERR_UNSUPPORTED, "more than 2^30 active rows");
+    a.cache = cache(c, kv, page_table, pages_ld, pages_per_seq, n_seqs, cfg);
+    a.pages = page_table;
+    a.pages_ld = pages_ld;
+    a.pages_per_seq = pages_per_seq;
+    a.lens = kv_lens;
+    a.n = n_seqs;
+    a.T = static_cast<int32_t>(T);
+    if (c.st == UB_OK) workspace(c, ws, ws_bytes, ubx::attn_decode_bytes(a.H, a.G, a.D, n_seqs));
+    a.ws = ws;
+    if (windowed) a.win = window(c, win);
+    if (c.st != UB_OK) return c.st;
+    ub_status_t st = ubx::ctx_bind(h);
+    if (st != UB_OK) return st;
+    return launched(h, ubx::launch_attn_decode(a, static_cast<hipStream_t>(stream)), name);
+  });
+}
+
 }  // namespace
 
 extern "C" {
@@ -151,12 +271,18 @@ UB_API ub_status_t ub_attn_required_bytes(ub_attn_op_t op, const ub_attn_cfg_t* 
   if (!bytes || rows < 0 || rows > kMaxRows || n_seqs < 0) return UB_ERR_INVALID_ARG;
   switch (op) {
     case UB_ATTN_PROMPT:
+    case UB_ATTN_PROMPT_WINDOW:
       *bytes = 0;
+      return UB_OK;
+    case UB_ATTN_PROMPT_WINDOW_BWD:
+      *bytes = ubx::attn_prompt_bwd_bytes(cfg->n_heads, cfg->n_kv_heads, cfg->head_dim, rows) +
+               ubx::attn_prompt_bwd_sink_bytes(cfg->n_heads, cfg->n_kv_heads, cfg->head_dim, rows);
       return UB_OK;
     case UB_ATTN_PROMPT_BWD:
       *bytes = ubx::attn_prompt_bwd_bytes(cfg->n_heads, cfg->n_kv_heads, cfg->head_dim, rows);
       return UB_OK;
     case UB_ATTN_DECODE:
+    case UB_ATTN_DECODE_WINDOW:
       *bytes = ubx::attn_decode_bytes(cfg->n_heads, cfg->n_kv_heads, cfg->head_dim, n_seqs);
       return UB_OK;
     default:
@@ -211,33 +337,16 @@ UB_API ub_status_t ub_kv_append(ub_handle_t h, const ub_heads_t* q, const ub_hea
 UB_API ub_status_t ub_attn_prompt(ub_handle_t h, const ub_heads_t* q, const ub_heads_t* k,
                                   const ub_heads_t* v, const ub_heads_t* out, float* lse,
                                   const int32_t* cu_seqlens, int32_t n_seqs,
-                                  const ub_attn_cfg_t* cfg, void* ws, size_t ws_bytes,
-                                  ub_stream_t stream) {
-  const TraceRange range("ub_attn_prompt");
-  if (!h) return UB_ERR_NOT_INITIALIZED;
-  (void)ws;
-  (void)ws_bytes;
-  return guarded([&] {
-    Checks c{h};
-    check_cfg(c, cfg);
-    if (c.st != UB_OK) return c.st;
-    const int64_t T = ubx::ctx_rows(h);
-    ubx::PromptArgs a{};
-    a.H = cfg->n_heads;
-    a.G = cfg->n_kv_heads;
-    a.D = cfg->head_dim;
-    a.scale = cfg->softmax_scale;
-    a.q = heads(c, "q", q, a.H, T, cfg);
-    a.k = heads(c, "k", k, a.G, T, cfg);
-    a.v = heads(c, "v", v, a.G, T, cfg);
-    a.out = heads(c, "out", out, a.H, T, cfg);
-    a.lse = lse;
-    a.seqs = seqs(c, cu_seqlens, n_seqs, T);
-    if (c.st != UB_OK) return c.st;
-    ub_status_t st = ubx::ctx_bind(h);
-    if (st != UB_OK) return st;
-    return launched(h, ubx::launch_attn_prompt(a, static_cast<hipStream_t>(stream)), "ub_attn_prompt");
-  });
+                                  const ub_attn_cfg_t* cfg, void*, size_t, ub_stream_t stream) {
+  return prompt("ub_attn_prompt", h, q, k, v, out, lse, cu_seqlens, n_seqs, false, nullptr, cfg, stream);
+}
+
+UB_API ub_status_t ub_attn_prompt_window(ub_handle_t h, const ub_heads_t* q, const ub_heads_t* k,
+                                         const ub_heads_t* v, const ub_heads_t* out, float* lse,
+                                         const int32_t* cu_seqlens, int32_t n_seqs,
+                                         const ub_attn_window_t* win, const ub_attn_cfg_t* cfg,
+                                         void*, size_t, ub_stream_t stream) {
+  return prompt("ub_attn_prompt_window", h, q, k, v, out, lse, cu_seqlens, n_seqs, true, win, cfg, stream);
 }
 
 UB_API ub_status_t ub_attn_prompt_bwd(ub_handle_t h, const ub_heads_t* dout, const ub_heads_t* q,
@@ -247,37 +356,20 @@ UB_API ub_status_t ub_attn_prompt_bwd(ub_handle_t h, const ub_heads_t* dout, con
                                       const ub_heads_t* dv, const int32_t* cu_seqlens,
                                       int32_t n_seqs, const ub_attn_cfg_t* cfg, void* ws,
                                       size_t ws_bytes, ub_stream_t stream) {
-  const TraceRange range("ub_attn_prompt_bwd");
-  if (!h) return UB_ERR_NOT_INITIALIZED;
-  return guarded([&] {
-    Checks c{h};
-    check_cfg(c, cfg);
-    if (c.st != UB_OK) return c.st;
-    const int64_t T = ubx::ctx_rows(h);
-    ubx::PromptBwdArgs a{};
-    a.H = cfg->n_heads;
-    a.G = cfg->n_kv_heads;
-    a.D = cfg->head_dim;
-    a.scale = cfg->softmax_scale;
-    a.dout = heads(c, "dout", dout, a.H, T, cfg);
-    a.q = heads(c, "q", q, a.H, T, cfg);
-    a.k = heads(c, "k", k, a.G, T, cfg);
-    a.v = heads(c, "v", v, a.G, T, cfg);
-    a.out = heads(c, "out", out, a.H, T, cfg);
-    a.dq = heads(c, "dq", dq, a.H, T, cfg);
-    a.dk = heads(c, "dk", dk, a.G, T, cfg);
-    a.dv = heads(c, "dv", dv, a.G, T, cfg);
-    c.need(lse != nullptr, "lse is NULL");
-    a.lse = lse;
-    a.seqs = seqs(c, cu_seqlens, n_seqs, T);
-    if (c.st == UB_OK) workspace(c, ws, ws_bytes, ubx::attn_prompt_bwd_need(a.H, a.G, a.D, T));
-    a.ws = ws;
-    if (c.st != UB_OK) return c.st;
-    ub_status_t st = ubx::ctx_bind(h);
-    if (st != UB_OK) return st;
-    return launched(h, ubx::launch_attn_prompt_bwd(a, static_cast<hipStream_t>(stream)),
-                    "ub_attn_prompt_bwd");
-  });
+  return prompt_bwd("ub_attn_prompt_bwd", h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens, n_seqs,
+                    false, nullptr, cfg, ws, ws_bytes, stream);
+}
+
+UB_API ub_status_t ub_attn_prompt_window_bwd(ub_handle_t h, const ub_heads_t* dout,
+                                             const ub_heads_t* q, const ub_heads_t* k,
+                                             const ub_heads_t* v, const ub_heads_t* out,
+                                             const float* lse, const ub_heads_t* dq,
+                                             const ub_heads_t* dk, const ub_heads_t* dv,
+                                             const int32_t* cu_seqlens, int32_t n_seqs,
+                                             const ub_attn_window_t* win, const ub_attn_cfg_t* cfg,
+                                             void* ws, size_t ws_bytes, ub_stream_t stream) {
+  return prompt_bwd("ub_attn_prompt_window_bwd", h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens,
+                    n_seqs, true, win, cfg, ws, ws_bytes, stream);
 }
 
 UB_API ub_status_t ub_attn_decode(ub_handle_t h, const ub_heads_t* q, const ub_kv_cache_t* kv,
@@ -285,38 +377,19 @@ UB_API ub_status_t ub_attn_decode(ub_handle_t h, const ub_heads_t* q, const ub_k
                                   int32_t pages_per_seq, const int32_t* kv_lens, int32_t n_seqs,
                                   const ub_heads_t* out, float* lse, const ub_attn_cfg_t* cfg,
                                   void* ws, size_t ws_bytes, ub_stream_t stream) {
-  const TraceRange range("ub_attn_decode");
-  if (!h) return UB_ERR_NOT_INITIALIZED;
-  return guarded([&] {
-    Checks c{h};
-    check_cfg(c, cfg);
-    if (c.st != UB_OK) return c.st;
-    const int64_t T = ubx::ctx_rows(h);
-    ubx::DecodeArgs a{};
-    a.H = cfg->n_heads;
-    a.G = cfg->n_kv_heads;
-    a.D = cfg->head_dim;
-    a.scale = cfg->softmax_scale;
-    a.q = heads(c, "q", q, a.H, T, cfg);
-    a.out = heads(c, "out", out, a.H, T, cfg);
-    a.lse = lse;
-    c.need(n_seqs >= 0 && n_seqs <= T, "n_seqs must be in [0, T]: one row of q per sequence");
-    c.need(n_seqs == 0 || kv_lens != nullptr, "kv_lens is NULL");
-    if (c.st == UB_OK && T > kMaxRows) c.bad(UB_ERR_UNSUPPORTED, "more than 2^30 active rows");
-    a.cache = cache(c, kv, page_table, pages_ld, pages_per_seq, n_seqs, cfg);
-    a.pages = page_table;
-    a.pages_ld = pages_ld;
-    a.pages_per_seq = pages_per_seq;
-    a.lens = kv_lens;
-    a.n = n_seqs;
-    a.T = static_cast<int32_t>(T);
-    if (c.st == UB_OK) workspace(c, ws, ws_bytes, ubx::attn_decode_bytes(a.H, a.G, a.D, n_seqs));
-    a.ws = ws;
-    if (c.st != UB_OK) return c.st;
-    ub_status_t st = ubx::ctx_bind(h);
-    if (st != UB_OK) return st;
-    return launched(h, ubx::launch_attn_decode(a, static_cast<hipStream_t>(stream)), "ub_attn_decode");
-  });
+  return decode("ub_attn_decode", h, q, kv, page_table, pages_ld, pages_per_seq, kv_lens, n_seqs, false,
+                nullptr, out, lse, cfg, ws, ws_bytes, stream);
+}
+
+UB_API ub_status_t ub_attn_decode_window(ub_handle_t h, const ub_heads_t* q,
+                                         const ub_kv_cache_t* kv, const int32_t* page_table,
+                                         int64_t pages_ld, int32_t pages_per_seq,
+                                         const int32_t* kv_lens, int32_t n_seqs,
+                                         const ub_attn_window_t* win, const ub_heads_t* out,
+                                         float* lse, const ub_attn_cfg_t* cfg, void* ws,
+                                         size_t ws_bytes, ub_stream_t stream) {
+  return decode("ub_attn_decode_window", h, q, kv, page_table, pages_ld, pages_per_seq, kv_lens, n_seqs,
+                true, win, out, lse, cfg, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -193,6 +193,47 @@ __device__ inline f32x4 seen_product(bf16x8 a, bf16x8 b, f32x4 acc, int row, int
   return r;
 }
 
+// The same under a window: row r of the tile for column c if it comes no later than row at + c
+// and either fewer than win.size rows before it or among the first win.sinks of the sequence.
+__device__ inline bool seen(int key, int row, Window win) {
+  return key <= row && (key > row - win.size || key < win.sinks);
+}
+// KEYS: the tile's rows are keys and the columns rows that see them; otherwise the reverse.
+template <bool KEYS>
+__device__ inline f32x4 seen_product(bf16x8 a, bf16x8 b, f32x4 acc, int row, int at, int lane, Window win) {
+  f32x4 r = acc;
+#pragma unroll 1
+  for (int c = 0; c < 16; ++c) {
+    u32x4 m = __builtin_bit_cast(u32x4, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = row + 4 * (lane >> 4) + (i & 1) * 2 + (i >> 1) * 16;
+      const bool lo = KEYS ? seen(t, at + c, win) : seen(at + c, t, win);
+      const bool hi = KEYS ? seen(t + 1, at + c, win) : seen(at + c, t + 1, win);
+      m[i] &= (lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+    }
+    const f32x4 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, m), b, acc, 0, 0, 0);
+    if ((lane & 15) == c) r = y;
+  }
+  return r;
+}
+
+// The key tiles of BN keys that rows q0 .. q0 + BM - 1 see, as one list: `sink` tiles of the
+// first tokens, then those from `first` on.  Of `tiles` in all, the first `head` hold keys
+// that the window hides from one of the rows.
+struct KeyTiles {
+  int sink, first, head, tiles;
+  __device__ int at(int j) const { return j < sink ? j : j - sink + first; }
+};
+__device__ inline KeyTiles key_tiles(int q0, int BM, int BN, int n_keys, Window win) {
+  KeyTiles k;
+  k.first = max(q0 - win.size + 1, 0) / BN;
+  k.sink = min((win.sinks + BN - 1) / BN, k.first);
+  k.tiles = k.sink + (n_keys + BN - 1) / BN - k.first;
+  k.head = min(k.sink + (max(q0 + BM - win.size, 0) + BN - 1) / BN - k.first, k.tiles);
+  return k;
+}
+
 // Makes the compiler wait here for a value it loads.  It does not count the direct-to-LDS
 // loads, so a wait that it left to a value's first use, inside a loop, would be one for all
 // loads in flight there: the next tile's among them, in every iteration.

@@ -52,7 +52,24 @@ struct DecodeParams {
 // Cached tokens of sequence i, as far as the page table reaches.
 __device__ inline int kv_len(const DecodeParams& p, int i) { return clamp_len(p.a.lens[i], p.cap); }
 
-__device__ inline int units(int len) { return (len + STEP - 1) / STEP; }
+// Units of a sequence of len tokens that its new token sees: all, or under a window `sink` of
+// the first tokens and those from unit sink + gap on.  Tokens before `from` are hidden but for
+// the first win.sinks.
+struct Units {
+  int n, sink, gap, from;
+  __device__ int token(int u) const { return (u < sink ? u : u + gap) * STEP; }
+};
+template <bool WIN>
+__device__ inline Units units(int len, Window win) {
+  Units u{(len + STEP - 1) / STEP, 0, 0, 0};
+  if (WIN) {
+    u.from = max(len - win.size, 0);
+    u.sink = min((win.sinks + STEP - 1) / STEP, u.from / STEP);
+    u.gap = u.from / STEP - u.sink;
+    u.n -= u.gap;
+  }
+  return u;
+}
 
 // All n sequences' units, S, dealt in W ranges: the first `more` hold q + 1 units, the others q.
 // A range takes MIN_UNITS units at least, unless sequences are shorter: each that a range
@@ -81,25 +98,28 @@ struct Deal {
 };
 
 // Units of sequences c + lane, up to 2^25 each: 64 of them fit 32 unsigned bits.
+template <bool WIN>
 __device__ inline uint32_t units_of(const DecodeParams& p, int c) {
   const int i = c + (threadIdx.x & 63);
-  return i < p.a.n ? units(kv_len(p, i)) : 0;
+  return i < p.a.n ? units<WIN>(kv_len(p, i), p.a.win).n : 0;
 }
 
 // head: units_of(p, 0)
+template <bool WIN>
 __device__ inline Deal deal_units(const DecodeParams& p, uint32_t head) {
   int64_t S = (uint32_t)wave_sum((int)head);
-  for (int c = 64; c < p.a.n; c += 64) S += (uint32_t)wave_sum((int)units_of(p, c));
+  for (int c = 64; c < p.a.n; c += 64) S += (uint32_t)wave_sum((int)units_of<WIN>(p, c));
   Deal d;
   d.init(S, p.a.n, p.ranges);
   return d;
 }
 
 // The sequence that holds a unit, and the units before that sequence.
+template <bool WIN>
 __device__ inline int find_sequence(const DecodeParams& p, uint32_t head, int64_t unit, int64_t& first) {
   int64_t before = 0;
   for (int c = 0; c < p.a.n; c += 64) {
-    const uint32_t u = c == 0 ? head : units_of(p, c);
+    const uint32_t u = c == 0 ? head : units_of<WIN>(p, c);
     const uint32_t incl = (uint32_t)wave_scan((int)u);
     const uint64_t m = __ballot(before + incl > unit);
     if (m) {
@@ -146,7 +166,9 @@ __device__ inline int64_t lane_of(int64_t x, int lane) {  // uniform lane
 // WHOLE: pages of a multiple of 16 tokens, so that a block of 16 tokens lies in one page: its
 // place is uniform over the wave, and its rows' offsets from there are the same in all steps.
 // Otherwise every token's place is looked up.
-template <int DS, bool F8, bool WHOLE>
+// WIN: under a window (a.win).  Hidden tokens of a unit count as those past the end, and their
+// pages, which may be gone, are not looked up where a block or token is hidden whole.
+template <int DS, bool F8, bool WHOLE, bool WIN>
 __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodeParams p) {
   using L = Tile<DS>;
   using Y = Layout<DS, F8>;
@@ -162,8 +184,8 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
   const int gq = blockIdx.x % GQ, rank = blockIdx.x / GQ;
   const int kvh = gq / p.qb, group = a.H / a.G, col0 = (gq - kvh * p.qb) * COLS;
   const int cols = min(group - col0, COLS);
-  const uint32_t head = units_of(p, 0);
-  const Deal deal = deal_units(p, head);
+  const uint32_t head = units_of<WIN>(p, 0);
+  const Deal deal = deal_units<WIN>(p, head);
   if (rank >= deal.W) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
@@ -190,13 +212,15 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
   const uint32_t vofs = (WHOLE ? lane / VPR * row_bytes : 0) + vpiece * 16;
 
   int64_t first = 0;  // units before the sequence
-  int seq = find_sequence(p, head, unit0, first);
+  int seq = find_sequence<WIN>(p, head, unit0, first);
   for (int64_t unit = unit0; unit < unit1 && seq < a.n; ++seq) {
     const int len = kv_len(p, seq);
-    const int64_t last = first + units(len);  // units up to the sequence's end
+    const Units un = units<WIN>(len, a.win);
+    const int64_t last = first + un.n;  // units up to the sequence's end
     if (last == first) continue;
-    const int begin = (int)(unit - first) * STEP;
-    const int end = (int)min((min(last, unit1) - first) * STEP, (int64_t)len);
+    const int ubegin = (int)(unit - first), uend = (int)(min(last, unit1) - first);
+    const int begin = ubegin * STEP;
+    const int end = WIN ? len : (int)min((int64_t)uend * STEP, (int64_t)len);
     const bool alone = unit == first && last <= unit1;
     const int64_t item = (int64_t)(2 * rank + (unit != unit0)) * GQ + gq;
     if (unit == first && gq == 0 && threadIdx.x == 0)
@@ -218,9 +242,13 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
     for (int d = 0; d < L::DB; ++d) o[d] = f32x4{0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
 
-    // The wave's steps: tokens t0 + NW STEP j .. + 31, j < n.
+    // The wave's steps: tokens t0 + NW STEP j .. + 31, j < n; under a window those of unit
+    // ubegin + wave + NW j.
     const int t0 = begin + wave * STEP;
-    const int n = t0 < end ? (end - t0 + NW * STEP - 1) / (NW * STEP) : 0;
+    const int n = WIN ? max(uend - ubegin - wave + NW - 1, 0) / NW
+                      : t0 < end ? (end - t0 + NW * STEP - 1) / (NW * STEP) : 0;
+    auto token_of = [&](int j) { return WIN ? un.token(ubegin + wave + j * NW) : t0 + j * (NW * STEP); };
+    auto hidden = [&](int t) { return t >= end || (WIN && t < un.from && t >= a.win.sinks); };
     int64_t place = 0;  // element offset of a token in head 0, or -1
     auto look_up = [&](int t) {
       place = token_offset(t, pages[page_entry(t, a.cache.page_size, a.pages_per_seq)], a.cache.n_pages,
@@ -238,10 +266,17 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
       return F8 ? __builtin_nontemporal_load(GLOBAL_PTR(const u32x4, at)) : *GLOBAL_PTR(const u32x4, at);
     };
     auto fetch = [&](int j, S& x) {
-      const int t = t0 + j * (NW * STEP);
+      const int t = token_of(j);
       if (WHOLE) {
         // lane 2 i + b: block b of the i-th step from here, 32 steps at a time
-        if (j % 32 == 0) look_up(min(t + (lane >> 1) * (NW * STEP) + (lane & 1) * 16, (end - 1) / 16 * 16));
+        if (WIN) {
+          if (j % 32 == 0) {
+            const int b = token_of(min(j + (lane >> 1), n - 1)) + (lane & 1) * 16, sinks = a.win.sinks;
+            look_up(b >= end || (b >= sinks && b + 16 <= un.from) ? (end - 1) / 16 * 16 : b);
+          }
+        } else if (j % 32 == 0) {
+          look_up(min(t + (lane >> 1) * (NW * STEP) + (lane & 1) * 16, (end - 1) / 16 * 16));
+        }
         const int i = j % 32 * 2;
         const int64_t at[2] = {lane_of(place, i), lane_of(place, i + 1)};
 #pragma unroll
@@ -252,7 +287,8 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
         for (int i = 0; i < VI; ++i)
           x.v[i] = load(vb + at[i * RPI / 16] + (int64_t)(i * RPI % 16) * row_bytes + vofs);
       } else {
-        look_up(min(t + (lane & 31), end - 1));  // past the end: the last token again
+        if (WIN) look_up(hidden(t + (lane & 31)) ? end - 1 : t + (lane & 31));
+        else look_up(min(t + (lane & 31), end - 1));  // past the end: the last token again
         const int lo = (int)(uint32_t)place, hi = (int)(place >> 32);
         auto row = [&](int r) {
           return (int64_t)(((uint64_t)(uint32_t)__shfl(hi, r) << 32) | (uint32_t)__shfl(lo, r));
@@ -269,7 +305,7 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
       }
     };
     auto use = [&](int j, S& x) {
-      const int t = t0 + j * (NW * STEP);
+      const int t = token_of(j);
       f32x4 s[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
       for (int d = 0; d < DS; ++d)
@@ -280,16 +316,16 @@ __global__ __launch_bounds__(64 * NW, DS == 2 ? 3 : 2) void attn_decode(DecodePa
           const u32x4 w = F8 ? (d & 1 ? cvt8(y[2], y[3]) : cvt8(y[0], y[1])) : DS == 2 || d == DS - 1 ? y & in_key[d] : y;
           s[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), q[d], s[b], 0, 0, 0);
         }
-      if (t + STEP > end) {
+      if (t + STEP > end || (WIN && t < un.from)) {
         // rows past the end hold anything: no weight, and zeros, as 0 times anything is not 0
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (t + 16 * b + 4 * g + i >= end) s[b][i] = -INFINITY;
+            if (hidden(t + 16 * b + 4 * g + i)) s[b][i] = -INFINITY;
 #pragma unroll
         for (int i = 0; i < VI; ++i)
-          if (t + i * RPI + lane / VPR >= end) x.v[i] = u32x4{0, 0, 0, 0};
+          if (hidden(t + i * RPI + lane / VPR)) x.v[i] = u32x4{0, 0, 0, 0};
       }
 #pragma unroll
       for (int i = 0; i < VI; ++i) {
@@ -469,7 +505,7 @@ __global__ __launch_bounds__(64 * JW) void attn_decode_join(DecodeParams p) {
 int64_t head_blocks(int32_t H, int32_t G) { return (int64_t)G * ((H / G + COLS - 1) / COLS); }
 int32_t max_ranges(int64_t GQ) { return GQ < ITEMS ? (int32_t)(ITEMS / GQ) : 1; }
 
-template <int DS, bool F8, bool WHOLE>
+template <int DS, bool F8, bool WHOLE, bool WIN>
 hipError_t run(const DecodeArgs& a, hipStream_t s) {
   DecodeParams p{};
   p.a = a;
@@ -485,7 +521,7 @@ hipError_t run(const DecodeArgs& a, hipStream_t s) {
   p.parts_of = reinterpret_cast<int2*>(p.part + 2 * blocks * COLS * a.D);
   if ((int64_t)a.T * a.H > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipError_t e = hipSuccess;
-  if (a.n > 0) e = launch_k(&attn_decode<DS, F8, WHOLE>, dim3((unsigned)blocks), dim3(64 * NW), 0, s, p);
+  if (a.n > 0) e = launch_k(&attn_decode<DS, F8, WHOLE, WIN>, dim3((unsigned)blocks), dim3(64 * NW), 0, s, p);
   if (e == hipSuccess)
     // Few rows: long sequences of many parts, so more waves share them (one sequence of 32520
     // tokens, 8 heads on 1, 127 parts: both kernels 17.1 us with 4 waves, 15.2 with 16)
@@ -499,7 +535,8 @@ template <int DS, bool F8>
 hipError_t run_paged(const DecodeArgs& a, hipStream_t s) {
   // a block's offsets from its place take 32 bits
   const bool whole = a.cache.page_size % 16 == 0 && a.cache.ts < (1 << 26);
-  return whole ? run<DS, F8, true>(a, s) : run<DS, F8, false>(a, s);
+  if (a.win.size) return whole ? run<DS, F8, true, true>(a, s) : run<DS, F8, false, true>(a, s);
+  return whole ? run<DS, F8, true, false>(a, s) : run<DS, F8, false, false>(a, s);
 }
 
 }  // namespace

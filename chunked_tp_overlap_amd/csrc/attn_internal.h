@@ -53,12 +53,20 @@ struct AppendArgs {
 };
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s);
 
+// A row at position t of its sequence sees u <= t with t - u < size, or u < sinks; size 0: all
+// u <= t.
+struct Window {
+  int32_t size, sinks;
+};
+constexpr int32_t kMaxWindow = 1 << 30;  // no row's distance reaches it
+
 struct PromptArgs {
   Heads q, k, v, out;
   float* lse;
   Seqs seqs;
   int32_t H, G, D;
   float scale;
+  Window win;
 };
 hipError_t launch_attn_prompt(const PromptArgs& a, hipStream_t s);
 
@@ -69,10 +77,13 @@ struct PromptBwdArgs {
   int32_t H, G, D;
   float scale;
   void* ws;
+  Window win;
 };
 // Workspace of a call with `rows` rows, and the most any call with up to `rows` rows needs.
 size_t attn_prompt_bwd_need(int32_t H, int32_t G, int32_t D, int64_t rows);
 size_t attn_prompt_bwd_bytes(int32_t H, int32_t G, int32_t D, int64_t rows);
+// What first tokens that stay visible add to it, whatever the window.
+size_t attn_prompt_bwd_sink_bytes(int32_t H, int32_t G, int32_t D, int64_t rows);
 hipError_t launch_attn_prompt_bwd(const PromptBwdArgs& a, hipStream_t s);
 
 struct DecodeArgs {
@@ -87,6 +98,7 @@ struct DecodeArgs {
   int32_t H, G, D;
   float scale;
   void* ws;
+  Window win;
 };
 size_t attn_decode_bytes(int32_t H, int32_t G, int32_t D, int32_t n);
 hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t s);

@@ -72,7 +72,8 @@ struct Shape {
   static constexpr int LDS = KG == 1 || 2 * STAGE > NW * PART + STAT ? 2 * STAGE : NW * PART + STAT;
 };
 
-template <class S>
+// WIN: under a window (a.win); otherwise every earlier key is seen.
+template <class S, bool WIN>
 __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
   constexpr int DS = S::DS, QF = S::QF, KG = S::KG, BN = S::BN, BM = S::BM, TILE = S::TILE;
   using L = Tile<DS>;
@@ -90,7 +91,8 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
   const int q0 = st.tile * BM;
   const int wq0 = q0 + rw * 16 * QF;  // the wave's first query
   const int n_keys = min(q0 + BM, st.len);
-  const int tiles = (n_keys + BN - 1) / BN;
+  const KeyTiles kt = WIN ? key_tiles(q0, BM, BN, n_keys, a.win) : KeyTiles{};
+  const int tiles = WIN ? kt.tiles : (n_keys + BN - 1) / BN;
   const uint16_t* kbase = a.k.p + (int64_t)st.row0 * a.k.rs + kvh * a.k.hs;
   const uint16_t* vbase = a.v.p + (int64_t)st.row0 * a.v.rs + kvh * a.v.hs;
 
@@ -98,7 +100,8 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
   kl.init(rw, lane, a.k.rs, a.D);
   vl.init(rw, lane, a.v.rs, a.D);
   const uint32_t lds = lds_addr(smem) + kg * 2 * TILE;
-  auto load = [&](int j, int stage) {  // rows past the sequence's end read as zeros
+  auto load = [&](int i, int stage) {  // rows past the sequence's end read as zeros
+    const int j = WIN ? kt.at(i) : i;
     kl.issue(kbase + (int64_t)j * BN * a.k.rs, a.k.rs, a.D, st.len - j * BN, lds + stage * S::STAGE, rw);
     vl.issue(vbase + (int64_t)j * BN * a.v.rs, a.v.rs, a.D, st.len - j * BN, lds + stage * S::STAGE + TILE, rw);
   };
@@ -137,14 +140,14 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
       for (int d = 0; d < L::DB; ++d) o[d][f] = f32x4{0, 0, 0, 0};
     }
     if (late) phase_barrier();
-    // DIAGONAL: tiles that may hold keys after one of the workgroup's queries
+    // DIAGONAL: tiles that may hold keys that one of the workgroup's queries does not see
     auto step = [&](int i, auto diagonal) __attribute__((always_inline)) {
       constexpr bool DIAGONAL = decltype(diagonal)::value;
       const int j = i * KG + kg;
       const int stage = (i & 1) * S::STAGE;
       wait_vmcnt_and_barrier<0>();
       if (j + KG < tiles) load(j + KG, (i + 1) & 1);
-      const int k0 = j * BN;
+      const int k0 = (WIN ? kt.at(j) : j) * BN;
       const bool live = KG == 1 || j < tiles;
       f32x4 s[KB][QF];
       if (live) {
@@ -161,16 +164,18 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
             for (int f = 0; f < QF; ++f)
               s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
           }
-        if (DIAGONAL && k0 + BN - 1 > wq0) {
+        if (DIAGONAL && (k0 + BN - 1 > wq0 || (WIN && k0 <= wq0 + 16 * QF - 1 - a.win.size))) {
 #pragma unroll
           for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int f = 0; f < QF; ++f)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (k0 + b * 16 + 4 * g + i > wq0 + f * 16 + col) s[b][f][i] = -INFINITY;
+              for (int i = 0; i < 4; ++i) {
+                const int u = k0 + b * 16 + 4 * g + i, t = wq0 + f * 16 + col;
+                if (WIN ? !seen(u, t, a.win) : u > t) s[b][f][i] = -INFINITY;
+              }
         }
-        if (!FIXED || i == 0) {
+        if (!FIXED || (WIN ? DIAGONAL : i == 0)) {
 #pragma unroll
           for (int f = 0; f < QF; ++f) {
             float x = s[0][f][0];
@@ -179,7 +184,14 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) x = fmaxf(x, s[b][f][i]);
             x = col_max(x);
-            if (FIXED) {
+            if (FIXED && WIN) {
+              // The first of the row's tiles that it sees a key of: all before the first step
+              // without DIAGONAL, and that step, are looked at.
+              const int t = wq0 + f * 16 + col;
+              const bool sees = k0 <= t && (k0 + BN - 1 > t - a.win.size || k0 < a.win.sinks);
+              bad = bad || (m[f] == -INFINITY && x == -INFINITY && sees);
+              m[f] = m[f] == -INFINITY ? x : m[f];
+            } else if (FIXED) {
               // no score, though a key of the tile is not after the query
               bad = bad || (x == -INFINITY && wq0 + f * 16 + col >= k0);
               m[f] = x == -INFINITY ? 0.0f : x;
@@ -198,7 +210,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
       if (!live) return;
 #pragma unroll
       for (int f = 0; f < QF; ++f) {
-        const float base = !FIXED && m[f] == -INFINITY ? 0.0f : m[f] * p.c;
+        const float base = (!FIXED || WIN) && m[f] == -INFINITY ? 0.0f : m[f] * p.c;
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // short sums, so that a long row's l loses little
 #pragma unroll
         for (int b = 0; b < KB; ++b)
@@ -223,7 +235,8 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
           for (int d = 0; d < L::DB; ++d)
 #pragma unroll
             for (int f = 0; f < QF; ++f)
-              o[d][f] = seen_product<true>(vf.read(stage, t, d), pf[t][f], o[d][f], k0 + 32 * t, wq0 + f * 16, lane);
+              o[d][f] = WIN ? seen_product<true>(vf.read(stage, t, d), pf[t][f], o[d][f], k0 + 32 * t, wq0 + f * 16, lane, a.win)
+                            : seen_product<true>(vf.read(stage, t, d), pf[t][f], o[d][f], k0 + 32 * t, wq0 + f * 16, lane);
         return;
       }
 #pragma unroll
@@ -236,8 +249,13 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
             o[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[t][f], o[d][f], 0, 0, 0);
         }
     };
-    const int full = min(q0 / (BN * KG), steps);  // steps of tiles before every query
+    // steps of tiles before every query
+    const int full = WIN ? (q0 / BN - kt.first + kt.sink) / KG : min(q0 / (BN * KG), steps);
     int i = 0;
+    if (WIN) {  // and the first that every row sees whole
+      const int head = min((kt.head + KG - 1) / KG + 1, steps);
+      for (; i < head; ++i) step(i, std::true_type{});
+    }
     for (; i < full; ++i) step(i, std::false_type{});
     for (; i < steps; ++i) step(i, std::true_type{});
     if (KG > 1 && !late) phase_barrier();
@@ -329,12 +347,12 @@ __global__ __launch_bounds__(64 * S::NW, 2) void attn_prompt(PromptParams p) {
   }
 }
 
-template <class S>
+template <class S, bool WIN>
 hipError_t run(const PromptArgs& a, hipStream_t s) {
   const int64_t ranks = max_tiles(a.seqs.T, a.seqs.n, S::BM) + (a.seqs.n == 0);
   if (ranks * a.H > 0x7FFFFFFF) return hipErrorInvalidValue;
   PromptParams p{a, a.scale * LOG2E, (int32_t)ranks};
-  auto kernel = &attn_prompt<S>;
+  auto kernel = &attn_prompt<S, WIN>;
   hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kernel), S::LDS);
   if (e != hipSuccess) return e;
   return launch_k(kernel, dim3((unsigned)(ranks * a.H)), dim3(64 * S::NW), S::LDS, s, p);
@@ -348,8 +366,9 @@ hipError_t choose(const PromptArgs& a, hipStream_t s) {
   // against one: 4096 rows of 8 heads on 8 (8 sequences) 33 and 37 us, 8184 of 4 on 4 (2) 55 and
   // 76; 5120 of 8 on 1 (2) 57 and 55, of 8 on 8 (8) 41 and 43; 6144 of 8 on 1 70 and 65, on 8
   // 53 and 49.
-  if ((int64_t)a.seqs.T * a.H < 44 * 1024 && few_sequences(a.seqs.n, a.H)) return run<Shape<DS, 2, 2, 4, 32>>(a, s);
-  return run<Shape<DS, 2, 4, 1, 64>>(a, s);
+  if ((int64_t)a.seqs.T * a.H < 44 * 1024 && few_sequences(a.seqs.n, a.H))
+    return a.win.size ? run<Shape<DS, 2, 2, 4, 32>, true>(a, s) : run<Shape<DS, 2, 2, 4, 32>, false>(a, s);
+  return a.win.size ? run<Shape<DS, 2, 4, 1, 64>, true>(a, s) : run<Shape<DS, 2, 4, 1, 64>, false>(a, s);
 }
 
 }  // namespace

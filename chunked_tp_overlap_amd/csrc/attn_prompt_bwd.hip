@@ -44,7 +44,71 @@ struct BwdParams {
   float* part;   // [parts, 2, G, T, D] when parts > 1
   int32_t ranks;
   int32_t parts;
+  float* sink_part;      // [slots, 2, G parts, MAX_SINKS, D], see SinkSlots
+  int32_t slots, chunk;  // slots: 0 without first tokens that stay visible
 };
+
+constexpr int MAX_SINKS = UB_ATTN_MAX_SINKS;
+constexpr int MIN_CHUNK = 512;
+
+// The first tokens that stay visible under a window are seen by all later rows: the workgroup of
+// a sequence's first keys would walk all of it where every other walks a window's rows.  It
+// takes the rows up to `rows`, as far as its other keys are seen, and further workgroups take
+// `chunk` rows each.  Their sums for the first tokens go to slots of the workspace, one for the
+// first workgroup and one for each of the others, the sequences' one after another, and
+// attn_bwd_sinks adds them in order.  Where what is left is no longer than MIN_CHUNK the first
+// workgroup takes it all.
+struct SinkSlots {
+  int rows;   // of a sequence's first workgroup, all or a multiple of 32
+  int count;  // slots of the sequence: 0 or 1 + chunks
+};
+__device__ inline SinkSlots sink_slots(int len, int BK, Window win, int chunk) {
+  SinkSlots s;
+  s.rows = min((BK - 1 + win.size + 31) / 32 * 32, len);
+  s.count = 0;
+  if (len - s.rows <= MIN_CHUNK) s.rows = len;
+  else s.count = 1 + (len - s.rows + chunk - 1) / chunk;
+  return s;
+}
+
+__device__ inline int seq_len(const Seqs& s, int i) {
+  return i < s.n ? max(clamp_row(s.cu[i + 1], s.T) - clamp_row(s.cu[i], s.T), 0) : 0;
+}
+
+// Slots of the sequences that start before row `row`.
+__device__ inline int slots_before(const BwdParams& p, int row, int BK) {
+  const Seqs& s = p.a.seqs;
+  int sum = 0;
+  for (int c = 0; c < s.n; c += 64) {
+    const int i = c + (threadIdx.x & 63);
+    if (i < s.n && clamp_row(s.cu[i], s.T) < row) sum += sink_slots(seq_len(s, i), BK, p.a.win, p.chunk).count;
+  }
+  return wave_sum(sum);
+}
+
+// The sequence of slot `slot` and the slot's number there (0: the first workgroup's); len 0: none.
+__device__ inline SeqTile find_slot(const BwdParams& p, int slot, int BK) {
+  const Seqs& s = p.a.seqs;
+  SeqTile r{0, 0, 0};
+  int before = 0;
+  for (int c = 0; c < s.n; c += 64) {
+    const int i = c + (threadIdx.x & 63);
+    const int len = seq_len(s, i);
+    const int n = i < s.n ? sink_slots(len, BK, p.a.win, p.chunk).count : 0;
+    const int incl = wave_scan(n);
+    const uint64_t m = __ballot(before + incl > slot);
+    if (m) {
+      const int at = __builtin_ctzll(m);
+      r.row0 = __builtin_amdgcn_readlane(clamp_row(s.cu[min(i, s.n)], s.T), at);
+      r.len = __builtin_amdgcn_readlane(len, at);
+      r.tile = slot - before - __builtin_amdgcn_readlane(incl - n, at);
+      if (r.tile < 0 || r.tile >= __builtin_amdgcn_readlane(n, at)) r.tile = 0;
+      return r;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return r;
+}
 
 __device__ inline void dma4(i32x4 rsrc, uint32_t lds, uint32_t voffset) {
   __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(voffset),
@@ -134,7 +198,7 @@ __device__ inline bf16x8 rest8(f32x4 a, f32x4 b, bf16x8 hi) {
   return pack8(a, b);
 }
 
-template <class S>
+template <class S, bool WIN>
 __device__ __forceinline__ void bwd_q(const BwdParams& p, int head, int rank, unsigned char* smem) {
   constexpr int DS = S::DS, QF = S::F, NG = S::NG, BN = S::ROWS, BM = S::BM, TILE = S::TILE;
   using L = Tile<DS>;
@@ -150,14 +214,16 @@ __device__ __forceinline__ void bwd_q(const BwdParams& p, int head, int rank, un
   const int q0 = st.tile * BM;
   const int wq0 = q0 + w * 16 * QF;
   const int n_keys = min(q0 + BM, st.len);
-  const int tiles = (n_keys + BN - 1) / BN;
+  const KeyTiles kt = WIN ? key_tiles(q0, BM, BN, n_keys, a.win) : KeyTiles{};
+  const int tiles = WIN ? kt.tiles : (n_keys + BN - 1) / BN;
   const uint16_t* kbase = a.k.p + (int64_t)st.row0 * a.k.rs + kvh * a.k.hs;
   const uint16_t* vbase = a.v.p + (int64_t)st.row0 * a.v.rs + kvh * a.v.hs;
   TileLoad<DS, BN, S::NR> kl, vl;
   kl.init(w, lane, a.k.rs, a.D);
   vl.init(w, lane, a.v.rs, a.D);
   const uint32_t lds = lds_addr(smem) + grp * 2 * TILE;
-  auto load = [&](int j, int stage) {
+  auto load = [&](int i, int stage) {
+    const int j = WIN ? kt.at(i) : i;
     kl.issue(kbase + (int64_t)j * BN * a.k.rs, a.k.rs, a.D, st.len - j * BN, lds + stage * STAGE, w);
     vl.issue(vbase + (int64_t)j * BN * a.v.rs, a.v.rs, a.D, st.len - j * BN, lds + stage * STAGE + TILE, w);
   };
@@ -192,6 +258,9 @@ __device__ __forceinline__ void bwd_q(const BwdParams& p, int head, int rank, un
   rf.init(smem + grp * 2 * TILE, lane);
   cf.init(smem + grp * 2 * TILE, lane);
   f32x4 acc[L::DB][QF];
+  auto product = [&](bf16x8 x, bf16x8 y, f32x4 z, int row, int at) {
+    return WIN ? seen_product<true>(x, y, z, row, at, lane, a.win) : seen_product<true>(x, y, z, row, at, lane);
+  };
   const int steps = (tiles + NG - 1) / NG;
   const bool late = grp >= (NG + 1) / 2;
   // All key tiles, the first of which is being loaded; true if a diagonal one holds values that
@@ -204,7 +273,7 @@ __device__ __forceinline__ void bwd_q(const BwdParams& p, int head, int rank, un
 #pragma unroll
       for (int f = 0; f < QF; ++f) acc[d][f] = f32x4{0, 0, 0, 0};
     if (late) phase_barrier();
-    // DIAGONAL: tiles that may hold keys after one of the workgroup's queries
+    // DIAGONAL: tiles that may hold keys that one of the workgroup's queries does not see
     auto step = [&](int i, auto diagonal) __attribute__((always_inline)) {
       constexpr bool DIAGONAL = decltype(diagonal)::value;
       const int j = i * NG + grp;
@@ -212,7 +281,7 @@ __device__ __forceinline__ void bwd_q(const BwdParams& p, int head, int rank, un
       wait_vmcnt_and_barrier<0>();
       if (j + NG < tiles) load(j + NG, (i + 1) & 1);
       const bool live = NG == 1 || j < tiles;
-      const int k0 = j * BN;
+      const int k0 = (WIN ? kt.at(j) : j) * BN;
       if (!CAREFUL && DIAGONAL && live)
         bad = bad || not_finite<TILE, S::NR>(smem + grp * 2 * TILE + stage, w, lane);
 #pragma unroll
@@ -248,14 +317,16 @@ __device__ __forceinline__ void bwd_q(const BwdParams& p, int head, int rank, un
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               s[b][f][i] = exp2_(s[b][f][i] * p.c - lse2[f]) * (dp[b][f][i] - delta[f]);
-        if (DIAGONAL && k0 + BN - 1 > wq0) {
+        if (DIAGONAL && (k0 + BN - 1 > wq0 || (WIN && k0 <= wq0 + 16 * QF - 1 - a.win.size))) {
 #pragma unroll
           for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int f = 0; f < QF; ++f)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (k0 + t * 32 + b * 16 + 4 * g + i > wq0 + f * 16 + col) s[b][f][i] = 0.0f;
+              for (int i = 0; i < 4; ++i) {
+                const int key = k0 + t * 32 + b * 16 + 4 * g + i, row = wq0 + f * 16 + col;
+                if (WIN ? !seen(key, row, a.win) : key > row) s[b][f][i] = 0.0f;
+              }
         }
         bf16x8 ds[QF], rest[QF];
 #pragma unroll
@@ -268,8 +339,8 @@ __device__ __forceinline__ void bwd_q(const BwdParams& p, int head, int rank, un
           for (int d = 0; d < L::DB; ++d)
 #pragma unroll
             for (int f = 0; f < QF; ++f) {
-              acc[d][f] = seen_product<true>(cf.read(stage, t, d), ds[f], acc[d][f], k0 + t * 32, wq0 + f * 16, lane);
-              acc[d][f] = seen_product<true>(cf.read(stage, t, d), rest[f], acc[d][f], k0 + t * 32, wq0 + f * 16, lane);
+              acc[d][f] = product(cf.read(stage, t, d), ds[f], acc[d][f], k0 + t * 32, wq0 + f * 16);
+              acc[d][f] = product(cf.read(stage, t, d), rest[f], acc[d][f], k0 + t * 32, wq0 + f * 16);
             }
           continue;
         }
@@ -284,8 +355,13 @@ __device__ __forceinline__ void bwd_q(const BwdParams& p, int head, int rank, un
         }
       }
     };
-    const int full = min(q0 / (BN * NG), steps);  // steps of tiles before every query
+    // steps of tiles before every query
+    const int full = WIN ? (q0 / BN - kt.first + kt.sink) / NG : min(q0 / (BN * NG), steps);
     int i = 0;
+    if (WIN) {
+      const int head = min((kt.head + NG - 1) / NG, steps);
+      for (; i < head; ++i) step(i, std::true_type{});
+    }
     for (; i < full; ++i) step(i, std::false_type{});
     for (; i < steps; ++i) step(i, std::true_type{});
     if (NG > 1 && !late) phase_barrier();
@@ -311,8 +387,10 @@ __device__ __forceinline__ void bwd_q(const BwdParams& p, int head, int rank, un
 
 // The values stay in LDS beside the query tiles: with them in registers too, the 128
 // accumulators of 32 keys left too few for the rest.
-template <class S>
-__device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, unsigned char* smem) {
+// WIN, with `slot` >= 0: a chunk of rows beyond a sequence's first workgroup's, for the first tokens
+// alone.
+template <class S, bool WIN>
+__device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, int slot, unsigned char* smem) {
   constexpr int DS = S::DS, KF = S::F, NG = S::NG, BQ = S::ROWS, BK = S::BM, TILE = S::TILE;
   using L = Tile<DS>;
   constexpr int SET = 2 * TILE + 2 * BQ * 4;  // q rows, dout rows, lse2, delta
@@ -321,19 +399,40 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
   static_assert(BQ == 32, "one step of the second products");
   const PromptBwdArgs& a = p.a;
   const int kvh = gp / p.parts, part = gp - kvh * p.parts;
-  if (part == 0) {
+  if (part == 0 && slot < 0) {
     fill_pad(a.dk, a.seqs, a.D, kvh, rank, p.ranks);
     fill_pad(a.dv, a.seqs, a.D, kvh, rank, p.ranks);
   }
-  const SeqTile st = find_tile(a.seqs, BK, rank, true);
+  SeqTile st;
+  if (WIN && slot >= 0) {
+    st = find_slot(p, slot, BK);
+    if (st.tile == 0) return;  // the first workgroup's, or none
+  } else {
+    st = find_tile(a.seqs, BK, rank, true);
+  }
   if (st.len == 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w = wave % S::NR, grp = wave / S::NR;
   const int col = lane & 15, g = lane >> 4;
-  const int k0 = st.tile * BK;
+  const bool sinks = WIN && slot >= 0;
+  const int k0 = sinks ? 0 : st.tile * BK;
   const int wk0 = k0 + w * 16 * KF;
   const int heads = a.H / a.G / p.parts, head0 = kvh * (a.H / a.G) + part * heads;
-  const int qt0 = k0 / BQ, qtiles = (st.len + BQ - 1) / BQ - qt0;
+  // query tiles: from the first key's row to the last row that sees one of the keys
+  int qt0 = k0 / BQ, last = st.len;
+  SinkSlots span{};  // of a sequence's first keys
+  if (WIN) {
+    last = (int)min((int64_t)k0 + BK - 1 + a.win.size, (int64_t)st.len);
+    if (k0 == 0 && a.win.sinks > 0) {
+      span = sink_slots(st.len, BK, a.win, p.chunk);
+      last = span.rows;
+    }
+    if (sinks) {
+      qt0 = (span.rows + (st.tile - 1) * p.chunk) / BQ;
+      last = min(span.rows + st.tile * p.chunk, st.len);
+    }
+  }
+  const int qtiles = (last + BQ - 1) / BQ - qt0;
   const int total = heads * qtiles;
   const int64_t T = a.seqs.T;
   const uint32_t lds = lds_addr(smem);
@@ -341,8 +440,13 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
   ql.init(w, lane, a.q.rs, a.D);
   dl.init(w, lane, a.dout.rs, a.D);
   // The query tiles that may hold rows before one of the workgroup's keys come first, head by
-  // head, then the others: item j of the group's j = grp, grp + NG, ...
-  const int edge = min(BK / BQ, qtiles);
+  // head, then the others: item j of the group's j = grp, grp + NG, ...  Under a window those that
+  // may hold rows which do not see one of the keys any more belong to the first kind: tiles
+  // `tail` and on, of which all are where the first tokens are among the keys.
+  const int diag = sinks ? qtiles : min(BK / BQ, qtiles);
+  const int tail = !WIN || sinks ? qtiles : min(max((int)(((int64_t)k0 + a.win.size) / BQ) - qt0, diag), qtiles);
+  const int edge = diag + qtiles - tail;
+  auto tile_of = [&](int q) { return !WIN ? q : q < diag ? q : q < edge ? q - diag + tail : q - edge + diag; };
   struct Item {
     int h, q, end;  // head, query tile, and where the head's tiles of this kind end
   };
@@ -363,7 +467,7 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
   };
   start();
   auto load = [&](int stage) {
-    const int head = head0 + next.h, r = (qt0 + next.q) * BQ, valid = st.len - r;
+    const int head = head0 + next.h, r = (qt0 + tile_of(next.q)) * BQ, valid = st.len - r;
     const uint32_t at = lds + stage * STAGE + grp * SET;
     const int64_t row = st.row0 + r;
     ql.issue(a.q.p + row * a.q.rs + head * a.q.hs, a.q.rs, a.D, valid, at, w);
@@ -400,6 +504,9 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
   rf.init(smem, lane);
   cf.init(smem, lane);
   f32x4 dk[L::DB][KF], dv[L::DB][KF];
+  auto product = [&](bf16x8 x, bf16x8 y, f32x4 z, int row, int at) {
+    return WIN ? seen_product<false>(x, y, z, row, at, lane, a.win) : seen_product<false>(x, y, z, row, at, lane);
+  };
   const int steps = (total + NG - 1) / NG;
   const bool late = grp >= (NG + 1) / 2;
   // As in bwd_q.  A tile's rows past the sequence's end are zeros, and so are their products, but
@@ -421,8 +528,9 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
       const int stage = (i & 1) * STAGE + grp * SET;
       wait_vmcnt_and_barrier<0>();
       if (j + NG < total) load((i + 1) & 1);
-      const bool live = NG == 1 || j < total;
-      const int q0 = (qt0 + now.q) * BQ;
+      bool live = NG == 1 || j < total;
+      if (WIN && sinks && wk0 >= a.win.sinks) live = false;  // none of the wave's keys
+      const int q0 = (qt0 + tile_of(now.q)) * BQ;
       advance(now, NG);
       const float* rows = reinterpret_cast<const float*>(smem + stage + 2 * TILE);
       f32x4 s[2][KF], dp[2][KF];
@@ -466,14 +574,16 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
             dp[b][f][i] *= s[b][f][i];
           }
       }
-      if (DIAGONAL && q0 < wk0 + 16 * KF - 1) {
+      if (DIAGONAL && (q0 < wk0 + 16 * KF - 1 || (WIN && wk0 <= q0 + BQ - 1 - a.win.size))) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int f = 0; f < KF; ++f)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (wk0 + f * 16 + col > q0 + b * 16 + 4 * g + i) s[b][f][i] = dp[b][f][i] = 0.0f;
+            for (int i = 0; i < 4; ++i) {
+              const int key = wk0 + f * 16 + col, row = q0 + b * 16 + 4 * g + i;
+              if (WIN ? !seen(key, row, a.win) : key > row) s[b][f][i] = dp[b][f][i] = 0.0f;
+            }
       }
       if (CAREFUL && q0 + BQ > st.len) {
 #pragma unroll
@@ -498,9 +608,9 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
         for (int d = 0; d < L::DB; ++d)
 #pragma unroll
           for (int f = 0; f < KF; ++f) {
-            dv[d][f] = seen_product<false>(cf.read(stage + TILE, 0, d), pf[f], dv[d][f], q0, wk0 + f * 16, lane);
-            dk[d][f] = seen_product<false>(cf.read(stage, 0, d), ds[f], dk[d][f], q0, wk0 + f * 16, lane);
-            dk[d][f] = seen_product<false>(cf.read(stage, 0, d), rest[f], dk[d][f], q0, wk0 + f * 16, lane);
+            dv[d][f] = product(cf.read(stage + TILE, 0, d), pf[f], dv[d][f], q0, wk0 + f * 16);
+            dk[d][f] = product(cf.read(stage, 0, d), ds[f], dk[d][f], q0, wk0 + f * 16);
+            dk[d][f] = product(cf.read(stage, 0, d), rest[f], dk[d][f], q0, wk0 + f * 16);
           }
         return;
       }
@@ -542,12 +652,28 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
     join_groups<NG, S::NR>(dk, smem, grp, w, lane);
     join_groups<NG, S::NR>(dv, smem, grp, w, lane);
   }
+  // Sequences that overlap, of boundaries that do not rise, can ask for more slots than there are.
+  const int own_slot = WIN && span.count > 0 && !sinks ? slots_before(p, st.row0, BK) : slot;
+  const bool to_slot = WIN && span.count > 0 && own_slot >= 0 && own_slot < p.slots;
 #pragma unroll
   for (int f = 0; f < KF; ++f) {
     const int u = wk0 + f * 16 + col;
     if (u >= st.len) continue;
     const int64_t row = st.row0 + u;
-    if (p.parts == 1) {
+    if (to_slot && u < a.win.sinks) {
+      float* ok = p.sink_part + (((int64_t)own_slot * 2 * a.G * p.parts + gp) * MAX_SINKS + u) * a.D;
+      float* ov = ok + (int64_t)a.G * p.parts * MAX_SINKS * a.D;
+#pragma unroll
+      for (int i = 0; i < (L::DB + NG - 1) / NG; ++i) {
+        const int e = 16 * (i * NG + grp) + 4 * g;
+        if (e < a.D) {
+          *reinterpret_cast<f32x4*>(ok + e) = dk[i][f];
+          *reinterpret_cast<f32x4*>(ov + e) = dv[i][f];
+        }
+      }
+    } else if (sinks) {
+      continue;
+    } else if (p.parts == 1) {
       uint16_t* ok = a.dk.p + row * a.dk.rs + kvh * a.dk.hs;
       uint16_t* ov = a.dv.p + row * a.dv.rs + kvh * a.dv.hs;
 #pragma unroll
@@ -576,12 +702,43 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, uns
 // Both kinds in one launch, each by falling work, so that the second starts where the last and
 // longest of the first still run.  Measured on an earlier version of the two, 8184 rows of 4 heads on
 // 4 in 5 sequences: 190 us, where a launch for each took 84 and 125; rank by rank in turns 230.
-template <class SQ, class SK>
+template <class SQ, class SK, bool WIN>
 __global__ __launch_bounds__(64 * SQ::NW, 2) void attn_bwd(BwdParams p) {
   extern __shared__ __align__(256) unsigned char smem[];
-  const int H = p.a.H, GP = p.a.G * p.parts, b = blockIdx.x, kv = p.ranks * GP;
-  if (b < kv) bwd_kv<SK>(p, b % GP, b / GP, smem);
-  else bwd_q<SQ>(p, (b - kv) % H, (b - kv) / H, smem);
+  const int H = p.a.H, GP = p.a.G * p.parts, kv = (p.ranks + p.slots) * GP;
+  const int b = blockIdx.x;
+  if (b < kv) {
+    const int rank = b / GP - p.slots;
+    bwd_kv<SK, WIN>(p, b % GP, rank, rank < 0 ? b / GP : -1, smem);
+  } else {
+    bwd_q<SQ, WIN>(p, (b - kv) % H, (b - kv) / H, smem);
+  }
+}
+
+// dk and dv of a sequence's first tokens from their slots, in order; blockIdx: sequence, head, and
+// dk or dv.
+template <int BK>
+__global__ __launch_bounds__(256) void attn_bwd_sinks(BwdParams p) {
+  const PromptBwdArgs& a = p.a;
+  const int which = blockIdx.x & 1, kvh = (blockIdx.x >> 1) % a.G, i = (blockIdx.x >> 1) / a.G;
+  const int len = seq_len(a.seqs, i);
+  const int count = sink_slots(len, BK, a.win, p.chunk).count;
+  if (count == 0) return;
+  const int row0 = clamp_row(a.seqs.cu[i], a.seqs.T);
+  const int64_t slot = slots_before(p, row0, BK);
+  if (slot < 0 || slot + count > p.slots) return;
+  const int64_t GP = a.G * p.parts, step = MAX_SINKS * a.D;
+  const int vec = a.D / 4;
+  const Heads& o = which ? a.dv : a.dk;
+  for (int j = threadIdx.x; j < a.win.sinks * vec; j += 256) {
+    const int u = j / vec, e = (j - u * vec) * 4;
+    f32x4 x = {0, 0, 0, 0};
+    for (int c = 0; c < count; ++c) {
+      const float* at = p.sink_part + (((slot + c) * 2 + which) * GP + kvh * p.parts) * step + u * a.D + e;
+      for (int k = 0; k < p.parts; ++k) x += *reinterpret_cast<const f32x4*>(at + k * step);
+    }
+    store4(o.p + (int64_t)(row0 + u) * o.rs + kvh * o.hs + e, x * (which ? 1.0f : a.scale));
+  }
 }
 
 // dk and dv from their parts, in part order; 8 elements per thread.
@@ -640,7 +797,11 @@ int bwd_parts(int H, int G, int64_t rows, bool small) {
   return parts;
 }
 
-template <class SQ, class SK>
+// Slots that sequences of T rows together can take: each of them has more than MIN_CHUNK rows left.
+int64_t max_slots(int64_t T, int64_t chunk) { return T / chunk + 2 * (T / MIN_CHUNK); }
+int64_t slot_bytes(int G, int parts, int D) { return (int64_t)2 * G * parts * MAX_SINKS * D * 4; }
+
+template <class SQ, class SK, bool WIN>
 hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
   static_assert(SQ::BM == SK::BM && SQ::NW == SK::NW, "one count of tiles, one of waves");
   constexpr int DS = SQ::DS;
@@ -655,14 +816,20 @@ hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
   p.delta = reinterpret_cast<float*>(w + stat);
   p.part = reinterpret_cast<float*>(w + 2 * stat);
   const int64_t ranks = max_tiles(T, a.seqs.n, SQ::BM) + (a.seqs.n == 0);
-  const int64_t blocks = ranks * (a.H + a.G * p.parts);
+  if (WIN && a.win.sinks > 0) {
+    // as many rows as another workgroup of one window takes
+    p.chunk = (int32_t)std::min<int64_t>(std::max<int64_t>(MIN_CHUNK, (a.win.size + 31) / 32 * 32), 1 << 20);
+    p.slots = (int32_t)std::min<int64_t>(max_slots(T, p.chunk), T / p.chunk + 2 * (int64_t)a.seqs.n);
+    p.sink_part = p.part + (p.parts > 1 ? (int64_t)p.parts * 2 * a.G * T * a.D : 0);
+  }
+  const int64_t blocks = ranks * (a.H + a.G * p.parts) + (int64_t)p.slots * a.G * p.parts;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   p.ranks = (int32_t)ranks;
   constexpr int lds_q = std::max(2 * SQ::NG * 2 * SQ::TILE, SQ::JOIN);
   constexpr int lds_kv = std::max(2 * SK::NG * (2 * SK::TILE + 2 * SK::ROWS * 4) + SK::BM * Tile<DS>::RB,
                                   SK::JOIN);
   constexpr int lds = std::max(lds_q, lds_kv);
-  auto kernel = &attn_bwd<SQ, SK>;
+  auto kernel = &attn_bwd<SQ, SK, WIN>;
   hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kernel), lds);
   if (e == hipSuccess && T > 0) {
     auto rows = DS <= 2 ? &attn_bwd_rows<8> : &attn_bwd_rows<16>;
@@ -674,13 +841,25 @@ hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     e = launch_k(&attn_bwd_join, dim3((unsigned)blocks), dim3(256), 0, s, p);
   }
+  if (WIN && e == hipSuccess && p.slots > 0) {
+    const int64_t blocks = 2 * (int64_t)a.G * a.seqs.n;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (blocks > 0) e = launch_k(&attn_bwd_sinks<SK::BM>, dim3((unsigned)blocks), dim3(256), 0, s, p);
+  }
   return e;
 }
 
-template <int DS>
+template <int DS, bool WIN>
 hipError_t choose(const PromptBwdArgs& a, hipStream_t s) {
-  if (grouped(a.H, a.seqs.T, a.seqs.n)) return run<Shape<DS, 2, 4, 32>, Shape<DS, 2, 4, 32>>(a, s);
-  return run<Shape<DS, 4, 1, 64>, Shape<DS, 4, 1, 32>>(a, s);
+  if (grouped(a.H, a.seqs.T, a.seqs.n)) return run<Shape<DS, 2, 4, 32>, Shape<DS, 2, 4, 32>, WIN>(a, s);
+  return run<Shape<DS, 4, 1, 64>, Shape<DS, 4, 1, 32>, WIN>(a, s);
+}
+
+template <bool WIN>
+hipError_t by_dim(const PromptBwdArgs& a, hipStream_t s) {
+  if (a.D <= 64) return choose<2, WIN>(a, s);
+  if (a.D <= 96) return choose<3, WIN>(a, s);
+  return choose<4, WIN>(a, s);
 }
 
 }  // namespace
@@ -700,10 +879,13 @@ size_t attn_prompt_bwd_bytes(int32_t H, int32_t G, int32_t D, int64_t rows) {
   return most;
 }
 
+size_t attn_prompt_bwd_sink_bytes(int32_t H, int32_t G, int32_t D, int64_t rows) {
+  // a call has at most H / G parts
+  return static_cast<size_t>(max_slots(rows, MIN_CHUNK) * slot_bytes(G, H / G, D));
+}
+
 hipError_t launch_attn_prompt_bwd(const PromptBwdArgs& a, hipStream_t s) {
-  if (a.D <= 64) return choose<2>(a, s);
-  if (a.D <= 96) return choose<3>(a, s);
-  return choose<4>(a, s);
+  return a.win.size ? by_dim<true>(a, s) : by_dim<false>(a, s);
 }
 
 }  // namespace ubx

@@ -38,7 +38,9 @@ METHODS = {"ring_exchange": UB_RING_EXCHANGE, "pipeline": UB_PIPELINE, "bulk": U
 UB_REDUCE_ASCENDING, UB_REDUCE_RING = 0, 1
 REDUCE_ORDERS = {"ascending": UB_REDUCE_ASCENDING, "ring": UB_REDUCE_RING}
 UB_ATTN_PROMPT, UB_ATTN_PROMPT_BWD, UB_ATTN_DECODE = 0, 1, 2
+UB_ATTN_PROMPT_WINDOW, UB_ATTN_PROMPT_WINDOW_BWD, UB_ATTN_DECODE_WINDOW = 3, 4, 5
 UB_ATTN_MAX_HEAD_DIM = 128
+UB_ATTN_MAX_SINKS = 64
 
 # Every symbol include/ub.h declares.
 EXPORTS = (
@@ -52,6 +54,7 @@ EXPORTS = (
     "ub_set_kernel_timing", "ub_get_kernel_timing", "ub_prepare_streams", "ub_debug_set",
     "ub_debug_last_plan", "ub_register_scratch", "ub_destroy", "ub_status_string", "ub_last_error",
     "ub_attn_required_bytes", "ub_kv_append", "ub_attn_prompt", "ub_attn_prompt_bwd", "ub_attn_decode",
+    "ub_attn_prompt_window", "ub_attn_prompt_window_bwd", "ub_attn_decode_window",
 )
 
 
@@ -87,6 +90,10 @@ class ub_attn_cfg_t(ctypes.Structure):
                                               "rope_interleaved")] + [("softmax_scale", ctypes.c_float)]
 
 
+class ub_attn_window_t(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
+
+
 class ub_heads_t(ctypes.Structure):
     tensor = held = None  # what heads() describes; the (heads, dim) it was last checked against
     _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
@@ -115,7 +122,7 @@ _P = ctypes.c_void_p
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _CFGP = ctypes.POINTER(ub_overlap_cfg_t)
 
-_ATTNP, _HEADSP, _KVP = (ctypes.POINTER(t) for t in (ub_attn_cfg_t, ub_heads_t, ub_kv_cache_t))
+_ATTNP, _HEADSP, _KVP, _WINP = (ctypes.POINTER(t) for t in (ub_attn_cfg_t, ub_heads_t, ub_kv_cache_t, ub_attn_window_t))
 
 _sig = {
     "ub_overlap_cfg_default": (None, [_CFGP]),
@@ -153,6 +160,10 @@ _sig = {
     "ub_attn_prompt": (_I32, [_H, _HEADSP, _HEADSP, _HEADSP, _HEADSP, _P, _P, _I32, _ATTNP, _P, _SZ, _P]),
     "ub_attn_prompt_bwd": (_I32, [_H] + [_HEADSP] * 5 + [_P] + [_HEADSP] * 3 + [_P, _I32, _ATTNP, _P, _SZ, _P]),
     "ub_attn_decode": (_I32, [_H, _HEADSP, _KVP, _P, _I64, _I32, _P, _I32, _HEADSP, _P, _ATTNP, _P, _SZ, _P]),
+    "ub_attn_prompt_window": (_I32, [_H, _HEADSP, _HEADSP, _HEADSP, _HEADSP, _P, _P, _I32, _WINP, _ATTNP, _P, _SZ, _P]),
+    "ub_attn_prompt_window_bwd": (_I32, [_H] + [_HEADSP] * 5 + [_P] + [_HEADSP] * 3 +
+                                  [_P, _I32, _WINP, _ATTNP, _P, _SZ, _P]),
+    "ub_attn_decode_window": (_I32, [_H, _HEADSP, _KVP, _P, _I64, _I32, _P, _I32, _WINP, _HEADSP, _P, _ATTNP, _P, _SZ, _P]),
     "ub_destroy": (_I32, [_H]),
     "ub_status_string": (ctypes.c_char_p, [_I32]),
     "ub_last_error": (ctypes.c_char_p, [_H]),
@@ -406,6 +417,14 @@ def make_attn_cfg(n_heads, n_kv_heads, head_dim, rotary_dim=None, rope_interleav
     return cfg
 
 
+def make_attn_window(window, sinks=0):
+    """A ``ub_attn_window_t``: a token sees itself, the window - 1 tokens before it and the first
+    ``sinks``."""
+    w = ub_attn_window_t()
+    w.window, w.sinks = min(int(window), 0x7FFFFFFF), int(sinks)
+    return w
+
+
 def heads(x, col=0):
     """A ``ub_heads_t`` over a bf16 device tensor: the heads that start at column ``col`` of a 2-D
     [rows, columns] matrix, head_dim columns each, or a 3-D [rows, heads, head_dim] view with
@@ -578,21 +597,32 @@ def ub_kv_append(h, q, k, v, q_out, k_out, inv_freq, cu_seqlens, past_lens, n_se
         _check(st, h)
 
 
-def ub_attn_prompt(h, q, k, v, out, lse, cu_seqlens, n_seqs, cfg, workspace=None, stream=None):
+def _prompt_args(h, q, k, v, out, lse, cu_seqlens, n_seqs, cfg, workspace):
     D = cfg.head_dim
     H, G = (cfg.n_heads, D), (cfg.n_kv_heads, D)
     for x, layout, what in ((q, H, "q"), (k, G, "k"), (v, G, "v"), (out, H, "out")):
         if x is not None and x.held != layout:
             _hold_heads(x, layout, what)
     ws, ws_bytes = _ws_arg(workspace)
-    st = _lib.ub_attn_prompt(h, q, k, v, out, _lse_arg(lse, h, cfg, out), _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"),
-                             n_seqs, cfg, ws, ws_bytes, _stream(stream))
+    return _lse_arg(lse, h, cfg, out), _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), ws, ws_bytes
+
+
+def ub_attn_prompt(h, q, k, v, out, lse, cu_seqlens, n_seqs, cfg, workspace=None, stream=None):
+    lse, cu, ws, ws_bytes = _prompt_args(h, q, k, v, out, lse, cu_seqlens, n_seqs, cfg, workspace)
+    st = _lib.ub_attn_prompt(h, q, k, v, out, lse, cu, n_seqs, cfg, ws, ws_bytes, _stream(stream))
     if st:
         _check(st, h)
 
 
-def ub_attn_prompt_bwd(h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens, n_seqs, cfg, workspace,
-                       stream=None):
+def ub_attn_prompt_window(h, q, k, v, out, lse, cu_seqlens, n_seqs, window, cfg, workspace=None, stream=None):
+    """window: ``make_attn_window(...)``."""
+    lse, cu, ws, ws_bytes = _prompt_args(h, q, k, v, out, lse, cu_seqlens, n_seqs, cfg, workspace)
+    st = _lib.ub_attn_prompt_window(h, q, k, v, out, lse, cu, n_seqs, window, cfg, ws, ws_bytes, _stream(stream))
+    if st:
+        _check(st, h)
+
+
+def _prompt_bwd_args(h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens, n_seqs, cfg, workspace):
     D = cfg.head_dim
     H, G = (cfg.n_heads, D), (cfg.n_kv_heads, D)
     for x, layout, what in ((dout, H, "dout"), (q, H, "q"), (k, G, "k"), (v, G, "v"), (out, H, "out"), (dq, H, "dq"),
@@ -600,14 +630,27 @@ def ub_attn_prompt_bwd(h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens, n_seq
         if x is not None and x.held != layout:
             _hold_heads(x, layout, what)
     ws, ws_bytes = _ws_arg(workspace)
-    st = _lib.ub_attn_prompt_bwd(h, dout, q, k, v, out, _lse_arg(lse, h, cfg, out), dq, dk, dv,
-                                 _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), n_seqs, cfg, ws, ws_bytes,
-                                 _stream(stream))
+    return _lse_arg(lse, h, cfg, out), _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), ws, ws_bytes
+
+
+def ub_attn_prompt_bwd(h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens, n_seqs, cfg, workspace,
+                       stream=None):
+    lse, cu, ws, ws_bytes = _prompt_bwd_args(h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens, n_seqs, cfg, workspace)
+    st = _lib.ub_attn_prompt_bwd(h, dout, q, k, v, out, lse, dq, dk, dv, cu, n_seqs, cfg, ws, ws_bytes, _stream(stream))
     if st:
         _check(st, h)
 
 
-def ub_attn_decode(h, q, cache, pages, kv_lens, n_seqs, out, lse, cfg, workspace, stream=None):
+def ub_attn_prompt_window_bwd(h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens, n_seqs, window, cfg, workspace,
+                              stream=None):
+    lse, cu, ws, ws_bytes = _prompt_bwd_args(h, dout, q, k, v, out, lse, dq, dk, dv, cu_seqlens, n_seqs, cfg, workspace)
+    st = _lib.ub_attn_prompt_window_bwd(h, dout, q, k, v, out, lse, dq, dk, dv, cu, n_seqs, window, cfg, ws, ws_bytes,
+                                        _stream(stream))
+    if st:
+        _check(st, h)
+
+
+def _hold_cached(q, out, cache, cfg):
     D = cfg.head_dim
     H, G = (cfg.n_heads, D), (cfg.n_kv_heads, D)
     if q is not None and q.held != H:
@@ -616,10 +659,24 @@ def ub_attn_decode(h, q, cache, pages, kv_lens, n_seqs, out, lse, cfg, workspace
         _hold_heads(out, H, "out")
     if cache is not None and cache.held != G:
         _hold_cache(cache, G)
+
+
+def ub_attn_decode(h, q, cache, pages, kv_lens, n_seqs, out, lse, cfg, workspace, stream=None):
+    _hold_cached(q, out, cache, cfg)
     table, ld, per_seq = _table(pages, n_seqs)
     ws, ws_bytes = _ws_arg(workspace)
     st = _lib.ub_attn_decode(h, q, cache, table, ld, per_seq, _int32(kv_lens, n_seqs, "kv_lens"), n_seqs, out,
                              _lse_arg(lse, h, cfg, out), cfg, ws, ws_bytes, _stream(stream))
+    if st:
+        _check(st, h)
+
+
+def ub_attn_decode_window(h, q, cache, pages, kv_lens, n_seqs, window, out, lse, cfg, workspace, stream=None):
+    _hold_cached(q, out, cache, cfg)
+    table, ld, per_seq = _table(pages, n_seqs)
+    ws, ws_bytes = _ws_arg(workspace)
+    st = _lib.ub_attn_decode_window(h, q, cache, table, ld, per_seq, _int32(kv_lens, n_seqs, "kv_lens"), n_seqs, window,
+                                    out, _lse_arg(lse, h, cfg, out), cfg, ws, ws_bytes, _stream(stream))
     if st:
         _check(st, h)
 

@@ -473,6 +473,7 @@ UB_API ub_status_t ub_reduce_partials(ub_handle_t h, void* out, int64_t ldo,
  *   ub_attn_prompt     causal attention within each packed sequence
  *   ub_attn_prompt_bwd its gradient
  *   ub_attn_decode     attention of one new token per sequence over the paged cache
+ *   ub_attn_*_window   the three attention calls under a sliding window
  *
  * Rows.  Every call works on the handle's active rows T (ub_set_active_shape): T rows of
  * every matrix, of which the packed sequences use a prefix.  Sequence i holds rows
@@ -498,6 +499,8 @@ UB_API ub_status_t ub_reduce_partials(ub_handle_t h, void* out, int64_t ldo,
  * on timing.
  */
 #define UB_ATTN_MAX_HEAD_DIM 128
+/* Most first tokens that a window leaves visible. */
+#define UB_ATTN_MAX_SINKS 64
 
 typedef struct {
   int32_t n_heads;          /* query heads of this rank, >= 1 */
@@ -542,6 +545,9 @@ typedef enum {
   UB_ATTN_PROMPT = 0,
   UB_ATTN_PROMPT_BWD = 1,
   UB_ATTN_DECODE = 2,
+  UB_ATTN_PROMPT_WINDOW = 3,
+  UB_ATTN_PROMPT_WINDOW_BWD = 4,
+  UB_ATTN_DECODE_WINDOW = 5,
   UB_ATTN_OP_INT32_RANGE_ = 0x7FFFFFFF
 } ub_attn_op_t;
 
@@ -618,6 +624,46 @@ UB_API ub_status_t ub_attn_decode(ub_handle_t h, const ub_heads_t* q, const ub_k
                                   int32_t pages_per_seq, const int32_t* kv_lens, int32_t n_seqs,
                                   const ub_heads_t* out, float* lse, const ub_attn_cfg_t* cfg,
                                   void* workspace, size_t workspace_bytes, ub_stream_t stream);
+
+/* ---- Attention with a sliding window -----------------------------------------------------
+ *
+ * A token at position t of its sequence sees the tokens u <= t with t - u < window, and the
+ * first `sinks` tokens (of which it sees those up to itself).  Everything else is as for the
+ * call without a window: rows, layouts, workspaces (ub_attn_required_bytes of the window's own
+ * op), padding, what is not seen does not matter.  A window of T or more (of a sequence's
+ * length, in decode) sees what the call without one does. */
+typedef struct {
+  int32_t window; /* >= 1: a token sees itself and window - 1 before it */
+  int32_t sinks;  /* 0 .. UB_ATTN_MAX_SINKS */
+} ub_attn_window_t;
+
+UB_API ub_status_t ub_attn_prompt_window(ub_handle_t h, const ub_heads_t* q, const ub_heads_t* k,
+                                         const ub_heads_t* v, const ub_heads_t* out, float* lse,
+                                         const int32_t* cu_seqlens, int32_t n_seqs,
+                                         const ub_attn_window_t* window,
+                                         const ub_attn_cfg_t* cfg, void* workspace,
+                                         size_t workspace_bytes, ub_stream_t stream);
+
+/* Gradient of ub_attn_prompt_window with the same window. */
+UB_API ub_status_t ub_attn_prompt_window_bwd(ub_handle_t h, const ub_heads_t* dout,
+                                             const ub_heads_t* q, const ub_heads_t* k,
+                                             const ub_heads_t* v, const ub_heads_t* out,
+                                             const float* lse, const ub_heads_t* dq,
+                                             const ub_heads_t* dk, const ub_heads_t* dv,
+                                             const int32_t* cu_seqlens, int32_t n_seqs,
+                                             const ub_attn_window_t* window,
+                                             const ub_attn_cfg_t* cfg, void* workspace,
+                                             size_t workspace_bytes, ub_stream_t stream);
+
+/* ub_attn_decode of a token at position kv_lens[i] - 1.  Table entries of pages that hold no
+ * visible token are not read: such pages may have been given back (ub_kv_resize). */
+UB_API ub_status_t ub_attn_decode_window(ub_handle_t h, const ub_heads_t* q,
+                                         const ub_kv_cache_t* cache, const int32_t* page_table,
+                                         int64_t pages_ld, int32_t pages_per_seq,
+                                         const int32_t* kv_lens, int32_t n_seqs,
+                                         const ub_attn_window_t* window, const ub_heads_t* out,
+                                         float* lse, const ub_attn_cfg_t* cfg, void* workspace,
+                                         size_t workspace_bytes, ub_stream_t stream);
 
 /* Per-launch kernel timing.  enable 1: every GEMM and reduction launch is bracketed by HIP
  * events on the stream it is launched on: a start event recorded before it, and an end
