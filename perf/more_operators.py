@@ -279,6 +279,8 @@ def _handles(s):
     s["buf"] = torch.empty(rows * H * D, dtype=BF16, device="cuda")
     s["h"] = ub.ub_init(rows, H * D, 1, ub.UB_DTYPE_BF16, s["buf"], rows * H * D * 2)
     s["cfg"] = ub.make_attn_cfg(H, G, D, rotary_dim=_rotary(c))
+    if kind in ("tree", "commit"):  # a value for each active row, those of no sequence too
+        s["row_parents"], s["row_depths"] = (torch.nn.functional.pad(s[x], (0, rows - s["nodes"])) for x in ("parents", "depths"))
     if "window" in c:
         s["win"] = ub.make_attn_window(c["window"], c["sinks"])
     s["hout"] = ub.heads(s["out"])
@@ -327,11 +329,11 @@ def _own(s, kind):
                                  s["ws"], stream)
         return {"out": s["out"], "lse": s["lse"]}
     if kind == "tree":
-        ub.ub_attn_tree(h, s["hq"], s["cache"], s["pages"], s["full"], s["parents"], s["cu"], s["n"], s["hout"], s["lse"],
+        ub.ub_attn_tree(h, s["hq"], s["cache"], s["pages"], s["full"], s["row_parents"], s["cu"], s["n"], s["hout"], s["lse"],
                         cfg, s["ws"], stream)
         return {"out": s["out"], "lse": s["lse"]}
     if kind == "commit":
-        ub.ub_kv_append_at(h, s["hq"], s["hk"], s["hv"], s["hout"], None, s["inv_freq"], s["depths"], s["cu"], s["lens"],
+        ub.ub_kv_append_at(h, s["hq"], s["hk"], s["hv"], s["hout"], None, s["inv_freq"], s["row_depths"], s["cu"], s["lens"],
                            s["n"], s["cache"], s["pages"], cfg, stream)
         ub.ub_kv_compact(h, s["cache"], s["pages"], s["lens"], s["kept"], s["kept_lens"], s["n"], s["lens_out"], cfg, stream)
         return {"q": s["out"], "k_cache": s["k_cache"], "v_cache": s["v_cache"], "lens": s["lens_out"]}
