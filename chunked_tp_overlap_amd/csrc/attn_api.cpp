@@ -285,20 +285,22 @@ UB_API ub_status_t ub_attn_required_bytes(ub_attn_op_t op, const ub_attn_cfg_t* 
     case UB_ATTN_DECODE_WINDOW:
       *bytes = ubx::attn_decode_bytes(cfg->n_heads, cfg->n_kv_heads, cfg->head_dim, n_seqs);
       return UB_OK;
+    case UB_ATTN_TREE:
+      *bytes = ubx::attn_tree_bytes(cfg->n_heads, cfg->n_kv_heads, cfg->head_dim, rows, n_seqs);
+      return UB_OK;
     default:
       return UB_ERR_INVALID_ARG;
   }
 }
 
-UB_API ub_status_t ub_kv_append(ub_handle_t h, const ub_heads_t* q, const ub_heads_t* k,
-                                const ub_heads_t* v, const ub_heads_t* q_out,
-                                const ub_heads_t* k_out, const float* inv_freq,
-                                const int32_t* cu_seqlens, const int32_t* past_lens,
-                                int32_t n_seqs, const ub_kv_cache_t* kv,
-                                const int32_t* page_table, int64_t pages_ld,
-                                int32_t pages_per_seq, const ub_attn_cfg_t* cfg,
-                                ub_stream_t stream) {
-  const TraceRange range("ub_kv_append");
+namespace {
+ub_status_t append(const char* name, ub_handle_t h, const ub_heads_t* q, const ub_heads_t* k,
+                   const ub_heads_t* v, const ub_heads_t* q_out, const ub_heads_t* k_out,
+                   const float* inv_freq, bool at, const int32_t* offsets,
+                   const int32_t* cu_seqlens, const int32_t* past_lens, int32_t n_seqs,
+                   const ub_kv_cache_t* kv, const int32_t* page_table, int64_t pages_ld,
+                   int32_t pages_per_seq, const ub_attn_cfg_t* cfg, ub_stream_t stream) {
+  const TraceRange range(name);
   if (!h) return UB_ERR_NOT_INITIALIZED;
   return guarded([&] {
     Checks c{h};
@@ -323,6 +325,8 @@ UB_API ub_status_t ub_kv_append(ub_handle_t h, const ub_heads_t* q, const ub_hea
     c.need(a.rotary == 0 || inv_freq != nullptr, "inv_freq is NULL");
     a.inv_freq = inv_freq;
     a.past = past_lens;
+    c.need(!at || offsets != nullptr, "offsets is NULL");
+    a.offsets = offsets;
     if (kv) a.cache = cache(c, kv, page_table, pages_ld, pages_per_seq, n_seqs, cfg);
     a.pages = page_table;
     a.pages_ld = pages_ld;
@@ -330,7 +334,212 @@ UB_API ub_status_t ub_kv_append(ub_handle_t h, const ub_heads_t* q, const ub_hea
     if (c.st != UB_OK) return c.st;
     ub_status_t st = ubx::ctx_bind(h);
     if (st != UB_OK) return st;
-    return launched(h, ubx::launch_kv_append(a, static_cast<hipStream_t>(stream)), "ub_kv_append");
+    return launched(h, ubx::launch_kv_append(a, static_cast<hipStream_t>(stream)), name);
+  });
+}
+
+// A table of pages by itself (without a cache).
+ubx::Table table(Checks& c, const char* name, const int32_t* p, int64_t ld, int32_t per, int32_t n) {
+  const std::string s(name);
+  if (n < 0) c.bad(UB_ERR_INVALID_ARG, s + ": the number of rows must be >= 0");
+  if (n > 0 && !p) c.bad(UB_ERR_INVALID_ARG, s + " is NULL");
+  if (per < 1 || ld < per) c.bad(UB_ERR_INVALID_ARG, s + ": entries per row must be >= 1 and the row stride >= that");
+  return ubx::Table{const_cast<int32_t*>(p), ld, per, n};
+}
+
+void pool(Checks& c, const int32_t* refs, int64_t n_pages, int32_t page_size) {
+  c.need(refs != nullptr && aligned16(refs), "refs must be non-NULL and 16-byte aligned");
+  c.need(n_pages >= 1 && n_pages <= INT32_MAX, "n_pages must be in [1, 2^31)");
+  c.need(page_size >= 1, "page_size must be >= 1");
+}
+}  // namespace
+
+UB_API ub_status_t ub_kv_append(ub_handle_t h, const ub_heads_t* q, const ub_heads_t* k,
+                                const ub_heads_t* v, const ub_heads_t* q_out,
+                                const ub_heads_t* k_out, const float* inv_freq,
+                                const int32_t* cu_seqlens, const int32_t* past_lens,
+                                int32_t n_seqs, const ub_kv_cache_t* kv,
+                                const int32_t* page_table, int64_t pages_ld,
+                                int32_t pages_per_seq, const ub_attn_cfg_t* cfg,
+                                ub_stream_t stream) {
+  return append("ub_kv_append", h, q, k, v, q_out, k_out, inv_freq, false, nullptr, cu_seqlens, past_lens,
+                n_seqs, kv, page_table, pages_ld, pages_per_seq, cfg, stream);
+}
+
+UB_API ub_status_t ub_kv_append_at(ub_handle_t h, const ub_heads_t* q, const ub_heads_t* k,
+                                   const ub_heads_t* v, const ub_heads_t* q_out,
+                                   const ub_heads_t* k_out, const float* inv_freq,
+                                   const int32_t* offsets, const int32_t* cu_seqlens,
+                                   const int32_t* past_lens, int32_t n_seqs,
+                                   const ub_kv_cache_t* kv, const int32_t* page_table,
+                                   int64_t pages_ld, int32_t pages_per_seq,
+                                   const ub_attn_cfg_t* cfg, ub_stream_t stream) {
+  return append("ub_kv_append_at", h, q, k, v, q_out, k_out, inv_freq, true, offsets, cu_seqlens, past_lens,
+                n_seqs, kv, page_table, pages_ld, pages_per_seq, cfg, stream);
+}
+
+UB_API ub_status_t ub_attn_tree(ub_handle_t h, const ub_heads_t* q, const ub_kv_cache_t* kv,
+                                const int32_t* page_table, int64_t pages_ld,
+                                int32_t pages_per_seq, const int32_t* kv_lens,
+                                const int32_t* parents, const int32_t* cu_seqlens, int32_t n_seqs,
+                                const ub_heads_t* out, float* lse, const ub_attn_cfg_t* cfg,
+                                void* ws, size_t ws_bytes, ub_stream_t stream) {
+  const TraceRange range("ub_attn_tree");
+  if (!h) return UB_ERR_NOT_INITIALIZED;
+  return guarded([&] {
+    Checks c{h};
+    check_cfg(c, cfg);
+    if (c.st != UB_OK) return c.st;
+    const int64_t T = ubx::ctx_rows(h);
+    ubx::TreeArgs a{};
+    a.H = cfg->n_heads;
+    a.G = cfg->n_kv_heads;
+    a.D = cfg->head_dim;
+    a.scale = cfg->softmax_scale;
+    a.q = heads(c, "q", q, a.H, T, cfg);
+    a.out = heads(c, "out", out, a.H, T, cfg);
+    a.lse = lse;
+    a.seqs = seqs(c, cu_seqlens, n_seqs, T);
+    c.need(n_seqs == 0 || kv_lens != nullptr, "kv_lens is NULL");
+    c.need(n_seqs == 0 || parents != nullptr, "parents is NULL");
+    a.cache = cache(c, kv, page_table, pages_ld, pages_per_seq, n_seqs, cfg);
+    a.pages = page_table;
+    a.pages_ld = pages_ld;
+    a.pages_per_seq = pages_per_seq;
+    a.lens = kv_lens;
+    a.parents = parents;
+    if (c.st == UB_OK) workspace(c, ws, ws_bytes, ubx::attn_tree_bytes(a.H, a.G, a.D, T, n_seqs));
+    a.ws = ws;
+    if (c.st != UB_OK) return c.st;
+    ub_status_t st = ubx::ctx_bind(h);
+    if (st != UB_OK) return st;
+    return launched(h, ubx::launch_attn_tree(a, static_cast<hipStream_t>(stream)), "ub_attn_tree");
+  });
+}
+
+UB_API ub_status_t ub_kv_compact(ub_handle_t h, const ub_kv_cache_t* kv, const int32_t* page_table,
+                                 int64_t pages_ld, int32_t pages_per_seq, const int32_t* lens,
+                                 const int32_t* kept, int64_t kept_ld, int32_t kept_per_seq,
+                                 const int32_t* kept_lens, int32_t n_seqs, int32_t* lens_out,
+                                 const ub_attn_cfg_t* cfg, ub_stream_t stream) {
+  const TraceRange range("ub_kv_compact");
+  if (!h) return UB_ERR_NOT_INITIALIZED;
+  return guarded([&] {
+    Checks c{h};
+    check_cfg(c, cfg);
+    if (c.st != UB_OK) return c.st;
+    c.need(n_seqs >= 0, "n_seqs must be >= 0");
+    ubx::CompactArgs a{};
+    a.G = cfg->n_kv_heads;
+    a.D = cfg->head_dim;
+    a.cache = cache(c, kv, page_table, pages_ld, pages_per_seq, n_seqs, cfg);
+    a.pages = page_table;
+    a.pages_ld = pages_ld;
+    a.pages_per_seq = pages_per_seq;
+    c.need(n_seqs == 0 || (lens && kept_lens && lens_out), "lens, kept_lens or lens_out is NULL");
+    c.need(n_seqs == 0 || lens != lens_out, "lens_out must not be lens");
+    c.need(n_seqs == 0 || kept_per_seq == 0 || kept != nullptr, "kept is NULL");
+    c.need(kept_per_seq >= 0 && kept_ld >= kept_per_seq, "kept_per_seq must be >= 0 and kept_ld >= kept_per_seq");
+    a.lens = lens;
+    a.kept = kept;
+    a.kept_ld = kept_ld;
+    a.most = kept_per_seq;
+    a.kept_lens = kept_lens;
+    a.lens_out = lens_out;
+    a.n = n_seqs;
+    if (c.st != UB_OK) return c.st;
+    ub_status_t st = ubx::ctx_bind(h);
+    if (st != UB_OK) return st;
+    return launched(h, ubx::launch_kv_compact(a, static_cast<hipStream_t>(stream)), "ub_kv_compact");
+  });
+}
+
+UB_API ub_status_t ub_kv_fork(ub_handle_t h, int32_t* refs, int64_t n_pages,
+                              const int32_t* page_table, int64_t pages_ld, int32_t pages_per_seq,
+                              const int32_t* lens, int32_t n_seqs, const int32_t* parents,
+                              int32_t* table_out, int64_t out_ld, int32_t out_per_seq,
+                              int32_t* lens_out, int32_t n_out, int32_t page_size,
+                              ub_stream_t stream) {
+  const TraceRange range("ub_kv_fork");
+  if (!h) return UB_ERR_NOT_INITIALIZED;
+  return guarded([&] {
+    Checks c{h};
+    pool(c, refs, n_pages, page_size);
+    ubx::ForkArgs a{};
+    a.refs = refs;
+    a.n_pages = static_cast<int32_t>(n_pages);
+    a.page = page_size;
+    a.in = table(c, "page_table", page_table, pages_ld, pages_per_seq, n_seqs);
+    a.out = table(c, "table_out", table_out, out_ld, out_per_seq, n_out);
+    c.need(n_seqs <= 0 || lens != nullptr, "lens is NULL");
+    c.need(n_out <= 0 || (parents && lens_out), "parents or lens_out is NULL");
+    c.need(out_per_seq >= pages_per_seq, "out_per_seq must be >= pages_per_seq");
+    c.need(!page_table || page_table != table_out, "table_out must not be page_table");
+    c.need(!lens || lens != lens_out, "lens_out must not be lens");
+    a.lens = lens;
+    a.parents = parents;
+    a.lens_out = lens_out;
+    if (c.st != UB_OK) return c.st;
+    ub_status_t st = ubx::ctx_bind(h);
+    if (st != UB_OK) return st;
+    return launched(h, ubx::launch_kv_fork(a, static_cast<hipStream_t>(stream)), "ub_kv_fork");
+  });
+}
+
+UB_API ub_status_t ub_kv_resize_bytes(int32_t n_seqs, size_t* bytes) {
+  if (!bytes || n_seqs < 0) return UB_ERR_INVALID_ARG;
+  *bytes = ubx::kv_resize_bytes(n_seqs);
+  return UB_OK;
+}
+
+UB_API ub_status_t ub_kv_resize(ub_handle_t h, int32_t* refs, int64_t n_pages, int32_t* page_table,
+                                int64_t pages_ld, int32_t pages_per_seq, const int32_t* lens,
+                                const int32_t* new_lens, int32_t n_seqs, int32_t* lens_out,
+                                int32_t* copies, int32_t page_size, const ub_attn_window_t* win,
+                                void* ws, size_t ws_bytes, ub_stream_t stream) {
+  const TraceRange range("ub_kv_resize");
+  if (!h) return UB_ERR_NOT_INITIALIZED;
+  return guarded([&] {
+    Checks c{h};
+    pool(c, refs, n_pages, page_size);
+    ubx::ResizeArgs a{};
+    a.refs = refs;
+    a.n_pages = static_cast<int32_t>(n_pages);
+    a.page = page_size;
+    a.table = table(c, "page_table", page_table, pages_ld, pages_per_seq, n_seqs);
+    c.need(n_seqs <= 0 || (lens && new_lens && lens_out && copies), "lens, new_lens, lens_out or copies is NULL");
+    c.need(n_seqs <= 0 || new_lens != lens_out, "lens_out must not be new_lens");
+    a.lens = lens;
+    a.new_lens = new_lens;
+    a.lens_out = lens_out;
+    a.copies = copies;
+    if (win) a.win = window(c, win);
+    if (c.st == UB_OK) workspace(c, ws, ws_bytes, ubx::kv_resize_bytes(n_seqs));
+    a.ws = ws;
+    if (c.st != UB_OK) return c.st;
+    ub_status_t st = ubx::ctx_bind(h);
+    if (st != UB_OK) return st;
+    return launched(h, ubx::launch_kv_resize(a, static_cast<hipStream_t>(stream)), "ub_kv_resize");
+  });
+}
+
+UB_API ub_status_t ub_kv_copy_pages(ub_handle_t h, const ub_kv_cache_t* kv, const int32_t* copies,
+                                    int32_t n, const ub_attn_cfg_t* cfg, ub_stream_t stream) {
+  const TraceRange range("ub_kv_copy_pages");
+  if (!h) return UB_ERR_NOT_INITIALIZED;
+  return guarded([&] {
+    Checks c{h};
+    check_cfg(c, cfg);
+    if (c.st != UB_OK) return c.st;
+    c.need(n >= 0, "n must be >= 0");
+    c.need(n == 0 || copies != nullptr, "copies is NULL");
+    const ubx::KvCache x = cache(c, kv, copies, 1, 1, n, cfg);
+    if (c.st != UB_OK) return c.st;
+    ub_status_t st = ubx::ctx_bind(h);
+    if (st != UB_OK) return st;
+    return launched(h, ubx::launch_kv_copy_pages(x, cfg->n_kv_heads, cfg->head_dim, copies, n,
+                                                 static_cast<hipStream_t>(stream)),
+                    "ub_kv_copy_pages");
   });
 }
 

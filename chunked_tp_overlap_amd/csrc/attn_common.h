@@ -415,6 +415,43 @@ inline bool few_sequences(int64_t n, int H) { return n * H < 96; }
 // Tiles of bm rows that n sequences of T rows together can have.
 inline int64_t max_tiles(int64_t T, int64_t n, int bm) { return T / bm + (n < T ? n : T); }
 
+__device__ inline uint32_t cvt2(uint32_t w, bool high) {
+  const auto r = high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
+                      : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// 8 E4M3 codes -> 8 bf16 (exact).
+__device__ inline u32x4 cvt8(uint32_t a, uint32_t b) {
+  return u32x4{cvt2(a, false), cvt2(a, true), cvt2(b, false), cvt2(b, true)};
+}
+
+__device__ inline int64_t lane_of(int64_t x, int lane) {  // uniform lane
+  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), lane) << 32) |
+                   (uint32_t)__builtin_amdgcn_readlane((int)x, lane));
+}
+
+// S units of work dealt in W equal contiguous ranges: the first `more` hold q + 1, the others q.
+struct Deal {
+  int64_t S, q;
+  int W, more;
+  __device__ void init(int64_t total, int ranges) {
+    S = total;
+    W = ranges;
+    q = W > 0 ? div(S, W) : 0;
+    more = (int)(S - q * W);
+  }
+  __device__ int64_t begin(int w) const { return w * q + min(w, more); }
+  __device__ int range_of(int64_t unit) const {
+    const int64_t big = more * (q + 1);
+    return unit < big ? (int)div(unit, q + 1) : more + (int)div(unit - big, q);
+  }
+  // a >= 0, b > 0; in 64 bits only where it takes them
+  __device__ static int64_t div(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+  }
+};
+
 // Whether row t lies in no sequence: before the first or after the last.
 __device__ inline int first_row(const Seqs& s) { return s.n > 0 ? clamp_row(s.cu[0], s.T) : s.T; }
 __device__ inline int last_row(const Seqs& s) { return s.n > 0 ? clamp_row(s.cu[s.n], s.T) : s.T; }

@@ -71,31 +71,14 @@ __device__ inline Units units(int len, Window win) {
   return u;
 }
 
-// All n sequences' units, S, dealt in W ranges: the first `more` hold q + 1 units, the others q.
-// A range takes MIN_UNITS units at least, unless sequences are shorter: each that a range
+// Ranges for S units of n sequences.  A range takes MIN_UNITS units at least, unless sequences are shorter: each that a range
 // covers costs it a chain of loads and a join of its waves, some 3 us, so that there are 4 n
 // ranges if there can be.  Measured with 0, n, 2 n and 4 n: 23 sequences of up to 3 tokens, 8 heads
 // on 1 35, 13, 13, 13 us; 64 of 20 to 200 29, 23, 18, 18; 160 of 50 to 500, 16 heads on 1 33, 33, 35,
 // 30.
-struct Deal {
-  int64_t S, q;
-  int W, more;
-  __device__ void init(int64_t total, int n, int ranges) {
-    S = total;
-    W = (int)min((int64_t)ranges, max((S + MIN_UNITS - 1) / MIN_UNITS, min(S, 4 * (int64_t)n)));
-    q = W > 0 ? div(S, W) : 0;
-    more = (int)(S - q * W);
-  }
-  __device__ int64_t begin(int w) const { return w * q + min(w, more); }
-  __device__ int range_of(int64_t unit) const {
-    const int64_t big = more * (q + 1);
-    return unit < big ? (int)div(unit, q + 1) : more + (int)div(unit - big, q);
-  }
-  // a >= 0, b > 0; in 64 bits only where it takes them
-  __device__ static int64_t div(int64_t a, int64_t b) {
-    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-  }
-};
+__device__ inline int ranges_of(int64_t S, int n, int most) {
+  return (int)min((int64_t)most, max((S + MIN_UNITS - 1) / MIN_UNITS, min(S, 4 * (int64_t)n)));
+}
 
 // Units of sequences c + lane, up to 2^25 each: 64 of them fit 32 unsigned bits.
 template <bool WIN>
@@ -110,7 +93,7 @@ __device__ inline Deal deal_units(const DecodeParams& p, uint32_t head) {
   int64_t S = (uint32_t)wave_sum((int)head);
   for (int c = 64; c < p.a.n; c += 64) S += (uint32_t)wave_sum((int)units_of<WIN>(p, c));
   Deal d;
-  d.init(S, p.a.n, p.ranges);
+  d.init(S, ranges_of(S, p.a.n, p.ranges));
   return d;
 }
 
@@ -132,17 +115,6 @@ __device__ inline int find_sequence(const DecodeParams& p, uint32_t head, int64_
   return p.a.n;
 }
 
-__device__ inline uint32_t cvt2(uint32_t w, bool high) {
-  const auto r = high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
-                      : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
-  return __builtin_bit_cast(uint32_t, r);
-}
-
-// 8 E4M3 codes -> 8 bf16 (exact).
-__device__ inline u32x4 cvt8(uint32_t a, uint32_t b) {
-  return u32x4{cvt2(a, false), cvt2(a, true), cvt2(b, false), cvt2(b, true)};
-}
-
 template <int DS, bool F8>
 struct Layout {
   static constexpr int EB = F8 ? 1 : 2;                                      // bytes per element
@@ -157,11 +129,6 @@ template <int DS, bool F8>
 struct Step {
   u32x4 k[2][Layout<DS, F8>::KV], v[Layout<DS, F8>::VI];
 };
-
-__device__ inline int64_t lane_of(int64_t x, int lane) {  // uniform lane
-  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), lane) << 32) |
-                   (uint32_t)__builtin_amdgcn_readlane((int)x, lane));
-}
 
 // WHOLE: pages of a multiple of 16 tokens, so that a block of 16 tokens lies in one page: its
 // place is uniform over the wave, and its rows' offsets from there are the same in all steps.

@@ -44,6 +44,7 @@ struct AppendArgs {
   const float* inv_freq;
   Seqs seqs;
   const int32_t* past;
+  const int32_t* offsets;  // a row's position for the rotation, from past; nullptr: its place
   KvCache cache;  // k == nullptr: no append
   const int32_t* pages;
   int64_t pages_ld;
@@ -102,5 +103,70 @@ struct DecodeArgs {
 };
 size_t attn_decode_bytes(int32_t H, int32_t G, int32_t D, int32_t n);
 hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t s);
+
+// The page operations (kv_manage.hip).  A table of n rows of `per` entries, ld apart.
+struct Table {
+  int32_t* p;
+  int64_t ld;
+  int32_t per, n;
+};
+struct ForkArgs {
+  int32_t* refs;
+  int32_t n_pages, page;
+  Table in, out;
+  const int32_t* lens;
+  const int32_t* parents;
+  int32_t* lens_out;
+};
+hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s);
+
+struct ResizeArgs {
+  int32_t* refs;
+  int32_t n_pages, page;
+  Table table;
+  const int32_t* lens;
+  const int32_t* new_lens;
+  int32_t* lens_out;
+  int32_t* copies;  // [n, 3]
+  Window win;       // size 0: none
+  void* ws;
+};
+size_t kv_resize_bytes(int32_t n);
+hipError_t launch_kv_resize(const ResizeArgs& a, hipStream_t s);
+
+hipError_t launch_kv_copy_pages(const KvCache& c, int32_t G, int32_t D, const int32_t* copies, int32_t n,
+                                hipStream_t s);
+
+struct CompactArgs {
+  KvCache cache;
+  const int32_t* pages;
+  int64_t pages_ld;
+  int32_t pages_per_seq;
+  const int32_t* lens;
+  const int32_t* kept;
+  int64_t kept_ld;
+  int32_t most;  // entries of a row of `kept`
+  const int32_t* kept_lens;
+  int32_t* lens_out;
+  int32_t n, G, D;
+};
+hipError_t launch_kv_compact(const CompactArgs& a, hipStream_t s);
+
+struct TreeArgs {
+  Heads q, out;
+  float* lse;
+  KvCache cache;
+  const int32_t* pages;
+  int64_t pages_ld;
+  int32_t pages_per_seq;
+  const int32_t* lens;
+  const int32_t* parents;
+  Seqs seqs;
+  int32_t H, G, D;
+  float scale;
+  void* ws;
+};
+size_t attn_tree_bytes(int32_t H, int32_t G, int32_t D, int64_t rows, int32_t n);
+hipError_t launch_attn_tree(const TreeArgs& a, hipStream_t s);
 
 }  // namespace ubx

@@ -1,0 +1,646 @@
+// Attention of a tree of drafted tokens over a paged key-value cache.
+//
+//   row j of a sequence sees the tokens before the drafted ones and the nodes on its own path:
+//   s_u = scale q . k_u,  lse = log sum_u exp(s_u),  out = sum_u exp(s_u - lse) v_u
+//
+// The rows of a key-value head's query heads are the columns of one product: a sequence of m
+// nodes has m (n_heads / n_kv_heads) of them, in strips of COLS.  A strip walks the sequence's
+// keys in tiles of BN; tiles of all strips of all sequences, one after another, are dealt in
+// equal contiguous ranges over as many workgroups as run at once (as the units of
+// attn_decode.hip).  A workgroup finishes a strip that lies whole in its range; of the first and
+// the last it may hold a part (maximum, sum and unnormalised output, fp32), which goes to the
+// workspace, and attn_tree_join adds a strip's parts in order.
+//
+// Keys and values come from their pages into registers while the tile before is used, and from
+// there as bf16 into LDS, where all waves read their fragments (attn_common.h).  RW waves take
+// 16 QF columns each; KG groups of them take parts of a tile's keys, where columns are few.
+//
+// The softmax has a reference per column that follows the maximum only when a score passes it by
+// 2^8, so that most tiles rescale nothing.
+//
+// The nodes that a node sees are bits, set once per strip by following the parents in LDS; only
+// the tiles of drafted tokens look at them.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "attn_common.h"
+#include "kv_pages.h"
+
+namespace ubx {
+namespace {
+
+constexpr int MAX_NODES = UB_ATTN_MAX_TREE;
+constexpr int WORDS = MAX_NODES / 64;
+constexpr int NW = 4;
+constexpr int ITEMS = 512;     // workgroups that run at once: two on each CU
+constexpr int MIN_TILES = 4;   // tiles that a workgroup takes at least, where there are so many
+constexpr float RISE = 8.0f;   // scores may pass the reference by so much, in powers of 2
+
+struct TreeParams {
+  TreeArgs a;
+  float c;         // scale * log2(e) (/ k_scale)
+  float v_inv;     // 1 / v_scale
+  int32_t cap;     // tokens the page table can hold per sequence
+  int32_t ranges;  // most ranges the tiles are dealt in; a workgroup for each and key-value head
+  int2* parts_of;  // [strips]: a strip's first part's row of `part`, and its number of parts
+  float* part;     // [2 ranges, G, COLS, D]: parts of a range's first and last strip
+  float2* stat;    // [2 ranges, G, COLS]: maximum (base 2, scaled), sum
+};
+
+template <int DS_, int QF_, int RW_, int KG_, int BN_, bool F8_>
+struct Shape {
+  static constexpr int DS = DS_, QF = QF_, RW = RW_, KG = KG_, BN = BN_;
+  static constexpr bool F8 = F8_;
+  using L = Tile<DS>;
+  static_assert(RW * KG == NW && BN / KG % 32 == 0 && BN / KG <= 64, "keys of a group: 32 or 64");
+  static constexpr int COLS = 16 * QF * RW, TILE = BN * L::RB;
+  static constexpr int STAGES = BN <= 64 ? 2 : 1;
+  static constexpr int EB = F8 ? 1 : 2;
+  static constexpr int PPR = F8 ? L::CPR / 2 : L::CPR;  // 16-byte pieces of a row, as loaded
+  static constexpr int RPL = 64 * NW / PPR;             // rows of a load by all threads
+  static constexpr int N = BN / RPL;                    // loads of a thread, of keys and of values
+  static constexpr int JOIN = KG > 1 ? NW * L::DB * QF * 1024 + NW * QF * 128 : 0;
+  static constexpr int KV = STAGES * 2 * TILE > JOIN ? STAGES * 2 * TILE : JOIN;
+  static constexpr int LDS = KV + MAX_NODES * WORDS * 8 + MAX_NODES * 4;
+};
+
+// A sequence's rows and tokens.  Not good: more nodes than MAX_NODES, fewer cached tokens than
+// nodes, or more than its row of the table holds.
+struct Seq {
+  int row0, m, len;
+  bool good;
+};
+__device__ inline Seq sequence(const TreeParams& p, int i) {
+  Seq s;
+  s.row0 = clamp_row(p.a.seqs.cu[i], p.a.seqs.T);
+  s.m = max(clamp_row(p.a.seqs.cu[i + 1], p.a.seqs.T) - s.row0, 0);
+  s.len = p.a.lens[i];
+  s.good = s.m <= MAX_NODES && s.len >= s.m && s.len <= p.cap;
+  return s;
+}
+
+template <class S>
+__device__ inline int64_t tiles_of(const TreeParams& p, int i) {
+  if (i >= p.a.seqs.n) return 0;
+  const Seq s = sequence(p, i);
+  if (!s.good || s.m == 0) return 0;
+  const int64_t cols = (int64_t)s.m * (p.a.H / p.a.G);
+  return (cols + S::COLS - 1) / S::COLS * ((s.len + S::BN - 1) / S::BN);
+}
+
+// Inclusive prefix sum over the wave.
+__device__ inline int64_t wave_scan64(int64_t v) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int64_t o = __shfl_up(v, d);
+    if ((int)(threadIdx.x & 63) >= d) v += o;
+  }
+  return v;
+}
+
+// Place of a strip in parts_of: no two strips share one, as a sequence of m
+// rows has at most m group / COLS + 1 of them.
+__device__ inline int64_t strip_of(int row0, int i, int group, int cols_per, int strip) {
+  return (int64_t)row0 * group / cols_per + i + strip;
+}
+
+// Bits of 64 keys from key `at` after the first drafted one (before it, if negative) that a node
+// with these path bits sees.
+__device__ inline uint64_t seen_bits(const uint64_t* path, int at) {
+  if (at <= -64) return ~0ull;
+  if (at < 0) return (path[0] << -at) | ((1ull << -at) - 1);
+  const int w = at >> 6, s = at & 63;
+  if (w >= WORDS) return 0;
+  uint64_t x = path[w] >> s;
+  if (s && w + 1 < WORDS) x |= path[w + 1] << (64 - s);
+  return x;
+}
+
+template <class S>
+__global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
+  constexpr int DS = S::DS, QF = S::QF, RW = S::RW, KG = S::KG, BN = S::BN, TILE = S::TILE, N = S::N, PPR = S::PPR;
+  constexpr int COLS = S::COLS, EB = S::EB;
+  constexpr bool F8 = S::F8;
+  constexpr int KB = BN / KG / 16;  // blocks of 16 keys of a group
+  using L = Tile<DS>;
+  extern __shared__ __align__(256) unsigned char smem[];
+  uint64_t* paths = reinterpret_cast<uint64_t*>(smem + S::KV);  // [MAX_NODES][WORDS]
+  int* up = reinterpret_cast<int*>(paths + MAX_NODES * WORDS);  // [MAX_NODES]
+  const TreeArgs& a = p.a;
+  const int kvh = blockIdx.x % a.G, rank = blockIdx.x / a.G, group = a.H / a.G;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rw = wave % RW, kg = wave / RW, col = lane & 15, g = lane >> 4;
+
+  int64_t total = 0;
+  for (int c = 0; c < a.seqs.n; c += 64) total += lane_of(wave_scan64(tiles_of<S>(p, c + lane)), 63);
+  Deal deal;
+  deal.init(total, (int)min((int64_t)p.ranges, (total + MIN_TILES - 1) / MIN_TILES));
+  if (rank >= deal.W) return;
+  const int64_t unit0 = deal.begin(rank), unit1 = deal.begin(rank + 1);
+  // the sequence that holds the first unit, and the units before it
+  int64_t first = 0;
+  int seq = 0;
+  for (int c = 0; c < a.seqs.n; c += 64) {
+    const int64_t t = tiles_of<S>(p, c + lane), incl = wave_scan64(t);
+    const uint64_t m = __ballot(first + incl > unit0);
+    if (m) {
+      const int at = __builtin_ctzll(m);
+      seq = c + at;
+      first += lane_of(incl - t, at);
+      break;
+    }
+    first += lane_of(incl, 63);
+    seq = a.seqs.n;
+  }
+
+  const unsigned char* kb = static_cast<const unsigned char*>(a.cache.k) + kvh * a.cache.hs * EB;
+  const unsigned char* vb = static_cast<const unsigned char*>(a.cache.v) + kvh * a.cache.hs * EB;
+  const int piece = threadIdx.x % PPR, prow = threadIdx.x / PPR;  // of a thread's loads
+  const bool in_row = piece * (16 / EB) < a.D;
+  RowFrag<DS> kf;
+  ColFrag<DS> vf;
+  kf.init(smem + kg * (BN / KG) * L::RB, lane);
+  vf.init(smem + TILE + kg * (BN / KG) * L::RB, lane);
+
+  int64_t unit = unit0;
+  for (; unit < unit1 && seq < a.seqs.n; ++seq) {
+    const Seq sq = sequence(p, seq);
+    const int tiles = (sq.len + BN - 1) / BN;
+    const int cols = sq.m * group;
+    const int64_t count = tiles_of<S>(p, seq);
+    const int64_t last = first + count;
+    const int32_t* pages = a.pages + (int64_t)seq * a.pages_ld;
+    const int past = sq.len - sq.m;
+    bool drawn = false;  // the paths of this sequence's nodes
+    while (unit < min(last, unit1)) {
+      const int strip = (int)Deal::div(unit - first, tiles);
+      const int j0 = (int)(unit - first - (int64_t)strip * tiles);
+      const int j1 = (int)min((int64_t)tiles, j0 + unit1 - unit);
+      const bool alone = j0 == 0 && j1 == tiles;
+      const int64_t item = (int64_t)(2 * rank + (unit != unit0)) * a.G + kvh;
+      if (j0 == 0 && kvh == 0 && threadIdx.x == 0)
+        p.parts_of[strip_of(sq.row0, seq, group, COLS, strip)] =
+            make_int2(2 * rank + (unit != unit0), alone ? 1 : deal.range_of(unit + tiles - 1) - rank + 1);
+      unit += j1 - j0;
+      if (!drawn && j1 * BN > past) {
+        drawn = true;
+        // every earlier reader of `paths` has passed the barrier at a strip's end
+        for (int i = threadIdx.x; i < sq.m; i += 64 * NW) {
+          const int q = a.parents[sq.row0 + i];
+          up[i] = q >= 0 && q < i ? q : -1;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < sq.m; i += 64 * NW) {
+          uint64_t w[WORDS] = {};
+          for (int n = i; n >= 0; n = up[n])
+#pragma unroll
+            for (int k = 0; k < WORDS; ++k)
+              if (n >> 6 == k) w[k] |= 1ull << (n & 63);
+#pragma unroll
+          for (int k = 0; k < WORDS; ++k) paths[i * WORDS + k] = w[k];
+        }
+        __syncthreads();
+      }
+
+      // the wave's columns
+      bf16x8 q[QF][DS];
+      int node[QF];
+#pragma unroll
+      for (int f = 0; f < QF; ++f) {
+        const int c = strip * COLS + (rw * QF + f) * 16 + col;
+        const bool live = c < cols;
+        node[f] = live ? c / group : 0;
+        const uint16_t* row = a.q.p + (int64_t)(sq.row0 + node[f]) * a.q.rs + (kvh * group + (live ? c % group : 0)) * a.q.hs;
+#pragma unroll
+        for (int s = 0; s < DS; ++s) q[f][s] = load_row8(row + 32 * s + 8 * g, live && 32 * s + 8 * g < a.D);
+      }
+      bool lost = false;  // a page that is not there
+
+      u32x4 kreg[N], vreg[N];
+      auto fetch = [&](int j) {
+        // a lane looks up a token, the threads take their rows' places from it
+        int64_t place[(BN + 63) / 64];
+#pragma unroll
+        for (int b = 0; b < (BN + 63) / 64; ++b) {
+          const int t = min(j * BN + b * 64 + lane, sq.len - 1);
+          const int64_t at = token_offset(t, pages[page_entry(t, a.cache.page_size, a.pages_per_seq)], a.cache.n_pages,
+                                          a.cache.page_size, a.cache.ps, a.cache.ts);
+          lost = lost || at < 0;
+          place[b] = max(at, (int64_t)0) * EB;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int r = i * S::RPL + prow;
+          int64_t at = __shfl(place[0], r & 63);
+          if (BN > 64 && r >= 64) at = __shfl(place[(BN + 63) / 64 - 1], r & 63);
+          at += (in_row ? piece : 0) * 16;
+          kreg[i] = *GLOBAL_PTR(const u32x4, kb + at);
+          vreg[i] = *GLOBAL_PTR(const u32x4, vb + at);
+        }
+      };
+      // rows past the end and pieces past head_dim: zeros, as 0 times anything is not 0
+      auto keep = [&](int j, int stage) {
+        unsigned char* kt = smem + stage * 2 * TILE;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int r = i * S::RPL + prow;
+          const bool in = in_row && j * BN + r < sq.len;
+          const u32x4 zero = {0, 0, 0, 0};
+          const u32x4 k = in ? kreg[i] : zero, v = in ? vreg[i] : zero;
+          unsigned char* at = kt + r * L::RB;
+          if (F8) {
+            const int s0 = ((2 * piece) ^ L::swz(r)) * 16, s1 = ((2 * piece + 1) ^ L::swz(r)) * 16;
+            *LDS_PTR(u32x4, at + s0) = cvt8(k[0], k[1]);
+            *LDS_PTR(u32x4, at + s1) = cvt8(k[2], k[3]);
+            *LDS_PTR(u32x4, at + TILE + s0) = cvt8(v[0], v[1]);
+            *LDS_PTR(u32x4, at + TILE + s1) = cvt8(v[2], v[3]);
+          } else {
+            const int s0 = (piece ^ L::swz(r)) * 16;
+            *LDS_PTR(u32x4, at + s0) = k;
+            *LDS_PTR(u32x4, at + TILE + s0) = v;
+          }
+        }
+      };
+
+      f32x4 o[L::DB][QF];
+      float m[QF], l[QF];
+      // All tiles of the segment; true if a hidden value is not finite, unless it is CAREFUL of
+      // them (0 times such a value would be NaN).
+      auto pass = [&](auto careful) __attribute__((always_inline)) {
+        constexpr bool CAREFUL = decltype(careful)::value;
+        bool bad = false;
+#pragma unroll
+        for (int f = 0; f < QF; ++f) {
+          m[f] = -INFINITY;
+          l[f] = 0.0f;
+#pragma unroll
+          for (int d = 0; d < L::DB; ++d) o[d][f] = f32x4{0, 0, 0, 0};
+        }
+        auto step = [&](int j, int off, auto drafted) __attribute__((always_inline)) {
+          constexpr bool DRAFTED = decltype(drafted)::value;  // tiles that hold drafted tokens
+          f32x4 s[KB][QF];
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int f = 0; f < QF; ++f) s[b][f] = f32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int d = 0; d < DS; ++d)
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+              const bf16x8 kk = kf.read(off, b, d);
+#pragma unroll
+              for (int f = 0; f < QF; ++f)
+                s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
+            }
+          uint64_t see[QF];
+          if (DRAFTED) {
+            const int at = j * BN + kg * (BN / KG) - past;
+#pragma unroll
+            for (int f = 0; f < QF; ++f) {
+              see[f] = seen_bits(paths + node[f] * WORDS, at);
+              const uint64_t mine = see[f] >> (4 * g);
+#pragma unroll
+              for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (!((mine >> (16 * b + i)) & 1)) s[b][f][i] = -INFINITY;
+            }
+            if (!CAREFUL) bad = bad || not_finite<TILE, NW>(smem + off + TILE, wave, lane);
+          }
+          bool rises = false;
+          float top[QF];
+#pragma unroll
+          for (int f = 0; f < QF; ++f) {
+            float x = s[0][f][0];
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x = fmaxf(x, s[b][f][i]);
+            top[f] = col_max(x);
+            rises = rises || (top[f] - m[f]) * p.c > RISE || (m[f] == -INFINITY && top[f] > -INFINITY);
+          }
+          if (__ballot(rises)) {
+#pragma unroll
+            for (int f = 0; f < QF; ++f) {
+              const float x = fmaxf(top[f], m[f]);
+              const float r = exp2_(m[f] * p.c - (x == -INFINITY ? 0.0f : x * p.c));  // 0 the first time
+              m[f] = x;
+              l[f] *= r;
+#pragma unroll
+              for (int d = 0; d < L::DB; ++d) o[d][f] *= r;
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < QF; ++f) {
+            const float base = m[f] == -INFINITY ? 0.0f : m[f] * p.c;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                s[b][f][i] = exp2_(s[b][f][i] * p.c - base);
+                sum[i] += s[b][f][i];
+              }
+            l[f] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          }
+#pragma unroll
+          for (int t = 0; t < KB / 2; ++t) {
+            bf16x8 pf[QF];
+#pragma unroll
+            for (int f = 0; f < QF; ++f) pf[f] = pack8(s[2 * t][f], s[2 * t + 1][f]);
+            if (CAREFUL && DRAFTED) {
+              // every column by itself, from the keys that it sees
+#pragma unroll
+              for (int d = 0; d < L::DB; ++d)
+#pragma unroll
+                for (int f = 0; f < QF; ++f) {
+                  const u32x4 v = __builtin_bit_cast(u32x4, vf.read(off, t, d));
+                  f32x4 r = o[d][f];
+#pragma unroll 1
+                  for (int c = 0; c < 16; ++c) {
+                    const uint64_t w = __shfl(see[f], c) >> (32 * t + 4 * g);
+                    u32x4 x = v;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      const uint32_t two = (uint32_t)(w >> ((i & 1) * 2 + (i >> 1) * 16));
+                      x[i] &= (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
+                    }
+                    const f32x4 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), pf[f], o[d][f], 0, 0, 0);
+                    if (col == c) r = y;
+                  }
+                  o[d][f] = r;
+                }
+              continue;
+            }
+#pragma unroll
+            for (int d = 0; d < L::DB; ++d) {
+              const bf16x8 vv = vf.read(off, t, d);
+#pragma unroll
+              for (int f = 0; f < QF; ++f)
+                o[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[f], o[d][f], 0, 0, 0);
+            }
+          }
+        };
+        const int full = min(max(past / BN, j0), j1);  // tiles of tokens that every row sees
+        fetch(j0);
+        int stage = 0;
+        if (S::STAGES == 2) {
+          keep(j0, 0);
+          if (j0 + 1 < j1) fetch(j0 + 1);
+          __syncthreads();
+        }
+        auto turn = [&](int j, auto drafted) __attribute__((always_inline)) {
+          if (S::STAGES == 2) {
+            if (j + 1 < j1) keep(j + 1, stage ^ 1);
+            if (j + 2 < j1) fetch(j + 2);
+            step(j, stage * 2 * TILE, drafted);
+            __syncthreads();
+            stage ^= 1;
+          } else {
+            keep(j, 0);
+            if (j + 1 < j1) fetch(j + 1);
+            __syncthreads();
+            step(j, 0, drafted);
+            __syncthreads();
+          }
+        };
+        int j = j0;
+        for (; j < full; ++j) turn(j, std::false_type{});
+        for (; j < j1; ++j) turn(j, std::true_type{});
+        return bad;
+      };
+      if (any_wave<NW>(pass(std::false_type{}), smem, wave, lane)) pass(std::true_type{});
+      lost = __ballot(lost) != 0;
+
+      float base[QF], sum[QF];
+#pragma unroll
+      for (int f = 0; f < QF; ++f) {
+        sum[f] = col_sum(l[f]);
+        base[f] = m[f] == -INFINITY ? -INFINITY : m[f] * p.c;
+        if (lost) sum[f] = NAN;
+      }
+      constexpr int MINE = (L::DB + KG - 1) / KG;  // blocks of the output that a wave writes
+      if (KG > 1) {
+        f32x4* parts = reinterpret_cast<f32x4*>(smem);  // [KG][RW][DB][QF][64]
+        float2* stats = reinterpret_cast<float2*>(smem + NW * L::DB * QF * 1024);  // [KG][RW][QF][16]
+        f32x4* mine = parts + wave * L::DB * QF * 64 + lane;
+#pragma unroll
+        for (int f = 0; f < QF; ++f) {
+#pragma unroll
+          for (int d = 0; d < L::DB; ++d) mine[(d * QF + f) * 64] = o[d][f];
+          if (g == 0) stats[(wave * QF + f) * 16 + col] = make_float2(base[f], sum[f]);
+        }
+        __syncthreads();
+        const f32x4* all = parts + (rw * L::DB + kg) * QF * 64 + lane;
+#pragma unroll
+        for (int f = 0; f < QF; ++f) {
+          float2 x[KG];
+          float top = -INFINITY, tot = 0.0f;
+#pragma unroll
+          for (int k = 0; k < KG; ++k) {
+            x[k] = stats[((k * RW + rw) * QF + f) * 16 + col];
+            top = fmaxf(top, x[k].x);
+          }
+          const float b = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+          for (int k = 0; k < KG; ++k) {
+            x[k].x = exp2_(x[k].x - b);
+            tot += x[k].x * x[k].y;
+          }
+          base[f] = top;
+          sum[f] = tot;
+#pragma unroll
+          for (int i = 0; i < MINE; ++i) {
+            if (i * KG + kg >= L::DB) break;
+            f32x4 y = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < KG; ++k) y += all[((k * RW * L::DB + i * KG) * QF + f) * 64] * x[k].x;
+            o[i][f] = y;
+          }
+        }
+      }
+#pragma unroll
+      for (int f = 0; f < QF; ++f) {
+        const int c0 = (rw * QF + f) * 16 + col, c = strip * COLS + c0;
+        if (c >= cols) continue;
+        const int head = kvh * group + c % group;
+        const int64_t row = sq.row0 + c / group;
+        const float inv = sum[f] == 0.0f ? 0.0f : p.v_inv / sum[f];
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+          const int e = 16 * (i * KG + kg) + 4 * g;
+          if (e >= a.D) continue;
+          if (alone) {
+            const f32x4 x = o[i][f] * inv;
+            *reinterpret_cast<uint2*>(a.out.p + row * a.out.rs + head * a.out.hs + e) =
+                make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+          } else {
+            *reinterpret_cast<f32x4*>(p.part + (item * COLS + c0) * a.D + e) = o[i][f];
+          }
+        }
+        if (g == 0 && kg == 0) {
+          if (!alone) p.stat[item * COLS + c0] = make_float2(base[f], sum[f]);
+          else if (a.lse) a.lse[(int64_t)head * a.seqs.T + row] = sum[f] == 0.0f ? -INFINITY : base[f] * LN2 + logf(sum[f]);
+        }
+      }
+      __syncthreads();  // the next strip's tiles take the place of what was joined
+    }
+    first = last;
+  }
+}
+
+// Rows of no sequence (zeros) and of sequences that are not good (NaN), and the sum of the parts,
+// in order, of strips of several ranges.  JW waves to a row and head; wave w of them adds parts
+// w, w + JW, ..., eight loads ahead; lane i holds elements 2 i, 2 i + 1.
+template <int JW, int COLS>
+__global__ __launch_bounds__(JW > 4 ? 64 * JW : 256) void attn_tree_join(TreeParams p) {
+  constexpr int WAVES = JW > 4 ? JW : 4, AHEAD = 8;
+  __shared__ float2 red[WAVES][64];
+  __shared__ float2 tops[WAVES];
+  const TreeArgs& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t task = (int64_t)blockIdx.x * (WAVES / JW) + wave / JW;
+  const int w = wave % JW;
+  const int T = a.seqs.T, row = (int)(task / a.H), head = (int)(task % a.H);
+  if (JW < WAVES && row >= T) return;
+  // sequences that end at or before the row come first: their number is its sequence
+  int seq = 0;
+  for (int c = 0; c < a.seqs.n; c += 64) {
+    const int i = c + lane;
+    const int m = __popcll(__ballot((i < a.seqs.n ? a.seqs.cu[i + 1] : 0x7FFFFFFF) <= row));
+    seq += m;
+    if (m < 64) break;
+  }
+  uint16_t* out = a.out.p + (int64_t)row * a.out.rs + head * a.out.hs;
+  float* lse = a.lse ? a.lse + (int64_t)head * T + row : nullptr;
+  Seq s{0, 0, 0, true};
+  if (seq < a.seqs.n) s = sequence(p, seq);
+  const bool none = seq >= a.seqs.n || row < s.row0;
+  if (none || !s.good) {
+    if (w == 0) {
+      const float x = none ? 0.0f : NAN;
+      if (2 * lane < a.D) *reinterpret_cast<uint32_t*>(out + 2 * lane) = pack_bf16x2(x, x);
+      if (lane == 0 && lse) *lse = none ? -INFINITY : NAN;
+    }
+    return;
+  }
+  const int group = a.H / a.G, kvh = head / group, c = (row - s.row0) * group + head - kvh * group;
+  const int2 parts = p.parts_of[strip_of(s.row0, seq, group, COLS, c / COLS)];
+  const int count = parts.y;
+  if (count == 1) return;
+  // (sequences that overlap, of boundaries that do not rise, may have left none)
+  if (count < 1 || parts.x < 0 || (int64_t)(parts.x >> 1) + count > p.ranges) return;
+  auto at = [&](int i) {
+    return ((int64_t)(i == 0 ? parts.x : (parts.x & ~1) + 2 * i) * a.G + kvh) * COLS + c % COLS;
+  };
+  float m = -INFINITY, sum = 0.0f;
+  float2 x = make_float2(0.0f, 0.0f);
+  for (int i0 = w; i0 < count; i0 += AHEAD * JW) {
+    float2 st[AHEAD], v[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int i = i0 + j * JW;
+      const int64_t k = at(min(i, count - 1));
+      st[j] = i < count ? p.stat[k] : make_float2(-INFINITY, 0.0f);
+      v[j] = *reinterpret_cast<const float2*>(p.part + k * a.D + min(2 * lane, a.D - 2));
+    }
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) top = fmaxf(top, st[j].x);
+    const float b = top == -INFINITY ? 0.0f : top;
+    const float r = exp2_(m - b);
+    m = top;
+    sum *= r;
+    x.x *= r;
+    x.y *= r;
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (i0 + j * JW >= count) break;
+      const float f = exp2_(st[j].x - b);
+      sum += f * st[j].y;
+      x.x += f * v[j].x;
+      x.y += f * v[j].y;
+    }
+  }
+  if (JW > 1) {
+    red[wave][lane] = x;
+    if (lane == 0) tops[wave] = make_float2(m, sum);
+    __syncthreads();
+    if (w != 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < JW; ++k) top = fmaxf(top, tops[wave + k].x);
+    const float b = top == -INFINITY ? 0.0f : top;
+    m = top;
+    sum = 0.0f;
+    x = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < JW; ++k) {
+      const float f = exp2_(tops[wave + k].x - b);
+      sum += f * tops[wave + k].y;
+      x.x += f * red[wave + k][lane].x;
+      x.y += f * red[wave + k][lane].y;
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : p.v_inv / sum;
+  if (2 * lane < a.D) *reinterpret_cast<uint32_t*>(out + 2 * lane) = pack_bf16x2(x.x * inv, x.y * inv);
+  if (lane == 0 && lse) *lse = sum == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * LN2 + logf(sum);
+}
+
+constexpr int MOST_COLS = 128;
+int max_ranges(int G) { return G < ITEMS ? ITEMS / G : 1; }
+int64_t part_bytes(int G, int D, int cols) { return (int64_t)2 * max_ranges(G) * G * cols * (8 + 4 * (int64_t)D); }
+
+template <class S>
+hipError_t run(const TreeArgs& a, hipStream_t s) {
+  TreeParams p{};
+  p.a = a;
+  p.cap = table_cap(a.pages_per_seq, a.cache.page_size);
+  p.c = a.scale * LOG2E * (S::F8 ? 1.0f / a.cache.k_scale : 1.0f);
+  p.v_inv = S::F8 ? 1.0f / a.cache.v_scale : 1.0f;
+  p.ranges = max_ranges(a.G);
+  const int64_t blocks = (int64_t)p.ranges * a.G, rows = 2 * blocks * S::COLS;
+  p.stat = static_cast<float2*>(a.ws);
+  p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + rows * 8);
+  p.parts_of = reinterpret_cast<int2*>(p.part + rows * a.D);
+  const int64_t outputs = (int64_t)a.seqs.T * a.H;
+  if (outputs > 0x7FFFFFFF) return hipErrorInvalidValue;
+  auto kernel = &attn_tree<S>;
+  hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kernel), S::LDS);
+  if (e == hipSuccess && a.seqs.n > 0) e = launch_k(kernel, dim3((unsigned)blocks), dim3(64 * NW), S::LDS, s, p);
+  if (e != hipSuccess || outputs == 0) return e;
+  // few outputs have many parts, which more waves then share
+  if (outputs <= 512) return launch_k(&attn_tree_join<16, S::COLS>, dim3((unsigned)outputs), dim3(1024), 0, s, p);
+  if (outputs <= 4096) return launch_k(&attn_tree_join<4, S::COLS>, dim3((unsigned)outputs), dim3(256), 0, s, p);
+  return launch_k(&attn_tree_join<1, S::COLS>, dim3((unsigned)((outputs + 3) / 4)), dim3(256), 0, s, p);
+}
+
+template <int DS, bool F8>
+hipError_t choose(const TreeArgs& a, hipStream_t s) {
+  // by the columns of a sequence, on average: the host knows no more
+  const int64_t cols = a.seqs.n > 0 ? ((int64_t)a.seqs.T * (a.H / a.G) + a.seqs.n - 1) / a.seqs.n : 1;
+  if (cols <= 16) return run<Shape<DS, 1, 1, 4, 128, F8>>(a, s);
+  if (cols <= 32) return run<Shape<DS, 2, 1, 4, 128, F8>>(a, s);
+  if (cols <= 64) return run<Shape<DS, 2, 2, 2, 64, F8>>(a, s);
+  return run<Shape<DS, 2, 4, 1, 64, F8>>(a, s);
+}
+
+template <bool F8>
+hipError_t by_dim(const TreeArgs& a, hipStream_t s) {
+  if (a.D <= 64) return choose<2, F8>(a, s);
+  if (a.D <= 96) return choose<3, F8>(a, s);
+  return choose<4, F8>(a, s);
+}
+
+}  // namespace
+
+size_t attn_tree_bytes(int32_t H, int32_t G, int32_t D, int64_t rows, int32_t n) {
+  return (size_t)(part_bytes(G, D, MOST_COLS) + (rows * (H / G) / 16 + n + 1) * 8);
+}
+
+hipError_t launch_attn_tree(const TreeArgs& a, hipStream_t s) {
+  return a.cache.e4m3 ? by_dim<true>(a, s) : by_dim<false>(a, s);
+}
+
+}  // namespace ubx

@@ -55,7 +55,7 @@ struct AppendParams {
 
 struct Token {
   int64_t slot;  // element offset of the token's slot in head 0 of the cache, or -1
-  int64_t pos;
+  int64_t pos;   // for the rotation
   int32_t live;  // belongs to a sequence
 };
 
@@ -201,6 +201,7 @@ __global__ __launch_bounds__(THREADS, 8) void kv_append(AppendParams p) {
           const int64_t pos = (int64_t)past + (t - start);
           k.live = 1;
           k.pos = pos;
+          if (a.offsets) k.pos = (int64_t)past + a.offsets[t];
           const int e = a.cache.k ? page_entry(pos, a.cache.page_size, a.pages_per_seq) : -1;
           if (e >= 0)
             k.slot = token_offset(pos, a.pages[(int64_t)seq * a.pages_ld + e], a.cache.n_pages,

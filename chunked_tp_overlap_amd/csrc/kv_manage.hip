@@ -1,0 +1,342 @@
+// The pages of a paged key-value cache: sequences that share pages, pages given and taken back,
+// copies of pages, and tokens moved to the places after their sequence's kept ones.
+//
+// What holds a page is counted: refs[page] rows of the table have it, and a page of count 0 is
+// free.  There is no list of free pages: giving pages takes the free ones of the lowest numbers,
+// so that the same calls give the same pages on every run, whatever order counts changed in.
+// Counts and tables are a few integers per page; what bounds these calls is their chains of
+// loads and launches.  kv_resize is two launches: one workgroup gives pages, as a row's pages
+// depend on all rows before it, then a workgroup for each row takes back what it gives up.
+// kv_copy_pages and kv_compact move tokens, 16 bytes to a lane.
+#include <hip/hip_runtime.h>
+
+#include "attn_internal.h"
+#include "gemm_common.h"
+#include "kv_pages.h"
+
+namespace ubx {
+namespace {
+
+__device__ inline int pages_of(int len, int page) { return len / page + (len % page != 0); }
+__device__ inline int row_len(const Table& t, int len, int page) { return clamp_len(len, table_cap(t.per, page)); }
+
+// ---- fork -----------------------------------------------------------------------------------
+// A workgroup for each row of `in`, whose pages' counts change by its uses less one, then one
+// for each row of `out`.
+__global__ __launch_bounds__(256) void kv_fork(ForkArgs a) {
+  const int r = blockIdx.x;
+  if (r < a.in.n) {
+    __shared__ int uses;
+    if (threadIdx.x == 0) uses = -1;
+    __syncthreads();
+    int mine = 0;
+    for (int i = threadIdx.x; i < a.out.n; i += 256) mine += a.parents[i] == r;
+    if (mine) atomicAdd(&uses, mine);
+    __syncthreads();
+    const int change = uses, n = pages_of(row_len(a.in, a.lens[r], a.page), a.page);
+    if (change == 0) return;
+    const int32_t* row = a.in.p + (int64_t)r * a.in.ld;
+    for (int e = threadIdx.x; e < n; e += 256) {
+      const int id = row[e];
+      if (id >= 0 && id < a.n_pages) atomicAdd(a.refs + id, change);
+    }
+    return;
+  }
+  const int i = r - a.in.n, of = a.parents[i];
+  const bool some = of >= 0 && of < a.in.n;
+  const int len = some ? row_len(a.in, a.lens[of], a.page) : 0, n = pages_of(len, a.page);
+  const int32_t* from = a.in.p + (int64_t)(some ? of : 0) * a.in.ld;
+  int32_t* to = a.out.p + (int64_t)i * a.out.ld;
+  for (int e = threadIdx.x; e < a.out.per; e += 256) to[e] = e < n ? from[e] : -1;
+  if (threadIdx.x == 0) a.lens_out[i] = len;
+}
+
+// ---- resize ---------------------------------------------------------------------------------
+constexpr int GIVERS = 1024, GIVE_WAVES = GIVERS / 64;
+constexpr int PER = 8;  // counts a thread looks at at a time
+
+// What a row asks for: table entries `begin` and on, the last of which would be page number
+// `end` (less one) of those that all rows up to it ask for.
+struct Ask {
+  int64_t end;
+  int32_t begin, had;
+  int32_t part, src;  // tokens of a shared last page, which goes to another row's holders; its id
+};
+// The workspace: free pages, or at least as many as are asked for, then the rows' asks.
+constexpr int ASKS_AT = 16;
+__device__ inline int64_t* free_of(void* ws) { return static_cast<int64_t*>(ws); }
+__device__ inline Ask* asks_of(void* ws) {
+  return reinterpret_cast<Ask*>(static_cast<unsigned char*>(ws) + ASKS_AT);
+}
+
+// Sum over the workgroup's threads before this one; all: over all of them.
+__device__ inline int64_t scan_before(int64_t v, int64_t* sums, int64_t& all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t incl = v;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int64_t o = __shfl_up(incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 63) sums[wave] = incl;
+  __syncthreads();
+  int64_t before = 0;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < GIVE_WAVES; ++w) {
+    if (w < wave) before += sums[w];
+    all += sums[w];
+  }
+  __syncthreads();
+  return before + incl - v;
+}
+
+// The lengths that a row has and is to have, within its table; a new length past it is none.
+struct Lens {
+  int has, wants;
+  bool fits;
+};
+__device__ inline Lens lens_of(const ResizeArgs& a, int i) {
+  const int cap = table_cap(a.table.per, a.page), len = a.lens[i], want = a.new_lens[i];
+  Lens l;
+  l.has = clamp_len(len, cap);
+  l.fits = want <= cap;
+  l.wants = l.fits ? max(want, 0) : l.has;
+  return l;
+}
+
+__global__ __launch_bounds__(GIVERS) void kv_give(ResizeArgs a) {
+  __shared__ int64_t sums[GIVE_WAVES];
+  Ask* ask = asks_of(a.ws);
+  const int n = a.table.n;
+  int64_t total = 0;
+  for (int c = 0; c < n; c += GIVERS) {
+    const int i = c + threadIdx.x;
+    Ask k{0, 0, 0, 0, -1};
+    int need = 0;
+    if (i < n) {
+      const Lens l = lens_of(a, i);
+      k.had = pages_of(l.has, a.page);
+      k.begin = k.had;
+      if (l.wants > l.has) {
+        const int part = l.has % a.page;
+        if (part) {
+          const int id = a.table.p[(int64_t)i * a.table.ld + k.had - 1];
+          if (id >= 0 && id < a.n_pages && a.refs[id] > 1) {
+            k.src = id;
+            k.part = part;
+            --k.begin;
+          }
+        }
+        need = pages_of(l.wants, a.page) - k.begin;
+      }
+    }
+    int64_t all;
+    const int64_t before = scan_before(need, sums, all);
+    if (i < n) {
+      k.end = total + before + need;
+      ask[i] = k;
+    }
+    total += all;
+  }
+  // GIVE: pages of ranks below `limit` go to the rows that ask for them; otherwise they are only
+  // counted, as far as `limit`
+  auto walk = [&](int64_t limit, bool give) {
+    int64_t found = 0;
+    for (int64_t c = 0; c < a.n_pages && found < limit; c += GIVERS * PER) {
+      const int64_t id0 = c + (int64_t)threadIdx.x * PER;
+      int32_t r[PER];
+      if (id0 + PER <= a.n_pages) {
+        const i32x4 lo = *GLOBAL_PTR(const i32x4, a.refs + id0), hi = *GLOBAL_PTR(const i32x4, a.refs + id0 + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          r[j] = lo[j];
+          r[4 + j] = hi[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) r[j] = id0 + j < a.n_pages ? a.refs[id0 + j] : 1;
+      }
+      int mine = 0;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) mine += r[j] == 0;
+      int64_t all;
+      int64_t rank = found + scan_before(mine, sums, all);
+      found += all;
+      if (!give || mine == 0) continue;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        if (r[j] != 0 || rank >= limit) continue;
+        int lo = 0, hi = n - 1;  // the first row whose end lies past the rank
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (ask[mid].end > rank) hi = mid;
+          else lo = mid + 1;
+        }
+        const int64_t before = lo > 0 ? ask[lo - 1].end : 0;
+        a.table.p[(int64_t)lo * a.table.ld + ask[lo].begin + (rank - before)] = (int32_t)(id0 + j);
+        a.refs[id0 + j] = 1;
+        ++rank;
+      }
+    }
+    return found;
+  };
+  if (total == 0) {
+    if (threadIdx.x == 0) *free_of(a.ws) = 0;
+    return;
+  }
+  const int64_t free = walk(total, false);
+  // as many as go to rows that get all they ask for
+  int64_t limit = total;
+  if (free < total) {
+    int lo = 0, hi = n - 1;  // the first row that does not
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (ask[mid].end > free) hi = mid;
+      else lo = mid + 1;
+    }
+    limit = lo > 0 ? ask[lo - 1].end : 0;
+  }
+  if (threadIdx.x == 0) *free_of(a.ws) = free;
+  if (limit > 0) walk(limit, true);
+}
+
+__global__ __launch_bounds__(64) void kv_take(ResizeArgs a) {
+  const Ask* ask = asks_of(a.ws);
+  const int i = blockIdx.x;
+  const Ask k = ask[i];
+  const int64_t before = i > 0 ? ask[i - 1].end : 0;
+  const Lens l = lens_of(a, i);
+  const bool given = k.end == before || k.end <= *free_of(a.ws);
+  const int len = given ? l.wants : l.has;
+  int32_t* row = a.table.p + (int64_t)i * a.table.ld;
+  auto take = [&](int e) {
+    const int id = row[e];
+    if (id >= 0 && id < a.n_pages) atomicAdd(a.refs + id, -1);
+    row[e] = -1;
+  };
+  const int has = pages_of(len, a.page);
+  for (int e = has + threadIdx.x; e < k.had; e += 64) take(e);
+  if (a.win.size > 0 && len > a.win.size) {
+    // pages of hidden tokens alone
+    const int end = min((len - a.win.size) / a.page, has);
+    for (int e = pages_of(a.win.sinks, a.page) + threadIdx.x; e < end; e += 64) take(e);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const bool own = given && k.part > 0;
+    const int to = own ? row[k.had - 1] : -1;  // -1 also where the window hides all of the page
+    int32_t* c = a.copies + 3 * (int64_t)i;
+    c[0] = to >= 0 ? k.src : -1;
+    c[1] = to;
+    c[2] = to >= 0 ? k.part : 0;
+    if (own) atomicAdd(a.refs + k.src, -1);
+    a.lens_out[i] = len;
+  }
+}
+
+// ---- copies ---------------------------------------------------------------------------------
+// A workgroup for each record, head, and keys or values.
+__global__ __launch_bounds__(256) void kv_copy_pages(KvCache c, int G, int vec, const int32_t* copies) {
+  const int kv = blockIdx.x & 1, head = (blockIdx.x >> 1) % G, i = (blockIdx.x >> 1) / G;
+  const int src = copies[3 * (int64_t)i], dst = copies[3 * (int64_t)i + 1];
+  const int tokens = min(copies[3 * (int64_t)i + 2], c.page_size);
+  if (src < 0 || src >= c.n_pages || dst < 0 || dst >= c.n_pages || src == dst) return;
+  const int eb = c.e4m3 ? 1 : 2;
+  unsigned char* base = static_cast<unsigned char*>(kv ? c.v : c.k) + head * c.hs * eb;
+  const unsigned char* from = base + src * c.ps * eb;
+  unsigned char* to = base + dst * c.ps * eb;
+  const int at_once = 256 / vec, piece = threadIdx.x % vec, first = threadIdx.x / vec;
+  if (first >= at_once) return;
+  for (int64_t t = first; t < tokens; t += at_once) {
+    const int64_t at = t * c.ts * eb + piece * 16;
+    *GLOBAL_PTR(u32x4, to + at) = *GLOBAL_PTR(const u32x4, from + at);
+  }
+}
+
+// ---- compaction -----------------------------------------------------------------------------
+// A workgroup for each sequence, head, and keys or values.  A thread moves 16 bytes of AHEAD
+// tokens at a time.  As the kept places rise, token d comes from place d or a later one: all
+// loads of a turn before its stores, and turn after turn, no place is written before it is read.
+__global__ __launch_bounds__(256) void kv_compact(CompactArgs a, int vec) {
+  constexpr int AHEAD = 4;
+  __shared__ int count;
+  const int kv = blockIdx.x & 1, head = (blockIdx.x >> 1) % a.G, i = (blockIdx.x >> 1) / a.G;
+  const int cap = table_cap(a.pages_per_seq, a.cache.page_size);
+  const int len = clamp_len(a.lens[i], cap);
+  const int32_t* kept = a.kept + (int64_t)i * a.kept_ld;
+  const int given = min(max(a.kept_lens[i], 0), a.most);
+  if (threadIdx.x == 0) count = given;
+  __syncthreads();
+  for (int d = threadIdx.x; d < given; d += 256) {
+    const int x = kept[d];
+    if (x <= (d > 0 ? kept[d - 1] : -1) || x >= cap - len) {
+      atomicMin(&count, d);
+      break;
+    }
+  }
+  __syncthreads();
+  const int n = count;
+  if (blockIdx.x % (2 * a.G) == 0 && threadIdx.x == 0) a.lens_out[i] = len + n;
+  const int eb = a.cache.e4m3 ? 1 : 2;
+  unsigned char* base = static_cast<unsigned char*>(kv ? a.cache.v : a.cache.k) + head * a.cache.hs * eb;
+  const int32_t* pages = a.pages + (int64_t)i * a.pages_ld;
+  auto place = [&](int t) {
+    return token_offset(t, pages[page_entry(t, a.cache.page_size, a.pages_per_seq)], a.cache.n_pages, a.cache.page_size,
+                        a.cache.ps, a.cache.ts);
+  };
+  const int at_once = 256 / vec, piece = threadIdx.x % vec, first = threadIdx.x / vec;
+  for (int d0 = 0; d0 < n; d0 += at_once * AHEAD) {
+    u32x4 x[AHEAD];
+    int64_t to[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int d = d0 + j * at_once + first;
+      to[j] = -1;
+      if (first < at_once && d < n && kept[d] != d) {
+        const int64_t from = place(len + kept[d]);
+        to[j] = place(len + d);
+        if (from < 0) to[j] = -1;
+        else x[j] = *GLOBAL_PTR(const u32x4, base + from * eb + piece * 16);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (to[j] >= 0) *GLOBAL_PTR(u32x4, base + to[j] * eb + piece * 16) = x[j];
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s) {
+  const int64_t blocks = (int64_t)a.in.n + a.out.n;
+  if (blocks == 0) return hipSuccess;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  return launch_k(&kv_fork, dim3((unsigned)blocks), dim3(256), 0, s, a);
+}
+
+size_t kv_resize_bytes(int32_t n) { return n > 0 ? ASKS_AT + sizeof(Ask) * (size_t)n : 0; }
+
+hipError_t launch_kv_resize(const ResizeArgs& a, hipStream_t s) {
+  if (a.table.n == 0) return hipSuccess;
+  const hipError_t e = launch_k(&kv_give, dim3(1), dim3(GIVERS), 0, s, a);
+  return e == hipSuccess ? launch_k(&kv_take, dim3((unsigned)a.table.n), dim3(64), 0, s, a) : e;
+}
+
+hipError_t launch_kv_copy_pages(const KvCache& c, int32_t G, int32_t D, const int32_t* copies, int32_t n,
+                                hipStream_t s) {
+  const int64_t blocks = 2 * (int64_t)G * n;
+  if (blocks == 0) return hipSuccess;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  return launch_k(&kv_copy_pages, dim3((unsigned)blocks), dim3(256), 0, s, c, G, D / (c.e4m3 ? 16 : 8), copies);
+}
+
+hipError_t launch_kv_compact(const CompactArgs& a, hipStream_t s) {
+  const int64_t blocks = 2 * (int64_t)a.G * a.n;
+  if (blocks == 0) return hipSuccess;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  return launch_k(&kv_compact, dim3((unsigned)blocks), dim3(256), 0, s, a, a.D / (a.cache.e4m3 ? 16 : 8));
+}
+
+}  // namespace ubx

@@ -39,8 +39,9 @@ UB_REDUCE_ASCENDING, UB_REDUCE_RING = 0, 1
 REDUCE_ORDERS = {"ascending": UB_REDUCE_ASCENDING, "ring": UB_REDUCE_RING}
 UB_ATTN_PROMPT, UB_ATTN_PROMPT_BWD, UB_ATTN_DECODE = 0, 1, 2
 UB_ATTN_PROMPT_WINDOW, UB_ATTN_PROMPT_WINDOW_BWD, UB_ATTN_DECODE_WINDOW = 3, 4, 5
+UB_ATTN_TREE = 6
 UB_ATTN_MAX_HEAD_DIM = 128
-UB_ATTN_MAX_SINKS = 64
+UB_ATTN_MAX_SINKS, UB_ATTN_MAX_TREE = 64, 256
 
 # Every symbol include/ub.h declares.
 EXPORTS = (
@@ -55,6 +56,8 @@ EXPORTS = (
     "ub_debug_last_plan", "ub_register_scratch", "ub_destroy", "ub_status_string", "ub_last_error",
     "ub_attn_required_bytes", "ub_kv_append", "ub_attn_prompt", "ub_attn_prompt_bwd", "ub_attn_decode",
     "ub_attn_prompt_window", "ub_attn_prompt_window_bwd", "ub_attn_decode_window",
+    "ub_kv_append_at", "ub_attn_tree", "ub_kv_compact", "ub_kv_fork", "ub_kv_resize_bytes", "ub_kv_resize",
+    "ub_kv_copy_pages",
 )
 
 
@@ -163,7 +166,16 @@ _sig = {
     "ub_attn_prompt_window": (_I32, [_H, _HEADSP, _HEADSP, _HEADSP, _HEADSP, _P, _P, _I32, _WINP, _ATTNP, _P, _SZ, _P]),
     "ub_attn_prompt_window_bwd": (_I32, [_H] + [_HEADSP] * 5 + [_P] + [_HEADSP] * 3 +
                                   [_P, _I32, _WINP, _ATTNP, _P, _SZ, _P]),
-    "ub_attn_decode_window": (_I32, [_H, _HEADSP, _KVP, _P, _I64, _I32, _P, _I32, _WINP, _HEADSP, _P, _ATTNP, _P, _SZ, _P]),
+    "ub_attn_decode_window": (_I32, [_H, _HEADSP, _KVP, _P, _I64, _I32, _P, _I32, _WINP, _HEADSP, _P, _ATTNP, _P, _SZ,
+                                     _P]),
+    "ub_kv_append_at": (_I32, [_H, _HEADSP, _HEADSP, _HEADSP, _HEADSP, _HEADSP, _P, _P, _P, _P, _I32, _KVP, _P,
+                               _I64, _I32, _ATTNP, _P]),
+    "ub_attn_tree": (_I32, [_H, _HEADSP, _KVP, _P, _I64, _I32, _P, _P, _P, _I32, _HEADSP, _P, _ATTNP, _P, _SZ, _P]),
+    "ub_kv_compact": (_I32, [_H, _KVP, _P, _I64, _I32, _P, _P, _I64, _I32, _P, _I32, _P, _ATTNP, _P]),
+    "ub_kv_fork": (_I32, [_H, _P, _I64, _P, _I64, _I32, _P, _I32, _P, _P, _I64, _I32, _P, _I32, _I32, _P]),
+    "ub_kv_resize_bytes": (_I32, [_I32, ctypes.POINTER(_SZ)]),
+    "ub_kv_resize": (_I32, [_H, _P, _I64, _P, _I64, _I32, _P, _P, _I32, _P, _P, _I32, _WINP, _P, _SZ, _P]),
+    "ub_kv_copy_pages": (_I32, [_H, _KVP, _P, _I32, _ATTNP, _P]),
     "ub_destroy": (_I32, [_H]),
     "ub_status_string": (ctypes.c_char_p, [_I32]),
     "ub_last_error": (ctypes.c_char_p, [_H]),
@@ -515,7 +527,7 @@ def _int32(x, n, what):
     return _ptr(x)
 
 
-def _table(pages, n):
+def _table(pages, n, what="pages"):
     """(pointer, row stride, pages per sequence) of a [sequences, pages] int32 tensor."""
     if pages is None:
         return None, 0, 0
@@ -527,9 +539,9 @@ def _table(pages, n):
         # are not what the calls read
         if rows >= n and (one == 1 or rows * per == 0) and (ld >= per or n <= 1):
             if not pages.is_cuda:
-                _host(pages, "pages")
+                _host(pages, what)
             return pages.data_ptr(), ld if ld > per else per, per
-    raise ValueError(f"pages: an int32 [at least {n}, pages] tensor with contiguous rows that do not overlap")
+    raise ValueError(f"{what}: an int32 [at least {n}, pages] tensor with contiguous rows that do not overlap")
 
 
 def _lse_arg(lse, h, cfg, out):
@@ -562,10 +574,7 @@ def ub_attn_required_bytes(op, cfg, rows, n_seqs):
     return n.value
 
 
-def ub_kv_append(h, q, k, v, q_out, k_out, inv_freq, cu_seqlens, past_lens, n_seqs, cache, pages, cfg,
-                 stream=None):
-    """q, k, v, q_out, k_out: ``heads(...)`` or None; cache: ``make_kv_cache(...)`` or None; pages:
-    a [sequences, pages] int32 tensor; inv_freq: rotary_dim / 2 floats."""
+def _append_args(q, k, v, q_out, k_out, inv_freq, cache, pages, n_seqs, cfg):
     D = cfg.head_dim
     H, G = (cfg.n_heads, D), (cfg.n_kv_heads, D)
     if q is not None and q.held != H:
@@ -589,10 +598,28 @@ def ub_kv_append(h, q, k, v, q_out, k_out, inv_freq, cu_seqlens, past_lens, n_se
         inv_freq = inv_freq.data_ptr()
     else:
         inv_freq = _ptr(inv_freq)
-    table, ld, per_seq = _table(pages, n_seqs)
+    return (inv_freq, *_table(pages, n_seqs))
+
+
+def ub_kv_append(h, q, k, v, q_out, k_out, inv_freq, cu_seqlens, past_lens, n_seqs, cache, pages, cfg,
+                 stream=None):
+    """q, k, v, q_out, k_out: ``heads(...)`` or None; cache: ``make_kv_cache(...)`` or None; pages:
+    a [sequences, pages] int32 tensor; inv_freq: rotary_dim / 2 floats."""
+    inv_freq, table, ld, per_seq = _append_args(q, k, v, q_out, k_out, inv_freq, cache, pages, n_seqs, cfg)
     st = _lib.ub_kv_append(h, q, k, v, q_out, k_out, inv_freq, _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"),
                            _int32(past_lens, n_seqs, "past_lens"), n_seqs, cache, table, ld, per_seq, cfg,
                            _stream(stream))
+    if st:
+        _check(st, h)
+
+
+def ub_kv_append_at(h, q, k, v, q_out, k_out, inv_freq, offsets, cu_seqlens, past_lens, n_seqs, cache, pages, cfg,
+                    stream=None):
+    """offsets: an int32 value for each active row."""
+    inv_freq, table, ld, per_seq = _append_args(q, k, v, q_out, k_out, inv_freq, cache, pages, n_seqs, cfg)
+    st = _lib.ub_kv_append_at(h, q, k, v, q_out, k_out, inv_freq, _rows_int32(h, offsets, "offsets"),
+                              _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), _int32(past_lens, n_seqs, "past_lens"),
+                              n_seqs, cache, table, ld, per_seq, cfg, _stream(stream))
     if st:
         _check(st, h)
 
@@ -677,6 +704,77 @@ def ub_attn_decode_window(h, q, cache, pages, kv_lens, n_seqs, window, out, lse,
     ws, ws_bytes = _ws_arg(workspace)
     st = _lib.ub_attn_decode_window(h, q, cache, table, ld, per_seq, _int32(kv_lens, n_seqs, "kv_lens"), n_seqs, window,
                                     out, _lse_arg(lse, h, cfg, out), cfg, ws, ws_bytes, _stream(stream))
+    if st:
+        _check(st, h)
+
+
+def _rows_int32(h, x, what):
+    """A pointer to an int32 value for each row that a sequence may use: as many as the handle's
+    active rows, or as the tensor holds where only those are sequences' rows."""
+    if type(x) is torch.Tensor or isinstance(x, torch.Tensor):
+        return _int32(x, ub_get_active_shape(h)[0], what)
+    return _ptr(x)
+
+
+def ub_attn_tree(h, q, cache, pages, kv_lens, parents, cu_seqlens, n_seqs, out, lse, cfg, workspace, stream=None):
+    """parents: an int32 value for each active row."""
+    _hold_cached(q, out, cache, cfg)
+    table, ld, per_seq = _table(pages, n_seqs)
+    ws, ws_bytes = _ws_arg(workspace)
+    st = _lib.ub_attn_tree(h, q, cache, table, ld, per_seq, _int32(kv_lens, n_seqs, "kv_lens"),
+                           _rows_int32(h, parents, "parents"), _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), n_seqs, out,
+                           _lse_arg(lse, h, cfg, out), cfg, ws, ws_bytes, _stream(stream))
+    if st:
+        _check(st, h)
+
+
+def ub_kv_compact(h, cache, pages, lens, kept, kept_lens, n_seqs, lens_out, cfg, stream=None):
+    """kept: an int32 [sequences, most] tensor of rising places."""
+    G = (cfg.n_kv_heads, cfg.head_dim)
+    if cache is not None and cache.held != G:
+        _hold_cache(cache, G)
+    table, ld, per_seq = _table(pages, n_seqs)
+    kept, kept_ld, most = _table(kept, n_seqs, "kept")
+    st = _lib.ub_kv_compact(h, cache, table, ld, per_seq, _int32(lens, n_seqs, "lens"), kept, kept_ld, most,
+                            _int32(kept_lens, n_seqs, "kept_lens"), n_seqs, _int32(lens_out, n_seqs, "lens_out"), cfg,
+                            _stream(stream))
+    if st:
+        _check(st, h)
+
+
+def ub_kv_fork(h, refs, pages, lens, n_seqs, parents, pages_out, lens_out, n_out, page_size, stream=None):
+    """refs: an int32 tensor with a count for each page."""
+    table, ld, per_seq = _table(pages, n_seqs)
+    out, out_ld, out_per = _table(pages_out, n_out, "pages_out")
+    st = _lib.ub_kv_fork(h, _int32(refs, 1, "refs"), refs.numel(), table, ld, per_seq, _int32(lens, n_seqs, "lens"), n_seqs,
+                         _int32(parents, n_out, "parents"), out, out_ld, out_per, _int32(lens_out, n_out, "lens_out"),
+                         n_out, page_size, _stream(stream))
+    if st:
+        _check(st, h)
+
+
+def ub_kv_resize_bytes(n_seqs):
+    n = _SZ()
+    _check(_lib.ub_kv_resize_bytes(n_seqs, ctypes.byref(n)))
+    return n.value
+
+
+def ub_kv_resize(h, refs, pages, lens, new_lens, n_seqs, lens_out, copies, page_size, window, workspace, stream=None):
+    """copies: an int32 [sequences, 3] tensor; window: ``make_attn_window(...)`` or None."""
+    table, ld, per_seq = _table(pages, n_seqs)
+    ws, ws_bytes = _ws_arg(workspace)
+    st = _lib.ub_kv_resize(h, _int32(refs, 1, "refs"), refs.numel(), table, ld, per_seq, _int32(lens, n_seqs, "lens"),
+                           _int32(new_lens, n_seqs, "new_lens"), n_seqs, _int32(lens_out, n_seqs, "lens_out"),
+                           _int32(copies, 3 * n_seqs, "copies"), page_size, window, ws, ws_bytes, _stream(stream))
+    if st:
+        _check(st, h)
+
+
+def ub_kv_copy_pages(h, cache, copies, n, cfg, stream=None):
+    G = (cfg.n_kv_heads, cfg.head_dim)
+    if cache is not None and cache.held != G:
+        _hold_cache(cache, G)
+    st = _lib.ub_kv_copy_pages(h, cache, _int32(copies, 3 * n, "copies"), n, cfg, _stream(stream))
     if st:
         _check(st, h)
 

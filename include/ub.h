@@ -474,6 +474,8 @@ UB_API ub_status_t ub_reduce_partials(ub_handle_t h, void* out, int64_t ldo,
  *   ub_attn_prompt_bwd its gradient
  *   ub_attn_decode     attention of one new token per sequence over the paged cache
  *   ub_attn_*_window   the three attention calls under a sliding window
+ *   ub_attn_tree       attention of a tree of drafted tokens over the paged cache
+ *   ub_kv_*            the pages of a cache: shared, given, taken back, copied; accepted tokens
  *
  * Rows.  Every call works on the handle's active rows T (ub_set_active_shape): T rows of
  * every matrix, of which the packed sequences use a prefix.  Sequence i holds rows
@@ -499,6 +501,8 @@ UB_API ub_status_t ub_reduce_partials(ub_handle_t h, void* out, int64_t ldo,
  * on timing.
  */
 #define UB_ATTN_MAX_HEAD_DIM 128
+/* Most rows of a sequence in ub_attn_tree. */
+#define UB_ATTN_MAX_TREE 256
 /* Most first tokens that a window leaves visible. */
 #define UB_ATTN_MAX_SINKS 64
 
@@ -548,6 +552,7 @@ typedef enum {
   UB_ATTN_PROMPT_WINDOW = 3,
   UB_ATTN_PROMPT_WINDOW_BWD = 4,
   UB_ATTN_DECODE_WINDOW = 5,
+  UB_ATTN_TREE = 6,
   UB_ATTN_OP_INT32_RANGE_ = 0x7FFFFFFF
 } ub_attn_op_t;
 
@@ -664,6 +669,113 @@ UB_API ub_status_t ub_attn_decode_window(ub_handle_t h, const ub_heads_t* q,
                                          const ub_attn_window_t* window, const ub_heads_t* out,
                                          float* lse, const ub_attn_cfg_t* cfg, void* workspace,
                                          size_t workspace_bytes, ub_stream_t stream);
+
+/* ---- Drafted tokens ------------------------------------------------------------------------
+ *
+ * A step that verifies drafts: each sequence has some new rows, the nodes of a tree of guesses
+ * about its next tokens.  ub_kv_append_at stores them after the cached tokens and rotates each
+ * by its depth; ub_attn_tree lets each see the cached tokens and the nodes on its own path;
+ * once some path is accepted, ub_kv_compact moves its tokens to the places after the cached
+ * ones, where their rotation already says they are.
+ *
+ * ub_kv_append with the rotation by position past_lens[i] + offsets[t] (offsets: T int32); the
+ * token of row t = cu_seqlens[i] + j is still stored at place past_lens[i] + j. */
+UB_API ub_status_t ub_kv_append_at(ub_handle_t h, const ub_heads_t* q, const ub_heads_t* k,
+                                   const ub_heads_t* v, const ub_heads_t* q_out,
+                                   const ub_heads_t* k_out, const float* inv_freq,
+                                   const int32_t* offsets, const int32_t* cu_seqlens,
+                                   const int32_t* past_lens, int32_t n_seqs,
+                                   const ub_kv_cache_t* cache, const int32_t* page_table,
+                                   int64_t pages_ld, int32_t pages_per_seq,
+                                   const ub_attn_cfg_t* cfg, ub_stream_t stream);
+
+/* Attention of drafted trees.  Sequence i's m = cu_seqlens[i + 1] - cu_seqlens[i] rows are the
+ * last m of its kv_lens[i] cached tokens.  parents[t] is the node before row t on its path, as
+ * its number among the sequence's rows, which is below the row's own; any other value (-1) says
+ * that it follows the last token before the tree.  Row t sees the kv_lens[i] - m tokens before
+ * the tree, and the nodes on its path, itself among them; with u over those,
+ *   lse[h, t] = log sum_u exp(s),   out[t, h] = sum_u exp(s - lse[h, t]) v[u, g].
+ * Rows of one token each (m = 1) attend as in ub_attn_decode; a chain (parents 0, 1, 2, ...) is
+ * a causal chunk after cached tokens.  Rows of no sequence get out 0 and lse -inf.  A sequence
+ * with more than UB_ATTN_MAX_TREE rows, fewer cached tokens than rows, a length past
+ * pages_per_seq pages or a page id outside [0, n_pages) among its length's pages gets NaN in out
+ * and lse.  lse: [n_heads, T] fp32 or NULL. */
+UB_API ub_status_t ub_attn_tree(ub_handle_t h, const ub_heads_t* q, const ub_kv_cache_t* cache,
+                                const int32_t* page_table, int64_t pages_ld,
+                                int32_t pages_per_seq, const int32_t* kv_lens,
+                                const int32_t* parents, const int32_t* cu_seqlens, int32_t n_seqs,
+                                const ub_heads_t* out, float* lse, const ub_attn_cfg_t* cfg,
+                                void* workspace, size_t workspace_bytes, ub_stream_t stream);
+
+/* Moves tokens to the places after their sequence's first lens[i]: for d = 0, 1, ...,
+ * the key and value at place lens[i] + kept[i kept_ld + d] go to place lens[i] + d, as if all
+ * were read before any is written; kept_lens[i] of them, at most kept_per_seq.  A list ends
+ * before an entry that is negative, not above the one before it, or past the sequence's
+ * pages_per_seq pages.  lens_out[i] becomes lens[i] (bounded by 0 and the table) and the number
+ * of its entries; it must not be lens.  Tokens on a page whose id is outside [0, n_pages) are
+ * neither read nor written.  The places from lens[i] on must be on pages that the sequence
+ * shares with none (ub_kv_resize sees to it).  Accepted nodes of a tree are one such list;
+ * what an eviction keeps, with lens 0, is another. */
+UB_API ub_status_t ub_kv_compact(ub_handle_t h, const ub_kv_cache_t* cache,
+                                 const int32_t* page_table, int64_t pages_ld,
+                                 int32_t pages_per_seq, const int32_t* lens, const int32_t* kept,
+                                 int64_t kept_ld, int32_t kept_per_seq, const int32_t* kept_lens,
+                                 int32_t n_seqs, int32_t* lens_out, const ub_attn_cfg_t* cfg,
+                                 ub_stream_t stream);
+
+/* ---- The pages of a cache ------------------------------------------------------------------
+ *
+ * refs[n_pages] (int32 in device memory, 16-byte aligned) counts the table rows that hold each
+ * page; a page of count 0 is free.  The counts are all there is of a pool: a program starts
+ * with zeros and empty rows (lens 0).  A row of `len` tokens holds the pages of its first
+ * ceil(len / page_size) entries; entries of -1 among them (which a window left behind) hold
+ * none.  Lengths are bounded by 0 and the row's entries, ids outside [0, n_pages) are skipped,
+ * so that nothing outside the caller's arrays is touched; a table that disagrees with the counts
+ * gives counts that disagree.  Calls on one pool must be ordered, on one stream or by events;
+ * of a handle they use the device binding and the error message.
+ *
+ * ub_kv_fork: row i of table_out becomes a copy of row parents[i] of table (an empty row if that
+ * is not in [0, n_seqs)), lens_out[i] its length, entries past it -1; the rows of table_out take
+ * the place of all rows of table, so that a page's count changes by the rows that now hold it
+ * less those that did.  Forks share their parent's pages; rows that are nobody's parent give
+ * theirs back; a permutation reorders.  table_out has at least as many entries per row, and
+ * neither it nor lens_out may overlap the inputs. */
+UB_API ub_status_t ub_kv_fork(ub_handle_t h, int32_t* refs, int64_t n_pages,
+                              const int32_t* page_table, int64_t pages_ld, int32_t pages_per_seq,
+                              const int32_t* lens, int32_t n_seqs, const int32_t* parents,
+                              int32_t* table_out, int64_t out_ld, int32_t out_per_seq,
+                              int32_t* lens_out, int32_t n_out, int32_t page_size,
+                              ub_stream_t stream);
+
+/* Bytes of workspace ub_kv_resize needs for n_seqs rows (16-byte aligned, no preparation). */
+UB_API ub_status_t ub_kv_resize_bytes(int32_t n_seqs, size_t* bytes);
+
+/* Gives every row pages for new_lens[i] tokens, or takes back those past it.
+ *   - A row that grows gets the free pages of the lowest numbers, rows and their entries in
+ *     order.  If it has tokens on a last page that other rows hold too, it gives that up and
+ *     gets one of its own; copies[3 i ..] = (old page, new page, tokens on it), for
+ *     ub_kv_copy_pages.  All other rows' copies are (-1, -1, 0).
+ *   - Where the free pages do not suffice, rows are served in order up to the first that would
+ *     not get all its pages; that one and all later ones that need a page keep what they have.
+ *     So does a row whose new length is past its table's entries.
+ *   - window (NULL: none): entries of a row that hold only tokens which a token at its last
+ *     position and later ones do not see give their pages back and become -1.
+ * Pages given up in a call are free for the next one.  lens_out[i] is the row's length after
+ * the call; it may be lens.  copies: n_seqs x 3 int32. */
+UB_API ub_status_t ub_kv_resize(ub_handle_t h, int32_t* refs, int64_t n_pages,
+                                int32_t* page_table, int64_t pages_ld, int32_t pages_per_seq,
+                                const int32_t* lens, const int32_t* new_lens, int32_t n_seqs,
+                                int32_t* lens_out, int32_t* copies, int32_t page_size,
+                                const ub_attn_window_t* window, void* workspace,
+                                size_t workspace_bytes, ub_stream_t stream);
+
+/* For each of n records (source page, target page, tokens): the first tokens of the source's
+ * keys and values go to the target, all key-value heads.  A record with a page outside
+ * [0, n_pages), equal pages or no tokens copies nothing; more tokens than a page holds are a
+ * page.  A target may occur in no other record.  One call for each layer's cache. */
+UB_API ub_status_t ub_kv_copy_pages(ub_handle_t h, const ub_kv_cache_t* cache,
+                                    const int32_t* copies, int32_t n, const ub_attn_cfg_t* cfg,
+                                    ub_stream_t stream);
 
 /* Per-launch kernel timing.  enable 1: every GEMM and reduction launch is bracketed by HIP
  * events on the stream it is launched on: a start event recorded before it, and an end
