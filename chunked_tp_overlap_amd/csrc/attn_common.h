@@ -113,6 +113,12 @@ struct ColFrag {
     const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, q + 16 * L::RB));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   }
+  // rows 0 .. 15 alone: 4 elements, twice
+  __device__ bf16x8 read_half(int off, int d) const {
+    const uint32_t at = ((uint32_t)(size_t)LDS_PTR(const unsigned char, p) + off) ^ (32 * d);
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, at));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, lo, 0, 1, 2, 3, 0, 1, 2, 3));
+  }
 };
 
 // Max (sum) over the four lanes that share a column: lanes c, c + 16, c + 32, c + 48.

@@ -48,22 +48,30 @@ struct TreeParams {
   float2* stat;    // [2 ranges, G, COLS]: maximum (base 2, scaled), sum
 };
 
-template <int DS_, int QF_, int RW_, int KG_, int BN_, bool F8_>
+constexpr int BN = 64;         // keys of a tile: one to a lane in the lookup of their pages
+
+template <int DS_, int QF_, int RW_, bool F8_>
 struct Shape {
-  static constexpr int DS = DS_, QF = QF_, RW = RW_, KG = KG_, BN = BN_;
+  static constexpr int DS = DS_, QF = QF_, RW = RW_, KG = NW / RW;
   static constexpr bool F8 = F8_;
   using L = Tile<DS>;
-  static_assert(RW * KG == NW && BN / KG % 32 == 0 && BN / KG <= 64, "keys of a group: 32 or 64");
-  static constexpr int COLS = 16 * QF * RW, TILE = BN * L::RB;
-  static constexpr int STAGES = BN <= 64 ? 2 : 1;
+  static constexpr int COLS = 16 * QF * RW, TILE = BN * L::RB, STAGE = 2 * TILE;
   static constexpr int EB = F8 ? 1 : 2;
   static constexpr int PPR = F8 ? L::CPR / 2 : L::CPR;  // 16-byte pieces of a row, as loaded
-  static constexpr int RPL = 64 * NW / PPR;             // rows of a load by all threads
-  static constexpr int N = BN / RPL;                    // loads of a thread, of keys and of values
+  static constexpr int RPL = 64 / PPR;                  // rows of a wave's load
+  static constexpr int N = BN / RPL / NW;               // loads of a wave, of keys and of values
   static constexpr int JOIN = KG > 1 ? NW * L::DB * QF * 1024 + NW * QF * 128 : 0;
-  static constexpr int KV = STAGES * 2 * TILE > JOIN ? STAGES * 2 * TILE : JOIN;
+  static constexpr int KV = 2 * STAGE > JOIN ? 2 * STAGE : JOIN;
   static constexpr int LDS = KV + MAX_NODES * WORDS * 8 + MAX_NODES * 4;
 };
+
+// What rows past the end and pieces past head_dim are loaded from.
+__device__ const u32x4 ZEROS = {0, 0, 0, 0};
+
+// 16 bytes per lane from its own address into LDS at lds + 16 * lane.
+__device__ inline void gather16(const unsigned char* from, uint32_t lds) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory");
+}
 
 // A sequence's rows and tokens.  Not good: more nodes than MAX_NODES, fewer cached tokens than
 // nodes, or more than its row of the table holds.
@@ -86,7 +94,7 @@ __device__ inline int64_t tiles_of(const TreeParams& p, int i) {
   const Seq s = sequence(p, i);
   if (!s.good || s.m == 0) return 0;
   const int64_t cols = (int64_t)s.m * (p.a.H / p.a.G);
-  return (cols + S::COLS - 1) / S::COLS * ((s.len + S::BN - 1) / S::BN);
+  return (cols + S::COLS - 1) / S::COLS * ((s.len + BN - 1) / BN);
 }
 
 // Inclusive prefix sum over the wave.
@@ -117,10 +125,22 @@ __device__ inline uint64_t seen_bits(const uint64_t* path, int at) {
   return x;
 }
 
+// The wave's LDS writes are done, then every wave's; direct or register loads stay in flight.
+__device__ inline void lds_barrier() { __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// acc + A B over 32 keys, or over 16 whose halves of the operands hold the first 4 elements.
+template <bool HALF>
+__device__ inline f32x4 product(bf16x8 a, bf16x8 b, f32x4 acc) {
+  if (!HALF) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+  const i16x4 x = __builtin_bit_cast(i16x4, __builtin_shufflevector(a, a, 0, 1, 2, 3));
+  const i16x4 y = __builtin_bit_cast(i16x4, __builtin_shufflevector(b, b, 0, 1, 2, 3));
+  return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(x, y, acc, 0, 0, 0);
+}
+
 template <class S>
 __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
-  constexpr int DS = S::DS, QF = S::QF, RW = S::RW, KG = S::KG, BN = S::BN, TILE = S::TILE, N = S::N, PPR = S::PPR;
-  constexpr int COLS = S::COLS, EB = S::EB;
+  constexpr int DS = S::DS, QF = S::QF, RW = S::RW, KG = S::KG, TILE = S::TILE, STAGE = S::STAGE, N = S::N;
+  constexpr int COLS = S::COLS, EB = S::EB, PPR = S::PPR, RPL = S::RPL;
   constexpr bool F8 = S::F8;
   constexpr int KB = BN / KG / 16;  // blocks of 16 keys of a group
   using L = Tile<DS>;
@@ -156,8 +176,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
 
   const unsigned char* kb = static_cast<const unsigned char*>(a.cache.k) + kvh * a.cache.hs * EB;
   const unsigned char* vb = static_cast<const unsigned char*>(a.cache.v) + kvh * a.cache.hs * EB;
-  const int piece = threadIdx.x % PPR, prow = threadIdx.x / PPR;  // of a thread's loads
-  const bool in_row = piece * (16 / EB) < a.D;
+  const int piece = lane % PPR;
+  const uint32_t lds = lds_addr(smem);
   RowFrag<DS> kf;
   ColFrag<DS> vf;
   kf.init(smem + kg * (BN / KG) * L::RB, lane);
@@ -216,50 +236,44 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
         for (int s = 0; s < DS; ++s) q[f][s] = load_row8(row + 32 * s + 8 * g, live && 32 * s + 8 * g < a.D);
       }
       bool lost = false;  // a page that is not there
-
-      u32x4 kreg[N], vreg[N];
-      auto fetch = [&](int j) {
-        // a lane looks up a token, the threads take their rows' places from it
-        int64_t place[(BN + 63) / 64];
-#pragma unroll
-        for (int b = 0; b < (BN + 63) / 64; ++b) {
-          const int t = min(j * BN + b * 64 + lane, sq.len - 1);
-          const int64_t at = token_offset(t, pages[page_entry(t, a.cache.page_size, a.pages_per_seq)], a.cache.n_pages,
-                                          a.cache.page_size, a.cache.ps, a.cache.ts);
-          lost = lost || at < 0;
-          place[b] = max(at, (int64_t)0) * EB;
-        }
+      // A lane looks up a token: the page's id, then, with the tile before in use, its place.
+      int id = 0;
+      auto look = [&](int j) { id = pages[page_entry(min(j * BN + lane, sq.len - 1), a.cache.page_size, a.pages_per_seq)]; };
+      u32x4 kreg[N], vreg[N];  // E4M3 alone
+      auto fetch = [&](int j, int stage) {
+        const int t = min(j * BN + lane, sq.len - 1);
+        int64_t place = token_offset(t, id, a.cache.n_pages, a.cache.page_size, a.cache.ps, a.cache.ts);
+        lost = lost || place < 0;
+        place = max(place, (int64_t)0) * EB;
+        const int lo = (int)(uint32_t)place, hi = (int)(place >> 32);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const int r = i * S::RPL + prow;
-          int64_t at = __shfl(place[0], r & 63);
-          if (BN > 64 && r >= 64) at = __shfl(place[(BN + 63) / 64 - 1], r & 63);
-          at += (in_row ? piece : 0) * 16;
-          kreg[i] = *GLOBAL_PTR(const u32x4, kb + at);
-          vreg[i] = *GLOBAL_PTR(const u32x4, vb + at);
+          const int r = (i * NW + wave) * RPL + lane / PPR;
+          const int chunk = F8 ? piece : piece ^ L::swz(r);
+          const int64_t at = (int64_t)(((uint64_t)(uint32_t)__shfl(hi, r) << 32) | (uint32_t)__shfl(lo, r)) + chunk * 16;
+          const bool in = chunk * (16 / EB) < a.D && j * BN + r < sq.len;
+          const unsigned char* zeros = reinterpret_cast<const unsigned char*>(&ZEROS);
+          const unsigned char *k = in ? kb + at : zeros, *v = in ? vb + at : zeros;
+          if (F8) {
+            kreg[i] = *GLOBAL_PTR(const u32x4, k);
+            vreg[i] = *GLOBAL_PTR(const u32x4, v);
+          } else {
+            const uint32_t to = lds + stage + (i * NW + wave) * 1024;
+            gather16(k, to);
+            gather16(v, to + TILE);
+          }
         }
       };
-      // rows past the end and pieces past head_dim: zeros, as 0 times anything is not 0
-      auto keep = [&](int j, int stage) {
-        unsigned char* kt = smem + stage * 2 * TILE;
+      auto keep = [&](int stage) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const int r = i * S::RPL + prow;
-          const bool in = in_row && j * BN + r < sq.len;
-          const u32x4 zero = {0, 0, 0, 0};
-          const u32x4 k = in ? kreg[i] : zero, v = in ? vreg[i] : zero;
-          unsigned char* at = kt + r * L::RB;
-          if (F8) {
-            const int s0 = ((2 * piece) ^ L::swz(r)) * 16, s1 = ((2 * piece + 1) ^ L::swz(r)) * 16;
-            *LDS_PTR(u32x4, at + s0) = cvt8(k[0], k[1]);
-            *LDS_PTR(u32x4, at + s1) = cvt8(k[2], k[3]);
-            *LDS_PTR(u32x4, at + TILE + s0) = cvt8(v[0], v[1]);
-            *LDS_PTR(u32x4, at + TILE + s1) = cvt8(v[2], v[3]);
-          } else {
-            const int s0 = (piece ^ L::swz(r)) * 16;
-            *LDS_PTR(u32x4, at + s0) = k;
-            *LDS_PTR(u32x4, at + TILE + s0) = v;
-          }
+          const int r = (i * NW + wave) * RPL + lane / PPR;
+          unsigned char* at = smem + stage + r * L::RB;
+          const int s0 = ((2 * piece) ^ L::swz(r)) * 16, s1 = ((2 * piece + 1) ^ L::swz(r)) * 16;
+          *LDS_PTR(u32x4, at + s0) = cvt8(kreg[i][0], kreg[i][1]);
+          *LDS_PTR(u32x4, at + s1) = cvt8(kreg[i][2], kreg[i][3]);
+          *LDS_PTR(u32x4, at + TILE + s0) = cvt8(vreg[i][0], vreg[i][1]);
+          *LDS_PTR(u32x4, at + TILE + s1) = cvt8(vreg[i][2], vreg[i][3]);
         }
       };
 
@@ -344,70 +358,62 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
               }
             l[f] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           }
+          // products over 32 keys, or the 16 that each of four groups has
+          constexpr int NT = KB > 1 ? KB / 2 : 1;
 #pragma unroll
-          for (int t = 0; t < KB / 2; ++t) {
+          for (int t = 0; t < NT; ++t) {
             bf16x8 pf[QF];
 #pragma unroll
-            for (int f = 0; f < QF; ++f) pf[f] = pack8(s[2 * t][f], s[2 * t + 1][f]);
-            if (CAREFUL && DRAFTED) {
-              // every column by itself, from the keys that it sees
-#pragma unroll
-              for (int d = 0; d < L::DB; ++d)
-#pragma unroll
-                for (int f = 0; f < QF; ++f) {
-                  const u32x4 v = __builtin_bit_cast(u32x4, vf.read(off, t, d));
-                  f32x4 r = o[d][f];
-#pragma unroll 1
-                  for (int c = 0; c < 16; ++c) {
-                    const uint64_t w = __shfl(see[f], c) >> (32 * t + 4 * g);
-                    u32x4 x = v;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                      const uint32_t two = (uint32_t)(w >> ((i & 1) * 2 + (i >> 1) * 16));
-                      x[i] &= (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
-                    }
-                    const f32x4 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), pf[f], o[d][f], 0, 0, 0);
-                    if (col == c) r = y;
-                  }
-                  o[d][f] = r;
-                }
-              continue;
-            }
+            for (int f = 0; f < QF; ++f) pf[f] = pack8(s[KB > 1 ? 2 * t : 0][f], s[KB > 1 ? 2 * t + 1 : 0][f]);
 #pragma unroll
             for (int d = 0; d < L::DB; ++d) {
-              const bf16x8 vv = vf.read(off, t, d);
+              const bf16x8 vv = KB > 1 ? vf.read(off, t, d) : vf.read_half(off, d);
 #pragma unroll
-              for (int f = 0; f < QF; ++f)
-                o[d][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[f], o[d][f], 0, 0, 0);
+              for (int f = 0; f < QF; ++f) {
+                if (!(CAREFUL && DRAFTED)) {
+                  o[d][f] = product<KB == 1>(vv, pf[f], o[d][f]);
+                  continue;
+                }
+                // every column by itself, from the keys that it sees
+                f32x4 r = o[d][f];
+#pragma unroll 1
+                for (int c = 0; c < 16; ++c) {
+                  const uint64_t w = __shfl(see[f], c) >> (32 * t + 4 * g);
+                  u32x4 x = __builtin_bit_cast(u32x4, vv);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const uint32_t two = (uint32_t)(w >> ((i & 1) * 2 + (i >> 1) * 16));
+                    x[i] &= (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
+                  }
+                  const f32x4 y = product<KB == 1>(__builtin_bit_cast(bf16x8, x), pf[f], o[d][f]);
+                  if (col == c) r = y;
+                }
+                o[d][f] = r;
+              }
             }
           }
         };
         const int full = min(max(past / BN, j0), j1);  // tiles of tokens that every row sees
-        fetch(j0);
         int stage = 0;
-        if (S::STAGES == 2) {
-          keep(j0, 0);
-          if (j0 + 1 < j1) fetch(j0 + 1);
-          __syncthreads();
-        }
+        look(j0);
+        fetch(j0, 0);
+        if (j0 + 1 < j1) look(j0 + 1);
+        // bf16: the next tile's direct loads are in flight while this one is used; E4M3: its
+        // registers' loads are.  In both each of the two stages is written after the barrier that
+        // ends its last use.
         auto turn = [&](int j, auto drafted) __attribute__((always_inline)) {
-          if (S::STAGES == 2) {
-            if (j + 1 < j1) keep(j + 1, stage ^ 1);
-            if (j + 2 < j1) fetch(j + 2);
-            step(j, stage * 2 * TILE, drafted);
-            __syncthreads();
-            stage ^= 1;
-          } else {
-            keep(j, 0);
-            if (j + 1 < j1) fetch(j + 1);
-            __syncthreads();
-            step(j, 0, drafted);
-            __syncthreads();
-          }
+          if (F8) keep(stage);
+          else wait_vmcnt_and_barrier<0>();
+          if (j + 1 < j1) fetch(j + 1, stage ^ STAGE);
+          if (j + 2 < j1) look(j + 2);
+          if (F8) lds_barrier();
+          step(j, stage, drafted);
+          stage ^= STAGE;
         };
         int j = j0;
         for (; j < full; ++j) turn(j, std::false_type{});
         for (; j < j1; ++j) turn(j, std::true_type{});
+        __syncthreads();
         return bad;
       };
       if (any_wave<NW>(pass(std::false_type{}), smem, wave, lane)) pass(std::true_type{});
@@ -620,10 +626,10 @@ template <int DS, bool F8>
 hipError_t choose(const TreeArgs& a, hipStream_t s) {
   // by the columns of a sequence, on average: the host knows no more
   const int64_t cols = a.seqs.n > 0 ? ((int64_t)a.seqs.T * (a.H / a.G) + a.seqs.n - 1) / a.seqs.n : 1;
-  if (cols <= 16) return run<Shape<DS, 1, 1, 4, 128, F8>>(a, s);
-  if (cols <= 32) return run<Shape<DS, 2, 1, 4, 128, F8>>(a, s);
-  if (cols <= 64) return run<Shape<DS, 2, 2, 2, 64, F8>>(a, s);
-  return run<Shape<DS, 2, 4, 1, 64, F8>>(a, s);
+  if (cols <= 16) return run<Shape<DS, 1, 1, F8>>(a, s);
+  if (cols <= 32) return run<Shape<DS, 2, 1, F8>>(a, s);
+  if (cols <= 64) return run<Shape<DS, 2, 2, F8>>(a, s);
+  return run<Shape<DS, 2, 4, F8>>(a, s);
 }
 
 template <bool F8>
