@@ -15,8 +15,10 @@
 // there as bf16 into LDS, where all waves read their fragments (attn_common.h).  RW waves take
 // 16 QF columns each; KG groups of them take parts of a tile's keys, where columns are few.
 //
-// The softmax has a reference per column that follows the maximum only when a score passes it by
-// 2^8, so that most tiles rescale nothing.
+// The softmax's reference is the maximum of the first tile that a column sees a key of, as in
+// attn_prompt.hip: where a sum passes 2^60, or what is hidden from a column is not finite, the
+// pass over the segment's tiles is repeated with the running maximum, column by column where it
+// has to be.
 //
 // The nodes that a node sees are bits, set once per strip by following the parents in LDS; only
 // the tiles of drafted tokens look at them.
@@ -35,13 +37,14 @@ constexpr int WORDS = MAX_NODES / 64;
 constexpr int NW = 4;
 constexpr int ITEMS = 512;     // workgroups that run at once: two on each CU
 constexpr int MIN_TILES = 4;   // tiles that a workgroup takes at least, where there are so many
-constexpr float RISE = 8.0f;   // scores may pass the reference by so much, in powers of 2
+constexpr float MOST = 0x1p60f;  // a lane's sum beyond which the pass is done again
 
 struct TreeParams {
   TreeArgs a;
   float c;         // scale * log2(e) (/ k_scale)
   float v_inv;     // 1 / v_scale
   int32_t cap;     // tokens the page table can hold per sequence
+  uint32_t page_mul, page_shift;  // t / page_size = (umulhi(t, page_mul) + t) >> page_shift, t < 2^30
   int32_t ranges;  // most ranges the tiles are dealt in; a workgroup for each and key-value head
   int2* parts_of;  // [strips]: a strip's first part's row of `part`, and its number of parts
   float* part;     // [2 ranges, G, COLS, D]: parts of a range's first and last strip
@@ -238,22 +241,27 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
       bool lost = false;  // a page that is not there
       // A lane looks up a token: the page's id, then, with the tile before in use, its place.
       int id = 0;
-      auto look = [&](int j) { id = pages[page_entry(min(j * BN + lane, sq.len - 1), a.cache.page_size, a.pages_per_seq)]; };
+      auto look = [&](int j) {
+        const uint32_t t = min(j * BN + lane, sq.len - 1);
+        id = pages[(__umulhi(t, p.page_mul) + t) >> p.page_shift];  // inside the row: len <= cap
+      };
       u32x4 kreg[N], vreg[N];  // E4M3 alone
       auto fetch = [&](int j, int stage) {
-        const int t = min(j * BN + lane, sq.len - 1);
-        int64_t place = token_offset(t, id, a.cache.n_pages, a.cache.page_size, a.cache.ps, a.cache.ts);
-        lost = lost || place < 0;
-        place = max(place, (int64_t)0) * EB;
+        const uint32_t t = min(j * BN + lane, sq.len - 1);
+        const uint32_t o = t - ((__umulhi(t, p.page_mul) + t) >> p.page_shift) * (uint32_t)a.cache.page_size;
+        const bool there = (uint32_t)id < (uint32_t)a.cache.n_pages;
+        lost = lost || !there;
+        const int64_t place = ((there ? id : 0) * a.cache.ps + o * a.cache.ts) * EB;
         const int lo = (int)(uint32_t)place, hi = (int)(place >> 32);
+        const bool all = (j + 1) * BN <= sq.len && a.D == 32 * DS;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int r = (i * NW + wave) * RPL + lane / PPR;
           const int chunk = F8 ? piece : piece ^ L::swz(r);
           const int64_t at = (int64_t)(((uint64_t)(uint32_t)__shfl(hi, r) << 32) | (uint32_t)__shfl(lo, r)) + chunk * 16;
-          const bool in = chunk * (16 / EB) < a.D && j * BN + r < sq.len;
-          const unsigned char* zeros = reinterpret_cast<const unsigned char*>(&ZEROS);
-          const unsigned char *k = in ? kb + at : zeros, *v = in ? vb + at : zeros;
+          const unsigned char *k = kb + at, *v = vb + at;
+          if (!all && !(chunk * (16 / EB) < a.D && j * BN + r < sq.len))
+            k = v = reinterpret_cast<const unsigned char*>(&ZEROS);
           if (F8) {
             kreg[i] = *GLOBAL_PTR(const u32x4, k);
             vreg[i] = *GLOBAL_PTR(const u32x4, v);
@@ -279,10 +287,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
 
       f32x4 o[L::DB][QF];
       float m[QF], l[QF];
-      // All tiles of the segment; true if a hidden value is not finite, unless it is CAREFUL of
-      // them (0 times such a value would be NaN).
-      auto pass = [&](auto careful) __attribute__((always_inline)) {
-        constexpr bool CAREFUL = decltype(careful)::value;
+      // All tiles of the segment.  FIXED: the reference is the first tile's maximum, and hidden
+      // values are finite (0 times another would be NaN); true where that will not do.
+      auto pass = [&](auto fixed) __attribute__((always_inline)) {
+        constexpr bool FIXED = decltype(fixed)::value;
         bool bad = false;
 #pragma unroll
         for (int f = 0; f < QF; ++f) {
@@ -291,8 +299,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
 #pragma unroll
           for (int d = 0; d < L::DB; ++d) o[d][f] = f32x4{0, 0, 0, 0};
         }
-        auto step = [&](int j, int off, auto drafted) __attribute__((always_inline)) {
-          constexpr bool DRAFTED = decltype(drafted)::value;  // tiles that hold drafted tokens
+        // DRAFTED: tiles that hold drafted tokens; FIRST: or a column's first
+        auto step = [&](int j, int off, auto drafted, auto begins) __attribute__((always_inline)) {
+          constexpr bool DRAFTED = decltype(drafted)::value, FIRST = decltype(begins)::value;
           f32x4 s[KB][QF];
 #pragma unroll
           for (int b = 0; b < KB; ++b)
@@ -320,34 +329,34 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
                 for (int i = 0; i < 4; ++i)
                   if (!((mine >> (16 * b + i)) & 1)) s[b][f][i] = -INFINITY;
             }
-            if (!CAREFUL) bad = bad || not_finite<TILE, NW>(smem + off + TILE, wave, lane);
+            if (FIXED) bad = bad || not_finite<TILE, NW>(smem + off + TILE, wave, lane);
           }
-          bool rises = false;
-          float top[QF];
-#pragma unroll
-          for (int f = 0; f < QF; ++f) {
-            float x = s[0][f][0];
-#pragma unroll
-            for (int b = 0; b < KB; ++b)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) x = fmaxf(x, s[b][f][i]);
-            top[f] = col_max(x);
-            rises = rises || (top[f] - m[f]) * p.c > RISE || (m[f] == -INFINITY && top[f] > -INFINITY);
-          }
-          if (__ballot(rises)) {
+          if (!FIXED || FIRST) {
 #pragma unroll
             for (int f = 0; f < QF; ++f) {
-              const float x = fmaxf(top[f], m[f]);
-              const float r = exp2_(m[f] * p.c - (x == -INFINITY ? 0.0f : x * p.c));  // 0 the first time
-              m[f] = x;
-              l[f] *= r;
+              float x = s[0][f][0];
 #pragma unroll
-              for (int d = 0; d < L::DB; ++d) o[d][f] *= r;
+              for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x = fmaxf(x, s[b][f][i]);
+              x = col_max(x);
+              if (FIXED) {
+                // no score, though the column sees a key
+                bad = bad || (m[f] == -INFINITY && x == -INFINITY && (!DRAFTED || see[f] != 0));
+                m[f] = m[f] == -INFINITY ? x : m[f];
+              } else {
+                x = fmaxf(x, m[f]);
+                const float r = exp2_(m[f] * p.c - (x == -INFINITY ? 0.0f : x * p.c));  // 0 the first time
+                m[f] = x;
+                l[f] *= r;
+#pragma unroll
+                for (int d = 0; d < L::DB; ++d) o[d][f] *= r;
+              }
             }
           }
 #pragma unroll
           for (int f = 0; f < QF; ++f) {
-            const float base = m[f] == -INFINITY ? 0.0f : m[f] * p.c;
+            const float base = (!FIXED || FIRST) && m[f] == -INFINITY ? 0.0f : m[f] * p.c;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int b = 0; b < KB; ++b)
@@ -370,7 +379,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
               const bf16x8 vv = KB > 1 ? vf.read(off, t, d) : vf.read_half(off, d);
 #pragma unroll
               for (int f = 0; f < QF; ++f) {
-                if (!(CAREFUL && DRAFTED)) {
+                if (FIXED || !DRAFTED) {
                   o[d][f] = product<KB == 1>(vv, pf[f], o[d][f]);
                   continue;
                 }
@@ -401,22 +410,35 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
         // bf16: the next tile's direct loads are in flight while this one is used; E4M3: its
         // registers' loads are.  In both each of the two stages is written after the barrier that
         // ends its last use.
-        auto turn = [&](int j, auto drafted) __attribute__((always_inline)) {
+        auto turn = [&](int j, auto drafted, auto begins) __attribute__((always_inline)) {
           if (F8) keep(stage);
           else wait_vmcnt_and_barrier<0>();
           if (j + 1 < j1) fetch(j + 1, stage ^ STAGE);
           if (j + 2 < j1) look(j + 2);
           if (F8) lds_barrier();
-          step(j, stage, drafted);
+          step(j, stage, drafted, begins);
           stage ^= STAGE;
         };
         int j = j0;
-        for (; j < full; ++j) turn(j, std::false_type{});
-        for (; j < j1; ++j) turn(j, std::true_type{});
+        if (FIXED && j < full) turn(j++, std::false_type{}, std::true_type{});
+        for (; j < full; ++j) turn(j, std::false_type{}, std::false_type{});
+        for (; j < j1; ++j) turn(j, std::true_type{}, std::true_type{});
+        if (FIXED) {
+          float z = 0.0f;  // NaN if an output is not finite
+#pragma unroll
+          for (int f = 0; f < QF; ++f) {
+            bad = bad || !(l[f] < MOST);
+#pragma unroll
+            for (int d = 0; d < L::DB; ++d)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) z += o[d][f][i] * 0.0f;
+          }
+          bad = bad || z != 0.0f;
+        }
         __syncthreads();
         return bad;
       };
-      if (any_wave<NW>(pass(std::false_type{}), smem, wave, lane)) pass(std::true_type{});
+      if (any_wave<NW>(pass(std::true_type{}), smem, wave, lane)) pass(std::false_type{});
       lost = __ballot(lost) != 0;
 
       float base[QF], sum[QF];
@@ -606,6 +628,9 @@ hipError_t run(const TreeArgs& a, hipStream_t s) {
   p.c = a.scale * LOG2E * (S::F8 ? 1.0f / a.cache.k_scale : 1.0f);
   p.v_inv = S::F8 ? 1.0f / a.cache.v_scale : 1.0f;
   p.ranges = max_ranges(a.G);
+  const uint32_t page = (uint32_t)a.cache.page_size;
+  while ((1ull << p.page_shift) < page) ++p.page_shift;
+  p.page_mul = (uint32_t)(((((1ull << p.page_shift) - page) << 32) / page) + 1);
   const int64_t blocks = (int64_t)p.ranges * a.G, rows = 2 * blocks * S::COLS;
   p.stat = static_cast<float2*>(a.ws);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + rows * 8);
