@@ -4,16 +4,19 @@
 //   s_u = scale q . k_u,  lse = log sum_u exp(s_u),  out = sum_u exp(s_u - lse) v_u
 //
 // The rows of a key-value head's query heads are the columns of one product: a sequence of m
-// nodes has m (n_heads / n_kv_heads) of them, in strips of COLS.  A strip walks the sequence's
-// keys in tiles of BN; tiles of all strips of all sequences, one after another, are dealt in
-// equal contiguous ranges over as many workgroups as run at once (as the units of
-// attn_decode.hip).  A workgroup finishes a strip that lies whole in its range; of the first and
-// the last it may hold a part (maximum, sum and unnormalised output, fp32), which goes to the
-// workspace, and attn_tree_join adds a strip's parts in order.
+// nodes has m (n_heads / n_kv_heads) of them, in strips of COLS.  A workgroup takes one strip and
+// some of the sequence's tiles of BN keys.  The lengths are on the device, so the cut is made
+// there: sequence i's tiles go in k_i = ceil(tiles_i / c) equal parts, with the smallest c for
+// which all strips' parts are as many workgroups as run at once (c no smaller than MIN_TILES;
+// one part each where the strips are more than that).  The strips of one part of a sequence read
+// the same keys at the same time, so they are neighbours on one XCD, whose L2 then serves all
+// but one of them.  A strip in one part is finished by its workgroup; others leave parts (maximum,
+// sum and unnormalised output, fp32) in the workspace, and attn_tree_join adds them in order.
 //
-// Keys and values come from their pages into registers while the tile before is used, and from
-// there as bf16 into LDS, where all waves read their fragments (attn_common.h).  RW waves take
-// 16 QF columns each; KG groups of them take parts of a tile's keys, where columns are few.
+// Keys and values come from their pages (a lane looks up a token, a tile ahead): bf16 by direct
+// loads to LDS, E4M3 by registers that are stored there as bf16, so that all waves read their
+// fragments as in attn_common.h.  RW waves take 16 QF columns each; KG groups of them take parts
+// of a tile's keys, where columns are few.
 //
 // The softmax's reference is the maximum of the first tile that a column sees a key of, as in
 // attn_prompt.hip: where a sum passes 2^60, or what is hidden from a column is not finite, the
@@ -36,7 +39,7 @@ constexpr int MAX_NODES = UB_ATTN_MAX_TREE;
 constexpr int WORDS = MAX_NODES / 64;
 constexpr int NW = 4;
 constexpr int ITEMS = 512;     // workgroups that run at once: two on each CU
-constexpr int MIN_TILES = 4;   // tiles that a workgroup takes at least, where there are so many
+constexpr int MIN_TILES = 4;   // tiles of a part at least, where there are so many
 constexpr float MOST = 0x1p60f;  // a lane's sum beyond which the pass is done again
 
 struct TreeParams {
@@ -45,10 +48,10 @@ struct TreeParams {
   float v_inv;     // 1 / v_scale
   int32_t cap;     // tokens the page table can hold per sequence
   uint32_t page_mul, page_shift;  // t / page_size = (umulhi(t, page_mul) + t) >> page_shift, t < 2^30
-  int32_t ranges;  // most ranges the tiles are dealt in; a workgroup for each and key-value head
-  int2* parts_of;  // [strips]: a strip's first part's row of `part`, and its number of parts
-  float* part;     // [2 ranges, G, COLS, D]: parts of a range's first and last strip
-  float2* stat;    // [2 ranges, G, COLS]: maximum (base 2, scaled), sum
+  int32_t at_once;  // workgroups of a key-value head that run at once
+  int4* seqs;       // [n]: a sequence's first workgroup among `w` of a head, its k_i, its strips, w
+  float* part;      // [at_once G, COLS, D]: a workgroup's output where a strip has several parts
+  float2* stat;     // [at_once G, COLS]: maximum (base 2, scaled), sum
 };
 
 constexpr int BN = 64;         // keys of a tile: one to a lane in the lookup of their pages
@@ -91,29 +94,54 @@ __device__ inline Seq sequence(const TreeParams& p, int i) {
   return s;
 }
 
+// Strips and tiles of a sequence: none of one that is not good, or has no rows.
+struct Work {
+  int strips, tiles;
+};
 template <class S>
-__device__ inline int64_t tiles_of(const TreeParams& p, int i) {
-  if (i >= p.a.seqs.n) return 0;
+__device__ inline Work work_of(const TreeParams& p, int i) {
+  if (i >= p.a.seqs.n) return Work{0, 0};
   const Seq s = sequence(p, i);
-  if (!s.good || s.m == 0) return 0;
-  const int64_t cols = (int64_t)s.m * (p.a.H / p.a.G);
-  return (cols + S::COLS - 1) / S::COLS * ((s.len + BN - 1) / BN);
+  if (!s.good || s.m == 0) return Work{0, 0};
+  return Work{(s.m * (p.a.H / p.a.G) + S::COLS - 1) / S::COLS, (s.len + BN - 1) / BN};
 }
 
-// Inclusive prefix sum over the wave.
-__device__ inline int64_t wave_scan64(int64_t v) {
+constexpr int MANY = 1 << 20;  // counts past this only have to stay past it
+__device__ inline int parts_for(Work w, int c) {  // strips k_i, of one sequence
+  return w.strips == 0 ? 0 : (int)min((int64_t)w.strips * ((w.tiles + c - 1) / c), (int64_t)MANY);
+}
+
+// Tiles to a part, and the workgroups that makes for a head.
+struct Cut {
+  int c, w;
+};
+template <class S>
+__device__ inline Cut cut_of(const TreeParams& p, Work head) {  // head: of sequence `lane`
+  const int n = p.a.seqs.n, lane = threadIdx.x & 63;
+  auto all = [&](int c) {
+    int sum = 0;
+    for (int i = 0; i < n; i += 64) sum = min(sum + wave_sum(parts_for(i == 0 ? head : work_of<S>(p, i + lane), c)), 1 << 30);
+    return sum;
+  };
+  int most = 0;
+  for (int i = 0; i < n; i += 64) {
+    int x = i == 0 ? head.tiles : work_of<S>(p, i + lane).tiles;
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int64_t o = __shfl_up(v, d);
-    if ((int)(threadIdx.x & 63) >= d) v += o;
+    for (int d = 1; d < 64; d *= 2) x = max(x, __shfl_xor(x, d));
+    most = max(most, __builtin_amdgcn_readfirstlane(x));
   }
-  return v;
-}
-
-// Place of a strip in parts_of: no two strips share one, as a sequence of m
-// rows has at most m group / COLS + 1 of them.
-__device__ inline int64_t strip_of(int row0, int i, int group, int cols_per, int strip) {
-  return (int64_t)row0 * group / cols_per + i + strip;
+  Cut cut{max(most, MIN_TILES), 0};
+  cut.w = all(cut.c);
+  if (cut.w >= p.at_once) return cut;
+  int lo = MIN_TILES, hi = cut.c;  // hi will do
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (all(mid) <= p.at_once) hi = mid;
+    else lo = mid + 1;
+  }
+  cut.c = hi;
+  cut.w = all(hi);
+  return cut;
 }
 
 // Bits of 64 keys from key `at` after the first drafted one (before it, if negative) that a node
@@ -151,31 +179,47 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
   uint64_t* paths = reinterpret_cast<uint64_t*>(smem + S::KV);  // [MAX_NODES][WORDS]
   int* up = reinterpret_cast<int*>(paths + MAX_NODES * WORDS);  // [MAX_NODES]
   const TreeArgs& a = p.a;
-  const int kvh = blockIdx.x % a.G, rank = blockIdx.x / a.G, group = a.H / a.G;
+  const int group = a.H / a.G;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rw = wave % RW, kg = wave / RW, col = lane & 15, g = lane >> 4;
 
-  int64_t total = 0;
-  for (int c = 0; c < a.seqs.n; c += 64) total += lane_of(wave_scan64(tiles_of<S>(p, c + lane)), 63);
-  Deal deal;
-  deal.init(total, (int)min((int64_t)p.ranges, (total + MIN_TILES - 1) / MIN_TILES));
-  if (rank >= deal.W) return;
-  const int64_t unit0 = deal.begin(rank), unit1 = deal.begin(rank + 1);
-  // the sequence that holds the first unit, and the units before it
-  int64_t first = 0;
-  int seq = 0;
+  const Work head = work_of<S>(p, lane);
+  const Cut cut = cut_of<S>(p, head);
+  // XCD blockIdx % 8 takes one contiguous share of the heads' workgroups
+  const int xcd = blockIdx.x % NUM_XCD, place = blockIdx.x / NUM_XCD;
+  const int64_t total = (int64_t)cut.w * a.G;
+  const int share = (int)(total / NUM_XCD), more = (int)(total % NUM_XCD);
+  if (place >= share + (xcd < more)) return;
+  const int64_t self = (int64_t)xcd * share + min(xcd, more) + place;
+  const int kvh = (int)(self / cut.w);
+  int item = (int)(self - (int64_t)kvh * cut.w);
+  // its sequence, its strip and its part
+  int seq = 0, begin = 0;
+  Work w{0, 0};
   for (int c = 0; c < a.seqs.n; c += 64) {
-    const int64_t t = tiles_of<S>(p, c + lane), incl = wave_scan64(t);
-    const uint64_t m = __ballot(first + incl > unit0);
+    const Work x = c == 0 ? head : work_of<S>(p, c + lane);
+    const int n = parts_for(x, cut.c), incl = wave_scan(n);
+    const uint64_t m = __ballot(begin + incl > item);
     if (m) {
       const int at = __builtin_ctzll(m);
       seq = c + at;
-      first += lane_of(incl - t, at);
+      begin += __builtin_amdgcn_readlane(incl - n, at);
+      w.strips = __builtin_amdgcn_readlane(x.strips, at);
+      w.tiles = __builtin_amdgcn_readlane(x.tiles, at);
       break;
     }
-    first += lane_of(incl, 63);
-    seq = a.seqs.n;
+    begin += __builtin_amdgcn_readlane(incl, 63);
   }
+  if (w.strips == 0) return;
+  const int parts = (w.tiles + cut.c - 1) / cut.c;
+  const int part = (item - begin) / w.strips, strip = item - begin - part * w.strips;
+  if (part >= parts) return;
+  const int j0 = (int)((int64_t)part * w.tiles / parts), j1 = (int)((int64_t)(part + 1) * w.tiles / parts);
+  const bool alone = parts == 1;
+  if (item == begin && kvh == 0 && threadIdx.x == 0) p.seqs[seq] = make_int4(begin, parts, w.strips, cut.w);
+  const Seq sq = sequence(p, seq);
+  const int cols = sq.m * group, past = sq.len - sq.m;
+  const int32_t* pages = a.pages + (int64_t)seq * a.pages_ld;
 
   const unsigned char* kb = static_cast<const unsigned char*>(a.cache.k) + kvh * a.cache.hs * EB;
   const unsigned char* vb = static_cast<const unsigned char*>(a.cache.v) + kvh * a.cache.hs * EB;
@@ -186,341 +230,316 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
   kf.init(smem + kg * (BN / KG) * L::RB, lane);
   vf.init(smem + TILE + kg * (BN / KG) * L::RB, lane);
 
-  int64_t unit = unit0;
-  for (; unit < unit1 && seq < a.seqs.n; ++seq) {
-    const Seq sq = sequence(p, seq);
-    const int tiles = (sq.len + BN - 1) / BN;
-    const int cols = sq.m * group;
-    const int64_t count = tiles_of<S>(p, seq);
-    const int64_t last = first + count;
-    const int32_t* pages = a.pages + (int64_t)seq * a.pages_ld;
-    const int past = sq.len - sq.m;
-    bool drawn = false;  // the paths of this sequence's nodes
-    while (unit < min(last, unit1)) {
-      const int strip = (int)Deal::div(unit - first, tiles);
-      const int j0 = (int)(unit - first - (int64_t)strip * tiles);
-      const int j1 = (int)min((int64_t)tiles, j0 + unit1 - unit);
-      const bool alone = j0 == 0 && j1 == tiles;
-      const int64_t item = (int64_t)(2 * rank + (unit != unit0)) * a.G + kvh;
-      if (j0 == 0 && kvh == 0 && threadIdx.x == 0)
-        p.parts_of[strip_of(sq.row0, seq, group, COLS, strip)] =
-            make_int2(2 * rank + (unit != unit0), alone ? 1 : deal.range_of(unit + tiles - 1) - rank + 1);
-      unit += j1 - j0;
-      if (!drawn && j1 * BN > past) {
-        drawn = true;
-        // every earlier reader of `paths` has passed the barrier at a strip's end
-        for (int i = threadIdx.x; i < sq.m; i += 64 * NW) {
-          const int q = a.parents[sq.row0 + i];
-          up[i] = q >= 0 && q < i ? q : -1;
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < sq.m; i += 64 * NW) {
-          uint64_t w[WORDS] = {};
-          for (int n = i; n >= 0; n = up[n])
+  if (j1 * BN > past) {
+    for (int i = threadIdx.x; i < sq.m; i += 64 * NW) {
+      const int q = a.parents[sq.row0 + i];
+      up[i] = q >= 0 && q < i ? q : -1;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < sq.m; i += 64 * NW) {
+      uint64_t w[WORDS] = {};
+      for (int n = i; n >= 0; n = up[n])
 #pragma unroll
-            for (int k = 0; k < WORDS; ++k)
-              if (n >> 6 == k) w[k] |= 1ull << (n & 63);
+        for (int k = 0; k < WORDS; ++k)
+          if (n >> 6 == k) w[k] |= 1ull << (n & 63);
 #pragma unroll
-          for (int k = 0; k < WORDS; ++k) paths[i * WORDS + k] = w[k];
-        }
-        __syncthreads();
-      }
+      for (int k = 0; k < WORDS; ++k) paths[i * WORDS + k] = w[k];
+    }
+    __syncthreads();
+  }
 
-      // the wave's columns
-      bf16x8 q[QF][DS];
-      int node[QF];
+  // the wave's columns
+  bf16x8 q[QF][DS];
+  int node[QF];
 #pragma unroll
-      for (int f = 0; f < QF; ++f) {
-        const int c = strip * COLS + (rw * QF + f) * 16 + col;
-        const bool live = c < cols;
-        node[f] = live ? c / group : 0;
-        const uint16_t* row = a.q.p + (int64_t)(sq.row0 + node[f]) * a.q.rs + (kvh * group + (live ? c % group : 0)) * a.q.hs;
+  for (int f = 0; f < QF; ++f) {
+    const int c = strip * COLS + (rw * QF + f) * 16 + col;
+    const bool live = c < cols;
+    node[f] = live ? c / group : 0;
+    const uint16_t* row = a.q.p + (int64_t)(sq.row0 + node[f]) * a.q.rs + (kvh * group + (live ? c % group : 0)) * a.q.hs;
 #pragma unroll
-        for (int s = 0; s < DS; ++s) q[f][s] = load_row8(row + 32 * s + 8 * g, live && 32 * s + 8 * g < a.D);
+    for (int s = 0; s < DS; ++s) q[f][s] = load_row8(row + 32 * s + 8 * g, live && 32 * s + 8 * g < a.D);
+  }
+  bool lost = false;  // a page that is not there
+  // A lane looks up a token: the page's id, then, with the tile before in use, its place.
+  int id = 0;
+  auto look = [&](int j) {
+    const uint32_t t = min(j * BN + lane, sq.len - 1);
+    id = pages[(__umulhi(t, p.page_mul) + t) >> p.page_shift];  // inside the row: len <= cap
+  };
+  u32x4 kreg[N], vreg[N];  // E4M3 alone
+  auto fetch = [&](int j, int stage) {
+    const uint32_t t = min(j * BN + lane, sq.len - 1);
+    const uint32_t o = t - ((__umulhi(t, p.page_mul) + t) >> p.page_shift) * (uint32_t)a.cache.page_size;
+    const bool there = (uint32_t)id < (uint32_t)a.cache.n_pages;
+    lost = lost || !there;
+    const int64_t place = ((there ? id : 0) * a.cache.ps + o * a.cache.ts) * EB;
+    const int lo = (int)(uint32_t)place, hi = (int)(place >> 32);
+    const bool all = (j + 1) * BN <= sq.len && a.D == 32 * DS;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = (i * NW + wave) * RPL + lane / PPR;
+      const int chunk = F8 ? piece : piece ^ L::swz(r);
+      const int64_t at = (int64_t)(((uint64_t)(uint32_t)__shfl(hi, r) << 32) | (uint32_t)__shfl(lo, r)) + chunk * 16;
+      const unsigned char *k = kb + at, *v = vb + at;
+      if (!all && !(chunk * (16 / EB) < a.D && j * BN + r < sq.len))
+        k = v = reinterpret_cast<const unsigned char*>(&ZEROS);
+      if (F8) {
+        kreg[i] = *GLOBAL_PTR(const u32x4, k);
+        vreg[i] = *GLOBAL_PTR(const u32x4, v);
+      } else {
+        const uint32_t to = lds + stage + (i * NW + wave) * 1024;
+        gather16(k, to);
+        gather16(v, to + TILE);
       }
-      bool lost = false;  // a page that is not there
-      // A lane looks up a token: the page's id, then, with the tile before in use, its place.
-      int id = 0;
-      auto look = [&](int j) {
-        const uint32_t t = min(j * BN + lane, sq.len - 1);
-        id = pages[(__umulhi(t, p.page_mul) + t) >> p.page_shift];  // inside the row: len <= cap
-      };
-      u32x4 kreg[N], vreg[N];  // E4M3 alone
-      auto fetch = [&](int j, int stage) {
-        const uint32_t t = min(j * BN + lane, sq.len - 1);
-        const uint32_t o = t - ((__umulhi(t, p.page_mul) + t) >> p.page_shift) * (uint32_t)a.cache.page_size;
-        const bool there = (uint32_t)id < (uint32_t)a.cache.n_pages;
-        lost = lost || !there;
-        const int64_t place = ((there ? id : 0) * a.cache.ps + o * a.cache.ts) * EB;
-        const int lo = (int)(uint32_t)place, hi = (int)(place >> 32);
-        const bool all = (j + 1) * BN <= sq.len && a.D == 32 * DS;
+    }
+  };
+  auto keep = [&](int stage) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int r = (i * NW + wave) * RPL + lane / PPR;
-          const int chunk = F8 ? piece : piece ^ L::swz(r);
-          const int64_t at = (int64_t)(((uint64_t)(uint32_t)__shfl(hi, r) << 32) | (uint32_t)__shfl(lo, r)) + chunk * 16;
-          const unsigned char *k = kb + at, *v = vb + at;
-          if (!all && !(chunk * (16 / EB) < a.D && j * BN + r < sq.len))
-            k = v = reinterpret_cast<const unsigned char*>(&ZEROS);
-          if (F8) {
-            kreg[i] = *GLOBAL_PTR(const u32x4, k);
-            vreg[i] = *GLOBAL_PTR(const u32x4, v);
-          } else {
-            const uint32_t to = lds + stage + (i * NW + wave) * 1024;
-            gather16(k, to);
-            gather16(v, to + TILE);
-          }
-        }
-      };
-      auto keep = [&](int stage) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int r = (i * NW + wave) * RPL + lane / PPR;
-          unsigned char* at = smem + stage + r * L::RB;
-          const int s0 = ((2 * piece) ^ L::swz(r)) * 16, s1 = ((2 * piece + 1) ^ L::swz(r)) * 16;
-          *LDS_PTR(u32x4, at + s0) = cvt8(kreg[i][0], kreg[i][1]);
-          *LDS_PTR(u32x4, at + s1) = cvt8(kreg[i][2], kreg[i][3]);
-          *LDS_PTR(u32x4, at + TILE + s0) = cvt8(vreg[i][0], vreg[i][1]);
-          *LDS_PTR(u32x4, at + TILE + s1) = cvt8(vreg[i][2], vreg[i][3]);
-        }
-      };
+    for (int i = 0; i < N; ++i) {
+      const int r = (i * NW + wave) * RPL + lane / PPR;
+      unsigned char* at = smem + stage + r * L::RB;
+      const int s0 = ((2 * piece) ^ L::swz(r)) * 16, s1 = ((2 * piece + 1) ^ L::swz(r)) * 16;
+      *LDS_PTR(u32x4, at + s0) = cvt8(kreg[i][0], kreg[i][1]);
+      *LDS_PTR(u32x4, at + s1) = cvt8(kreg[i][2], kreg[i][3]);
+      *LDS_PTR(u32x4, at + TILE + s0) = cvt8(vreg[i][0], vreg[i][1]);
+      *LDS_PTR(u32x4, at + TILE + s1) = cvt8(vreg[i][2], vreg[i][3]);
+    }
+  };
 
-      f32x4 o[L::DB][QF];
-      float m[QF], l[QF];
-      // All tiles of the segment.  FIXED: the reference is the first tile's maximum, and hidden
-      // values are finite (0 times another would be NaN); true where that will not do.
-      auto pass = [&](auto fixed) __attribute__((always_inline)) {
-        constexpr bool FIXED = decltype(fixed)::value;
-        bool bad = false;
+  f32x4 o[L::DB][QF];
+  float m[QF], l[QF];
+  // All tiles of the segment.  FIXED: the reference is the first tile's maximum, and hidden
+  // values are finite (0 times another would be NaN); true where that will not do.
+  auto pass = [&](auto fixed) __attribute__((always_inline)) {
+    constexpr bool FIXED = decltype(fixed)::value;
+    bool bad = false;
+#pragma unroll
+    for (int f = 0; f < QF; ++f) {
+      m[f] = -INFINITY;
+      l[f] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < L::DB; ++d) o[d][f] = f32x4{0, 0, 0, 0};
+    }
+    // DRAFTED: tiles that hold drafted tokens; FIRST: or a column's first
+    auto step = [&](int j, int off, auto drafted, auto begins) __attribute__((always_inline)) {
+      constexpr bool DRAFTED = decltype(drafted)::value, FIRST = decltype(begins)::value;
+      f32x4 s[KB][QF];
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+#pragma unroll
+        for (int f = 0; f < QF; ++f) s[b][f] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int d = 0; d < DS; ++d)
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+          const bf16x8 kk = kf.read(off, b, d);
+#pragma unroll
+          for (int f = 0; f < QF; ++f)
+            s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
+        }
+      uint64_t see[QF];
+      if (DRAFTED) {
+        const int at = j * BN + kg * (BN / KG) - past;
 #pragma unroll
         for (int f = 0; f < QF; ++f) {
-          m[f] = -INFINITY;
-          l[f] = 0.0f;
-#pragma unroll
-          for (int d = 0; d < L::DB; ++d) o[d][f] = f32x4{0, 0, 0, 0};
-        }
-        // DRAFTED: tiles that hold drafted tokens; FIRST: or a column's first
-        auto step = [&](int j, int off, auto drafted, auto begins) __attribute__((always_inline)) {
-          constexpr bool DRAFTED = decltype(drafted)::value, FIRST = decltype(begins)::value;
-          f32x4 s[KB][QF];
+          see[f] = seen_bits(paths + node[f] * WORDS, at);
+          const uint64_t mine = see[f] >> (4 * g);
 #pragma unroll
           for (int b = 0; b < KB; ++b)
 #pragma unroll
-            for (int f = 0; f < QF; ++f) s[b][f] = f32x4{0, 0, 0, 0};
+            for (int i = 0; i < 4; ++i)
+              if (!((mine >> (16 * b + i)) & 1)) s[b][f][i] = -INFINITY;
+        }
+        if (FIXED) bad = bad || not_finite<TILE, NW>(smem + off + TILE, wave, lane);
+      }
+      if (!FIXED || FIRST) {
 #pragma unroll
-          for (int d = 0; d < DS; ++d)
+        for (int f = 0; f < QF; ++f) {
+          float x = s[0][f][0];
 #pragma unroll
-            for (int b = 0; b < KB; ++b) {
-              const bf16x8 kk = kf.read(off, b, d);
+          for (int b = 0; b < KB; ++b)
 #pragma unroll
-              for (int f = 0; f < QF; ++f)
-                s[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[f][d], s[b][f], 0, 0, 0);
-            }
-          uint64_t see[QF];
-          if (DRAFTED) {
-            const int at = j * BN + kg * (BN / KG) - past;
+            for (int i = 0; i < 4; ++i) x = fmaxf(x, s[b][f][i]);
+          x = col_max(x);
+          if (FIXED) {
+            // no score, though the column sees a key
+            bad = bad || (m[f] == -INFINITY && x == -INFINITY && (!DRAFTED || see[f] != 0));
+            m[f] = m[f] == -INFINITY ? x : m[f];
+          } else {
+            x = fmaxf(x, m[f]);
+            const float r = exp2_(m[f] * p.c - (x == -INFINITY ? 0.0f : x * p.c));  // 0 the first time
+            m[f] = x;
+            l[f] *= r;
 #pragma unroll
-            for (int f = 0; f < QF; ++f) {
-              see[f] = seen_bits(paths + node[f] * WORDS, at);
-              const uint64_t mine = see[f] >> (4 * g);
-#pragma unroll
-              for (int b = 0; b < KB; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (!((mine >> (16 * b + i)) & 1)) s[b][f][i] = -INFINITY;
-            }
-            if (FIXED) bad = bad || not_finite<TILE, NW>(smem + off + TILE, wave, lane);
+            for (int d = 0; d < L::DB; ++d) o[d][f] *= r;
           }
-          if (!FIXED || FIRST) {
+        }
+      }
 #pragma unroll
-            for (int f = 0; f < QF; ++f) {
-              float x = s[0][f][0];
+      for (int f = 0; f < QF; ++f) {
+        const float base = (!FIXED || FIRST) && m[f] == -INFINITY ? 0.0f : m[f] * p.c;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-              for (int b = 0; b < KB; ++b)
+        for (int b = 0; b < KB; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x = fmaxf(x, s[b][f][i]);
-              x = col_max(x);
-              if (FIXED) {
-                // no score, though the column sees a key
-                bad = bad || (m[f] == -INFINITY && x == -INFINITY && (!DRAFTED || see[f] != 0));
-                m[f] = m[f] == -INFINITY ? x : m[f];
-              } else {
-                x = fmaxf(x, m[f]);
-                const float r = exp2_(m[f] * p.c - (x == -INFINITY ? 0.0f : x * p.c));  // 0 the first time
-                m[f] = x;
-                l[f] *= r;
-#pragma unroll
-                for (int d = 0; d < L::DB; ++d) o[d][f] *= r;
-              }
-            }
+          for (int i = 0; i < 4; ++i) {
+            s[b][f][i] = exp2_(s[b][f][i] * p.c - base);
+            sum[i] += s[b][f][i];
           }
+        l[f] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      }
+      // products over 32 keys, or the 16 that each of four groups has
+      constexpr int NT = KB > 1 ? KB / 2 : 1;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        bf16x8 pf[QF];
+#pragma unroll
+        for (int f = 0; f < QF; ++f) pf[f] = pack8(s[KB > 1 ? 2 * t : 0][f], s[KB > 1 ? 2 * t + 1 : 0][f]);
+#pragma unroll
+        for (int d = 0; d < L::DB; ++d) {
+          const bf16x8 vv = KB > 1 ? vf.read(off, t, d) : vf.read_half(off, d);
 #pragma unroll
           for (int f = 0; f < QF; ++f) {
-            const float base = (!FIXED || FIRST) && m[f] == -INFINITY ? 0.0f : m[f] * p.c;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int b = 0; b < KB; ++b)
+            if (FIXED || !DRAFTED) {
+              o[d][f] = product<KB == 1>(vv, pf[f], o[d][f]);
+              continue;
+            }
+            // every column by itself, from the keys that it sees
+            f32x4 r = o[d][f];
+#pragma unroll 1
+            for (int c = 0; c < 16; ++c) {
+              const uint64_t w = __shfl(see[f], c) >> (32 * t + 4 * g);
+              u32x4 x = __builtin_bit_cast(u32x4, vv);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                s[b][f][i] = exp2_(s[b][f][i] * p.c - base);
-                sum[i] += s[b][f][i];
+                const uint32_t two = (uint32_t)(w >> ((i & 1) * 2 + (i >> 1) * 16));
+                x[i] &= (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
               }
-            l[f] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          }
-          // products over 32 keys, or the 16 that each of four groups has
-          constexpr int NT = KB > 1 ? KB / 2 : 1;
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            bf16x8 pf[QF];
-#pragma unroll
-            for (int f = 0; f < QF; ++f) pf[f] = pack8(s[KB > 1 ? 2 * t : 0][f], s[KB > 1 ? 2 * t + 1 : 0][f]);
-#pragma unroll
-            for (int d = 0; d < L::DB; ++d) {
-              const bf16x8 vv = KB > 1 ? vf.read(off, t, d) : vf.read_half(off, d);
-#pragma unroll
-              for (int f = 0; f < QF; ++f) {
-                if (FIXED || !DRAFTED) {
-                  o[d][f] = product<KB == 1>(vv, pf[f], o[d][f]);
-                  continue;
-                }
-                // every column by itself, from the keys that it sees
-                f32x4 r = o[d][f];
-#pragma unroll 1
-                for (int c = 0; c < 16; ++c) {
-                  const uint64_t w = __shfl(see[f], c) >> (32 * t + 4 * g);
-                  u32x4 x = __builtin_bit_cast(u32x4, vv);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const uint32_t two = (uint32_t)(w >> ((i & 1) * 2 + (i >> 1) * 16));
-                    x[i] &= (two & 1 ? 0xFFFFu : 0u) | (two & 2 ? 0xFFFF0000u : 0u);
-                  }
-                  const f32x4 y = product<KB == 1>(__builtin_bit_cast(bf16x8, x), pf[f], o[d][f]);
-                  if (col == c) r = y;
-                }
-                o[d][f] = r;
-              }
+              const f32x4 y = product<KB == 1>(__builtin_bit_cast(bf16x8, x), pf[f], o[d][f]);
+              if (col == c) r = y;
             }
+            o[d][f] = r;
           }
-        };
-        const int full = min(max(past / BN, j0), j1);  // tiles of tokens that every row sees
-        int stage = 0;
-        look(j0);
-        fetch(j0, 0);
-        if (j0 + 1 < j1) look(j0 + 1);
-        // bf16: the next tile's direct loads are in flight while this one is used; E4M3: its
-        // registers' loads are.  In both each of the two stages is written after the barrier that
-        // ends its last use.
-        auto turn = [&](int j, auto drafted, auto begins) __attribute__((always_inline)) {
-          if (F8) keep(stage);
-          else wait_vmcnt_and_barrier<0>();
-          if (j + 1 < j1) fetch(j + 1, stage ^ STAGE);
-          if (j + 2 < j1) look(j + 2);
-          if (F8) lds_barrier();
-          step(j, stage, drafted, begins);
-          stage ^= STAGE;
-        };
-        int j = j0;
-        if (FIXED && j < full) turn(j++, std::false_type{}, std::true_type{});
-        for (; j < full; ++j) turn(j, std::false_type{}, std::false_type{});
-        for (; j < j1; ++j) turn(j, std::true_type{}, std::true_type{});
-        if (FIXED) {
-          float z = 0.0f;  // NaN if an output is not finite
-#pragma unroll
-          for (int f = 0; f < QF; ++f) {
-            bad = bad || !(l[f] < MOST);
-#pragma unroll
-            for (int d = 0; d < L::DB; ++d)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) z += o[d][f][i] * 0.0f;
-          }
-          bad = bad || z != 0.0f;
         }
-        __syncthreads();
-        return bad;
-      };
-      if (any_wave<NW>(pass(std::true_type{}), smem, wave, lane)) pass(std::false_type{});
-      lost = __ballot(lost) != 0;
-
-      float base[QF], sum[QF];
+      }
+    };
+    const int full = min(max(past / BN, j0), j1);  // tiles of tokens that every row sees
+    // bf16: the next tile's direct loads are in flight while this one is used; E4M3: its
+    // registers' loads are.  In both each of the two stages is written after the barrier that
+    // ends its last use.
+    int stage = 0;
+    look(j0);
+    fetch(j0, 0);
+    if (j0 + 1 < j1) look(j0 + 1);
+    auto turn = [&](int j, auto drafted, auto begins) __attribute__((always_inline)) {
+      if (F8) keep(stage);
+      else wait_vmcnt_and_barrier<0>();
+      if (j + 1 < j1) fetch(j + 1, stage ^ STAGE);
+      if (j + 2 < j1) look(j + 2);
+      if (F8) lds_barrier();
+      step(j, stage, drafted, begins);
+      stage ^= STAGE;
+    };
+    int j = j0;
+    if (FIXED && j < full) turn(j++, std::false_type{}, std::true_type{});
+    for (; j < full; ++j) turn(j, std::false_type{}, std::false_type{});
+    for (; j < j1; ++j) turn(j, std::true_type{}, std::true_type{});
+    if (FIXED) {
+      float z = 0.0f;  // NaN if an output is not finite
 #pragma unroll
       for (int f = 0; f < QF; ++f) {
-        sum[f] = col_sum(l[f]);
-        base[f] = m[f] == -INFINITY ? -INFINITY : m[f] * p.c;
-        if (lost) sum[f] = NAN;
+        bad = bad || !(l[f] < MOST);
+#pragma unroll
+        for (int d = 0; d < L::DB; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z += o[d][f][i] * 0.0f;
       }
-      constexpr int MINE = (L::DB + KG - 1) / KG;  // blocks of the output that a wave writes
-      if (KG > 1) {
-        f32x4* parts = reinterpret_cast<f32x4*>(smem);  // [KG][RW][DB][QF][64]
-        float2* stats = reinterpret_cast<float2*>(smem + NW * L::DB * QF * 1024);  // [KG][RW][QF][16]
-        f32x4* mine = parts + wave * L::DB * QF * 64 + lane;
-#pragma unroll
-        for (int f = 0; f < QF; ++f) {
-#pragma unroll
-          for (int d = 0; d < L::DB; ++d) mine[(d * QF + f) * 64] = o[d][f];
-          if (g == 0) stats[(wave * QF + f) * 16 + col] = make_float2(base[f], sum[f]);
-        }
-        __syncthreads();
-        const f32x4* all = parts + (rw * L::DB + kg) * QF * 64 + lane;
-#pragma unroll
-        for (int f = 0; f < QF; ++f) {
-          float2 x[KG];
-          float top = -INFINITY, tot = 0.0f;
-#pragma unroll
-          for (int k = 0; k < KG; ++k) {
-            x[k] = stats[((k * RW + rw) * QF + f) * 16 + col];
-            top = fmaxf(top, x[k].x);
-          }
-          const float b = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-          for (int k = 0; k < KG; ++k) {
-            x[k].x = exp2_(x[k].x - b);
-            tot += x[k].x * x[k].y;
-          }
-          base[f] = top;
-          sum[f] = tot;
-#pragma unroll
-          for (int i = 0; i < MINE; ++i) {
-            if (i * KG + kg >= L::DB) break;
-            f32x4 y = {0, 0, 0, 0};
-#pragma unroll
-            for (int k = 0; k < KG; ++k) y += all[((k * RW * L::DB + i * KG) * QF + f) * 64] * x[k].x;
-            o[i][f] = y;
-          }
-        }
-      }
-#pragma unroll
-      for (int f = 0; f < QF; ++f) {
-        const int c0 = (rw * QF + f) * 16 + col, c = strip * COLS + c0;
-        if (c >= cols) continue;
-        const int head = kvh * group + c % group;
-        const int64_t row = sq.row0 + c / group;
-        const float inv = sum[f] == 0.0f ? 0.0f : p.v_inv / sum[f];
-#pragma unroll
-        for (int i = 0; i < MINE; ++i) {
-          const int e = 16 * (i * KG + kg) + 4 * g;
-          if (e >= a.D) continue;
-          if (alone) {
-            const f32x4 x = o[i][f] * inv;
-            *reinterpret_cast<uint2*>(a.out.p + row * a.out.rs + head * a.out.hs + e) =
-                make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-          } else {
-            *reinterpret_cast<f32x4*>(p.part + (item * COLS + c0) * a.D + e) = o[i][f];
-          }
-        }
-        if (g == 0 && kg == 0) {
-          if (!alone) p.stat[item * COLS + c0] = make_float2(base[f], sum[f]);
-          else if (a.lse) a.lse[(int64_t)head * a.seqs.T + row] = sum[f] == 0.0f ? -INFINITY : base[f] * LN2 + logf(sum[f]);
-        }
-      }
-      __syncthreads();  // the next strip's tiles take the place of what was joined
+      bad = bad || z != 0.0f;
     }
-    first = last;
+    __syncthreads();
+    return bad;
+  };
+  if (any_wave<NW>(pass(std::true_type{}), smem, wave, lane)) pass(std::false_type{});
+  lost = __ballot(lost) != 0;
+
+  float base[QF], sum[QF];
+#pragma unroll
+  for (int f = 0; f < QF; ++f) {
+    sum[f] = col_sum(l[f]);
+    base[f] = m[f] == -INFINITY ? -INFINITY : m[f] * p.c;
+    if (lost) sum[f] = NAN;
+  }
+  constexpr int MINE = (L::DB + KG - 1) / KG;  // blocks of the output that a wave writes
+  if (KG > 1) {
+    f32x4* parts = reinterpret_cast<f32x4*>(smem);  // [KG][RW][DB][QF][64]
+    float2* stats = reinterpret_cast<float2*>(smem + NW * L::DB * QF * 1024);  // [KG][RW][QF][16]
+    f32x4* mine = parts + wave * L::DB * QF * 64 + lane;
+#pragma unroll
+    for (int f = 0; f < QF; ++f) {
+#pragma unroll
+      for (int d = 0; d < L::DB; ++d) mine[(d * QF + f) * 64] = o[d][f];
+      if (g == 0) stats[(wave * QF + f) * 16 + col] = make_float2(base[f], sum[f]);
+    }
+    __syncthreads();
+    const f32x4* all = parts + (rw * L::DB + kg) * QF * 64 + lane;
+#pragma unroll
+    for (int f = 0; f < QF; ++f) {
+      float2 x[KG];
+      float top = -INFINITY, tot = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KG; ++k) {
+        x[k] = stats[((k * RW + rw) * QF + f) * 16 + col];
+        top = fmaxf(top, x[k].x);
+      }
+      const float b = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int k = 0; k < KG; ++k) {
+        x[k].x = exp2_(x[k].x - b);
+        tot += x[k].x * x[k].y;
+      }
+      base[f] = top;
+      sum[f] = tot;
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) {
+        if (i * KG + kg >= L::DB) break;
+        f32x4 y = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < KG; ++k) y += all[((k * RW * L::DB + i * KG) * QF + f) * 64] * x[k].x;
+        o[i][f] = y;
+      }
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < QF; ++f) {
+    const int c0 = (rw * QF + f) * 16 + col, c = strip * COLS + c0;
+    if (c >= cols) continue;
+    const int head = kvh * group + c % group;
+    const int64_t row = sq.row0 + c / group;
+    const float inv = sum[f] == 0.0f ? 0.0f : p.v_inv / sum[f];
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+      const int e = 16 * (i * KG + kg) + 4 * g;
+      if (e >= a.D) continue;
+      if (alone) {
+        const f32x4 x = o[i][f] * inv;
+        *reinterpret_cast<uint2*>(a.out.p + row * a.out.rs + head * a.out.hs + e) =
+            make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+      } else {
+        *reinterpret_cast<f32x4*>(p.part + (self * COLS + c0) * a.D + e) = o[i][f];
+      }
+    }
+    if (g == 0 && kg == 0) {
+      if (!alone) p.stat[self * COLS + c0] = make_float2(base[f], sum[f]);
+      else if (a.lse) a.lse[(int64_t)head * a.seqs.T + row] = sum[f] == 0.0f ? -INFINITY : base[f] * LN2 + logf(sum[f]);
+    }
   }
 }
 
 // Rows of no sequence (zeros) and of sequences that are not good (NaN), and the sum of the parts,
-// in order, of strips of several ranges.  JW waves to a row and head; wave w of them adds parts
-// w, w + JW, ..., eight loads ahead; lane i holds elements 2 i, 2 i + 1.
+// in order, of strips that have several.  A workgroup takes a row's heads, a wave each in turn
+// (JW 1), or JW waves share a row and head: wave w adds parts w, w + JW, ..., eight loads
+// ahead.  Lane i holds elements 2 i, 2 i + 1.
 template <int JW, int COLS>
 __global__ __launch_bounds__(JW > 4 ? 64 * JW : 256) void attn_tree_join(TreeParams p) {
   constexpr int WAVES = JW > 4 ? JW : 4, AHEAD = 8;
@@ -528,10 +547,8 @@ __global__ __launch_bounds__(JW > 4 ? 64 * JW : 256) void attn_tree_join(TreePar
   __shared__ float2 tops[WAVES];
   const TreeArgs& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t task = (int64_t)blockIdx.x * (WAVES / JW) + wave / JW;
-  const int w = wave % JW;
-  const int T = a.seqs.T, row = (int)(task / a.H), head = (int)(task % a.H);
-  if (JW < WAVES && row >= T) return;
+  const int w = wave % JW, T = a.seqs.T, group = a.H / a.G;
+  const int row = JW == 1 ? blockIdx.x : blockIdx.x / a.H;
   // sequences that end at or before the row come first: their number is its sequence
   int seq = 0;
   for (int c = 0; c < a.seqs.n; c += 64) {
@@ -540,85 +557,90 @@ __global__ __launch_bounds__(JW > 4 ? 64 * JW : 256) void attn_tree_join(TreePar
     seq += m;
     if (m < 64) break;
   }
-  uint16_t* out = a.out.p + (int64_t)row * a.out.rs + head * a.out.hs;
-  float* lse = a.lse ? a.lse + (int64_t)head * T + row : nullptr;
   Seq s{0, 0, 0, true};
-  if (seq < a.seqs.n) s = sequence(p, seq);
+  int4 in = make_int4(0, 1, 0, 0);
+  if (seq < a.seqs.n) {
+    s = sequence(p, seq);
+    in = p.seqs[seq];  // not written, and not used, for one that is not good
+  }
   const bool none = seq >= a.seqs.n || row < s.row0;
-  if (none || !s.good) {
-    if (w == 0) {
-      const float x = none ? 0.0f : NAN;
-      if (2 * lane < a.D) *reinterpret_cast<uint32_t*>(out + 2 * lane) = pack_bf16x2(x, x);
-      if (lane == 0 && lse) *lse = none ? -INFINITY : NAN;
-    }
-    return;
+  if (!none && s.good) {
+    if (in.y == 1) return;
+    // (sequences that overlap, of boundaries that do not rise, may have left anything)
+    if (in.x < 0 || in.y < 1 || in.z < 1 || in.w > p.at_once || in.x + (int64_t)in.y * in.z > in.w) return;
   }
-  const int group = a.H / a.G, kvh = head / group, c = (row - s.row0) * group + head - kvh * group;
-  const int2 parts = p.parts_of[strip_of(s.row0, seq, group, COLS, c / COLS)];
-  const int count = parts.y;
-  if (count == 1) return;
-  // (sequences that overlap, of boundaries that do not rise, may have left none)
-  if (count < 1 || parts.x < 0 || (int64_t)(parts.x >> 1) + count > p.ranges) return;
-  auto at = [&](int i) {
-    return ((int64_t)(i == 0 ? parts.x : (parts.x & ~1) + 2 * i) * a.G + kvh) * COLS + c % COLS;
-  };
-  float m = -INFINITY, sum = 0.0f;
-  float2 x = make_float2(0.0f, 0.0f);
-  for (int i0 = w; i0 < count; i0 += AHEAD * JW) {
-    float2 st[AHEAD], v[AHEAD];
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j) {
-      const int i = i0 + j * JW;
-      const int64_t k = at(min(i, count - 1));
-      st[j] = i < count ? p.stat[k] : make_float2(-INFINITY, 0.0f);
-      v[j] = *reinterpret_cast<const float2*>(p.part + k * a.D + min(2 * lane, a.D - 2));
+  for (int head = JW == 1 ? wave : blockIdx.x % a.H; head < a.H; head += JW == 1 ? WAVES : a.H) {
+    uint16_t* out = a.out.p + (int64_t)row * a.out.rs + head * a.out.hs;
+    float* lse = a.lse ? a.lse + (int64_t)head * T + row : nullptr;
+    if (none || !s.good) {
+      if (w == 0) {
+        const float x = none ? 0.0f : NAN;
+        if (2 * lane < a.D) *reinterpret_cast<uint32_t*>(out + 2 * lane) = pack_bf16x2(x, x);
+        if (lane == 0 && lse) *lse = none ? -INFINITY : NAN;
+      }
+      continue;
     }
-    float top = m;
+    const int kvh = head / group, c = (row - s.row0) * group + head - kvh * group;
+    if (c / COLS >= in.z) continue;
+    const int64_t first = ((int64_t)kvh * in.w + in.x + c / COLS) * COLS + c % COLS, step = (int64_t)in.z * COLS;
+    float m = -INFINITY, sum = 0.0f;
+    float2 x = make_float2(0.0f, 0.0f);
+    for (int i0 = w; i0 < in.y; i0 += AHEAD * JW) {
+      float2 st[AHEAD], v[AHEAD];
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j) top = fmaxf(top, st[j].x);
-    const float b = top == -INFINITY ? 0.0f : top;
-    const float r = exp2_(m - b);
-    m = top;
-    sum *= r;
-    x.x *= r;
-    x.y *= r;
+      for (int j = 0; j < AHEAD; ++j) {
+        const int i = i0 + j * JW;
+        const int64_t k = first + min(i, in.y - 1) * step;
+        st[j] = i < in.y ? p.stat[k] : make_float2(-INFINITY, 0.0f);
+        v[j] = *reinterpret_cast<const float2*>(p.part + k * a.D + min(2 * lane, a.D - 2));
+      }
+      float top = m;
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j) {
-      if (i0 + j * JW >= count) break;
-      const float f = exp2_(st[j].x - b);
-      sum += f * st[j].y;
-      x.x += f * v[j].x;
-      x.y += f * v[j].y;
+      for (int j = 0; j < AHEAD; ++j) top = fmaxf(top, st[j].x);
+      const float b = top == -INFINITY ? 0.0f : top;
+      const float r = exp2_(m - b);
+      m = top;
+      sum *= r;
+      x.x *= r;
+      x.y *= r;
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        if (i0 + j * JW >= in.y) break;
+        const float f = exp2_(st[j].x - b);
+        sum += f * st[j].y;
+        x.x += f * v[j].x;
+        x.y += f * v[j].y;
+      }
     }
+    if (JW > 1) {
+      red[wave][lane] = x;
+      if (lane == 0) tops[wave] = make_float2(m, sum);
+      __syncthreads();
+      if (w != 0) return;
+      float top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < JW; ++k) top = fmaxf(top, tops[k].x);
+      const float b = top == -INFINITY ? 0.0f : top;
+      m = top;
+      sum = 0.0f;
+      x = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < JW; ++k) {
+        const float f = exp2_(tops[k].x - b);
+        sum += f * tops[k].y;
+        x.x += f * red[k][lane].x;
+        x.y += f * red[k][lane].y;
+      }
+    }
+    const float inv = sum == 0.0f ? 0.0f : p.v_inv / sum;
+    if (2 * lane < a.D) *reinterpret_cast<uint32_t*>(out + 2 * lane) = pack_bf16x2(x.x * inv, x.y * inv);
+    if (lane == 0 && lse) *lse = sum == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * LN2 + logf(sum);
   }
-  if (JW > 1) {
-    red[wave][lane] = x;
-    if (lane == 0) tops[wave] = make_float2(m, sum);
-    __syncthreads();
-    if (w != 0) return;
-    float top = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < JW; ++k) top = fmaxf(top, tops[wave + k].x);
-    const float b = top == -INFINITY ? 0.0f : top;
-    m = top;
-    sum = 0.0f;
-    x = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int k = 0; k < JW; ++k) {
-      const float f = exp2_(tops[wave + k].x - b);
-      sum += f * tops[wave + k].y;
-      x.x += f * red[wave + k][lane].x;
-      x.y += f * red[wave + k][lane].y;
-    }
-  }
-  const float inv = sum == 0.0f ? 0.0f : p.v_inv / sum;
-  if (2 * lane < a.D) *reinterpret_cast<uint32_t*>(out + 2 * lane) = pack_bf16x2(x.x * inv, x.y * inv);
-  if (lane == 0 && lse) *lse = sum == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * LN2 + logf(sum);
 }
 
 constexpr int MOST_COLS = 128;
-int max_ranges(int G) { return G < ITEMS ? ITEMS / G : 1; }
-int64_t part_bytes(int G, int D, int cols) { return (int64_t)2 * max_ranges(G) * G * cols * (8 + 4 * (int64_t)D); }
+int at_once(int G) { return G < ITEMS ? ITEMS / G : 1; }
+int64_t part_bytes(int G, int D, int cols) { return (int64_t)at_once(G) * G * cols * (8 + 4 * (int64_t)D); }
 
 template <class S>
 hipError_t run(const TreeArgs& a, hipStream_t s) {
@@ -627,16 +649,19 @@ hipError_t run(const TreeArgs& a, hipStream_t s) {
   p.cap = table_cap(a.pages_per_seq, a.cache.page_size);
   p.c = a.scale * LOG2E * (S::F8 ? 1.0f / a.cache.k_scale : 1.0f);
   p.v_inv = S::F8 ? 1.0f / a.cache.v_scale : 1.0f;
-  p.ranges = max_ranges(a.G);
+  p.at_once = at_once(a.G);
   const uint32_t page = (uint32_t)a.cache.page_size;
   while ((1ull << p.page_shift) < page) ++p.page_shift;
   p.page_mul = (uint32_t)(((((1ull << p.page_shift) - page) << 32) / page) + 1);
-  const int64_t blocks = (int64_t)p.ranges * a.G, rows = 2 * blocks * S::COLS;
+  const int64_t rows = (int64_t)p.at_once * a.G * S::COLS;
   p.stat = static_cast<float2*>(a.ws);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + rows * 8);
-  p.parts_of = reinterpret_cast<int2*>(p.part + rows * a.D);
+  p.seqs = reinterpret_cast<int4*>(p.part + rows * a.D);
+  // as many workgroups as strips there can be, if those are more than run at once
+  const int64_t strips = (int64_t)a.seqs.T * (a.H / a.G) / S::COLS + a.seqs.n;
+  const int64_t blocks = ((strips > p.at_once ? strips : p.at_once) * a.G + NUM_XCD - 1) / NUM_XCD * NUM_XCD;
   const int64_t outputs = (int64_t)a.seqs.T * a.H;
-  if (outputs > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (outputs > 0x7FFFFFFF || blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   auto kernel = &attn_tree<S>;
   hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kernel), S::LDS);
   if (e == hipSuccess && a.seqs.n > 0) e = launch_k(kernel, dim3((unsigned)blocks), dim3(64 * NW), S::LDS, s, p);
@@ -644,7 +669,7 @@ hipError_t run(const TreeArgs& a, hipStream_t s) {
   // few outputs have many parts, which more waves then share
   if (outputs <= 512) return launch_k(&attn_tree_join<16, S::COLS>, dim3((unsigned)outputs), dim3(1024), 0, s, p);
   if (outputs <= 4096) return launch_k(&attn_tree_join<4, S::COLS>, dim3((unsigned)outputs), dim3(256), 0, s, p);
-  return launch_k(&attn_tree_join<1, S::COLS>, dim3((unsigned)((outputs + 3) / 4)), dim3(256), 0, s, p);
+  return launch_k(&attn_tree_join<1, S::COLS>, dim3((unsigned)a.seqs.T), dim3(256), 0, s, p);
 }
 
 template <int DS, bool F8>
@@ -667,7 +692,7 @@ hipError_t by_dim(const TreeArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t attn_tree_bytes(int32_t H, int32_t G, int32_t D, int64_t rows, int32_t n) {
-  return (size_t)(part_bytes(G, D, MOST_COLS) + (rows * (H / G) / 16 + n + 1) * 8);
+  return (size_t)(part_bytes(G, D, MOST_COLS) + (int64_t)n * 16);
 }
 
 hipError_t launch_attn_tree(const TreeArgs& a, hipStream_t s) {
