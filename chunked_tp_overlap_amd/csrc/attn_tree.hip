@@ -7,8 +7,8 @@
 // nodes has m (n_heads / n_kv_heads) of them, in strips of COLS.  A workgroup takes one strip and
 // some of the sequence's tiles of BN keys.  The lengths are on the device, so the cut is made
 // there: sequence i's tiles go in k_i = ceil(tiles_i / c) equal parts, with the smallest c for
-// which all strips' parts are as many workgroups as run at once (c no smaller than MIN_TILES;
-// one part each where the strips are more than that).  The strips of one part of a sequence read
+// which all strips' parts are as many workgroups as run at once, or twice as many (c no smaller
+// than MIN_TILES; one part each where the strips are more than run at once).  The strips of one part of a sequence read
 // the same keys at the same time, so they are neighbours on one XCD, whose L2 then serves all
 // but one of them.  A strip in one part is finished by its workgroup; others leave parts (maximum,
 // sum and unnormalised output, fp32) in the workspace, and attn_tree_join adds them in order.
@@ -40,6 +40,9 @@ constexpr int WORDS = MAX_NODES / 64;
 constexpr int NW = 4;
 constexpr int ITEMS = 512;     // workgroups that run at once: two on each CU
 constexpr int MIN_TILES = 4;   // tiles of a part at least, where there are so many
+// Parts of LONG_PART tiles or more are cut again, for two rounds of workgroups: what the first
+// leaves idle for want of equal parts is more than what starting the second costs.
+constexpr int LONG_PART = 48, ROUNDS = 2;
 constexpr float MOST = 0x1p60f;  // a lane's sum beyond which the pass is done again
 
 struct TreeParams {
@@ -50,8 +53,8 @@ struct TreeParams {
   uint32_t page_mul, page_shift;  // t / page_size = (umulhi(t, page_mul) + t) >> page_shift, t < 2^30
   int32_t at_once;  // workgroups of a key-value head that run at once
   int4* seqs;       // [n]: a sequence's first workgroup among `w` of a head, its k_i, its strips, w
-  float* part;      // [at_once G, COLS, D]: a workgroup's output where a strip has several parts
-  float2* stat;     // [at_once G, COLS]: maximum (base 2, scaled), sum
+  float* part;      // [ROUNDS at_once G, COLS, D]: a workgroup's output where a strip has several parts
+  float2* stat;     // [ROUNDS at_once G, COLS]: maximum (base 2, scaled), sum
 };
 
 constexpr int BN = 64;         // keys of a tile: one to a lane in the lookup of their pages
@@ -124,23 +127,38 @@ __device__ inline Cut cut_of(const TreeParams& p, Work head) {  // head: of sequ
     return sum;
   };
   int most = 0;
+  float tiles = 0.0f;
   for (int i = 0; i < n; i += 64) {
-    int x = i == 0 ? head.tiles : work_of<S>(p, i + lane).tiles;
+    const Work w = i == 0 ? head : work_of<S>(p, i + lane);
+    int x = w.tiles;
+    float y = (float)w.strips * (float)x;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) x = max(x, __shfl_xor(x, d));
+    for (int d = 1; d < 64; d *= 2) {
+      x = max(x, __shfl_xor(x, d));
+      y += __shfl_xor(y, d);
+    }
     most = max(most, __builtin_amdgcn_readfirstlane(x));
+    tiles += __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(y)));
   }
   Cut cut{max(most, MIN_TILES), 0};
-  cut.w = all(cut.c);
+  cut.w = all(cut.c);  // the strips
   if (cut.w >= p.at_once) return cut;
-  int lo = MIN_TILES, hi = cut.c;  // hi will do
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (all(mid) <= p.at_once) hi = mid;
-    else lo = mid + 1;
-  }
-  cut.c = hi;
-  cut.w = all(hi);
+  // the smallest c that will do, for `slots` workgroups: w is at least tiles / c, and at most the
+  // strips more
+  auto search = [&](int slots) {
+    int lo = max(MIN_TILES, (int)(tiles * 0.999f / (float)slots));
+    int hi = max(lo, (int)min((float)cut.c, tiles * 1.001f / (float)(slots - cut.w) + 2.0f));
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (all(mid) <= slots) hi = mid;
+      else lo = mid + 1;
+    }
+    return hi;
+  };
+  int c = search(p.at_once);
+  if (c >= LONG_PART) c = search(p.at_once * ROUNDS);
+  cut.c = c;
+  cut.w = all(c);
   return cut;
 }
 
@@ -230,23 +248,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
   kf.init(smem + kg * (BN / KG) * L::RB, lane);
   vf.init(smem + TILE + kg * (BN / KG) * L::RB, lane);
 
-  if (j1 * BN > past) {
-    for (int i = threadIdx.x; i < sq.m; i += 64 * NW) {
-      const int q = a.parents[sq.row0 + i];
-      up[i] = q >= 0 && q < i ? q : -1;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < sq.m; i += 64 * NW) {
-      uint64_t w[WORDS] = {};
-      for (int n = i; n >= 0; n = up[n])
-#pragma unroll
-        for (int k = 0; k < WORDS; ++k)
-          if (n >> 6 == k) w[k] |= 1ull << (n & 63);
-#pragma unroll
-      for (int k = 0; k < WORDS; ++k) paths[i * WORDS + k] = w[k];
-    }
-    __syncthreads();
-  }
+  bool lost = false;  // a page that is not there
+  // A lane looks up a token: the page's id, then, with the tile before in use, its place.
+  int id = 0;
+  auto look = [&](int j) {
+    const uint32_t t = min(j * BN + lane, sq.len - 1);
+    id = pages[(__umulhi(t, p.page_mul) + t) >> p.page_shift];  // inside the row: len <= cap
+  };
+  look(j0);
 
   // the wave's columns
   bf16x8 q[QF][DS];
@@ -260,13 +269,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
 #pragma unroll
     for (int s = 0; s < DS; ++s) q[f][s] = load_row8(row + 32 * s + 8 * g, live && 32 * s + 8 * g < a.D);
   }
-  bool lost = false;  // a page that is not there
-  // A lane looks up a token: the page's id, then, with the tile before in use, its place.
-  int id = 0;
-  auto look = [&](int j) {
-    const uint32_t t = min(j * BN + lane, sq.len - 1);
-    id = pages[(__umulhi(t, p.page_mul) + t) >> p.page_shift];  // inside the row: len <= cap
-  };
   u32x4 kreg[N], vreg[N];  // E4M3 alone
   auto fetch = [&](int j, int stage) {
     const uint32_t t = min(j * BN + lane, sq.len - 1);
@@ -307,9 +309,33 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
     }
   };
 
+  auto start = [&] {  // the first tile, whose page ids are looked up
+    fetch(j0, 0);
+    if (j0 + 1 < j1) look(j0 + 1);
+  };
+  start();
+
+  if (j1 * BN > past) {
+    for (int i = threadIdx.x; i < sq.m; i += 64 * NW) {
+      const int q = a.parents[sq.row0 + i];
+      up[i] = q >= 0 && q < i ? q : -1;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < sq.m; i += 64 * NW) {
+      uint64_t w[WORDS] = {};
+      for (int n = i; n >= 0; n = up[n])
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k)
+          if (n >> 6 == k) w[k] |= 1ull << (n & 63);
+#pragma unroll
+      for (int k = 0; k < WORDS; ++k) paths[i * WORDS + k] = w[k];
+    }
+    __syncthreads();
+  }
+
   f32x4 o[L::DB][QF];
   float m[QF], l[QF];
-  // All tiles of the segment.  FIXED: the reference is the first tile's maximum, and hidden
+  // All tiles of the part, the first of which is being loaded.  FIXED: the reference is the first tile's maximum, and hidden
   // values are finite (0 times another would be NaN); true where that will not do.
   auto pass = [&](auto fixed) __attribute__((always_inline)) {
     constexpr bool FIXED = decltype(fixed)::value;
@@ -429,9 +455,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
     // registers' loads are.  In both each of the two stages is written after the barrier that
     // ends its last use.
     int stage = 0;
-    look(j0);
-    fetch(j0, 0);
-    if (j0 + 1 < j1) look(j0 + 1);
     auto turn = [&](int j, auto drafted, auto begins) __attribute__((always_inline)) {
       if (F8) keep(stage);
       else wait_vmcnt_and_barrier<0>();
@@ -460,7 +483,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
     __syncthreads();
     return bad;
   };
-  if (any_wave<NW>(pass(std::true_type{}), smem, wave, lane)) pass(std::false_type{});
+  if (any_wave<NW>(pass(std::true_type{}), smem, wave, lane)) {
+    look(j0);
+    start();
+    pass(std::false_type{});
+  }
   lost = __ballot(lost) != 0;
 
   float base[QF], sum[QF];
@@ -567,7 +594,7 @@ __global__ __launch_bounds__(JW > 4 ? 64 * JW : 256) void attn_tree_join(TreePar
   if (!none && s.good) {
     if (in.y == 1) return;
     // (sequences that overlap, of boundaries that do not rise, may have left anything)
-    if (in.x < 0 || in.y < 1 || in.z < 1 || in.w > p.at_once || in.x + (int64_t)in.y * in.z > in.w) return;
+    if (in.x < 0 || in.y < 1 || in.z < 1 || in.w > ROUNDS * p.at_once || in.x + (int64_t)in.y * in.z > in.w) return;
   }
   for (int head = JW == 1 ? wave : blockIdx.x % a.H; head < a.H; head += JW == 1 ? WAVES : a.H) {
     uint16_t* out = a.out.p + (int64_t)row * a.out.rs + head * a.out.hs;
@@ -640,7 +667,7 @@ __global__ __launch_bounds__(JW > 4 ? 64 * JW : 256) void attn_tree_join(TreePar
 
 constexpr int MOST_COLS = 128;
 int at_once(int G) { return G < ITEMS ? ITEMS / G : 1; }
-int64_t part_bytes(int G, int D, int cols) { return (int64_t)at_once(G) * G * cols * (8 + 4 * (int64_t)D); }
+int64_t part_bytes(int G, int D, int cols) { return (int64_t)ROUNDS * at_once(G) * G * cols * (8 + 4 * (int64_t)D); }
 
 template <class S>
 hipError_t run(const TreeArgs& a, hipStream_t s) {
@@ -653,13 +680,14 @@ hipError_t run(const TreeArgs& a, hipStream_t s) {
   const uint32_t page = (uint32_t)a.cache.page_size;
   while ((1ull << p.page_shift) < page) ++p.page_shift;
   p.page_mul = (uint32_t)(((((1ull << p.page_shift) - page) << 32) / page) + 1);
-  const int64_t rows = (int64_t)p.at_once * a.G * S::COLS;
+  const int64_t rows = (int64_t)ROUNDS * p.at_once * a.G * S::COLS;
   p.stat = static_cast<float2*>(a.ws);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + rows * 8);
   p.seqs = reinterpret_cast<int4*>(p.part + rows * a.D);
   // as many workgroups as strips there can be, if those are more than run at once
   const int64_t strips = (int64_t)a.seqs.T * (a.H / a.G) / S::COLS + a.seqs.n;
-  const int64_t blocks = ((strips > p.at_once ? strips : p.at_once) * a.G + NUM_XCD - 1) / NUM_XCD * NUM_XCD;
+  const int64_t most = (int64_t)ROUNDS * p.at_once;
+  const int64_t blocks = ((strips > most ? strips : most) * a.G + NUM_XCD - 1) / NUM_XCD * NUM_XCD;
   const int64_t outputs = (int64_t)a.seqs.T * a.H;
   if (outputs > 0x7FFFFFFF || blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   auto kernel = &attn_tree<S>;

@@ -135,6 +135,18 @@ def test_tree_many_sequences(ub):  # noqa: F811
     check_rows(out.cpu(), lse.cpu(), q, values(kc), values(vc), table, trees, full, 16, (H, G, D))
 
 
+@pytest.mark.parametrize("f8", [False, True])
+def test_tree_two_rounds_of_parts(ub, f8):  # noqa: F811
+    """So much work that parts are cut for two rounds of workgroups."""
+    H, G, D = 16, 1, 16
+    nodes, past = [30, 9] * 24, [9000, 14000] * 24
+    trees = [tree(m, "any", i) for i, m in enumerate(nodes)]
+    lens, T, full, kc, vc, table, q, parents = make_case(H, G, D, trees, past, 64, f8, False, 1)
+    ks, vs = (40.0, 60.0) if f8 else (1.0, 1.0)
+    out, lse = attend(ub, q, ub.make_kv_cache(kc, vc, ks, vs), table, full, parents, lens, (H, G, D), T)
+    check_rows(out.cpu(), lse.cpu(), q, values(kc) / ks, values(vc) / vs, table, trees, full, 64, (H, G, D))
+
+
 @pytest.mark.parametrize("low,high", [(0.0, 60.0), (-300.0, 300.0), (100.0, -100.0)])
 @pytest.mark.parametrize("H,m", [(1, 4), (2, 200), (8, 30)])
 def test_scores_that_rise_and_fall(ub, low, high, H, m):  # noqa: F811
