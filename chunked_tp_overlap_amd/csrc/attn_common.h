@@ -418,6 +418,11 @@ __device__ inline SeqTile find_tile(const Seqs& s, int bm, int rank, bool low_fi
 // 23 entries, 81 and 196 with 24 and more).
 inline bool few_sequences(int64_t n, int H) { return n * H < 96; }
 
+// Under a window every row has as much to do, and groups help as long as their workgroups, of 64
+// rows, make one round of the CUs: tiles of 64 rows times heads, where a sequence's last tile
+// counts for a half.
+inline int64_t window_tiles(int64_t T, int64_t n, int H) { return (T / 64 + n / 2) * H; }
+
 // Tiles of bm rows that n sequences of T rows together can have.
 inline int64_t max_tiles(int64_t T, int64_t n, int bm) { return T / bm + (n < T ? n : T); }
 

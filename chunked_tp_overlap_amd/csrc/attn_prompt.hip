@@ -358,8 +358,18 @@ hipError_t run(const PromptArgs& a, hipStream_t s) {
   return launch_k(kernel, dim3((unsigned)(ranks * a.H)), dim3(64 * S::NW), S::LDS, s, p);
 }
 
+// Under a window.  Measured, groups against one, windows of 64, 512 and 2048: 4096 rows of 4 heads in
+// one sequence (256 tiles) 13 and 14 us, 17 and 22, 31 and 46; in 5 (266) 20 and 14, 21 and 23, 30
+// and 47; 8184 (508) 25 and 16, 35 and 26, 61 and 51.
+bool window_grouped(const PromptArgs& a) {
+  const int64_t tiles = window_tiles(a.seqs.T, a.seqs.n, a.H);
+  return tiles <= 258 || (tiles <= 300 && a.win.size >= 512);
+}
+
 template <int DS>
 hipError_t choose(const PromptArgs& a, hipStream_t s) {
+  if (a.win.size)
+    return window_grouped(a) ? run<Shape<DS, 2, 2, 4, 32>, true>(a, s) : run<Shape<DS, 2, 4, 1, 64>, true>(a, s);
   // A workgroup of 128 rows at the end of a sequence takes about 65536 / (rows heads) times as
   // long as the whole call would on evenly loaded CUs.  64 rows and four groups of waves on the
   // keys take a quarter, but their tiles serve half the rows: 0.6 of the rate.  Measured, groups
@@ -367,8 +377,8 @@ hipError_t choose(const PromptArgs& a, hipStream_t s) {
   // 76; 5120 of 8 on 1 (2) 57 and 55, of 8 on 8 (8) 41 and 43; 6144 of 8 on 1 70 and 65, on 8
   // 53 and 49.
   if ((int64_t)a.seqs.T * a.H < 44 * 1024 && few_sequences(a.seqs.n, a.H))
-    return a.win.size ? run<Shape<DS, 2, 2, 4, 32>, true>(a, s) : run<Shape<DS, 2, 2, 4, 32>, false>(a, s);
-  return a.win.size ? run<Shape<DS, 2, 4, 1, 64>, true>(a, s) : run<Shape<DS, 2, 4, 1, 64>, false>(a, s);
+    return run<Shape<DS, 2, 2, 4, 32>, false>(a, s);
+  return run<Shape<DS, 2, 4, 1, 64>, false>(a, s);
 }
 
 }  // namespace

@@ -781,6 +781,14 @@ constexpr int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 // 195 us, 5 sequences 161 and 196; 5120 of 8 on 1 (2) 151 and 134, of 8 on 8 (8) 115 and 99.
 constexpr int64_t GROUPED_BELOW = 36 * 1024;
 bool grouped(int H, int64_t rows, int64_t n) { return rows * H < GROUPED_BELOW && few_sequences(n, H); }
+// Under a window, with two kinds of workgroups for a tile and head.  Measured, the gradient alone,
+// groups against one, windows of 64, 512 and 2048: 2000 rows of 4 heads on 4 in one sequence (124
+// tiles) 22 and 27 us, 29 and 45; 4096 (256) 36 and 31, 48 and 48, 81 and 104; 8184 (508) 66 and
+// 36, 89 and 58, 161 and 122.
+bool window_grouped(int H, int64_t rows, int64_t n, Window win) {
+  const int64_t tiles = window_tiles(rows, n, H);
+  return tiles <= 140 || (tiles <= 270 && win.size >= 1024);
+}
 
 // Parts a group's heads are split into, until the key-value workgroups make one round (of 512,
 // or of 256 of four groups): fewer leave much of the chip idle (half a round: 306 us against 252
@@ -851,7 +859,8 @@ hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
 
 template <int DS, bool WIN>
 hipError_t choose(const PromptBwdArgs& a, hipStream_t s) {
-  if (grouped(a.H, a.seqs.T, a.seqs.n)) return run<Shape<DS, 2, 4, 32>, Shape<DS, 2, 4, 32>, WIN>(a, s);
+  if (WIN ? window_grouped(a.H, a.seqs.T, a.seqs.n, a.win) : grouped(a.H, a.seqs.T, a.seqs.n))
+    return run<Shape<DS, 2, 4, 32>, Shape<DS, 2, 4, 32>, WIN>(a, s);
   return run<Shape<DS, 4, 1, 64>, Shape<DS, 4, 1, 32>, WIN>(a, s);
 }
 

@@ -105,10 +105,17 @@ __device__ inline Lens lens_of(const ResizeArgs& a, int i) {
   return l;
 }
 
+// One workgroup.  The rows' asks, the free pages counted as far as they are asked for, and then
+// turn by turn a list of free pages in LDS, from which each goes to its row: the first whose `end`
+// lies past the page's rank, found in LDS too (ROWS_IN_LDS rows and fewer).  With the search in
+// the workspace and a page's place from the count that its thread read, 576 rows took 19.6 us.
+constexpr int ROWS_IN_LDS = 4096;
 __global__ __launch_bounds__(GIVERS) void kv_give(ResizeArgs a) {
   __shared__ int64_t sums[GIVE_WAVES];
+  __shared__ int32_t ids[GIVERS * PER], ends[ROWS_IN_LDS];
   Ask* ask = asks_of(a.ws);
   const int n = a.table.n;
+  const bool in_lds = n <= ROWS_IN_LDS;
   int64_t total = 0;
   for (int c = 0; c < n; c += GIVERS) {
     const int i = c + threadIdx.x;
@@ -136,69 +143,82 @@ __global__ __launch_bounds__(GIVERS) void kv_give(ResizeArgs a) {
     if (i < n) {
       k.end = total + before + need;
       ask[i] = k;
+      if (in_lds) ends[i] = (int32_t)min(k.end, (int64_t)0x7FFFFFFF);  // ranks stay below it
     }
     total += all;
   }
-  // GIVE: pages of ranks below `limit` go to the rows that ask for them; otherwise they are only
-  // counted, as far as `limit`
-  auto walk = [&](int64_t limit, bool give) {
-    int64_t found = 0;
-    for (int64_t c = 0; c < a.n_pages && found < limit; c += GIVERS * PER) {
-      const int64_t id0 = c + (int64_t)threadIdx.x * PER;
-      int32_t r[PER];
-      if (id0 + PER <= a.n_pages) {
-        const i32x4 lo = *GLOBAL_PTR(const i32x4, a.refs + id0), hi = *GLOBAL_PTR(const i32x4, a.refs + id0 + 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          r[j] = lo[j];
-          r[4 + j] = hi[j];
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < PER; ++j) r[j] = id0 + j < a.n_pages ? a.refs[id0 + j] : 1;
-      }
-      int mine = 0;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) mine += r[j] == 0;
-      int64_t all;
-      int64_t rank = found + scan_before(mine, sums, all);
-      found += all;
-      if (!give || mine == 0) continue;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        if (r[j] != 0 || rank >= limit) continue;
-        int lo = 0, hi = n - 1;  // the first row whose end lies past the rank
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (ask[mid].end > rank) hi = mid;
-          else lo = mid + 1;
-        }
-        const int64_t before = lo > 0 ? ask[lo - 1].end : 0;
-        a.table.p[(int64_t)lo * a.table.ld + ask[lo].begin + (rank - before)] = (int32_t)(id0 + j);
-        a.refs[id0 + j] = 1;
-        ++rank;
-      }
+  // the first row whose end lies past `rank`, below n
+  auto row_of = [&](int64_t rank) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if ((in_lds ? (int64_t)ends[mid] : ask[mid].end) > rank) hi = mid;
+      else lo = mid + 1;
     }
-    return found;
+    return lo;
   };
-  if (total == 0) {
-    if (threadIdx.x == 0) *free_of(a.ws) = 0;
-    return;
+  int32_t r[PER];
+  auto read = [&](int64_t id0) {
+    if (id0 + PER <= a.n_pages) {
+      const i32x4 lo = *GLOBAL_PTR(const i32x4, a.refs + id0), hi = *GLOBAL_PTR(const i32x4, a.refs + id0 + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r[j] = lo[j];
+        r[4 + j] = hi[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) r[j] = id0 + j < a.n_pages ? a.refs[id0 + j] : 1;
+    }
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) mine += r[j] == 0;
+    return mine;
+  };
+  constexpr int TURN = GIVERS * PER;
+  int64_t free = 0;
+  bool first = true;  // r holds the first turn's counts
+  for (int64_t c = 0; c < a.n_pages && free < total; c += TURN) {
+    int64_t all;
+    first = c == 0;
+    scan_before(read(c + (int64_t)threadIdx.x * PER), sums, all);
+    free += all;
   }
-  const int64_t free = walk(total, false);
+  if (threadIdx.x == 0) *free_of(a.ws) = free;
+  if (total == 0 || free == 0) return;
   // as many as go to rows that get all they ask for
   int64_t limit = total;
   if (free < total) {
-    int lo = 0, hi = n - 1;  // the first row that does not
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (ask[mid].end > free) hi = mid;
-      else lo = mid + 1;
-    }
-    limit = lo > 0 ? ask[lo - 1].end : 0;
+    const int row = row_of(free);
+    limit = row > 0 ? (in_lds ? ends[row - 1] : ask[row - 1].end) : 0;
   }
-  if (threadIdx.x == 0) *free_of(a.ws) = free;
-  if (limit > 0) walk(limit, true);
+  int64_t found = 0;
+  for (int64_t c = 0; c < a.n_pages && found < limit; c += TURN) {
+    const int64_t id0 = c + (int64_t)threadIdx.x * PER;
+    int mine = 0;
+    if (c == 0 && first) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) mine += r[j] == 0;
+    } else {
+      mine = read(id0);
+    }
+    int64_t all;
+    int at = (int)scan_before(mine, sums, all);  // and the last turn's list is read
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (r[j] == 0) ids[at++] = (int32_t)(id0 + j);
+    __syncthreads();
+    const int give = (int)min(all, limit - found);
+    for (int i = threadIdx.x; i < give; i += GIVERS) {
+      const int64_t rank = found + i;
+      const int row = row_of(rank);
+      const int64_t before = row == 0 ? 0 : in_lds ? (int64_t)ends[row - 1] : ask[row - 1].end;
+      a.table.p[(int64_t)row * a.table.ld + ask[row].begin + (rank - before)] = ids[i];
+      a.refs[ids[i]] = 1;
+    }
+    found += all;
+    __syncthreads();
+  }
 }
 
 __global__ __launch_bounds__(64) void kv_take(ResizeArgs a) {
@@ -255,20 +275,24 @@ __global__ __launch_bounds__(256) void kv_copy_pages(KvCache c, int G, int vec, 
 }
 
 // ---- compaction -----------------------------------------------------------------------------
-// A workgroup for each sequence, head, and keys or values.  A thread moves 16 bytes of AHEAD
-// tokens at a time.  As the kept places rise, token d comes from place d or a later one: all
-// loads of a turn before its stores, and turn after turn, no place is written before it is read.
-__global__ __launch_bounds__(256) void kv_compact(CompactArgs a, int vec) {
-  constexpr int AHEAD = 4;
+// A workgroup for each sequence and `planes` of its planes, the heads' keys and values.  A thread
+// moves AHEAD pieces of 16 bytes at a time.  As the kept places rise, token d comes from place d or
+// a later one: with all loads of a turn before its stores, and turn after turn, no place is
+// written before it is read.  A turn holds whole planes if the list is short enough for one;
+// otherwise it is some tokens of one plane.
+constexpr int AHEAD = 4, MOVERS = 256;
+__global__ __launch_bounds__(MOVERS) void kv_compact(CompactArgs a, int vec, int planes) {
   __shared__ int count;
-  const int kv = blockIdx.x & 1, head = (blockIdx.x >> 1) % a.G, i = (blockIdx.x >> 1) / a.G;
+  const int groups = (2 * a.G + planes - 1) / planes;
+  const int i = blockIdx.x / groups, plane0 = (blockIdx.x - i * groups) * planes;
+  const int plane1 = min(plane0 + planes, 2 * a.G);
   const int cap = table_cap(a.pages_per_seq, a.cache.page_size);
   const int len = clamp_len(a.lens[i], cap);
   const int32_t* kept = a.kept + (int64_t)i * a.kept_ld;
   const int given = min(max(a.kept_lens[i], 0), a.most);
   if (threadIdx.x == 0) count = given;
   __syncthreads();
-  for (int d = threadIdx.x; d < given; d += 256) {
+  for (int d = threadIdx.x; d < given; d += MOVERS) {
     const int x = kept[d];
     if (x <= (d > 0 ? kept[d - 1] : -1) || x >= cap - len) {
       atomicMin(&count, d);
@@ -277,34 +301,39 @@ __global__ __launch_bounds__(256) void kv_compact(CompactArgs a, int vec) {
   }
   __syncthreads();
   const int n = count;
-  if (blockIdx.x % (2 * a.G) == 0 && threadIdx.x == 0) a.lens_out[i] = len + n;
+  if (plane0 == 0 && threadIdx.x == 0) a.lens_out[i] = len + n;
+  if (n == 0) return;
   const int eb = a.cache.e4m3 ? 1 : 2;
-  unsigned char* base = static_cast<unsigned char*>(kv ? a.cache.v : a.cache.k) + head * a.cache.hs * eb;
   const int32_t* pages = a.pages + (int64_t)i * a.pages_ld;
   auto place = [&](int t) {
     return token_offset(t, pages[page_entry(t, a.cache.page_size, a.pages_per_seq)], a.cache.n_pages, a.cache.page_size,
                         a.cache.ps, a.cache.ts);
   };
-  const int at_once = 256 / vec, piece = threadIdx.x % vec, first = threadIdx.x / vec;
-  for (int d0 = 0; d0 < n; d0 += at_once * AHEAD) {
-    u32x4 x[AHEAD];
-    int64_t to[AHEAD];
+  const int slots = MOVERS / vec, piece = threadIdx.x % vec, first = threadIdx.x / vec;  // of a turn's AHEAD shares
+  const int at_once = max(slots * AHEAD / n, 1), tokens = min(n, slots * AHEAD);         // planes and tokens of a turn
+  for (int p0 = plane0; p0 < plane1; p0 += at_once)
+    for (int d0 = 0; d0 < n; d0 += tokens) {
+      u32x4 x[AHEAD];
+      unsigned char* to[AHEAD];
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j) {
-      const int d = d0 + j * at_once + first;
-      to[j] = -1;
-      if (first < at_once && d < n && kept[d] != d) {
-        const int64_t from = place(len + kept[d]);
-        to[j] = place(len + d);
-        if (from < 0) to[j] = -1;
-        else x[j] = *GLOBAL_PTR(const u32x4, base + from * eb + piece * 16);
+      for (int j = 0; j < AHEAD; ++j) {
+        const int s = j * slots + first, dp = s / tokens;  // the turn's plane and token
+        const int d = d0 + s - dp * tokens, plane = p0 + dp;
+        to[j] = nullptr;
+        if (first < slots && dp < at_once && plane < plane1 && d < n && kept[d] != d) {
+          const int64_t from = place(len + kept[d]), into = place(len + d);
+          if (from < 0 || into < 0) continue;
+          unsigned char* base = static_cast<unsigned char*>(plane & 1 ? a.cache.v : a.cache.k) +
+                                (plane >> 1) * a.cache.hs * eb + piece * 16;
+          to[j] = base + into * eb;
+          x[j] = *GLOBAL_PTR(const u32x4, base + from * eb);
+        }
       }
-    }
-    __syncthreads();
+      __syncthreads();
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (to[j] >= 0) *GLOBAL_PTR(u32x4, base + to[j] * eb + piece * 16) = x[j];
-  }
+      for (int j = 0; j < AHEAD; ++j)
+        if (to[j]) *GLOBAL_PTR(u32x4, to[j]) = x[j];
+    }
 }
 
 }  // namespace
@@ -333,10 +362,13 @@ hipError_t launch_kv_copy_pages(const KvCache& c, int32_t G, int32_t D, const in
 }
 
 hipError_t launch_kv_compact(const CompactArgs& a, hipStream_t s) {
-  const int64_t blocks = 2 * (int64_t)a.G * a.n;
-  if (blocks == 0) return hipSuccess;
+  if (a.n == 0) return hipSuccess;
+  // a workgroup for each plane of a long list; what moves of a short one (a path of a tree) is a few
+  // turns of one workgroup, whose way to the first load is most of its time
+  const int planes = a.most <= 256 ? 2 * a.G : 1;
+  const int64_t blocks = (int64_t)a.n * (2 * a.G / planes);
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  return launch_k(&kv_compact, dim3((unsigned)blocks), dim3(256), 0, s, a, a.D / (a.cache.e4m3 ? 16 : 8));
+  return launch_k(&kv_compact, dim3((unsigned)blocks), dim3(MOVERS), 0, s, a, a.D / (a.cache.e4m3 ? 16 : 8), planes);
 }
 
 }  // namespace ubx
