@@ -613,11 +613,21 @@ def ub_kv_append(h, q, k, v, q_out, k_out, inv_freq, cu_seqlens, past_lens, n_se
         _check(st, h)
 
 
+def _rows_int32(h, x, rows, what):
+    """A pointer to an int32 value for each active row T.  A call refuses matrices of fewer than T
+    rows, so as many as one of them (`rows`) has are enough; asking the handle costs a call."""
+    if type(x) is torch.Tensor or isinstance(x, torch.Tensor):
+        return _int32(x, rows if x.numel() >= rows else ub_get_active_shape(h)[0], what)
+    return _ptr(x)
+
+
 def ub_kv_append_at(h, q, k, v, q_out, k_out, inv_freq, offsets, cu_seqlens, past_lens, n_seqs, cache, pages, cfg,
                     stream=None):
     """offsets: an int32 value for each active row."""
     inv_freq, table, ld, per_seq = _append_args(q, k, v, q_out, k_out, inv_freq, cache, pages, n_seqs, cfg)
-    st = _lib.ub_kv_append_at(h, q, k, v, q_out, k_out, inv_freq, _rows_int32(h, offsets, "offsets"),
+    some = q if q is not None else k
+    st = _lib.ub_kv_append_at(h, q, k, v, q_out, k_out, inv_freq,
+                              _rows_int32(h, offsets, 0 if some is None else some.rows, "offsets"),
                               _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), _int32(past_lens, n_seqs, "past_lens"),
                               n_seqs, cache, table, ld, per_seq, cfg, _stream(stream))
     if st:
@@ -708,21 +718,13 @@ def ub_attn_decode_window(h, q, cache, pages, kv_lens, n_seqs, window, out, lse,
         _check(st, h)
 
 
-def _rows_int32(h, x, what):
-    """A pointer to an int32 value for each row that a sequence may use: as many as the handle's
-    active rows, or as the tensor holds where only those are sequences' rows."""
-    if type(x) is torch.Tensor or isinstance(x, torch.Tensor):
-        return _int32(x, ub_get_active_shape(h)[0], what)
-    return _ptr(x)
-
-
 def ub_attn_tree(h, q, cache, pages, kv_lens, parents, cu_seqlens, n_seqs, out, lse, cfg, workspace, stream=None):
     """parents: an int32 value for each active row."""
     _hold_cached(q, out, cache, cfg)
     table, ld, per_seq = _table(pages, n_seqs)
     ws, ws_bytes = _ws_arg(workspace)
     st = _lib.ub_attn_tree(h, q, cache, table, ld, per_seq, _int32(kv_lens, n_seqs, "kv_lens"),
-                           _rows_int32(h, parents, "parents"), _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), n_seqs, out,
+                           _rows_int32(h, parents, 0 if q is None else q.rows, "parents"), _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), n_seqs, out,
                            _lse_arg(lse, h, cfg, out), cfg, ws, ws_bytes, _stream(stream))
     if st:
         _check(st, h)
