@@ -62,7 +62,7 @@ def check(ub, shape, lens, pad, window, sinks, times=2):
     assert bool(torch.isnan(dx[:, (H + 2 * G) * D:]).all())
 
 
-@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 64), (31, 0), (33, 5), (64, 0), (100, 33), (129, 4),
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 0), (3, 5), (8, 0), (9, 0), (2, 64), (31, 0), (33, 5), (64, 0), (100, 33), (129, 4),
                                           (1 << 31, 0), (200, 64)])
 @pytest.mark.parametrize("shape,lens,pad", [
     ((1, 1, 8), [1], 0),
