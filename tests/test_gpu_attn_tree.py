@@ -111,6 +111,13 @@ TREES = [
     (2, 1, 96, [1], [20000], 64, False, False, 0),
     (2, 1, 40, [100, 256, 17], [3000, 64, 4000], 48, False, False, 0),
     (8, 1, 128, [60, 31, 50, 44] * 3, [2000, 30, 900, 5] * 3, 64, True, False, 0),
+    # 17 to 32 columns, and few, of each type and size
+    (4, 1, 128, [6, 8, 5], [700, 64, 3], 16, False, False, 0),
+    (4, 1, 128, [6, 8, 5], [700, 64, 3], 16, True, True, 0),
+    (3, 1, 96, [9, 8], [128, 1000], 40, True, False, 1),
+    (3, 1, 80, [9, 8], [128, 1000], 40, False, True, 1),
+    (8, 8, 128, [3, 9], [5000, 100], 64, True, False, 0),
+    (2, 1, 48, [30, 25], [300, 77], 16, True, True, 3),
 ]
 
 
@@ -346,3 +353,55 @@ def test_compact_bad_lists(ub):  # noqa: F811
             if max(int(table[i, a // page]), int(table[i, b // page])) < n * per:
                 want[int(table[i, b // page]), b % page] = old[int(table[i, a // page]), a % page]
     assert torch.equal(raw(kc).view(n * per, page, -1), want)
+
+
+def far_cache(seed, n_pages=3, G=2, page=16, D=64):
+    """Pages 2^31 elements apart, each offset past 32 bits but the first's."""
+    caches = []
+    for s in (seed, seed + 1):
+        flat = torch.empty((n_pages - 1) * (1 << 31) + G * page * D, dtype=BF16, device="cuda")
+        c = flat.as_strided((n_pages, G, page, D), (1 << 31, page * D, D, 1))
+        c.copy_(normal(s, (n_pages, G, page, D)).cuda())
+        caches.append(c)
+    return caches
+
+
+def test_offsets_past_32_bits(ub):  # noqa: F811
+    """Trees, windowed decode, accepted tokens, copies and the append over pages far apart."""
+    H, G, D, page = 4, 2, 64, 16
+    kc, vc = far_cache(5)
+    trees = [[-1, 0, 0, 1, -1]]
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32)
+    q = normal(50, (5, H * D), 1.5)
+    cache = ub.make_kv_cache(kc, vc)
+    kv, vv = kc.double().cpu(), vc.double().cpu()
+    out, lse = attend(ub, q, cache, table, [45], torch.tensor(trees[0], dtype=torch.int32), [5], (H, G, D), 5)
+    check_rows(out.cpu(), lse.cpu(), q, kv, vv, table, trees, [45], page, (H, G, D))
+    cfg = ub.make_attn_cfg(H, G, D, rotary_dim=0)
+    dec, dl = torch.zeros((5, H * D), dtype=BF16, device="cuda"), torch.zeros((H, 5), device="cuda")
+    ws = workspace(ub, ub.UB_ATTN_DECODE_WINDOW, cfg, 5, 1)
+    x = normal(60, (5, 2 * G * D)).cuda()
+    td, qd = table.cuda(), q.cuda()
+    with Rank(ub, 5) as h:
+        ub.ub_attn_decode_window(h, ub.heads(qd), cache, td, i32([45]), 1, ub.make_attn_window(20, 3), ub.heads(dec), dl, cfg, ws)
+        ub.ub_kv_append_at(h, None, ub.heads(x), ub.heads(x, G * D), None, None, None, i32([0] * 5), i32([0, 5]), i32([40]), 1,
+                           cache, td, cfg)
+        ub.ub_kv_compact(h, cache, td, i32([10]), i32([[2, 8, 30, 33]]), i32([4]), 1, i32([0]), cfg)
+        ub.ub_kv_copy_pages(h, cache, i32([[2, 1, 7]]), 1, cfg)
+        torch.cuda.synchronize()
+    at = torch.tensor([0, 1, 2] + list(range(25, 45)))
+    pg, off = table[0].long()[at // page], at % page
+    for hh in range(H):
+        o, l, to, tl = ref.one(q[:1, hh * D: (hh + 1) * D].double(), kv[pg, hh // 2, off], vv[pg, hh // 2, off], D ** -0.5,
+                               torch.ones((1, len(at)), dtype=torch.bool))
+        ref.check(dec[:1, hh * D: (hh + 1) * D], o, to, "decode")
+        ref.check(dl[hh, :1], l, tl, "decode lse")
+    for c, want, col in ((kc, kv, 0), (vc, vv, G * D)):
+        for j in range(5):
+            want[1, :, 8 + j] = x[j, col: col + G * D].double().cpu().view(G, D)
+        old = want.clone()
+        for d, j in enumerate((2, 8, 30, 33)):
+            a, b = 10 + j, 10 + d
+            want[int(table[0, b // page]), :, b % page] = old[int(table[0, a // page]), :, a % page]
+        want[1, :, :7] = want[2, :, :7]
+        assert torch.equal(c.double().cpu(), want)
