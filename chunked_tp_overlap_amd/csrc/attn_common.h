@@ -199,11 +199,7 @@ __device__ inline f32x4 seen_product(bf16x8 a, bf16x8 b, f32x4 acc, int row, int
   return r;
 }
 
-// The same under a window: row r of the tile for column c if it comes no later than row at + c
-// and either fewer than win.size rows before it or among the first win.sinks of the sequence.
-__device__ inline bool seen(int key, int row, Window win) {
-  return key <= row && (key > row - win.size || key < win.sinks);
-}
+// The same under a window, from the rows that are `seen` (that see the column).
 // KEYS: the tile's rows are keys and the columns rows that see them; otherwise the reverse.
 template <bool KEYS>
 __device__ inline f32x4 seen_product(bf16x8 a, bf16x8 b, f32x4 acc, int row, int at, int lane, Window win) {
@@ -222,22 +218,6 @@ __device__ inline f32x4 seen_product(bf16x8 a, bf16x8 b, f32x4 acc, int row, int
     if ((lane & 15) == c) r = y;
   }
   return r;
-}
-
-// The key tiles of BN keys that rows q0 .. q0 + BM - 1 see, as one list: `sink` tiles of the
-// first tokens, then those from `first` on.  Of `tiles` in all, the first `head` hold keys
-// that the window hides from one of the rows.
-struct KeyTiles {
-  int sink, first, head, tiles;
-  __device__ int at(int j) const { return j < sink ? j : j - sink + first; }
-};
-__device__ inline KeyTiles key_tiles(int q0, int BM, int BN, int n_keys, Window win) {
-  KeyTiles k;
-  k.first = max(q0 - win.size + 1, 0) / BN;
-  k.sink = min((win.sinks + BN - 1) / BN, k.first);
-  k.tiles = k.sink + (n_keys + BN - 1) / BN - k.first;
-  k.head = min(k.sink + (max(q0 + BM - win.size, 0) + BN - 1) / BN - k.first, k.tiles);
-  return k;
 }
 
 // Makes the compiler wait here for a value it loads.  It does not count the direct-to-LDS

@@ -5,6 +5,7 @@
 
 #include <string>
 
+#include "attn_window.h"
 #include "ub_internal.h"
 
 namespace ubx {
@@ -53,13 +54,6 @@ struct AppendArgs {
   int32_t interleaved;
 };
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s);
-
-// A row at position t of its sequence sees u <= t with t - u < size, or u < sinks; size 0: all
-// u <= t.
-struct Window {
-  int32_t size, sinks;
-};
-constexpr int32_t kMaxWindow = 1 << 30;  // no row's distance reaches it
 
 struct PromptArgs {
   Heads q, k, v, out;

@@ -49,27 +49,6 @@ struct BwdParams {
 };
 
 constexpr int MAX_SINKS = UB_ATTN_MAX_SINKS;
-constexpr int MIN_CHUNK = 512;
-
-// The first tokens that stay visible under a window are seen by all later rows: the workgroup of
-// a sequence's first keys would walk all of it where every other walks a window's rows.  It
-// takes the rows up to `rows`, as far as its other keys are seen, and further workgroups take
-// `chunk` rows each.  Their sums for the first tokens go to slots of the workspace, one for the
-// first workgroup and one for each of the others, the sequences' one after another, and
-// attn_bwd_sinks adds them in order.  Where what is left is no longer than MIN_CHUNK the first
-// workgroup takes it all.
-struct SinkSlots {
-  int rows;   // of a sequence's first workgroup, all or a multiple of 32
-  int count;  // slots of the sequence: 0 or 1 + chunks
-};
-__device__ inline SinkSlots sink_slots(int len, int BK, Window win, int chunk) {
-  SinkSlots s;
-  s.rows = min((BK - 1 + win.size + 31) / 32 * 32, len);
-  s.count = 0;
-  if (len - s.rows <= MIN_CHUNK) s.rows = len;
-  else s.count = 1 + (len - s.rows + chunk - 1) / chunk;
-  return s;
-}
 
 __device__ inline int seq_len(const Seqs& s, int i) {
   return i < s.n ? max(clamp_row(s.cu[i + 1], s.T) - clamp_row(s.cu[i], s.T), 0) : 0;
@@ -500,20 +479,20 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, int
   const int wk0 = k0 + w * 16 * KF;
   const int heads = a.H / a.G / p.parts, head0 = kvh * (a.H / a.G) + part * heads;
   // query tiles: from the first key's row to the last row that sees one of the keys
-  int qt0 = k0 / BQ, last = st.len;
   SinkSlots span{};  // of a sequence's first keys
-  if (WIN) {
-    last = (int)min((int64_t)k0 + BK - 1 + a.win.size, (int64_t)st.len);
-    if (k0 == 0 && a.win.sinks > 0) {
-      span = sink_slots(st.len, BK, a.win, p.chunk);
-      last = span.rows;
-    }
-    if (sinks) {
-      qt0 = (span.rows + (st.tile - 1) * p.chunk) / BQ;
-      last = min(span.rows + st.tile * p.chunk, st.len);
+  QueryTiles qt;
+  if (!WIN) {
+    qt = query_tiles(k0, BK, BQ, st.len, Window{0, 0});
+  } else {
+    if (k0 == 0 && a.win.sinks > 0) span = sink_slots(st.len, BK, a.win, p.chunk);
+    qt = query_tiles(k0, BK, BQ, k0 == 0 && a.win.sinks > 0 ? span.rows : window_end(k0, BK, st.len, a.win), a.win);
+    if (sinks) {  // all of them may hold rows that do not see the keys after the first tokens
+      qt.qt0 = (span.rows + (st.tile - 1) * p.chunk) / BQ;
+      qt.n = (min(span.rows + st.tile * p.chunk, st.len) + BQ - 1) / BQ - qt.qt0;
+      qt.diag = qt.tail = qt.edge = qt.n;
     }
   }
-  const int qtiles = (last + BQ - 1) / BQ - qt0;
+  const int qt0 = qt.qt0, qtiles = qt.n, edge = qt.edge;
   const int total = heads * qtiles;
   const int64_t T = a.seqs.T;
   const uint32_t lds = lds_addr(smem);
@@ -522,12 +501,8 @@ __device__ __forceinline__ void bwd_kv(const BwdParams& p, int gp, int rank, int
   dl.init(w, lane, a.dout.rs, a.D);
   // The query tiles that may hold rows before one of the workgroup's keys come first, head by
   // head, then the others: item j of the group's j = grp, grp + NG, ...  Under a window those that
-  // may hold rows which do not see one of the keys any more belong to the first kind: tiles
-  // `tail` and on, of which all are where the first tokens are among the keys.
-  const int diag = sinks ? qtiles : min(BK / BQ, qtiles);
-  const int tail = !WIN || sinks ? qtiles : min(max((int)(((int64_t)k0 + a.win.size) / BQ) - qt0, diag), qtiles);
-  const int edge = diag + qtiles - tail;
-  auto tile_of = [&](int q) { return !WIN ? q : q < diag ? q : q < edge ? q - diag + tail : q - edge + diag; };
+  // may hold rows which do not see one of the keys any more are of the first kind.
+  auto tile_of = [&](int q) { return WIN ? qt.at(q) : q; };
   struct Item {
     int h, q, end;  // head, query tile, and where the head's tiles of this kind end
   };
@@ -886,8 +861,6 @@ int bwd_parts(int H, int G, int64_t rows, bool small) {
   return parts;
 }
 
-// Slots that sequences of T rows together can take: each of them has more than MIN_CHUNK rows left.
-int64_t max_slots(int64_t T, int64_t chunk) { return T / chunk + 2 * (T / MIN_CHUNK); }
 int64_t slot_bytes(int G, int parts, int D) { return (int64_t)2 * G * parts * MAX_SINKS * D * 4; }
 
 template <class SQ, class SK, bool WIN>
@@ -906,8 +879,7 @@ hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
   p.part = reinterpret_cast<float*>(w + 2 * stat);
   const int64_t ranks = max_tiles(T, a.seqs.n, SQ::BM) + (a.seqs.n == 0);
   if (WIN && a.win.sinks > 0) {
-    // as many rows as another workgroup of one window takes
-    p.chunk = (int32_t)std::min<int64_t>(std::max<int64_t>(MIN_CHUNK, (a.win.size + 31) / 32 * 32), 1 << 20);
+    p.chunk = sink_chunk(a.win);
     p.slots = (int32_t)std::min<int64_t>(max_slots(T, p.chunk), T / p.chunk + 2 * (int64_t)a.seqs.n);
     p.sink_part = p.part + (p.parts > 1 ? (int64_t)p.parts * 2 * a.G * T * a.D : 0);
   }

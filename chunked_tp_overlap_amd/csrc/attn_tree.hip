@@ -50,7 +50,7 @@ struct TreeParams {
   float c;         // scale * log2(e) (/ k_scale)
   float v_inv;     // 1 / v_scale
   int32_t cap;     // tokens the page table can hold per sequence
-  uint32_t page_mul, page_shift;  // t / page_size = (umulhi(t, page_mul) + t) >> page_shift, t < 2^30
+  PageDiv div;     // by the page size
   int32_t at_once;  // workgroups of a key-value head that run at once
   int4* seqs;       // [n]: a sequence's first workgroup among `w` of a head, its k_i, its strips, w
   float* part;      // [ROUNDS at_once G, COLS, D]: a workgroup's output where a strip has several parts
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
   int id = 0;
   auto look = [&](int j) {
     const uint32_t t = min(j * BN + lane, sq.len - 1);
-    id = pages[(__umulhi(t, p.page_mul) + t) >> p.page_shift];  // inside the row: len <= cap
+    id = pages[p.div.page(t)];  // inside the row: len <= cap
   };
   look(j0);
 
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
   u32x4 kreg[N], vreg[N];  // E4M3 alone
   auto fetch = [&](int j, int stage) {
     const uint32_t t = min(j * BN + lane, sq.len - 1);
-    const uint32_t o = t - ((__umulhi(t, p.page_mul) + t) >> p.page_shift) * (uint32_t)a.cache.page_size;
+    const uint32_t o = t - p.div.page(t) * (uint32_t)a.cache.page_size;
     const bool there = (uint32_t)id < (uint32_t)a.cache.n_pages;
     lost = lost || !there;
     const int64_t place = ((there ? id : 0) * a.cache.ps + o * a.cache.ts) * EB;
@@ -677,9 +677,7 @@ hipError_t run(const TreeArgs& a, hipStream_t s) {
   p.c = a.scale * LOG2E * (S::F8 ? 1.0f / a.cache.k_scale : 1.0f);
   p.v_inv = S::F8 ? 1.0f / a.cache.v_scale : 1.0f;
   p.at_once = at_once(a.G);
-  const uint32_t page = (uint32_t)a.cache.page_size;
-  while ((1ull << p.page_shift) < page) ++p.page_shift;
-  p.page_mul = (uint32_t)(((((1ull << p.page_shift) - page) << 32) / page) + 1);
+  p.div = page_div((uint32_t)a.cache.page_size);
   const int64_t rows = (int64_t)ROUNDS * p.at_once * a.G * S::COLS;
   p.stat = static_cast<float2*>(a.ws);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + rows * 8);

@@ -28,6 +28,18 @@ __host__ __device__ inline int page_entry(P pos, int page_size, int pages_per_se
   return e < pages_per_seq ? (int)e : -1;
 }
 
+// Division by the page size with a product: exact for 0 <= t < 2^30 and any size below 2^31.
+struct PageDiv {
+  uint32_t mul, shift;
+  __host__ __device__ uint32_t page(uint32_t t) const { return ((uint32_t)((uint64_t)t * mul >> 32) + t) >> shift; }
+};
+inline PageDiv page_div(uint32_t size) {
+  PageDiv d{0, 0};
+  while ((uint64_t(1) << d.shift) < size) ++d.shift;
+  d.mul = (uint32_t)((((uint64_t(1) << d.shift) - size) << 32) / size + 1);
+  return d;
+}
+
 // Element offset, in head 0, of token pos of a sequence whose table entry for it holds `id`;
 // -1 if there is no such page.
 template <class P>

@@ -3,10 +3,12 @@ C ABI, workspace sizes, and what the binding refuses before any address reaches 
 
 import ctypes
 import math
+import os
 
 import pytest
 import torch
 
+from tests import test_host_cpp as hc
 from tests.test_attn_binding import bf16, device, i32
 from tests.test_attn_host import BAD_CACHES, BAD_CFGS, BAD_HEADS, FAKE, T, cfg, heads, kv, status
 
@@ -186,3 +188,10 @@ def test_host_tensors_and_sizes(h):
         with pytest.raises(ValueError, match=match):
             call()
     assert math.isfinite(c.softmax_scale) and ctypes.sizeof(ub.ub_attn_window_t) == 8
+
+
+@pytest.mark.skipif(hc._cxx() is None, reason="clang++ not available")
+def test_window_arithmetic(tmp_path):
+    """The tiles and slots of windowed calls, and the page of a token by a product."""
+    out = hc._build_and_run(tmp_path, "attn_window_check", [os.path.join(hc.CPP, "attn_window_check.cpp")])
+    assert int(out.split()[1]) > 500000
