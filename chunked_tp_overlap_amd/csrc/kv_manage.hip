@@ -5,8 +5,9 @@
 // free.  There is no list of free pages: giving pages takes the free ones of the lowest numbers,
 // so that the same calls give the same pages on every run, whatever order counts changed in.
 // Counts and tables are a few integers per page; what bounds these calls is their chains of
-// loads and launches.  kv_resize is two launches: one workgroup gives pages, as a row's pages
-// depend on all rows before it, then a workgroup for each row takes back what it gives up.
+// loads and launches.  In kv_resize one workgroup gives pages, as a row's pages depend on all rows
+// before it; then a wave for each row takes back what it gives up, in a launch of its own where
+// rows are many.
 // kv_copy_pages and kv_compact move tokens, 16 bytes to a lane.
 #include <hip/hip_runtime.h>
 
@@ -105,11 +106,46 @@ __device__ inline Lens lens_of(const ResizeArgs& a, int i) {
   return l;
 }
 
+// A row's end of the call, by one wave: what it gives up, its copy and its length; k: its ask,
+// given: it gets what it asks for.
+__device__ inline void take_row(const ResizeArgs& a, int i, const Ask& k, bool given) {
+  const int lane = threadIdx.x & 63;
+  const Lens l = lens_of(a, i);
+  const int len = given ? l.wants : l.has, has = pages_of(len, a.page);
+  int32_t* row = a.table.p + (int64_t)i * a.table.ld;
+  const int to = given && k.part > 0 ? row[k.had - 1] : -1;
+  auto take = [&](int e) {
+    const int id = row[e];
+    if (id >= 0 && id < a.n_pages) atomicAdd(a.refs + id, -1);
+    row[e] = -1;
+  };
+  for (int e = has + lane; e < k.had; e += 64) take(e);
+  bool hidden = false;  // all of the page that would be copied to
+  if (a.win.size > 0 && len > a.win.size) {
+    // pages of hidden tokens alone
+    const int begin = pages_of(a.win.sinks, a.page), end = min((len - a.win.size) / a.page, has);
+    hidden = k.had - 1 >= begin && k.had - 1 < end;
+    for (int e = begin + lane; e < end; e += 64) take(e);
+  }
+  if (lane == 0) {
+    const bool copy = given && k.part > 0 && !hidden;
+    int32_t* c = a.copies + 3 * (int64_t)i;
+    c[0] = copy ? k.src : -1;
+    c[1] = copy ? to : -1;
+    c[2] = copy ? k.part : 0;
+    if (given && k.part > 0) atomicAdd(a.refs + k.src, -1);
+    a.lens_out[i] = len;
+  }
+}
+
 // One workgroup.  The rows' asks, the free pages counted as far as they are asked for, and then
 // turn by turn a list of free pages in LDS, from which each goes to its row: the first whose `end`
-// lies past the page's rank, found in LDS too (ROWS_IN_LDS rows and fewer).  With the search in
-// the workspace and a page's place from the count that its thread read, 576 rows took 19.6 us.
+// lies past the page's rank, found in LDS too (ROWS_IN_LDS rows and fewer).  576 rows that grow by
+// 2000 pages together take 10.2 us; with the search in the workspace, and a page's place from the
+// counts that its thread read, 19.6.  64 rows that get 500 pages each take some 50 us.
+// ALL: and then what kv_take does for every row.
 constexpr int ROWS_IN_LDS = 4096;
+template <bool ALL>
 __global__ __launch_bounds__(GIVERS) void kv_give(ResizeArgs a) {
   __shared__ int64_t sums[GIVE_WAVES];
   __shared__ int32_t ids[GIVERS * PER], ends[ROWS_IN_LDS];
@@ -185,7 +221,6 @@ __global__ __launch_bounds__(GIVERS) void kv_give(ResizeArgs a) {
     free += all;
   }
   if (threadIdx.x == 0) *free_of(a.ws) = free;
-  if (total == 0 || free == 0) return;
   // as many as go to rows that get all they ask for
   int64_t limit = total;
   if (free < total) {
@@ -219,40 +254,19 @@ __global__ __launch_bounds__(GIVERS) void kv_give(ResizeArgs a) {
     found += all;
     __syncthreads();
   }
+  if (!ALL) return;
+  __syncthreads();
+  for (int i = threadIdx.x >> 6; i < n; i += GIVE_WAVES) {
+    const Ask k = ask[i];
+    take_row(a, i, k, k.end == (i > 0 ? ask[i - 1].end : 0) || k.end <= free);
+  }
 }
 
 __global__ __launch_bounds__(64) void kv_take(ResizeArgs a) {
   const Ask* ask = asks_of(a.ws);
   const int i = blockIdx.x;
   const Ask k = ask[i];
-  const int64_t before = i > 0 ? ask[i - 1].end : 0;
-  const Lens l = lens_of(a, i);
-  const bool given = k.end == before || k.end <= *free_of(a.ws);
-  const int len = given ? l.wants : l.has;
-  int32_t* row = a.table.p + (int64_t)i * a.table.ld;
-  auto take = [&](int e) {
-    const int id = row[e];
-    if (id >= 0 && id < a.n_pages) atomicAdd(a.refs + id, -1);
-    row[e] = -1;
-  };
-  const int has = pages_of(len, a.page);
-  for (int e = has + threadIdx.x; e < k.had; e += 64) take(e);
-  if (a.win.size > 0 && len > a.win.size) {
-    // pages of hidden tokens alone
-    const int end = min((len - a.win.size) / a.page, has);
-    for (int e = pages_of(a.win.sinks, a.page) + threadIdx.x; e < end; e += 64) take(e);
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const bool own = given && k.part > 0;
-    const int to = own ? row[k.had - 1] : -1;  // -1 also where the window hides all of the page
-    int32_t* c = a.copies + 3 * (int64_t)i;
-    c[0] = to >= 0 ? k.src : -1;
-    c[1] = to;
-    c[2] = to >= 0 ? k.part : 0;
-    if (own) atomicAdd(a.refs + k.src, -1);
-    a.lens_out[i] = len;
-  }
+  take_row(a, i, k, k.end == (i > 0 ? ask[i - 1].end : 0) || k.end <= *free_of(a.ws));
 }
 
 // ---- copies ---------------------------------------------------------------------------------
@@ -350,9 +364,14 @@ hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s) {
 
 size_t kv_resize_bytes(int32_t n) { return n > 0 ? ASKS_AT + sizeof(Ask) * (size_t)n : 0; }
 
+constexpr int ONE_LAUNCH = 64, ONE_LAUNCH_WINDOW = 16;
 hipError_t launch_kv_resize(const ResizeArgs& a, hipStream_t s) {
   if (a.table.n == 0) return hipSuccess;
-  const hipError_t e = launch_k(&kv_give, dim3(1), dim3(GIVERS), 0, s, a);
+  // Few rows are done by the one workgroup's waves, a launch less (of a call's 7 us on the host, 2).  On
+  // the device, in a graph, 64 rows that grow take 8.5 us with one launch, 65 take 7.8 with two;
+  // under a window, whose pages left behind each wave looks for, 14.4 and 9.2, and 16 rows 7.9.
+  if (a.table.n <= (a.win.size > 0 ? ONE_LAUNCH_WINDOW : ONE_LAUNCH)) return launch_k(&kv_give<true>, dim3(1), dim3(GIVERS), 0, s, a);
+  const hipError_t e = launch_k(&kv_give<false>, dim3(1), dim3(GIVERS), 0, s, a);
   return e == hipSuccess ? launch_k(&kv_take, dim3((unsigned)a.table.n), dim3(64), 0, s, a) : e;
 }
 
