@@ -26,6 +26,13 @@
 // more waves of 16 rows each 57.3; two such workgroups to a CU 62; the product with the values one
 // step late, beside the next scores, 68.
 //
+// Under a window a workgroup's tiles are those of the first tokens that stay visible and those from
+// its first row's first key on (attn_window.h); the ones that hide keys from some row, at both
+// ends, are masked.  The reference is then that of the first tile that a row sees a key of.  Measured:
+// the same sequence of 24392 tokens under a window of 2048 and 4 first tokens 216 us, 0.91 PFLOP/s
+// counted; three rounds of workgroups of 35 tiles, 9% of their pairs hidden, and each round's
+// start, some 6 us, shows.
+//
 // Rows past a sequence's end (of any input) are never read: their loads fall outside the
 // buffer resource and give zeros.
 #include <hip/hip_runtime.h>

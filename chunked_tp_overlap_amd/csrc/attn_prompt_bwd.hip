@@ -16,6 +16,11 @@
 // are busy 52% of the time at the 2.1 GHz that the power limit leaves.  8184 tokens in 5 sequences,
 // 4 heads of 128 on 4: 170-174 us, bounded by the steps of the longest rows, as the forward pass.
 // (One call at a time, under a profiler, its kernels take 187.)
+//
+// Under a window both kinds walk the tiles that their rows and keys meet (attn_window.h), and the
+// first tokens that stay visible get further workgroups, whose sums attn_bwd_sinks adds.  Measured,
+// 16264 tokens in 2 sequences, 8 heads on 1, a window of 2048 and 4 first tokens: 455 us, 0.92
+// PFLOP/s of the seven products done; 8184 tokens in 5, 4 heads on 4, 512 and none: 56 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -784,14 +789,24 @@ __global__ __launch_bounds__(256) void attn_bwd_sinks(BwdParams p) {
   const int64_t slot = slots_before(p, row0, BK);
   if (slot < 0 || slot + count > p.slots) return;
   const int64_t GP = a.G * p.parts, step = MAX_SINKS * a.D;
+  constexpr int AHEAD = 8;
   const int vec = a.D / 4;
   const Heads& o = which ? a.dv : a.dk;
   for (int j = threadIdx.x; j < a.win.sinks * vec; j += 256) {
     const int u = j / vec, e = (j - u * vec) * 4;
+    const float* at = p.sink_part + (slot * 2 * GP + which * GP + kvh * p.parts) * step + u * a.D + e;
     f32x4 x = {0, 0, 0, 0};
-    for (int c = 0; c < count; ++c) {
-      const float* at = p.sink_part + (((slot + c) * 2 + which) * GP + kvh * p.parts) * step + u * a.D + e;
-      for (int k = 0; k < p.parts; ++k) x += *reinterpret_cast<const f32x4*>(at + k * step);
+    const int n = count * p.parts;  // slot by slot, part by part, AHEAD loads at a time
+    for (int c0 = 0; c0 < n; c0 += AHEAD) {
+      f32x4 y[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int c = min(c0 + i, n - 1);
+        y[i] = *reinterpret_cast<const f32x4*>(at + (c / p.parts * 2 * GP + c % p.parts) * step);
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (c0 + i < n) x += y[i];
     }
     store4(o.p + (int64_t)(row0 + u) * o.rs + kvh * o.hs + e, x * (which ? 1.0f : a.scale));
   }

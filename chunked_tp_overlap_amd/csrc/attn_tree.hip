@@ -8,9 +8,9 @@
 // some of the sequence's tiles of BN keys.  The lengths are on the device, so the cut is made
 // there: sequence i's tiles go in k_i = ceil(tiles_i / c) equal parts, with the smallest c for
 // which all strips' parts are as many workgroups as run at once, or twice as many (c no smaller
-// than MIN_TILES; one part each where the strips are more than run at once).  The strips of one part of a sequence read
-// the same keys at the same time, so they are neighbours on one XCD, whose L2 then serves all
-// but one of them.  A strip in one part is finished by its workgroup; others leave parts (maximum,
+// than MIN_TILES; one part each where the strips are more than run at once).  The strips of one
+// part of a sequence read the same keys at the same time, so they are neighbours on one XCD, whose
+// L2 then serves all but one of them.  A strip in one part is finished by its workgroup; others leave parts (maximum,
 // sum and unnormalised output, fp32) in the workspace, and attn_tree_join adds them in order.
 //
 // Keys and values come from their pages (a lane looks up a token, a tile ahead): bf16 by direct
@@ -25,6 +25,21 @@
 //
 // The nodes that a node sees are bits, set once per strip by following the parents in LDS; only
 // the tiles of drafted tokens look at them.
+//
+// Sums and the softmax are fp32; the weights are rounded to bf16 as matrix-core operands, and each
+// output once.
+//
+// Measured on MI355X, both kernels.  64 sequences of 100 to 16264 tokens and up to 60 nodes, 8 heads
+// on 1, E4M3: 137 us, 0.63 PFLOP/s counted (86 GFLOP; 101 with the columns that fill the strips up);
+// a step of 64 keys and 128 columns takes 1.95 us on each of a CU's two workgroups, as in
+// attn_prompt.hip, 92 us if all had as many; the rest is parts of unequal length, 4 us before and
+// 2 after a part's tiles, and 17 of the join.  One sequence of 32520 and 24 nodes, bf16: 22 us: 4 us to
+// the first load's issue (lengths, cut, page ids), 1.6 and 6 for four tiles as memory delivers them,
+// 2 to the end, and the join's 6.  Bound by memory: 64 of 8192 with 2 nodes 61 us (4.4 TB/s), E4M3 35.
+// Not kept: ranges of equal length over the strips one after another, as attn_decode.hip deals
+// its tokens (every part ends at once, but no two strips read the same keys together: 3.4 us a
+// step in bf16, 157 us for the first case); the running maximum in every tile (185); E4M3 tiles
+// stored beside the step before (162).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -39,9 +54,12 @@ constexpr int MAX_NODES = UB_ATTN_MAX_TREE;
 constexpr int WORDS = MAX_NODES / 64;
 constexpr int NW = 4;
 constexpr int ITEMS = 512;     // workgroups that run at once: two on each CU
-constexpr int MIN_TILES = 4;   // tiles of a part at least, where there are so many
-// Parts of LONG_PART tiles or more are cut again, for two rounds of workgroups: what the first
-// leaves idle for want of equal parts is more than what starting the second costs.
+// Tiles of a part at least, where there are so many: the second case above takes 26.9 us with 2, 23.7
+// with 4, 27.4 with 8.
+constexpr int MIN_TILES = 4;
+// Parts of LONG_PART tiles or more are cut again, for two rounds of workgroups: what one round
+// leaves idle for want of equal parts is more than what starting another costs.  64 sequences of
+// 8192, 48 nodes: 158 us with one, 146 with two; 16 of 100 to 16264, 60 nodes (parts of 10) 47 and 62.
 constexpr int LONG_PART = 48, ROUNDS = 2;
 constexpr float MOST = 0x1p60f;  // a lane's sum beyond which the pass is done again
 
@@ -270,6 +288,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
     for (int s = 0; s < DS; ++s) q[f][s] = load_row8(row + 32 * s + 8 * g, live && 32 * s + 8 * g < a.D);
   }
   u32x4 kreg[N], vreg[N];  // E4M3 alone
+  // The row of a lane's i-th load.  Direct loads fill LDS in order; E4M3 rows r and r + 8 are
+  // neighbours, as a wave's stores of every other 16 bytes of their rows then meet all banks
+  // (in order each took twice as long).
+  auto row_of = [&](int i) {
+    const int n = (i * NW + wave) * RPL + lane / PPR;
+    return F8 ? (n & ~15) | ((n & 1) << 3) | ((n >> 1) & 7) : n;
+  };
   auto fetch = [&](int j, int stage) {
     const uint32_t t = min(j * BN + lane, sq.len - 1);
     const uint32_t o = t - p.div.page(t) * (uint32_t)a.cache.page_size;
@@ -280,7 +305,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
     const bool all = (j + 1) * BN <= sq.len && a.D == 32 * DS;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int r = (i * NW + wave) * RPL + lane / PPR;
+      const int r = row_of(i);
       const int chunk = F8 ? piece : piece ^ L::swz(r);
       const int64_t at = (int64_t)(((uint64_t)(uint32_t)__shfl(hi, r) << 32) | (uint32_t)__shfl(lo, r)) + chunk * 16;
       const unsigned char *k = kb + at, *v = vb + at;
@@ -299,7 +324,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
   auto keep = [&](int stage) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int r = (i * NW + wave) * RPL + lane / PPR;
+      const int r = row_of(i);
       unsigned char* at = smem + stage + r * L::RB;
       const int s0 = ((2 * piece) ^ L::swz(r)) * 16, s1 = ((2 * piece + 1) ^ L::swz(r)) * 16;
       *LDS_PTR(u32x4, at + s0) = cvt8(kreg[i][0], kreg[i][1]);
@@ -692,7 +717,8 @@ hipError_t run(const TreeArgs& a, hipStream_t s) {
   hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kernel), S::LDS);
   if (e == hipSuccess && a.seqs.n > 0) e = launch_k(kernel, dim3((unsigned)blocks), dim3(64 * NW), S::LDS, s, p);
   if (e != hipSuccess || outputs == 0) return e;
-  // few outputs have many parts, which more waves then share
+  // few outputs have many parts, which more waves then share; many are a row's heads to a workgroup
+  // (a wave each, 19.5 us in the first case above, now 17)
   if (outputs <= 512) return launch_k(&attn_tree_join<16, S::COLS>, dim3((unsigned)outputs), dim3(1024), 0, s, p);
   if (outputs <= 4096) return launch_k(&attn_tree_join<4, S::COLS>, dim3((unsigned)outputs), dim3(256), 0, s, p);
   return launch_k(&attn_tree_join<1, S::COLS>, dim3((unsigned)a.seqs.T), dim3(256), 0, s, p);
@@ -700,7 +726,8 @@ hipError_t run(const TreeArgs& a, hipStream_t s) {
 
 template <int DS, bool F8>
 hipError_t choose(const TreeArgs& a, hipStream_t s) {
-  // by the columns of a sequence, on average: the host knows no more
+  // By the columns of a sequence, on average: the host knows no more.  Fewer columns to a wave or
+  // workgroup read the same keys more often, more of them multiply by columns that are not there.
   const int64_t cols = a.seqs.n > 0 ? ((int64_t)a.seqs.T * (a.H / a.G) + a.seqs.n - 1) / a.seqs.n : 1;
   if (cols <= 16) return run<Shape<DS, 1, 1, F8>>(a, s);
   if (cols <= 32) return run<Shape<DS, 2, 1, F8>>(a, s);

@@ -2,6 +2,9 @@
 //
 //   angle = pos * inv_freq[m];  (a, b) -> (a cos - b sin, b cos + a sin)
 //
+// pos is the token's place in its sequence, or (drafted trees) past_lens and an offset of its own;
+// the place says where it is stored.
+//
 // HBM-bound: each of the token's (H + 2 G) D bf16 values is read once, each output written
 // once; the arithmetic per element is a few operations.  What would cost is the angle: far
 // positions need its reduction in 64 bits, pos * inv_freq / (2 pi) less its nearest integer,
