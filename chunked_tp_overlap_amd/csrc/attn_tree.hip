@@ -288,13 +288,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
     for (int s = 0; s < DS; ++s) q[f][s] = load_row8(row + 32 * s + 8 * g, live && 32 * s + 8 * g < a.D);
   }
   u32x4 kreg[N], vreg[N];  // E4M3 alone
-  // The row of a lane's i-th load.  Direct loads fill LDS in order; E4M3 rows r and r + 8 are
-  // neighbours, as a wave's stores of every other 16 bytes of their rows then meet all banks
-  // (in order each took twice as long).
-  auto row_of = [&](int i) {
-    const int n = (i * NW + wave) * RPL + lane / PPR;
-    return F8 ? (n & ~15) | ((n & 1) << 3) | ((n >> 1) & 7) : n;
-  };
   auto fetch = [&](int j, int stage) {
     const uint32_t t = min(j * BN + lane, sq.len - 1);
     const uint32_t o = t - p.div.page(t) * (uint32_t)a.cache.page_size;
@@ -305,7 +298,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
     const bool all = (j + 1) * BN <= sq.len && a.D == 32 * DS;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int r = row_of(i);
+      const int r = (i * NW + wave) * RPL + lane / PPR;
       const int chunk = F8 ? piece : piece ^ L::swz(r);
       const int64_t at = (int64_t)(((uint64_t)(uint32_t)__shfl(hi, r) << 32) | (uint32_t)__shfl(lo, r)) + chunk * 16;
       const unsigned char *k = kb + at, *v = vb + at;
@@ -324,7 +317,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
   auto keep = [&](int stage) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int r = row_of(i);
+      const int r = (i * NW + wave) * RPL + lane / PPR;
       unsigned char* at = smem + stage + r * L::RB;
       const int s0 = ((2 * piece) ^ L::swz(r)) * 16, s1 = ((2 * piece + 1) ^ L::swz(r)) * 16;
       *LDS_PTR(u32x4, at + s0) = cvt8(kreg[i][0], kreg[i][1]);
