@@ -19,8 +19,9 @@
 //
 // Under a window both kinds walk the tiles that their rows and keys meet (attn_window.h), and the
 // first tokens that stay visible get further workgroups, whose sums attn_bwd_sinks adds.  Measured,
-// 16264 tokens in 2 sequences, 8 heads on 1, a window of 2048 and 4 first tokens: 455 us, 0.92
-// PFLOP/s of the seven products done; 8184 tokens in 5, 4 heads on 4, 512 and none: 56 us.
+// 16264 tokens in 2 sequences, 8 heads on 1, a window of 2048 and 4 first tokens: 455-485 us (cards
+// differ), 0.86-0.92 PFLOP/s of the seven products done; 8184 tokens in 5, 4 heads on 4, 512 and
+// none: 58-63 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -128,83 +129,21 @@ __device__ inline float row_sum(float x) {
   return x;
 }
 
-// delta and lse log2(e) of all rows, 32 of one head to a wave; what they are in rows of no
-// sequence is not read.
-template <int LPR>
-__global__ __launch_bounds__(256) void attn_bwd_rows(BwdParams p) {
-  constexpr int AT_ONCE = 64 / LPR, N = 32 / AT_ONCE;
-  const PromptBwdArgs& a = p.a;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t T = a.seqs.T, task = (int64_t)blockIdx.x * 4 + wave;
-  const int head = (int)(task % a.H);
-  const int64_t row0 = task / a.H * 32;
-  if (row0 >= T) return;
-  const int e = lane % LPR * 8;
-  bf16x8 d[N], o[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int64_t row = row0 + i * AT_ONCE + lane / LPR;
-    const bool in = row < T && e < a.D;
-    d[i] = load_row8(a.dout.p + row * a.dout.rs + head * a.dout.hs + e, in);
-    o[i] = load_row8(a.out.p + row * a.out.rs + head * a.out.hs + e, in);
-  }
-  if (lane < 32 && row0 + lane < T) {
-    const int64_t at = head * T + row0 + lane;
-    const float l = a.lse[at];
-    p.lse2[at] = l == -INFINITY ? 0.0f : l * LOG2E;
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float x = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x += (float)d[i][k] * (float)o[i][k];
-    x = row_sum<LPR>(x);
-    const int64_t row = row0 + i * AT_ONCE + lane / LPR;
-    if (lane % LPR == 0 && row < T) p.delta[head * T + row] = x;
-  }
-}
-
-// The same under a window of few keys, with delta from its definition, the sum of P dP over a row's
-// keys.  From out, rounded to bf16, it is off by much of the dS of a row of few keys: the error of
-// dq and dk was 2.5, 2.0 and 1.5 times that of their own rounding with 2, 3 and 8 keys, and is 1.0
-// with this.  A row's keys are read 16 bytes to a lane, 4 at a time; neighbouring rows' are the
-// same ones.  The gradient of 8184 rows, 4 heads on 4, takes 52 us with 2 keys, 56 with 8 and 48 with 17
-// (without this; 64 if it were used for 16, where the error is 1.3).
+// Under a window, rows of up to FEW keys (a narrow window's, or the first of a sequence) get delta
+// from its definition, the sum of P dP over them.  From out, rounded to bf16, it is off by much of
+// the dS of a row of few keys: the error of dq and dk was 2.5, 2.0 and 1.5 times that of their own
+// rounding with 2, 3 and 8 keys, and is 1.0 with this.  8 rows of one head to a wave; a row's keys
+// are read 16 bytes to a lane, 4 at a time (neighbouring rows' are the same ones).  The gradient
+// of 8184 rows, 4 heads on 4, takes 52 us with 2 keys, 55 with 8 and 50 with 17 (64 if FEW were 16,
+// where the error is 1.3 without it); 2.5 of the last are the first rows'.  Lane i < 8 has where
+// row0 + i's sequence starts (past the row: none) and the row's lse log2(e).
 constexpr int FEW = 8, FEW_ROWS = 8;  // keys; rows of a wave
 template <int LPR>
-__global__ __launch_bounds__(256) void attn_bwd_rows_few(BwdParams p) {
+__device__ inline void bwd_delta_few(const BwdParams& p, int head, int64_t row0, int64_t end, int start, float lse2) {
   constexpr int AT_ONCE = 64 / LPR, N = FEW_ROWS / AT_ONCE, AHEAD = 4;
   const PromptBwdArgs& a = p.a;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t T = a.seqs.T, task = (int64_t)blockIdx.x * 4 + wave;
-  const int head = (int)(task % a.H);
-  const int64_t row0 = task / a.H * FEW_ROWS;
-  if (row0 >= T) return;
-  const int kvh = head / (a.H / a.G), e = lane % LPR * 8;
-  // lane i < FEW_ROWS: where row0 + i's sequence starts.  Sequences that end at or before the row come
-  // first
-  int seq = 0;
-  for (int c = 0; c < a.seqs.n; c += 64) {
-    const int end = c + lane < a.seqs.n ? a.seqs.cu[c + lane + 1] : 0x7FFFFFFF;
-    int more = 0;
-#pragma unroll
-    for (int j = 0; j < FEW_ROWS; ++j) {
-      const int m = __popcll(__ballot(end <= row0 + j));
-      seq += lane == j ? m : 0;
-      more |= m == 64;
-    }
-    if (!more) break;
-  }
-  const bool rows = lane < FEW_ROWS;
-  const int start = rows && seq < a.seqs.n ? max(a.seqs.cu[seq], 0) : 0x7FFFFFFF;  // past the row: none
-  float lse2 = 0.0f;
-  if (rows && row0 + lane < T) {
-    const int64_t at = head * T + row0 + lane;
-    const float l = a.lse[at];
-    lse2 = l == -INFINITY ? 0.0f : l * LOG2E;
-    p.lse2[at] = lse2;
-  }
-  const int window = a.win.size, keys = window + a.win.sinks;
+  const int lane = threadIdx.x & 63, kvh = head / (a.H / a.G), e = lane % LPR * 8;
+  const int window = a.win.size, keys = window + a.win.sinks, most = min(keys, FEW);
   auto dot = [](bf16x8 x, bf16x8 y) {
     float s = 0.0f;
 #pragma unroll
@@ -217,13 +156,13 @@ __global__ __launch_bounds__(256) void attn_bwd_rows_few(BwdParams p) {
     const int64_t row = row0 + r;
     const int64_t first = __shfl(start, r);
     const float l2 = __shfl(lse2, r);
-    const bool in = row < T && first <= row, mine = in && e < a.D;
+    const bool in = row < end && first <= row, mine = in && e < a.D;
     const int64_t t = row - first;
     const bf16x8 q = load_row8(a.q.p + row * a.q.rs + head * a.q.hs + e, mine);
     const bf16x8 d = load_row8(a.dout.p + row * a.dout.rs + head * a.dout.hs + e, mine);
     float delta = 0.0f;
 #pragma unroll 1
-    for (int j0 = 0; j0 < keys; j0 += AHEAD) {
+    for (int j0 = 0; j0 < most; j0 += AHEAD) {
       bf16x8 k[AHEAD], v[AHEAD];
       bool sees[AHEAD];
 #pragma unroll
@@ -241,8 +180,112 @@ __global__ __launch_bounds__(256) void attn_bwd_rows_few(BwdParams p) {
         delta += sees[j] ? exp2_(s * p.c - l2) * dp : 0.0f;
       }
     }
-    if (lane % LPR == 0 && row < T) p.delta[head * T + row] = delta;
+    if (lane % LPR == 0 && row < end) p.delta[head * a.seqs.T + row] = delta;
   }
+}
+
+// delta and lse log2(e) of all rows, 32 of one head to a wave; what they are in rows of no
+// sequence is not read.  Under a window the first waves, which take longer, have the first rows of
+// one sequence each, in one head, and the others leave those rows' delta to them.
+template <int LPR, bool WIN>
+__global__ __launch_bounds__(256) void attn_bwd_rows(BwdParams p) {
+  constexpr int AT_ONCE = 64 / LPR, N = 32 / AT_ONCE;
+  const PromptBwdArgs& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t T = a.seqs.T, task = (int64_t)blockIdx.x * 4 + wave;
+  const int head = (int)(task % a.H);
+  const int64_t row0 = (task / a.H - (WIN ? a.seqs.n : 0)) * 32;
+  if (row0 >= T) return;
+  if constexpr (WIN) {
+    const int64_t seq = task / a.H;
+    if (seq < a.seqs.n) {
+      const int64_t first = max(a.seqs.cu[seq], 0), end = min(min((int64_t)a.seqs.cu[seq + 1], T), first + FEW);
+      float lse2 = 0.0f;
+      if (lane < FEW_ROWS && first + lane < end) {
+        const float l = a.lse[head * T + first + lane];
+        lse2 = l == -INFINITY ? 0.0f : l * LOG2E;
+      }
+      bwd_delta_few<LPR>(p, head, first, end, (int)first, lse2);
+      return;
+    }
+  }
+  // lane l: where sequence c + l starts and its first FEW rows end, from row0 on, in the wave's 32
+  auto starts = [&](int c, int& from, int& to) {
+    const int l = min(c + lane, a.seqs.n - 1);
+    const int64_t start = max(a.seqs.cu[l], 0), end = min((int64_t)a.seqs.cu[l + 1], start + FEW);
+    from = (int)min(max(start - row0, (int64_t)0), (int64_t)32);
+    to = (int)min(max(end - row0, (int64_t)0), (int64_t)32);
+  };
+  int from = 0, to = 0;
+  if (WIN && a.seqs.n > 0) starts(0, from, to);
+  const int e = lane % LPR * 8;
+  bf16x8 d[N], o[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t row = row0 + i * AT_ONCE + lane / LPR;
+    const bool in = row < T && e < a.D;
+    d[i] = load_row8(a.dout.p + row * a.dout.rs + head * a.dout.hs + e, in);
+    o[i] = load_row8(a.out.p + row * a.out.rs + head * a.out.hs + e, in);
+  }
+  if (lane < 32 && row0 + lane < T) {
+    const int64_t at = head * T + row0 + lane;
+    const float l = a.lse[at];
+    p.lse2[at] = l == -INFINITY ? 0.0f : l * LOG2E;
+  }
+  unsigned first_rows = 0;  // bit i: row0 + i is one of the first FEW of its sequence
+  if constexpr (WIN) {
+    for (int c = 0; c < a.seqs.n; c += 64) {
+      if (c) starts(c, from, to);
+      for (uint64_t m = __ballot(from < to); m; m &= m - 1) {
+        const int l = __ffsll((unsigned long long)m) - 1;
+        first_rows |= (unsigned)((1ull << __shfl(to, l)) - (1ull << __shfl(from, l)));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float x = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x += (float)d[i][k] * (float)o[i][k];
+    x = row_sum<LPR>(x);
+    const int64_t row = row0 + i * AT_ONCE + lane / LPR;
+    const bool left = first_rows >> (row - row0) & 1;
+    if (lane % LPR == 0 && row < T && !left) p.delta[head * T + row] = x;
+  }
+}
+
+// The same under a window of up to FEW keys, first tokens included.
+template <int LPR>
+__global__ __launch_bounds__(256) void attn_bwd_rows_few(BwdParams p) {
+  const PromptBwdArgs& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t T = a.seqs.T, task = (int64_t)blockIdx.x * 4 + wave;
+  const int head = (int)(task % a.H);
+  const int64_t row0 = task / a.H * FEW_ROWS;
+  if (row0 >= T) return;
+  // where the rows' sequences start.  Sequences that end at or before the row come first
+  int seq = 0;
+  for (int c = 0; c < a.seqs.n; c += 64) {
+    const int end = c + lane < a.seqs.n ? a.seqs.cu[c + lane + 1] : 0x7FFFFFFF;
+    int more = 0;
+#pragma unroll
+    for (int j = 0; j < FEW_ROWS; ++j) {
+      const int m = __popcll(__ballot(end <= row0 + j));
+      seq += lane == j ? m : 0;
+      more |= m == 64;
+    }
+    if (!more) break;
+  }
+  const bool rows = lane < FEW_ROWS;
+  const int start = rows && seq < a.seqs.n ? max(a.seqs.cu[seq], 0) : 0x7FFFFFFF;
+  float lse2 = 0.0f;
+  if (rows && row0 + lane < T) {
+    const int64_t at = head * T + row0 + lane;
+    const float l = a.lse[at];
+    lse2 = l == -INFINITY ? 0.0f : l * LOG2E;
+    p.lse2[at] = lse2;
+  }
+  bwd_delta_few<LPR>(p, head, row0, T, start, lse2);
 }
 
 // What pack8 leaves of 8 values, as bf16.  P and dS are rounded to bf16 for the matrix cores, by
@@ -908,13 +951,16 @@ hipError_t run(const PromptBwdArgs& a, hipStream_t s) {
   auto kernel = &attn_bwd<SQ, SK, WIN>;
   hipError_t e = ensure_lds_attr(reinterpret_cast<const void*>(kernel), lds);
   if (e == hipSuccess && T > 0) {
-    auto rows = DS <= 2 ? &attn_bwd_rows<8> : &attn_bwd_rows<16>;
+    constexpr int LPR = DS <= 2 ? 8 : 16;
+    auto rows = &attn_bwd_rows<LPR, WIN>;
     int of_wave = 32;
+    int64_t first_rows = WIN ? a.seqs.n : 0;
     if (WIN && a.win.size + a.win.sinks <= FEW) {
-      rows = DS <= 2 ? &attn_bwd_rows_few<8> : &attn_bwd_rows_few<16>;
+      rows = &attn_bwd_rows_few<LPR>;
       of_wave = FEW_ROWS;
+      first_rows = 0;
     }
-    const int64_t blocks = ((T + of_wave - 1) / of_wave * a.H + 3) / 4;
+    const int64_t blocks = (((T + of_wave - 1) / of_wave + first_rows) * a.H + 3) / 4;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     e = launch_k(rows, dim3((unsigned)blocks), dim3(256), 0, s, p);
   }

@@ -31,8 +31,9 @@ def prompt(q, k, v, cu, scale, window, sinks):
 
 def prompt_bwd(do, q, k, v, cu, scale, window, sinks):
     """dq, dk, dv and their bounds (as in attn_ref.prompt_bwd; the sums over slots add fp32
-    roundings of at most as many terms as there are rows).  With up to 8 keys to a row delta is summed
-    from them in fp32, not from the bf16 output, and dS is used as two bf16 numbers throughout."""
+    roundings of at most as many terms as there are rows).  In a row of up to 8 keys delta is
+    summed from them in fp32, not from the bf16 output, and dS (of tiles next to the diagonal) is used
+    as two bf16 numbers."""
     T, H, D = q.shape
     group = H // k.shape[1]
     dq, dk, dv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
@@ -51,11 +52,10 @@ def prompt_bwd(do, q, k, v, cu, scale, window, sinks):
             d = (ref.score_error(x, y, s, scale, mask) + tl)[:, None]
             e_dp = (D + 2) * U32 * (w.abs() @ z.abs().t())
             e_delta = (w.abs() * to).sum(1, keepdim=True) + D * U32 * (w * o).abs().sum(1, keepdim=True)
-            u_ds = U16
-            if window + sinks <= 8:
-                pdp = p * (w @ z.t()).abs()
-                e_delta = ((2 * d + (n + 4) * U32) * pdp + p * e_dp).sum(1, keepdim=True)
-                u_ds = U16 * U16
+            few = mask.sum(1, keepdim=True) <= 8
+            pdp = p * (w @ z.t()).abs()
+            e_delta = torch.where(few, ((2 * d + (n + 4) * U32) * pdp + p * e_dp).sum(1, keepdim=True), e_delta)
+            u_ds = torch.where(few, U16 * U16, U16)
             ee = (u_ds + 2 * d) * e.abs() + p * (1 + 2 * d) * (e_dp + e_delta) * (1 + U16)
             dq[a:b, h] = scale * (e @ y)
             tq[a:b, h] = scale * ((ee + n * U32 * e.abs()) @ y.abs())
