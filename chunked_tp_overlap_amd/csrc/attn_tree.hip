@@ -582,13 +582,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
 }
 
 // Rows of no sequence (zeros) and of sequences that are not good (NaN), and the sum of the parts,
-// in order, of strips that have several.  A workgroup takes a row's heads, a wave each in turn
+// in order, of strips that have several.  A workgroup takes a row's heads, half a wave each in turn
 // (JW 1), or JW waves share a row and head: wave w adds parts w, w + JW, ..., eight loads
-// ahead.  Lane i holds elements 2 i, 2 i + 1.
+// ahead.  Lane i, of 32 or 64, holds the 4 or 2 elements from 4 i or 2 i on.
 template <int JW, int COLS>
 __global__ __launch_bounds__(JW > 4 ? 64 * JW : 256) void attn_tree_join(TreeParams p) {
-  constexpr int WAVES = JW > 4 ? JW : 4, AHEAD = 8;
-  __shared__ float2 red[WAVES][64];
+  constexpr int WAVES = JW > 4 ? JW : 4, AHEAD = 8, LANES = JW == 1 ? 32 : 64, E = 128 / LANES;
+  using Vec = float __attribute__((ext_vector_type(E)));
+  __shared__ Vec red[WAVES][64];
   __shared__ float2 tops[WAVES];
   const TreeArgs& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -614,14 +615,20 @@ __global__ __launch_bounds__(JW > 4 ? 64 * JW : 256) void attn_tree_join(TreePar
     // (sequences that overlap, of boundaries that do not rise, may have left anything)
     if (in.x < 0 || in.y < 1 || in.z < 1 || in.w > ROUNDS * p.at_once || in.x + (int64_t)in.y * in.z > in.w) return;
   }
-  for (int head = JW == 1 ? wave : blockIdx.x % a.H; head < a.H; head += JW == 1 ? WAVES : a.H) {
+  const int e = lane % LANES * E;
+  auto write = [&](uint16_t* out, Vec x) {
+    if (e >= a.D) return;
+#pragma unroll
+    for (int k = 0; k < E; k += 2) *reinterpret_cast<uint32_t*>(out + e + k) = pack_bf16x2(x[k], x[k + 1]);
+  };
+  for (int head = JW == 1 ? 2 * wave + lane / LANES : blockIdx.x % a.H; head < a.H; head += JW == 1 ? 2 * WAVES : a.H) {
     uint16_t* out = a.out.p + (int64_t)row * a.out.rs + head * a.out.hs;
     float* lse = a.lse ? a.lse + (int64_t)head * T + row : nullptr;
     if (none || !s.good) {
       if (w == 0) {
         const float x = none ? 0.0f : NAN;
-        if (2 * lane < a.D) *reinterpret_cast<uint32_t*>(out + 2 * lane) = pack_bf16x2(x, x);
-        if (lane == 0 && lse) *lse = none ? -INFINITY : NAN;
+        write(out, Vec(x));
+        if (e == 0 && lse) *lse = none ? -INFINITY : NAN;
       }
       continue;
     }
@@ -629,15 +636,16 @@ __global__ __launch_bounds__(JW > 4 ? 64 * JW : 256) void attn_tree_join(TreePar
     if (c / COLS >= in.z) continue;
     const int64_t first = ((int64_t)kvh * in.w + in.x + c / COLS) * COLS + c % COLS, step = (int64_t)in.z * COLS;
     float m = -INFINITY, sum = 0.0f;
-    float2 x = make_float2(0.0f, 0.0f);
+    Vec x = 0.0f;
     for (int i0 = w; i0 < in.y; i0 += AHEAD * JW) {
-      float2 st[AHEAD], v[AHEAD];
+      float2 st[AHEAD];
+      Vec v[AHEAD];
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
         const int i = i0 + j * JW;
         const int64_t k = first + min(i, in.y - 1) * step;
         st[j] = i < in.y ? p.stat[k] : make_float2(-INFINITY, 0.0f);
-        v[j] = *reinterpret_cast<const float2*>(p.part + k * a.D + min(2 * lane, a.D - 2));
+        v[j] = *reinterpret_cast<const Vec*>(p.part + k * a.D + min(e, a.D - E));
       }
       float top = m;
 #pragma unroll
@@ -646,15 +654,13 @@ __global__ __launch_bounds__(JW > 4 ? 64 * JW : 256) void attn_tree_join(TreePar
       const float r = exp2_(m - b);
       m = top;
       sum *= r;
-      x.x *= r;
-      x.y *= r;
+      x *= r;
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
         if (i0 + j * JW >= in.y) break;
         const float f = exp2_(st[j].x - b);
         sum += f * st[j].y;
-        x.x += f * v[j].x;
-        x.y += f * v[j].y;
+        x += f * v[j];
       }
     }
     if (JW > 1) {
@@ -668,18 +674,17 @@ __global__ __launch_bounds__(JW > 4 ? 64 * JW : 256) void attn_tree_join(TreePar
       const float b = top == -INFINITY ? 0.0f : top;
       m = top;
       sum = 0.0f;
-      x = make_float2(0.0f, 0.0f);
+      x = 0.0f;
 #pragma unroll
       for (int k = 0; k < JW; ++k) {
         const float f = exp2_(tops[k].x - b);
         sum += f * tops[k].y;
-        x.x += f * red[k][lane].x;
-        x.y += f * red[k][lane].y;
+        x += f * red[k][lane];
       }
     }
     const float inv = sum == 0.0f ? 0.0f : p.v_inv / sum;
-    if (2 * lane < a.D) *reinterpret_cast<uint32_t*>(out + 2 * lane) = pack_bf16x2(x.x * inv, x.y * inv);
-    if (lane == 0 && lse) *lse = sum == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * LN2 + logf(sum);
+    write(out, x * inv);
+    if (e == 0 && lse) *lse = sum == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * LN2 + logf(sum);
   }
 }
 
