@@ -30,10 +30,10 @@
 // output once.
 //
 // Measured on MI355X, both kernels.  64 sequences of 100 to 16264 tokens and up to 60 nodes, 8 heads
-// on 1, E4M3: 137 us, 0.63 PFLOP/s counted (86 GFLOP; 101 with the columns that fill the strips up);
+// on 1, E4M3: 135-138 us, 0.63 PFLOP/s counted (86 GFLOP; 101 with the columns that fill the strips up);
 // a step of 64 keys and 128 columns takes 1.95 us on each of a CU's two workgroups, as in
 // attn_prompt.hip, 92 us if all had as many; the rest is parts of unequal length, 4 us before and
-// 2 after a part's tiles, and 17 of the join.  One sequence of 32520 and 24 nodes, bf16: 22 us: 4 us to
+// 2 after a part's tiles, and 13 of the join.  One sequence of 32520 and 24 nodes, bf16: 22 us: 4 us to
 // the first load's issue (lengths, cut, page ids), 1.6 and 6 for four tiles as memory delivers them,
 // 2 to the end, and the join's 6.  Bound by memory: 64 of 8192 with 2 nodes 61 us (4.4 TB/s), E4M3 35.
 // Not kept: ranges of equal length over the strips one after another, as attn_decode.hip deals
@@ -716,7 +716,7 @@ hipError_t run(const TreeArgs& a, hipStream_t s) {
   if (e == hipSuccess && a.seqs.n > 0) e = launch_k(kernel, dim3((unsigned)blocks), dim3(64 * NW), S::LDS, s, p);
   if (e != hipSuccess || outputs == 0) return e;
   // few outputs have many parts, which more waves then share; many are a row's heads to a workgroup
-  // (a wave each, 19.5 us in the first case above, now 17)
+  // (13 us in the first case above; 19.5 with a workgroup of a wave each, 17-19 with a wave for a head)
   if (outputs <= 512) return launch_k(&attn_tree_join<16, S::COLS>, dim3((unsigned)outputs), dim3(1024), 0, s, p);
   if (outputs <= 4096) return launch_k(&attn_tree_join<4, S::COLS>, dim3((unsigned)outputs), dim3(256), 0, s, p);
   return launch_k(&attn_tree_join<1, S::COLS>, dim3((unsigned)a.seqs.T), dim3(256), 0, s, p);
