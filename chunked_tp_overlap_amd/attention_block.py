@@ -24,6 +24,7 @@ import torch
 import chunked_tp_overlap_amd.ub as ub
 
 BF16 = torch.bfloat16
+NOWHERE = 1 << 30  # a place past any table: nothing is stored there, and rows that would see it are NaN
 
 
 class AttentionBlock:
@@ -58,12 +59,14 @@ class AttentionBlock:
         self.inv_freq = (rope_base ** (-torch.arange(0, r, 2, dtype=torch.float64) / r)).float().cuda()
         per_seq = -(-max_len // page)
         self.pool = n_pages is not None
+        if self.pool and per_seq * page > NOWHERE:
+            raise ValueError(f"max_len: {NOWHERE} tokens at most with a pool, not {max_len}")
         shape = (n_pages if self.pool else max_seqs * per_seq, kv_heads, page, dim)
         self.k_cache, self.v_cache = (torch.zeros(shape, dtype=cache, device="cuda") for _ in range(2))
         self.cache = ub.make_kv_cache(self.k_cache, self.v_cache, k_scale, v_scale)
         self.pages = torch.arange(max_seqs * per_seq, dtype=torch.int32, device="cuda").view(max_seqs, per_seq)
-        self.lens, self.next_lens = (torch.zeros(max_seqs, dtype=torch.int32, device="cuda") for _ in range(2))
-        self.page = page
+        self.lens, self.next_lens, self.past = (torch.zeros(max_seqs, dtype=torch.int32, device="cuda") for _ in range(3))
+        self.page, self.drafted = page, 0
         if self.pool:  # no sequence holds any of them
             self.pages.fill_(-1)
             self.other_pages = torch.zeros_like(self.pages)
@@ -109,6 +112,15 @@ class AttentionBlock:
                         self.resize_ws, stream)
         ub.ub_kv_copy_pages(self.h, self.cache, self.copies, n, self.cfg, stream)
 
+    def _past(self, n):
+        """After `_hold` of next_lens: where the new tokens of the first n sequences go.  Nowhere where the
+        pool had no pages for them: a last page that others hold too is then still in the table."""
+        past = self.past[:n]
+        past.copy_(self.lens[:n])
+        if self.pool:
+            past.masked_fill_(self.held[:n] < self.next_lens[:n], NOWHERE)
+        return past
+
     def _project_out(self, rows):
         k = self.heads * self.dim
         ub.ub_gemm_rs_chunked(self.h, self.attn, k, k, self.wo, self.hidden, self.y, self.hidden, self.gemm,
@@ -120,6 +132,7 @@ class AttentionBlock:
         cache and returns the block's output rows (valid until the next call)."""
         cu = torch.tensor([0] + list(lens), dtype=torch.int32).cumsum(0, dtype=torch.int32).cuda()
         n = len(lens)
+        self.drafted = 0
         if self.pool:  # the sequences before them end
             self.lens.zero_()
             self._hold(self.lens, self.max_seqs)
@@ -140,18 +153,21 @@ class AttentionBlock:
         """The next token's rows x [sequences, hidden] of the sequences that prefill set up."""
         n = x.shape[0]
         self._project_in(x)
+        self.drafted = 0
+        past, lens = self.lens, self.lens
         if self.pool:
             torch.add(self.lens, 1, out=self.next_lens)
             self._hold(self.next_lens, n, self.window)
-        self._append(self.step, self.lens, n, self.cache)
+            past, lens = self._past(n), self.next_lens
+            torch.add(past, 1, out=lens[:n])
+        self._append(self.step, past, n, self.cache)
         self.lens[:n] += 1
         stream = torch.cuda.current_stream()
         if self.window is None:
-            ub.ub_attn_decode(self.h, self.hq, self.cache, self.pages, self.lens, n, self.hattn, None, self.cfg, self.ws,
-                              stream)
+            ub.ub_attn_decode(self.h, self.hq, self.cache, self.pages, lens, n, self.hattn, None, self.cfg, self.ws, stream)
         else:
-            ub.ub_attn_decode_window(self.h, self.hq, self.cache, self.pages, self.lens, n, self.window, self.hattn, None,
-                                     self.cfg, self.ws, stream)
+            ub.ub_attn_decode_window(self.h, self.hq, self.cache, self.pages, lens, n, self.window, self.hattn, None, self.cfg,
+                                     self.ws, stream)
         return self._project_out(n)
 
     def draft(self, x, trees):
@@ -177,21 +193,31 @@ class AttentionBlock:
         i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()
         cu, depths = i32([0] + [len(t) for t in trees]).cumsum(0, dtype=torch.int32), i32(depths + pad)
         parents = i32([p for t in trees for p in t] + pad)
-        torch.add(self.lens[:n], cu[1:] - cu[:-1], out=self.next_lens[:n])
+        nodes = cu[1:] - cu[:-1]
+        torch.add(self.lens[:n], nodes, out=self.next_lens[:n])
         self._hold(self.next_lens, n)
-        ub.ub_kv_append_at(self.h, *self.hqkv, self.hq, self.hk, self.inv_freq, depths, cu, self.lens, n, self.cache,
+        past = self._past(n)
+        torch.add(past, nodes, out=self.next_lens[:n])
+        self.drafted = n
+        ub.ub_kv_append_at(self.h, *self.hqkv, self.hq, self.hk, self.inv_freq, depths, cu, past, n, self.cache,
                            self.pages, self.cfg, stream)
         ub.ub_attn_tree(self.h, self.hq, self.cache, self.pages, self.next_lens, parents, cu, n, self.hattn, None, self.cfg,
                         self.ws, stream)
         return self._project_out(x.shape[0])
 
     def accept(self, kept, kept_lens):
-        """After `draft`: of sequence i the first kept_lens[i] nodes in row i of kept, a path from its
-        last token, become its next tokens (int32 tensors on the device)."""
+        """Of the trees of the `draft` just before, sequence i's first kept_lens[i] nodes in row i of kept, a
+        path from its last token, become its next tokens (int32 tensors on the device)."""
         n = kept.shape[0]
-        ub.ub_kv_compact(self.h, self.cache, self.pages, self.lens, kept, kept_lens, n, self.next_lens, self.cfg,
+        if n > self.drafted:
+            raise ValueError(f"accept: rows for {n} sequences, the call before it drafted for {self.drafted}")
+        ub.ub_kv_compact(self.h, self.cache, self.pages, self.past, kept, kept_lens, n, self.next_lens, self.cfg,
                          torch.cuda.current_stream())
-        self.lens[:n] = self.next_lens[:n]
+        self.drafted = 0
+        if self.pool:  # a tree without pages: none of its nodes was moved
+            self.lens[:n] = torch.where(self.past[:n] < NOWHERE, self.next_lens[:n], self.lens[:n] + kept_lens[:n].clamp(min=0))
+        else:
+            self.lens[:n] = self.next_lens[:n]
         self._hold(self.lens, n)  # what the other nodes had is given back
 
     def fork(self, parents):
@@ -202,6 +228,7 @@ class AttentionBlock:
         n = parents.shape[0]
         if n > self.max_seqs:
             raise ValueError(f"fork: {n} sequences, {self.max_seqs} at most")
+        self.drafted = 0
         ub.ub_kv_fork(self.h, self.refs, self.pages, self.held, self.max_seqs, parents, self.other_pages, self.next_lens, n,
                       self.page, torch.cuda.current_stream())
         self.other_pages[n:] = -1

@@ -1,0 +1,72 @@
+"""Host-side tests of the attention block over a pool of pages (no GPU): what its calls store and read,
+slot by slot, where the pages suffice and where they do not."""
+
+import pytest
+import torch
+
+pytest.importorskip("chunked_tp_overlap_amd.ub", reason="libub.so not built")
+from tests.block_model import block, i32, modelled, tokens  # noqa: E402
+
+
+@pytest.mark.parametrize("free", [0, 1, 2, 3])
+def test_no_page_for_a_shared_last_page(monkeypatch, free):
+    """Three sequences share a partly filled last page, and the pool has pages for `free` of them: the
+    others' next tokens are stored nowhere, least of all on that page, and their rows are NaN."""
+    with modelled(monkeypatch) as (m, calls):
+        b = block(m, 2 + free)
+        b.prefill(tokens(0, 20), [20])
+        b.fork(i32([0, 0, 0]))
+        before = dict(calls.slots)
+        b.decode(tokens(100, 3))
+        assert calls.given == [i < free for i in range(3)] and calls.shared == []
+        assert calls.rows == [list(range(20)) + [100 + i] if i < free else None for i in range(3)]
+        assert {s: t for s, t in calls.slots.items() if s in before} == before
+        b.close()
+
+
+@pytest.mark.parametrize("free", [0, 1, 2])
+def test_no_page_for_drafts(monkeypatch, free):
+    """The same with trees of drafted tokens, of which a path is accepted: no node of a tree without pages
+    is stored or moved, and a sequence of which none is accepted goes on."""
+    trees, n = [[-1, 0, 0, 2], [-1, -1, 1, 2]], 4
+    with modelled(monkeypatch) as (m, calls):
+        b = block(m, 2 + free, max_seqs=2)
+        b.prefill(tokens(0, 20), [20])
+        b.fork(i32([0, 0]))
+        before = dict(calls.slots)
+        b.draft(tokens(100, 2 * n), trees)
+        assert calls.given == [i < free for i in range(2)] and calls.shared == []
+        past = list(range(20))
+        want = [past + [100], past + [100, 101], past + [100, 102], past + [100, 102, 103],
+                past + [104], past + [105], past + [105, 106], past + [105, 106, 107]]
+        assert calls.rows == [w if i // n < free else None for i, w in enumerate(want)]
+        b.accept(i32([[0, 2, 3], [1, 2, 3]]), i32([3 * (free > 0), 3 * (free > 1)]))
+        assert calls.shared == [] and {s: t for s, t in calls.slots.items() if s in before} == before
+        assert b.lens.tolist() == [20 + 3 * (i < free) for i in range(2)]
+        if free == 1:  # the first gave back what the other nodes had; the second's page is its own now
+            b.decode(tokens(200, 2))
+            assert calls.rows == [past + [100, 102, 103, 200], past + [201]] and calls.shared == []
+        b.close()
+
+
+def test_accept_goes_with_the_draft_before_it(monkeypatch):
+    """Which sequences had pages for their drafts is known to the draft alone."""
+    with modelled(monkeypatch) as (m, calls):
+        b = block(m, 8, max_seqs=3)
+        kept, some = i32([[0], [0]]), i32([1, 1])
+        b.prefill(tokens(0, 30), [20, 10])
+        for between in (None, lambda: b.decode(tokens(70, 2)), lambda: b.fork(i32([1, 0])),
+                        lambda: b.prefill(tokens(0, 30), [20, 10])):
+            if between is not None:
+                b.draft(tokens(50, 2), [[-1], [-1]])
+                between()
+            with pytest.raises(ValueError, match="accept"):
+                b.accept(kept, some)
+        b.draft(tokens(50, 2), [[-1], [-1]])
+        with pytest.raises(ValueError, match="accept"):
+            b.accept(i32([[0]] * 3), i32([1] * 3))
+        before = b.lens.tolist()
+        b.accept(kept, some)
+        assert b.lens.tolist() == [before[0] + 1, before[1] + 1, 0]
+        assert torch.equal(b.held, b.lens)
+        b.close()
