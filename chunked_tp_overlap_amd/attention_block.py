@@ -24,16 +24,19 @@ import torch
 import chunked_tp_overlap_amd.ub as ub
 
 BF16 = torch.bfloat16
-NOWHERE = 1 << 30  # a place past any table: nothing is stored there, and rows that would see it are NaN
+NOWHERE = 1 << 30  # a place past any table: nothing is stored there, and a sequence that long is NaN
 
 
 class AttentionBlock:
     """Heads of one rank: wqkv [hidden, (heads + 2 kv_heads) dim] and wo [heads dim, hidden], both
     contiguous bf16 matrices, which are kept and not copied.  The cache has room for `max_len` tokens
     of each of `max_seqs` sequences, as bf16 or (with scales k_scale and v_scale) E4M3; with
-    `n_pages`, a pool of so many pages, for as many tokens of sequences up to that long as they hold
-    (where they run out a sequence's new tokens are not stored, and its rows are NaN).  window: how
-    many tokens a token sees, itself among them, besides the first `sinks`."""
+    `n_pages`, a pool of so many pages, for as many tokens of sequences up to that long as they hold.
+    Where the pool has no pages for a sequence's new tokens (or it gets longer than max_len) they are not
+    stored, and their rows are NaN; once it has lost a token so, all its later rows are, and its copies',
+    and its entry of `lens`, the cached tokens of each, is NOWHERE or more.  What it held is free when it
+    ends (`fork`, `prefill`).  Drafts are no tokens of their sequence before they are accepted.  window:
+    how many tokens a token sees, itself among them, besides the first `sinks`."""
 
     def __init__(self, wqkv, wo, heads, kv_heads, dim, capacity, max_seqs, max_len, page=64, tp=1, cache=BF16,
                  k_scale=1.0, v_scale=1.0, rope_base=10000.0, window=None, sinks=0, n_pages=None):
@@ -112,14 +115,11 @@ class AttentionBlock:
                         self.resize_ws, stream)
         ub.ub_kv_copy_pages(self.h, self.cache, self.copies, n, self.cfg, stream)
 
-    def _past(self, n):
-        """After `_hold` of next_lens: where the new tokens of the first n sequences go.  Nowhere where the
-        pool had no pages for them: a last page that others hold too is then still in the table."""
-        past = self.past[:n]
-        past.copy_(self.lens[:n])
-        if self.pool:
-            past.masked_fill_(self.held[:n] < self.next_lens[:n], NOWHERE)
-        return past
+    def _lose(self, lens, wanted):
+        """After `_hold` of so many tokens: where the pool had no pages for them, a sequence's next place is
+        nowhere (a last page that others hold too is then still in its table), and its length stays past
+        what the pool gives pages for."""
+        lens.masked_fill_(self.held[: lens.shape[0]] < wanted, NOWHERE)
 
     def _project_out(self, rows):
         k = self.heads * self.dim
@@ -139,6 +139,8 @@ class AttentionBlock:
         self._project_in(x)
         self.lens[:n] = cu[1:] - cu[:-1]
         self._hold(self.lens, n)
+        if self.pool:
+            self._lose(self.lens[:n], self.lens[:n])
         self._append(cu, None, n, self.cache)
         stream = torch.cuda.current_stream()
         if self.window is None:
@@ -146,6 +148,10 @@ class AttentionBlock:
         else:
             ub.ub_attn_prompt_window(self.h, self.hq, self.hk, self.hqkv[2], self.hattn, None, cu, n, self.window, self.cfg,
                                      self.ws, stream)
+        if self.pool:  # a prompt without pages is seen here, not only in the tokens after it
+            rows = torch.arange(x.shape[0], dtype=torch.int32, device="cuda")
+            lost = torch.cat((self.lens[:n] >= NOWHERE, torch.zeros(1, dtype=torch.bool, device="cuda")))
+            self.attn[: x.shape[0]].masked_fill_(lost[torch.bucketize(rows, cu[1:], right=True)][:, None], float("nan"))
         self.step = torch.arange(n + 1, dtype=torch.int32, device="cuda")
         return self._project_out(x.shape[0])
 
@@ -154,20 +160,19 @@ class AttentionBlock:
         n = x.shape[0]
         self._project_in(x)
         self.drafted = 0
-        past, lens = self.lens, self.lens
         if self.pool:
             torch.add(self.lens, 1, out=self.next_lens)
             self._hold(self.next_lens, n, self.window)
-            past, lens = self._past(n), self.next_lens
-            torch.add(past, 1, out=lens[:n])
-        self._append(self.step, past, n, self.cache)
+            self._lose(self.lens[:n], self.next_lens[:n])
+        self._append(self.step, self.lens, n, self.cache)
         self.lens[:n] += 1
         stream = torch.cuda.current_stream()
         if self.window is None:
-            ub.ub_attn_decode(self.h, self.hq, self.cache, self.pages, lens, n, self.hattn, None, self.cfg, self.ws, stream)
+            ub.ub_attn_decode(self.h, self.hq, self.cache, self.pages, self.lens, n, self.hattn, None, self.cfg, self.ws,
+                              stream)
         else:
-            ub.ub_attn_decode_window(self.h, self.hq, self.cache, self.pages, lens, n, self.window, self.hattn, None, self.cfg,
-                                     self.ws, stream)
+            ub.ub_attn_decode_window(self.h, self.hq, self.cache, self.pages, self.lens, n, self.window, self.hattn, None,
+                                     self.cfg, self.ws, stream)
         return self._project_out(n)
 
     def draft(self, x, trees):
@@ -196,8 +201,11 @@ class AttentionBlock:
         nodes = cu[1:] - cu[:-1]
         torch.add(self.lens[:n], nodes, out=self.next_lens[:n])
         self._hold(self.next_lens, n)
-        past = self._past(n)
-        torch.add(past, nodes, out=self.next_lens[:n])
+        past = self.past[:n]
+        past.copy_(self.lens[:n])
+        if self.pool:
+            self._lose(past, self.next_lens[:n])
+            torch.add(past, nodes, out=self.next_lens[:n])
         self.drafted = n
         ub.ub_kv_append_at(self.h, *self.hqkv, self.hq, self.hk, self.inv_freq, depths, cu, past, n, self.cache,
                            self.pages, self.cfg, stream)
@@ -214,8 +222,9 @@ class AttentionBlock:
         ub.ub_kv_compact(self.h, self.cache, self.pages, self.past, kept, kept_lens, n, self.next_lens, self.cfg,
                          torch.cuda.current_stream())
         self.drafted = 0
-        if self.pool:  # a tree without pages: none of its nodes was moved
-            self.lens[:n] = torch.where(self.past[:n] < NOWHERE, self.next_lens[:n], self.lens[:n] + kept_lens[:n].clamp(min=0))
+        if self.pool:  # of a tree without pages no node was stored
+            some = (kept_lens[:n] > 0) & (kept[:, :1] >= 0).any(1)
+            self.lens[:n] = torch.where(self.past[:n] < NOWHERE, self.next_lens[:n], self.lens[:n].masked_fill(some, NOWHERE))
         else:
             self.lens[:n] = self.next_lens[:n]
         self._hold(self.lens, n)  # what the other nodes had is given back

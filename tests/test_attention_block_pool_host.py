@@ -70,3 +70,64 @@ def test_accept_goes_with_the_draft_before_it(monkeypatch):
         assert b.lens.tolist() == [before[0] + 1, before[1] + 1, 0]
         assert torch.equal(b.held, b.lens)
         b.close()
+
+
+def test_a_lost_token_stays_lost(monkeypatch):
+    """A sequence whose token was not stored is NaN from then on, with pages to spare too: the places that
+    it never wrote hold other sequences' tokens.  It takes no more pages; what it has it keeps until it ends."""
+    with modelled(monkeypatch) as (m, calls):
+        b = block(m, 5)
+        b.prefill(tokens(0, 64), [32, 16, 16])
+        b.decode(tokens(100, 3))  # all three need a page, the first gets it
+        assert [r is None for r in calls.rows] == [False, True, True]
+        b.fork(i32([-1, 1, 2]))  # the first ends: three pages are free
+        for s in range(2):
+            before, held = dict(calls.slots), b.held.tolist()
+            b.decode(tokens(110 + 10 * s, 3))
+            assert [r is None for r in calls.rows] == [False, True, True]  # the first is a new sequence
+            assert b.held.tolist() == [held[0] + 1] + held[1:]
+            assert sum(calls.slots.get(k) != v for k, v in before.items()) + len(calls.slots) - len(before) <= 1
+        b.draft(tokens(150, 3), [[-1], [-1], [-1]])
+        assert [r is None for r in calls.rows] == [False, True, True]
+        b.accept(i32([[0]] * 3), i32([1, 1, 0]))
+        b.fork(i32([0, 1, 1, 2]))  # copies of it are lost too
+        b.decode(tokens(160, 4))
+        assert [r is None for r in calls.rows] == [False, True, True, True]
+        b.fork(i32([-1, -1, -1, -1]))
+        assert int((b.refs == 0).sum()) == 5 and b.lens.tolist() == b.held.tolist() == [0] * 4
+        b.prefill(tokens(0, 64), [32, 16, 16])
+        assert b.lens.tolist() == [32, 16, 16, 0] and not bool(torch.isnan(b.attn[:64]).any())
+        b.close()
+
+
+def test_prompts_without_pages(monkeypatch):
+    """A prompt that the pool has no pages for, or that is longer than a sequence can be: NaN, in its own rows
+    and in all later ones."""
+    with modelled(monkeypatch) as (m, calls):
+        for lens, n_pages, lost in (([40, 0, 33, 17], 5, [0, 0, 1, 1]), ([65, 64], 9, [1, 0]), ([20], 1, [1]), ([16, 17], 2, [0, 1])):
+            b = block(m, n_pages)
+            b.prefill(tokens(0, sum(lens)), lens)
+            nan = torch.isnan(b.attn[: sum(lens)].float())
+            assert nan.all(1).tolist() == nan.any(1).tolist() == [bool(x) for n, x in zip(lens, lost) for _ in range(n)]
+            b.fork(i32([i if x else -1 for i, x in enumerate(lost)]))  # the others end, pages are free
+            first = len(calls.slots)
+            b.decode(tokens(150, len(lens)))
+            assert [r is None for r in calls.rows] == [bool(x) for x in lost]
+            assert len(calls.slots) - first <= lost.count(0)
+            b.close()
+            calls.slots.clear()
+
+
+def test_a_path_of_a_tree_without_pages(monkeypatch):
+    """Its tokens were not stored: the sequence has lost them."""
+    with modelled(monkeypatch) as (m, calls):
+        b = block(m, 2, max_seqs=3)
+        b.prefill(tokens(0, 32), [16, 16])
+        b.draft(tokens(50, 4), [[-1, 0], [-1, 0]])
+        assert calls.rows == [None] * 4
+        b.accept(i32([[0, 1], [0, 1]]), i32([0, 2]))
+        assert b.lens[0] == 16 and b.lens[1] >= m.NOWHERE
+        b.fork(i32([-1, 1, -1]))
+        b.decode(tokens(60, 3))
+        assert [r is None for r in calls.rows] == [False, True, True]  # one page: the first's
+        b.close()

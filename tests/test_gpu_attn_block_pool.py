@@ -84,3 +84,92 @@ def test_no_page_for_drafts(free):
     assert b.lens.tolist() == [20 + 3 * (i < free) for i in range(2)]
     torch.cuda.synchronize()
     b.close()
+
+
+def test_a_lost_token_stays_lost():
+    """Pages that come free do not bring a lost token back; the other rows are what they would be."""
+    b = make_block(5)
+    b.prefill(normal(3, 64, HIDDEN), [32, 16, 16])
+    b.decode(normal(4, 3, HIDDEN))
+    check_row(b, 0, 0, list(range(33)), "served")
+    assert bool(torch.isnan(b.attn[1:3]).all())
+    b.fork(i32([-1, 1, 2]))
+    for s in range(3):
+        before, held = held_bytes(b), b.held.tolist()
+        y = b.decode(normal(5 + s, 3, HIDDEN))
+        check_row(b, 0, 0, list(range(s + 1)), f"new {s}")
+        assert bool(torch.isnan(b.attn[1:3]).all()) and bool(torch.isnan(y[1:3]).all()) and bool(torch.isfinite(y[0]).all())
+        assert b.held.tolist() == [s + 1] + held[1:]
+        at = int(b.pages[0, 0])
+        for c, old in zip(held_bytes(b), before):
+            c[at], old[at] = 0, 0
+            assert torch.equal(c, old)
+    b.draft(normal(9, 3, HIDDEN), [[-1], [-1], [-1]])
+    assert torch.isnan(b.attn[:3]).all(1).tolist() == [False, True, True]
+    b.accept(i32([[0]] * 3), i32([1, 1, 0]))
+    assert b.lens[0] == 4 and bool((b.lens[1:] >= 1 << 30).all())
+    torch.cuda.synchronize()
+    b.close()
+
+
+@pytest.mark.parametrize("window", [None, 10])
+def test_prompts_without_pages(window):
+    """The rows of prompts that found no pages are NaN, those of the others their definition's, as
+    are the tokens decoded after them."""
+    kw = {} if window is None else dict(window=window, sinks=2)
+    b, sound = make_block(5, max_seqs=4, **kw), make_block(50, max_seqs=4, **kw)
+    lens = [40, 0, 33, 17]
+    x = normal(3, sum(lens), HIDDEN)
+    y, want = b.prefill(x, lens).clone(), sound.prefill(x, lens).clone()
+    lost = torch.tensor([False] * 40 + [True] * 50, device="cuda")
+    assert torch.isnan(y).all(1).tolist() == torch.isnan(y).any(1).tolist() == lost.tolist()
+    assert torch.equal(y[:40], want[:40])
+    b.decode(normal(4, 4, HIDDEN))
+    seen = [u for u in range(41) if window is None or u < 2 or 40 - u < window]
+    check_row(b, 0, 0, seen, "decode 0")
+    check_row(b, 1, 1, [0], "decode 1")
+    assert bool(torch.isnan(b.attn[2:4]).all())
+    torch.cuda.synchronize()
+    b.close()
+    sound.close()
+
+
+def test_a_pool_that_runs_out_under_a_graph():
+    """A captured decode step, replayed until the pool has no pages: the eager steps' bits."""
+    tokens = [normal(10 + s, 3, HIDDEN) for s in range(8)]
+
+    def steps(b, step):
+        b.prefill(normal(3, 44, HIDDEN), [14, 13, 17])
+        out = []
+        for t in tokens:
+            out.append([x.clone().view(torch.uint8) for x in (step(t), b.lens, b.held, b.pages, b.refs, b.k_cache, b.v_cache)])
+            normal(50, 64, 64) @ normal(51, 64, 64)  # eager work between the steps
+            torch.cuda.synchronize()
+        return out
+
+    b = make_block(5)
+    want = steps(b, b.decode)
+    b.close()
+    b = make_block(5)
+    b.prefill(normal(3, 44, HIDDEN), [14, 13, 17])
+    token = torch.zeros_like(tokens[0])
+    b.decode(token)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = b.decode(token)
+    keep = b.step
+
+    def replay(t):
+        token.copy_(t)
+        graph.replay()
+        return y
+
+    got = steps(b, replay)
+    for s, (w, g) in enumerate(zip(want, got)):
+        # the rows of the cache that nothing has written since differ: the first block's are zeros
+        for n, (a, c) in enumerate(zip(w[:5], g[:5])):
+            assert torch.equal(a, c), (s, n)
+    assert b.lens.tolist()[0] == 22 and b.lens[1] >= 1 << 30 and b.lens[2] == 25
+    del keep
+    b.close()
