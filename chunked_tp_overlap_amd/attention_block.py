@@ -231,13 +231,15 @@ class AttentionBlock:
 
     def fork(self, parents):
         """Sequence i becomes a copy of sequence parents[i] (an int32 tensor on the device; -1: none),
-        sharing its pages; sequences that are nobody's parent end."""
+        sharing its pages; sequences that are nobody's parent end, and so do drafts that were not accepted."""
         if not self.pool:
             raise ValueError("fork: a block without a pool has no pages to share")
         n = parents.shape[0]
         if n > self.max_seqs:
             raise ValueError(f"fork: {n} sequences, {self.max_seqs} at most")
         self.drafted = 0
+        # A row that holds pages past its tokens would have them to write in, and share them
+        self._hold(self.lens, self.max_seqs)
         ub.ub_kv_fork(self.h, self.refs, self.pages, self.held, self.max_seqs, parents, self.other_pages, self.next_lens, n,
                       self.page, torch.cuda.current_stream())
         self.other_pages[n:] = -1

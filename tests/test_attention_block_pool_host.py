@@ -1,6 +1,8 @@
 """Host-side tests of the attention block over a pool of pages (no GPU): what its calls store and read,
 slot by slot, where the pages suffice and where they do not."""
 
+import random
+
 import pytest
 import torch
 
@@ -130,4 +132,116 @@ def test_a_path_of_a_tree_without_pages(monkeypatch):
         b.fork(i32([-1, 1, -1]))
         b.decode(tokens(60, 3))
         assert [r is None for r in calls.rows] == [False, True, True]  # one page: the first's
+        b.close()
+
+
+@pytest.mark.parametrize("accepted", [None, 1])
+def test_fork_after_drafts(monkeypatch, accepted):
+    """Drafts that were not accepted are no tokens of a sequence: its copies do not share their places,
+    which all of them write next."""
+    with modelled(monkeypatch) as (m, calls):
+        b = block(m, 12)
+        b.prefill(tokens(0, 36), [20, 16])
+        b.draft(tokens(50, 18), [[-1] + list(range(13)), [-1, 0, 1, 2]])
+        if accepted is not None:  # of the first alone
+            b.accept(i32([[0]]), i32([accepted]))
+        first = list(range(20)) + ([50] if accepted else [])
+        b.fork(i32([0, 0, 1, 1]))
+        assert b.held.tolist() == b.lens.tolist() == [len(first)] * 2 + [16] * 2
+        assert int((b.refs > 0).sum()) == 3
+        b.decode(tokens(100, 4))
+        assert calls.shared == []
+        assert calls.rows == [first + [100], first + [101], list(range(20, 36)) + [102], list(range(20, 36)) + [103]]
+        b.draft(tokens(110, 4), [[-1]] * 4)
+        assert calls.shared == [] and calls.rows[1] == first + [101, 111]
+        b.close()
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_steps(monkeypatch, seed):
+    """Prompts, decode steps, drafts, accepted paths and forks in any order, in pools that run out: a row sees
+    its sequence's own tokens, in order, or is NaN, and that from the first token that it lost."""
+    r = random.Random(seed)
+    window, sinks = (None, 0) if seed % 3 else (r.randint(1, 20), r.randint(0, 5))
+    with modelled(monkeypatch) as (m, calls):
+        b = block(m, r.randint(3, 14), max_seqs=6, max_len=40, page=r.choice([1, 4, 16]), window=window, sinks=sinks)
+        count, past, alive = 0, [[] for _ in range(6)], 0  # past: a sequence's tokens, or None: it has lost one
+
+        def new(n):
+            nonlocal count
+            count += n
+            return list(range(count - n, count))
+
+        def sees(tokens):
+            n = len(tokens)
+            return [t for u, t in enumerate(tokens) if window is None or n - 1 - u < window or u < sinks]
+
+        def write(x, f):
+            before = len(calls.shared)
+            rows = torch.zeros((len(x), 128), dtype=torch.bfloat16)
+            rows[:, 0], rows[:, 1] = torch.tensor(x) // 200, torch.tensor(x) % 200
+            f(rows)
+            assert len(calls.shared) == before
+
+        for step in range(40):
+            op = "prefill" if not alive else r.choice(["decode"] * 4 + ["draft"] * 3 * (window is None) + ["fork"] * 2 + ["prefill"])
+            if op == "prefill":
+                lens = [r.randint(0, 41) for _ in range(r.randint(1, 6))]
+                if sum(lens) == 0:
+                    continue
+                x = new(sum(lens))
+                write(x, lambda rows: b.prefill(rows, lens))
+                nan, at, alive, past = torch.isnan(b.attn[: len(x), 0].float()).tolist(), 0, len(lens), [[] for _ in range(6)]
+                for i, n in enumerate(lens):
+                    past[i] = x[at: at + n] if calls.given[i] else None
+                    assert nan[at: at + n] == [past[i] is None] * n
+                    at += n
+            elif op == "decode":
+                n = r.randint(1, alive)
+                x = new(n)
+                write(x, b.decode)
+                for i in range(n):
+                    past[i] = past[i] + [x[i]] if past[i] is not None and calls.given[i] else None
+                assert calls.rows == [None if past[i] is None else sees(past[i]) for i in range(n)]
+            elif op == "draft":
+                n = r.randint(1, alive)
+                trees = [[r.randint(-1, j - 1) for j in range(r.randint(0, 7))] for _ in range(n)]
+                if sum(map(len, trees)) == 0:
+                    continue
+                x = new(sum(map(len, trees)))
+                write(x, lambda rows: b.draft(rows, trees))
+                given, at, rows, paths, places = calls.given, 0, [], [], []
+                for i, t in enumerate(trees):
+                    of = []
+                    for j, p in enumerate(t):
+                        of.append((of[p] if p >= 0 else []) + [j])
+                        rows.append(past[i] + [x[at + q] for q in of[j]] if past[i] is not None and given[i] else None)
+                    places.append(of)
+                    at += len(t)
+                assert calls.rows == rows
+                if r.random() < 0.8:
+                    k, before, at = r.randint(1, n), len(calls.shared), 0
+                    paths = [r.choice(of + [[]]) for of in places[:k]]
+                    kept = torch.full((k, 8), -1, dtype=torch.int32)
+                    for i, q in enumerate(paths):
+                        kept[i, : len(q)] = torch.tensor(q, dtype=torch.int32)
+                    b.accept(kept, i32([len(q) for q in paths]))
+                    assert len(calls.shared) == before
+                    for i, q in enumerate(paths):
+                        if past[i] is not None and q:
+                            past[i] = past[i] + [x[at + j] for j in q] if given[i] else None
+                        at += len(trees[i])
+            else:
+                parents = [r.randint(-1, alive) for _ in range(r.randint(1, 6))]
+                b.fork(i32(parents))
+                past = [past[p] if 0 <= p < 6 else [] for p in parents] + [[] for _ in range(6 - len(parents))]
+                alive = len(parents)
+            for n, t in zip(b.lens.tolist(), past):
+                assert n >= m.NOWHERE if t is None else n == len(t)
+            want = torch.zeros_like(b.refs)
+            for row, n in zip(b.pages.tolist(), b.held.tolist()):
+                for p in row[: -(-n // b.page)]:
+                    if p >= 0:
+                        want[p] += 1
+            assert torch.equal(b.refs, want)
         b.close()

@@ -173,3 +173,21 @@ def test_a_pool_that_runs_out_under_a_graph():
     assert b.lens.tolist()[0] == 22 and b.lens[1] >= 1 << 30 and b.lens[2] == 25
     del keep
     b.close()
+
+
+def test_fork_after_drafts():
+    """Copies of a sequence whose drafts were not accepted write places of their own."""
+    b = make_block(12, max_seqs=4)
+    b.prefill(normal(3, 36, HIDDEN), [20, 16])
+    b.draft(normal(4, 18, HIDDEN), [[-1] + list(range(13)), [-1, 0, 1, 2]])
+    b.fork(i32([0, 0, 1, 1]))
+    assert b.held.tolist() == b.lens.tolist() == [20, 20, 16, 16] and int((b.refs > 0).sum()) == 3
+    b.decode(normal(5, 4, HIDDEN))
+    n = H * D
+    for i in range(4):
+        at = int(b.lens[i]) - 1
+        assert torch.equal(b.k_cache[b.pages[i, at // PAGE].long(), :, at % PAGE].reshape(-1), b.k[i])
+        assert torch.equal(b.v_cache[b.pages[i, at // PAGE].long(), :, at % PAGE].reshape(-1), b.qkv[i, n + G * D:])
+        check_row(b, i, i, list(range(at + 1)), f"decode {i}")
+    torch.cuda.synchronize()
+    b.close()
