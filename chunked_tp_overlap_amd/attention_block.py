@@ -69,7 +69,9 @@ class AttentionBlock:
         self.cache = ub.make_kv_cache(self.k_cache, self.v_cache, k_scale, v_scale)
         self.pages = torch.arange(max_seqs * per_seq, dtype=torch.int32, device="cuda").view(max_seqs, per_seq)
         self.lens, self.next_lens, self.past = (torch.zeros(max_seqs, dtype=torch.int32, device="cuda") for _ in range(3))
-        self.page, self.drafted = page, 0
+        # a decode step's boundaries, one row to a sequence, where a captured step finds them
+        self.step = torch.arange(max_seqs + 1, dtype=torch.int32, device="cuda")
+        self.page, self.seqs, self.drafted = page, 0, 0  # sequences there are; drafted for, not yet accepted
         if self.pool:  # no sequence holds any of them
             self.pages.fill_(-1)
             self.other_pages = torch.zeros_like(self.pages)
@@ -88,10 +90,13 @@ class AttentionBlock:
         self.hdqkv = [ub.heads(self.dqkv, c) for c in cols]
         self.hq, self.hk, self.hattn = ub.heads(self.q), ub.heads(self.k), ub.heads(self.attn)
 
-    def _project_in(self, x):
-        """QKV of x's rows; the active shape becomes their number, rounded up to tp."""
+    def _check(self, x):
         if x.dim() != 2 or x.shape[1] != self.hidden or x.dtype is not BF16:
             raise ValueError(f"x: a bf16 matrix of hidden size {self.hidden}, not {x.dtype} {tuple(x.shape)}")
+
+    def _project_in(self, x):
+        """QKV of x's rows; the active shape becomes their number, rounded up to tp."""
+        self._check(x)
         rows = x.shape[0]
         T = -(-rows // self.tp) * self.tp
         stream = torch.cuda.current_stream()
@@ -152,12 +157,15 @@ class AttentionBlock:
             rows = torch.arange(x.shape[0], dtype=torch.int32, device="cuda")
             lost = torch.cat((self.lens[:n] >= NOWHERE, torch.zeros(1, dtype=torch.bool, device="cuda")))
             self.attn[: x.shape[0]].masked_fill_(lost[torch.bucketize(rows, cu[1:], right=True)][:, None], float("nan"))
-        self.step = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+        self.seqs = n
         return self._project_out(x.shape[0])
 
     def decode(self, x):
-        """The next token's rows x [sequences, hidden] of the sequences that prefill set up."""
+        """The next token's rows x [sequences, hidden] of the sequences that prefill or fork set up."""
+        self._check(x)
         n = x.shape[0]
+        if n > self.seqs:
+            raise ValueError(f"decode: rows for {n} sequences, there are {self.seqs}")
         self._project_in(x)
         self.drafted = 0
         if self.pool:
@@ -244,13 +252,13 @@ class AttentionBlock:
                       self.page, torch.cuda.current_stream())
         self.other_pages[n:] = -1
         self.next_lens[n:] = 0
-        self.pages.copy_(self.other_pages)  # in place: a captured decode step reads them there
+        self.pages.copy_(self.other_pages)  # in place, as all that a captured decode step reads
         self.held.copy_(self.next_lens)
         some = (parents >= 0) & (parents < self.max_seqs)
         lens = torch.where(some, self.lens[parents.clamp(0, self.max_seqs - 1).long()], 0)
         self.lens.zero_()
         self.lens[:n] = lens
-        self.step = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+        self.seqs = n
 
     def train(self, x, lens, dattn):
         """A training step's attention: the block's output for documents x, and the gradient of

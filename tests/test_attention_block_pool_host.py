@@ -245,3 +245,42 @@ def test_random_steps(monkeypatch, seed):
                         want[p] += 1
             assert torch.equal(b.refs, want)
         b.close()
+
+
+@pytest.mark.parametrize("n_pages", [None, 20])
+def test_addresses_a_captured_step_keeps(monkeypatch, n_pages):
+    """A captured decode step holds the address of the rows' boundaries: it is the same, and says the same,
+    after prompts and forks."""
+    with modelled(monkeypatch) as (m, calls):
+        b = block(m, n_pages)
+        b.prefill(tokens(0, 30), [10, 20])
+        b.decode(tokens(50, 2))
+        step, boundaries = calls.appended[-1]
+        others = []  # what the allocator gives a freed tensor's memory to
+        if n_pages:
+            b.fork(i32([0, 1, 0, 1]))
+            others += [torch.full((k,), 77, dtype=torch.int32) for k in range(2, 6)]
+            b.decode(tokens(60, 4))
+            assert calls.appended[-1] == (step, [0, 1, 2, 3, 4])
+            b.fork(i32([1, 0]))
+        b.prefill(tokens(0, 30), [30])
+        others += [torch.full((k,), 77, dtype=torch.int32) for k in range(2, 6)]
+        b.prefill(tokens(0, 30), [20, 10])
+        b.decode(tokens(50, 2))
+        assert calls.appended[-1] == (step, boundaries)
+        with pytest.raises(ValueError):  # no third sequence
+            b.decode(tokens(50, 3))
+        b.close()
+
+
+def test_rows_of_no_sequence(monkeypatch):
+    """More rows than sequences, or rows before there are any: refused before a page is given."""
+    with modelled(monkeypatch) as (m, calls):
+        b = block(m, 20)
+        for f in (lambda: None, lambda: b.prefill(tokens(0, 30), [10, 20]), lambda: b.fork(i32([1]))):
+            f()
+            n = len(calls.calls)
+            with pytest.raises(ValueError, match="decode"):
+                b.decode(tokens(50, 3))
+            assert "ub_kv_resize" not in calls.calls[n:] and torch.equal(b.held, b.lens)
+        b.close()

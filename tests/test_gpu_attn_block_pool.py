@@ -191,3 +191,50 @@ def test_fork_after_drafts():
         check_row(b, i, i, list(range(at + 1)), f"decode {i}")
     torch.cuda.synchronize()
     b.close()
+
+
+def test_a_captured_step_across_forks():
+    """A decode step captured for two sequences, replayed after forks and new prompts, with eager work and
+    new tensors between: the bits of eager steps, every time."""
+    def steps(b, step):
+        out = []
+        b.prefill(normal(3, 50, HIDDEN), [20, 30])
+        for s in range(6):
+            if s in (2, 4):
+                b.fork(i32([0, 1, 0]))
+                b.decode(normal(30 + s, 3, HIDDEN))
+                b.fork(i32([2, 1]) if s == 2 else i32([1, 0]))
+            if s == 5:
+                b.prefill(normal(4, 40, HIDDEN), [33, 7])
+            junk = [torch.full((k,), 77, dtype=torch.int32, device="cuda") for k in range(1, 9)]
+            y = step(normal(10 + s, 2, HIDDEN))
+            out.append([x.clone().view(torch.uint8) for x in (y, b.attn[:2], b.lens, b.held, b.pages, b.refs)])
+            normal(50, 64, 64) @ normal(51, 64, 64)
+            torch.cuda.synchronize()
+            assert len(junk) == 8
+        return out
+
+    b = make_block(20)
+    want = steps(b, b.decode)
+    b.close()
+    b = make_block(20)
+    b.prefill(normal(3, 50, HIDDEN), [20, 30])
+    token = torch.zeros((2, HIDDEN), dtype=BF16, device="cuda")
+    b.decode(token)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = b.decode(token)
+
+    def replay(t):
+        # the active shape that eager calls between the replays have set is not what a replay reads
+        token.copy_(t)
+        graph.replay()
+        return y
+
+    got = steps(b, replay)
+    for s, (w, g) in enumerate(zip(want, got)):
+        for n, (a, c) in enumerate(zip(w, g)):
+            assert torch.equal(a, c), (s, n)
+        assert not bool(torch.isnan(g[0].view(BF16)).any())
+    b.close()
