@@ -135,13 +135,19 @@ class AttentionBlock:
     def prefill(self, x, lens):
         """Prompts x [sum(lens), hidden], one after another, of new sequences 0, 1, ...: fills the
         cache and returns the block's output rows (valid until the next call)."""
-        cu = torch.tensor([0] + list(lens), dtype=torch.int32).cumsum(0, dtype=torch.int32).cuda()
+        self._check(x)
+        lens = [int(m) for m in lens]
         n = len(lens)
+        if n > self.max_seqs:
+            raise ValueError(f"prefill: {n} prompts, {self.max_seqs} at most")
+        if min(lens, default=0) < 0 or sum(lens) > x.shape[0]:
+            raise ValueError(f"prefill: prompts of {lens} tokens, x is {tuple(x.shape)}")
+        self._project_in(x)  # whose checks come before the sequences end, too
+        cu = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0, dtype=torch.int32).cuda()
         self.drafted = 0
         if self.pool:  # the sequences before them end
             self.lens.zero_()
             self._hold(self.lens, self.max_seqs)
-        self._project_in(x)
         self.lens[:n] = cu[1:] - cu[:-1]
         self._hold(self.lens, n)
         if self.pool:
@@ -189,6 +195,8 @@ class AttentionBlock:
         after the sequence's last token.  Returns the nodes' output rows; `accept` says which stay."""
         if self.window is not None:
             raise ValueError("draft: no trees under a window")
+        if len(trees) > self.max_seqs:
+            raise ValueError(f"draft: {len(trees)} trees, {self.max_seqs} at most")
         depths = []
         for i, tree in enumerate(trees):
             first = len(depths)

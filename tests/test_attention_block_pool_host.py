@@ -284,3 +284,26 @@ def test_rows_of_no_sequence(monkeypatch):
                 b.decode(tokens(50, 3))
             assert "ub_kv_resize" not in calls.calls[n:] and torch.equal(b.held, b.lens)
         b.close()
+
+
+def test_refused_before_anything_changes(monkeypatch):
+    """Prompts and drafts that are refused leave every sequence its pages and tokens."""
+    with modelled(monkeypatch) as (m, calls):
+        b = block(m, 20, max_seqs=3)
+        x = tokens(0, 30)
+        b.prefill(x, [10, 20])
+        state = lambda: [t.clone() for t in (b.lens, b.held, b.pages, b.refs)] + [dict(calls.slots)]
+        before = state()
+        many = tokens(0, 4)
+        for f in (lambda: b.prefill(x.float(), [10, 20]), lambda: b.prefill(x[:, :100], [10, 20]), lambda: b.prefill(x[0], [30]),
+                  lambda: b.prefill(many, [1, 1, 1, 1]), lambda: b.prefill(x, [10, 21]), lambda: b.prefill(x, [-1, 20]),
+                  lambda: b.prefill(torch.cat([tokens(0, 200)] * 2), [400]),
+                  lambda: b.draft(many, [[-1]] * 4), lambda: b.draft(many.float(), [[-1, 0, 1, 2]]),
+                  lambda: b.draft(tokens(0, 300), [[-1] * 150] * 2)):
+            with pytest.raises((ValueError, m.ub.UBError)):
+                f()
+            after = state()
+            assert all(torch.equal(p, q) for p, q in zip(before, after[:-1])) and before[-1] == after[-1]
+        b.decode(tokens(100, 2))
+        assert calls.rows == [list(range(10)) + [100], list(range(10, 30)) + [101]]
+        b.close()
