@@ -131,6 +131,15 @@ void workspace(Checks& c, const void* ws, size_t have, size_t need) {
           "workspace of " + std::to_string(have) + " bytes, " + std::to_string(need) + " needed");
 }
 
+// Whether the n int32 at p share no byte with `rows` rows of `per` int32, ld >= per apart, at q.
+bool clear_of(const int32_t* p, int64_t n, const int32_t* q, int64_t ld, int64_t per, int64_t rows) {
+  if (!p || !q || n <= 0 || per <= 0 || rows <= 0) return true;
+  const int64_t bytes = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(q));
+  const int64_t begin = bytes >> 2, end = (bytes + 4 * n + 3) >> 2;  // of p's, in int32 from q
+  if (end <= 0 || begin >= static_cast<__int128>(rows - 1) * ld + per) return true;
+  return begin >= 0 && begin % ld >= per && end <= begin - begin % ld + ld;  // between two rows
+}
+
 ub_status_t launched(ub_handle_t h, hipError_t e, const char* what) {
   if (e == hipSuccess) return UB_OK;
   if (e == hipErrorInvalidValue)
@@ -437,9 +446,13 @@ UB_API ub_status_t ub_kv_compact(ub_handle_t h, const ub_kv_cache_t* kv, const i
     a.pages_ld = pages_ld;
     a.pages_per_seq = pages_per_seq;
     c.need(n_seqs == 0 || (lens && kept_lens && lens_out), "lens, kept_lens or lens_out is NULL");
-    c.need(n_seqs == 0 || lens != lens_out, "lens_out must not be lens");
     c.need(n_seqs == 0 || kept_per_seq == 0 || kept != nullptr, "kept is NULL");
     c.need(kept_per_seq >= 0 && kept_ld >= kept_per_seq, "kept_per_seq must be >= 0 and kept_ld >= kept_per_seq");
+    if (c.st == UB_OK)  // a sequence's workgroups read them all, while one of them writes its length
+      c.need(clear_of(lens_out, n_seqs, lens, n_seqs, n_seqs, 1) && clear_of(lens_out, n_seqs, kept_lens, n_seqs, n_seqs, 1) &&
+                 clear_of(lens_out, n_seqs, kept, kept_ld, kept_per_seq, n_seqs) &&
+                 clear_of(lens_out, n_seqs, page_table, pages_ld, pages_per_seq, n_seqs),
+             "lens_out must not overlap lens, kept, kept_lens or page_table");
     a.lens = lens;
     a.kept = kept;
     a.kept_ld = kept_ld;

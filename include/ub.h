@@ -712,10 +712,10 @@ UB_API ub_status_t ub_attn_tree(ub_handle_t h, const ub_heads_t* q, const ub_kv_
  * were read before any is written; kept_lens[i] of them, at most kept_per_seq.  A list ends
  * before an entry that is negative, not above the one before it, or past the sequence's
  * pages_per_seq pages.  lens_out[i] becomes lens[i] (bounded by 0 and the table) and the number
- * of its entries; it must not be lens.  Tokens on a page whose id is outside [0, n_pages) are
- * neither read nor written.  The places from lens[i] on must be on pages that the sequence
- * shares with none (ub_kv_resize sees to it).  Accepted nodes of a tree are one such list;
- * what an eviction keeps, with lens 0, is another. */
+ * of its entries; it must not overlap what the call reads.  Tokens on a page whose id is outside
+ * [0, n_pages) are neither read nor written.  The places from lens[i] on must be on pages that
+ * the sequence shares with none (ub_kv_resize sees to it).  Accepted nodes of a tree are one such
+ * list; what an eviction keeps, with lens 0, is another. */
 UB_API ub_status_t ub_kv_compact(ub_handle_t h, const ub_kv_cache_t* cache,
                                  const int32_t* page_table, int64_t pages_ld,
                                  int32_t pages_per_seq, const int32_t* lens, const int32_t* kept,

@@ -195,3 +195,27 @@ def test_window_arithmetic(tmp_path):
     """The tiles and slots of windowed calls, and the page of a token by a product."""
     out = hc._build_and_run(tmp_path, "attn_window_check", [os.path.join(hc.CPP, "attn_window_check.cpp")])
     assert int(out.split()[1]) > 500000
+
+
+def accepted(call, **kw):
+    """The call passes the checks.  Its addresses are no memory: it is made only where there is no GPU to
+    launch on."""
+    return torch.cuda.is_available() or call(**kw) != BAD
+
+
+def test_compact_outputs_clear_of_inputs(h):
+    """A sequence's workgroups read its lists while one of them writes lens_out: it lies on none of what
+    they read, in whole or in part.  (The next int32 after each, and the gap between rows, are free.)"""
+    at = lambda **kw: compact(h, **{**dict(lens=FAKE, klens=FAKE + 1024, kept=FAKE + 2048, table=FAKE + 4096, n=2), **kw})
+    for base, words in ((0, 2), (1024, 2), (2048, 8), (4096, 16)):
+        for w in (-1, 0, words // 2, words - 1):
+            assert at(out=FAKE + base + 4 * w) == BAD and "lens_out" in ub.ub_last_error(h), (base, w)
+        for w in (-2, words):
+            assert accepted(at, out=FAKE + base + 4 * w), (base, w, ub.ub_last_error(h))
+    # rows of 3 entries, 8 apart: 5 are free between them, and all after the second
+    for w in (2, 7, 8, 10):
+        assert at(kld=8, most=3, out=FAKE + 2048 + 4 * w) == BAD, w
+    for w in (3, 6, 11):
+        assert accepted(at, kld=8, most=3, out=FAKE + 2048 + 4 * w), w
+    assert at(kld=8, most=3, out=FAKE + 2048 + 2) == BAD and accepted(at, kld=1 << 61, most=3, out=FAKE + 64)
+    assert accepted(at, most=0, kept=None, out=FAKE + 64)
