@@ -131,13 +131,19 @@ void workspace(Checks& c, const void* ws, size_t have, size_t need) {
           "workspace of " + std::to_string(have) + " bytes, " + std::to_string(need) + " needed");
 }
 
-// Whether the n int32 at p share no byte with `rows` rows of `per` int32, ld >= per apart, at q.
-bool clear_of(const int32_t* p, int64_t n, const int32_t* q, int64_t ld, int64_t per, int64_t rows) {
-  if (!p || !q || n <= 0 || per <= 0 || rows <= 0) return true;
-  const int64_t bytes = static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(q));
-  const int64_t begin = bytes >> 2, end = (bytes + 4 * n + 3) >> 2;  // of p's, in int32 from q
+// Whether n int32, `bytes` after a table's first, share no byte with its `rows` rows of `per` int32,
+// ld >= per apart.
+bool clear_at(__int128 bytes, int64_t n, int64_t ld, int64_t per, int64_t rows) {
+  if (n <= 0 || per <= 0 || rows <= 0) return true;
+  const __int128 begin = bytes >> 2, end = (bytes + 4 * static_cast<__int128>(n) + 3) >> 2;
   if (end <= 0 || begin >= static_cast<__int128>(rows - 1) * ld + per) return true;
   return begin >= 0 && begin % ld >= per && end <= begin - begin % ld + ld;  // between two rows
+}
+__int128 bytes_from(const int32_t* q, const int32_t* p) {
+  return static_cast<__int128>(reinterpret_cast<uintptr_t>(p)) - static_cast<__int128>(reinterpret_cast<uintptr_t>(q));
+}
+bool clear_of(const int32_t* p, int64_t n, const int32_t* q, int64_t ld, int64_t per, int64_t rows) {
+  return !p || !q || clear_at(bytes_from(q, p), n, ld, per, rows);
 }
 
 ub_status_t launched(ub_handle_t h, hipError_t e, const char* what) {
@@ -361,6 +367,19 @@ void pool(Checks& c, const int32_t* refs, int64_t n_pages, int32_t page_size) {
   c.need(n_pages >= 1 && n_pages <= INT32_MAX, "n_pages must be in [1, 2^31)");
   c.need(page_size >= 1, "page_size must be >= 1");
 }
+
+bool clear_of_table(const int32_t* p, int64_t n, const ubx::Table& t) {
+  return clear_of(p, n, t.p, t.ld, t.per, t.n);
+}
+bool tables_apart(const ubx::Table& x, const ubx::Table& y) {
+  if (!x.p || !y.p || x.n <= 0 || y.n <= 0) return true;
+  const __int128 bytes = bytes_from(y.p, x.p);
+  auto all = [](const ubx::Table& t) { return 4 * (static_cast<__int128>(t.n - 1) * t.ld + t.per); };
+  if (bytes >= all(y) || -bytes >= all(x)) return true;
+  for (int64_t i = 0; i < x.n; ++i)
+    if (!clear_at(bytes + 4 * static_cast<__int128>(i) * x.ld, x.per, y.ld, y.per, y.n)) return false;
+  return true;
+}
 }  // namespace
 
 UB_API ub_status_t ub_kv_append(ub_handle_t h, const ub_heads_t* q, const ub_heads_t* k,
@@ -487,8 +506,13 @@ UB_API ub_status_t ub_kv_fork(ub_handle_t h, int32_t* refs, int64_t n_pages,
     c.need(n_seqs <= 0 || lens != nullptr, "lens is NULL");
     c.need(n_out <= 0 || (parents && lens_out), "parents or lens_out is NULL");
     c.need(out_per_seq >= pages_per_seq, "out_per_seq must be >= pages_per_seq");
-    c.need(!page_table || page_table != table_out, "table_out must not be page_table");
-    c.need(!lens || lens != lens_out, "lens_out must not be lens");
+    if (c.st == UB_OK) {  // all workgroups read the parents, and one for each row its length and entries
+      c.need(tables_apart(a.out, a.in) && clear_of_table(lens, n_seqs, a.out) && clear_of_table(parents, n_out, a.out),
+             "table_out must not overlap page_table, lens or parents");
+      c.need(clear_of(lens_out, n_out, lens, n_seqs, n_seqs, 1) && clear_of(lens_out, n_out, parents, n_out, n_out, 1) &&
+                 clear_of_table(lens_out, n_out, a.in) && clear_of_table(lens_out, n_out, a.out),
+             "lens_out must not overlap lens, parents, page_table or table_out");
+    }
     a.lens = lens;
     a.parents = parents;
     a.lens_out = lens_out;
@@ -521,7 +545,6 @@ UB_API ub_status_t ub_kv_resize(ub_handle_t h, int32_t* refs, int64_t n_pages, i
     a.page = page_size;
     a.table = table(c, "page_table", page_table, pages_ld, pages_per_seq, n_seqs);
     c.need(n_seqs <= 0 || (lens && new_lens && lens_out && copies), "lens, new_lens, lens_out or copies is NULL");
-    c.need(n_seqs <= 0 || new_lens != lens_out, "lens_out must not be new_lens");
     a.lens = lens;
     a.new_lens = new_lens;
     a.lens_out = lens_out;
@@ -529,6 +552,15 @@ UB_API ub_status_t ub_kv_resize(ub_handle_t h, int32_t* refs, int64_t n_pages, i
     if (win) a.win = window(c, win);
     if (c.st == UB_OK) workspace(c, ws, ws_bytes, ubx::kv_resize_bytes(n_seqs));
     a.ws = ws;
+    if (c.st == UB_OK) {  // a row's wave writes them while others' still read
+      const int64_t n = n_seqs;
+      c.need((lens_out == lens || clear_of(lens_out, n, lens, n, n, 1)) && clear_of(lens_out, n, new_lens, n, n, 1) &&
+                 clear_of_table(lens_out, n, a.table),
+             "lens_out must not overlap new_lens or page_table, nor lens unless it is lens");
+      c.need(clear_of(copies, 3 * n, lens, n, n, 1) && clear_of(copies, 3 * n, new_lens, n, n, 1) &&
+                 clear_of(copies, 3 * n, lens_out, n, n, 1) && clear_of_table(copies, 3 * n, a.table),
+             "copies must not overlap lens, new_lens, lens_out or page_table");
+    }
     if (c.st != UB_OK) return c.st;
     ub_status_t st = ubx::ctx_bind(h);
     if (st != UB_OK) return st;

@@ -739,7 +739,7 @@ UB_API ub_status_t ub_kv_compact(ub_handle_t h, const ub_kv_cache_t* cache,
  * the place of all rows of table, so that a page's count changes by the rows that now hold it
  * less those that did.  Forks share their parent's pages; rows that are nobody's parent give
  * theirs back; a permutation reorders.  table_out has at least as many entries per row, and
- * neither it nor lens_out may overlap the inputs. */
+ * neither it nor lens_out may overlap the inputs or each other. */
 UB_API ub_status_t ub_kv_fork(ub_handle_t h, int32_t* refs, int64_t n_pages,
                               const int32_t* page_table, int64_t pages_ld, int32_t pages_per_seq,
                               const int32_t* lens, int32_t n_seqs, const int32_t* parents,
@@ -761,7 +761,8 @@ UB_API ub_status_t ub_kv_resize_bytes(int32_t n_seqs, size_t* bytes);
  *   - window (NULL: none): entries of a row that hold only tokens which a token at its last
  *     position and later ones do not see give their pages back and become -1.
  * Pages given up in a call are free for the next one.  lens_out[i] is the row's length after
- * the call; it may be lens.  copies: n_seqs x 3 int32. */
+ * the call; it may be lens.  copies: n_seqs x 3 int32.  The outputs must not overlap anything
+ * else of the call. */
 UB_API ub_status_t ub_kv_resize(ub_handle_t h, int32_t* refs, int64_t n_pages,
                                 int32_t* page_table, int64_t pages_ld, int32_t pages_per_seq,
                                 const int32_t* lens, const int32_t* new_lens, int32_t n_seqs,

@@ -219,3 +219,34 @@ def test_compact_outputs_clear_of_inputs(h):
         assert accepted(at, kld=8, most=3, out=FAKE + 2048 + 4 * w), w
     assert at(kld=8, most=3, out=FAKE + 2048 + 2) == BAD and accepted(at, kld=1 << 61, most=3, out=FAKE + 64)
     assert accepted(at, most=0, kept=None, out=FAKE + 64)
+
+
+def test_page_outputs_clear_of_inputs(h):
+    """What ub_kv_fork and ub_kv_resize write lies on nothing that other workgroups or waves of the call still
+    read; lens_out of a resize may be lens itself.  Two tables may be the columns of one array."""
+    f = lambda **kw: fork(h, **{**dict(refs=FAKE + 65536, table=FAKE, lens=FAKE + 1024, parents=FAKE + 2048, tout=FAKE + 4096,
+                                       lout=FAKE + 8192), **kw})
+    r = lambda **kw: resize(h, **{**dict(refs=FAKE + 65536, table=FAKE, lens=FAKE + 1024, new=FAKE + 2048, out=FAKE + 4096,
+                                         copies=FAKE + 8192), **kw})
+    assert accepted(f) and accepted(r) and accepted(r, out=FAKE + 1024)
+    # n 2, 3 rows of the new table, 8 entries a row
+    for base, words in ((0, 16), (1024, 2), (2048, 3), (4096, 24)):
+        for w in (-2, 0, words - 1):
+            assert f(lout=FAKE + base + 4 * w) == BAD and "lens_out" in ub.ub_last_error(h), (base, w)
+        for w in (-3, words):
+            assert accepted(f, lout=FAKE + base + 4 * w), (base, w)
+    for base, words in ((0, 16), (1024, 2), (2048, 3)):
+        for w in (-23, 0, words - 1):
+            assert f(tout=FAKE + base + 4 * w) == BAD and "table_out" in ub.ub_last_error(h), (base, w)
+        for w in (-24, words):
+            assert accepted(f, tout=FAKE + base + 4 * w), (base, w)
+    assert accepted(f, ld=16, tout=FAKE + 32, old=16) and f(ld=16, tout=FAKE + 28, old=16) == BAD
+    for base, words in ((0, 16), (2048, 2)):
+        for w in (-1, 0, words - 1):
+            assert r(out=FAKE + base + 4 * w) == BAD and "lens_out" in ub.ub_last_error(h), (base, w)
+    assert r(out=FAKE + 1020) == BAD and r(out=FAKE + 1028) == BAD and accepted(r, out=FAKE + 1032)
+    for base, words in ((0, 16), (1024, 2), (2048, 2), (4096, 2)):
+        for w in (-5, 0, words - 1):
+            assert r(copies=FAKE + base + 4 * w) == BAD and "copies" in ub.ub_last_error(h), (base, w)
+        for w in (-6, words):
+            assert accepted(r, copies=FAKE + base + 4 * w), (base, w)
