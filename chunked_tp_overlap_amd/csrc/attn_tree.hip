@@ -45,13 +45,12 @@
 #include <type_traits>
 
 #include "attn_common.h"
+#include "attn_path.h"
 #include "kv_pages.h"
 
 namespace ubx {
 namespace {
 
-constexpr int MAX_NODES = UB_ATTN_MAX_TREE;
-constexpr int WORDS = MAX_NODES / 64;
 constexpr int NW = 4;
 constexpr int ITEMS = 512;     // workgroups that run at once: two on each CU
 // Tiles of a part at least, where there are so many: the second case above takes 26.9 us with 2, 23.7
@@ -178,18 +177,6 @@ __device__ inline Cut cut_of(const TreeParams& p, Work head) {  // head: of sequ
   cut.c = c;
   cut.w = all(c);
   return cut;
-}
-
-// Bits of 64 keys from key `at` after the first drafted one (before it, if negative) that a node
-// with these path bits sees.
-__device__ inline uint64_t seen_bits(const uint64_t* path, int at) {
-  if (at <= -64) return ~0ull;
-  if (at < 0) return (path[0] << -at) | ((1ull << -at) - 1);
-  const int w = at >> 6, s = at & 63;
-  if (w >= WORDS) return 0;
-  uint64_t x = path[w] >> s;
-  if (s && w + 1 < WORDS) x |= path[w + 1] << (64 - s);
-  return x;
 }
 
 // The wave's LDS writes are done, then every wave's; direct or register loads stay in flight.
@@ -387,7 +374,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
         const int at = j * BN + kg * (BN / KG) - past;
 #pragma unroll
         for (int f = 0; f < QF; ++f) {
-          see[f] = seen_bits(paths + node[f] * WORDS, at);
+          see[f] = seen_bits(paths + node[f] * WORDS, at, BN / KG);
           const uint64_t mine = see[f] >> (4 * g);
 #pragma unroll
           for (int b = 0; b < KB; ++b)
@@ -407,7 +394,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tree(TreeParams p) {
             for (int i = 0; i < 4; ++i) x = fmaxf(x, s[b][f][i]);
           x = col_max(x);
           if (FIXED) {
-            // no score, though the column sees a key
+            // no score, though the column sees a key of the group's
             bad = bad || (m[f] == -INFINITY && x == -INFINITY && (!DRAFTED || see[f] != 0));
             m[f] = m[f] == -INFINITY ? x : m[f];
           } else {

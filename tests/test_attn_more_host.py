@@ -250,3 +250,10 @@ def test_page_outputs_clear_of_inputs(h):
             assert r(copies=FAKE + base + 4 * w) == BAD and "copies" in ub.ub_last_error(h), (base, w)
         for w in (-6, words):
             assert accepted(r, copies=FAKE + base + 4 * w), (base, w)
+
+
+@pytest.mark.skipif(hc._cxx() is None, reason="clang++ not available")
+def test_path_bits(tmp_path):
+    """Which of a group's keys a drafted token sees: a key of another group's is none that it has no score of."""
+    out = hc._build_and_run(tmp_path, "attn_path_check", [os.path.join(hc.CPP, "attn_path_check.cpp")])
+    assert int(out.split()[1]) > 5000000

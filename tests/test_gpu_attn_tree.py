@@ -405,3 +405,18 @@ def test_offsets_past_32_bits(ub):  # noqa: F811
             want[int(table[0, b // page]), :, b % page] = old[int(table[0, a // page]), :, a % page]
         want[1, :, :7] = want[2, :, :7]
         assert torch.equal(c.double().cpu(), want)
+
+
+@pytest.mark.parametrize("shape", [(4, 4, 128), (2, 1, 64), (4, 2, 96)])
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("kind", ["roots", "chain", "any"])
+def test_short_pasts(ub, shape, f8, kind):  # noqa: F811
+    """Trees that begin in a group's first tile, after no token or a few: nodes that see none of a group's keys,
+    but some of another's."""
+    H, G, D = shape
+    nodes, past = [24, 30, 17, 1, 24, 16, 9, 30], [0, 0, 5, 0, 33, 40, 50, 63]
+    trees = [tree(m, kind, i) for i, m in enumerate(nodes)]
+    lens, T, full, kc, vc, table, q, parents = make_case(H, G, D, trees, past, 16, f8, False, 1)
+    ks, vs = (40.0, 60.0) if f8 else (1.0, 1.0)
+    out, lse = attend(ub, q, ub.make_kv_cache(kc, vc, ks, vs), table, full, parents, lens, shape, T)
+    check_rows(out.cpu(), lse.cpu(), q, values(kc) / ks, values(vc) / vs, table, trees, full, 16, shape)
