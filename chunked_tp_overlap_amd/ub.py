@@ -433,7 +433,8 @@ def make_attn_window(window, sinks=0):
     """A ``ub_attn_window_t``: a token sees itself, the window - 1 tokens before it and the first
     ``sinks``."""
     w = ub_attn_window_t()
-    w.window, w.sinks = min(int(window), 0x7FFFFFFF), int(sinks)
+    # (past an int32 as far as it reaches: the calls refuse what is no window, not its low bits)
+    w.window, w.sinks = (max(-1, min(int(x), 0x7FFFFFFF)) for x in (window, sinks))
     return w
 
 

@@ -257,3 +257,10 @@ def test_path_bits(tmp_path):
     """Which of a group's keys a drafted token sees: a key of another group's is none that it has no score of."""
     out = hc._build_and_run(tmp_path, "attn_path_check", [os.path.join(hc.CPP, "attn_path_check.cpp")])
     assert int(out.split()[1]) > 5000000
+
+
+@pytest.mark.parametrize("w,s", [(5 - (1 << 32), 0), (-(1 << 40) + 1, 0), (8, (1 << 32) + 3), (8, (1 << 31) + 1), (8, 4 - (1 << 32)), (0, 1 << 32)])
+def test_windows_that_are_none(h, w, s):
+    """What does not fit an int32 is not taken for its low bits, but refused like any window that is none."""
+    x = win(w, s)
+    assert prompt(h, w=x) == BAD and bwd(h, w=x) == BAD and decode(h, w=x) == BAD and resize(h, w=x) == BAD
