@@ -315,3 +315,34 @@ def test_graph():
         same(want, bits(s["outs"]))
         assert bool(torch.isfinite(s["outs"]["dx"]).all()) and math.isfinite(float(s["outs"]["tree"].float().sum()))
     s["ub"].ub_destroy(s["h"])
+
+
+@pytest.mark.parametrize("W,S", [(50, 3), (3, 2), (16, 0), (1, 64)])
+def test_windowed_training_step(W, S):
+    """The gradient of all three projections under a window, dq and dk back through the rotation."""
+    from chunked_tp_overlap_amd.attention_block import AttentionBlock
+
+    H, G, D, hidden = 4, 2, 64, 128
+    wqkv, wo = normal(1, hidden, (H + 2 * G) * D) / 11, normal(2, H * D, hidden) / 16
+    b = AttentionBlock(wqkv, wo, H, G, D, capacity=800, max_seqs=4, max_len=16, tp=4, window=W, sinks=S)
+    lens = [70, 0, 81, 600]
+    rows = sum(lens)
+    x, d = normal(3, rows, hidden), normal(4, rows, H * D)
+    y, dqkv = b.train(x, lens, d)
+    q, k = b.q[:rows].view(rows, H, D).double().cpu(), b.k[:rows].view(rows, G, D).double().cpu()
+    v = b.qkv[:rows, (H + G) * D:].reshape(rows, G, D).double().cpu()
+    cu = [0, 70, 70, 151, 751]
+    o, _, t, _ = wref.prompt(q, k, v, cu, D ** -0.5, W, S)
+    ref.check(b.attn[:rows].view(rows, H, D), o, t, "out")
+    (dq, dk, dv), (tq, tk, tv) = wref.prompt_bwd(d.double().cpu().view(rows, H, D), q, k, v, cu, D ** -0.5, W, S)
+    pos = torch.cat([torch.arange(n) for n in lens])
+    got = dqkv.double().cpu()
+    for name, w, t, c, n in (("dq", dq, tq, 0, H), ("dk", dk, tk, H * D, G)):
+        z, e = ref.rotate(w, pos, -b.inv_freq.cpu(), False, D)
+        # the bound of a pair's two entries, turned, and one more rounding
+        both = t[..., : D // 2] + t[..., D // 2:]
+        tol = (torch.cat([both, both], -1) + e) * (1 + ref.U16) + ref.U16 * z.abs()
+        ref.check(got[:, c: c + n * D].reshape(rows, n, D), z, tol, name)
+    ref.check(got[:, (H + G) * D:].reshape(rows, G, D), dv, tv, "dv")
+    torch.cuda.synchronize()
+    b.close()
