@@ -237,3 +237,24 @@ def test_bad_tables(ub):  # noqa: F811
         new = [2, 0, 12, 13]
         assert dev.resize(new).tolist() == pool.resize(new)
         dev.same(pool, "resize")
+
+
+@pytest.mark.parametrize("window", [None, (40, 3)])
+def test_thousands_of_rows(ub, window):  # noqa: F811
+    """More rows than the giving workgroup keeps at hand, with shared last pages, in a pool that runs out."""
+    rows, page, per = 5001, 16, 8
+    r = random.Random(7)
+    pool = Pool(9000, page, per)
+    pool.add_empty(rows)
+    with Rank(ub, 8) as h:
+        dev = Device(ub, h, pool)
+        for step in range(3):
+            new = [min(per * page, x + r.choice([0, 1, 5, 16, 30])) for x in pool.lens]
+            assert dev.resize(new, window).tolist() == pool.resize(new, window), step
+            dev.same(pool, step)
+            short = sum(a != b for a, b in zip(new, pool.lens))
+            parents = [r.randrange(rows) if r.random() < 0.1 else i for i in range(rows)]
+            pool.fork(parents)
+            dev.fork(parents)
+            dev.same(pool, f"fork {step}")
+        assert short > 1000  # the last step's pages ran out
