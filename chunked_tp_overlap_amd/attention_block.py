@@ -36,7 +36,8 @@ class AttentionBlock:
     stored, and their rows are NaN; once it has lost a token so, all its later rows are, and its copies',
     and its entry of `lens`, the cached tokens of each, is NOWHERE or more.  What it held is free when it
     ends (`fork`, `prefill`).  Drafts are no tokens of their sequence before they are accepted.  window:
-    how many tokens a token sees, itself among them, besides the first `sinks`."""
+    how many tokens a token sees, itself among them, besides the first `sinks`; a pool gets the pages of
+    tokens that no later one sees back with the next decoded token, and has to hold whole prompts till then."""
 
     def __init__(self, wqkv, wo, heads, kv_heads, dim, capacity, max_seqs, max_len, page=64, tp=1, cache=BF16,
                  k_scale=1.0, v_scale=1.0, rope_base=10000.0, window=None, sinks=0, n_pages=None):

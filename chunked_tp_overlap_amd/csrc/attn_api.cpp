@@ -376,6 +376,10 @@ bool tables_apart(const ubx::Table& x, const ubx::Table& y) {
   const __int128 bytes = bytes_from(y.p, x.p);
   auto all = [](const ubx::Table& t) { return 4 * (static_cast<__int128>(t.n - 1) * t.ld + t.per); };
   if (bytes >= all(y) || -bytes >= all(x)) return true;
+  if (x.ld == y.ld && (bytes & 3) == 0) {  // columns of one array
+    const __int128 at = ((bytes >> 2) % x.ld + x.ld) % x.ld;
+    if (at >= y.per && at + x.per <= x.ld) return true;
+  }
   for (int64_t i = 0; i < x.n; ++i)
     if (!clear_at(bytes + 4 * static_cast<__int128>(i) * x.ld, x.per, y.ld, y.per, y.n)) return false;
   return true;

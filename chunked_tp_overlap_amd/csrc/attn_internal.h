@@ -1,6 +1,6 @@
 // Internal contracts of the attention calls: what attn_api.cpp (argument checks) passes to
-// the launchers in kv_append.hip, attn_prompt.hip, attn_prompt_bwd.hip and attn_decode.hip,
-// and what it uses of a handle.
+// the launchers in kv_append.hip, attn_prompt.hip, attn_prompt_bwd.hip, attn_decode.hip, attn_tree.hip
+// and kv_manage.hip, and what it uses of a handle.
 #pragma once
 
 #include <string>

@@ -30,7 +30,7 @@
 // output once.
 //
 // Measured on MI355X, both kernels.  64 sequences of 100 to 16264 tokens and up to 60 nodes, 8 heads
-// on 1, E4M3: 135-138 us, 0.63 PFLOP/s counted (86 GFLOP; 101 with the columns that fill the strips up);
+// on 1, E4M3: 135-138 us (bf16 143), 0.63 PFLOP/s counted (86 GFLOP; 101 with the columns that fill the strips up);
 // a step of 64 keys and 128 columns takes 1.95 us on each of a CU's two workgroups, as in
 // attn_prompt.hip, 92 us if all had as many; the rest is parts of unequal length, 4 us before and
 // 2 after a part's tiles, and 13 of the join.  One sequence of 32520 and 24 nodes, bf16: 22 us: 4 us to

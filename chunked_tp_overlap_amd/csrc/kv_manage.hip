@@ -146,7 +146,8 @@ __device__ inline void take_row(const ResizeArgs& a, int i, const Ask& k, bool g
 // turn by turn a list of free pages in LDS, from which each goes to its row: the first whose `end`
 // lies past the page's rank, found in LDS too (ROWS_IN_LDS rows and fewer).  576 rows that grow by
 // 2000 pages together take 10.2 us; with the search in the workspace, and a page's place from the
-// counts that its thread read, 19.6.  64 rows that get 500 pages each take some 50 us.
+// counts that its thread read, 19.6.  64 rows that get 500 pages each take some 50 us: one workgroup
+// searches for the row of each of 32000 pages.
 // ALL: and then what kv_take does for every row.
 constexpr int ROWS_IN_LDS = 4096;
 template <bool ALL>

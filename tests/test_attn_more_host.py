@@ -241,6 +241,8 @@ def test_page_outputs_clear_of_inputs(h):
         for w in (-24, words):
             assert accepted(f, tout=FAKE + base + 4 * w), (base, w)
     assert accepted(f, ld=16, tout=FAKE + 32, old=16) and f(ld=16, tout=FAKE + 28, old=16) == BAD
+    assert accepted(f, ld=16, tout=FAKE - 32, old=16) and f(ld=16, tout=FAKE - 28, old=16) == BAD
+    assert accepted(f, ld=64, tout=FAKE + 32, old=16, nout=3) and f(ld=24, tout=FAKE + 32, old=16, nout=3) == BAD
     for base, words in ((0, 16), (2048, 2)):
         for w in (-1, 0, words - 1):
             assert r(out=FAKE + base + 4 * w) == BAD and "lens_out" in ub.ub_last_error(h), (base, w)
