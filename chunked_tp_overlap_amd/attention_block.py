@@ -32,7 +32,7 @@ class AttentionBlock:
     contiguous bf16 matrices, which are kept and not copied.  The cache has room for `max_len` tokens
     of each of `max_seqs` sequences, as bf16 or (with scales k_scale and v_scale) E4M3; with
     `n_pages`, a pool of so many pages, for as many tokens of sequences up to that long as they hold.
-    Where the pool has no pages for a sequence's new tokens (or it gets longer than max_len) they are not
+    Where the pool has no pages for a sequence's new tokens (or its row of the table no entries) they are not
     stored, and their rows are NaN; once it has lost a token so, all its later rows are, and its copies',
     and its entry of `lens`, the cached tokens of each, is NOWHERE or more.  What it held is free when it
     ends (`fork`, `prefill`).  Drafts are no tokens of their sequence before they are accepted.  window:

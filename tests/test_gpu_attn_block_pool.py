@@ -1,6 +1,8 @@
 """GPU tests of the attention block where its pool runs out of pages, and of captured decode steps as
 sequences fork: what the cache holds, byte by byte, and each row against its definition."""
 
+import random
+
 import pytest
 import torch
 
@@ -237,4 +239,90 @@ def test_a_captured_step_across_forks():
         for n, (a, c) in enumerate(zip(w, g)):
             assert torch.equal(a, c), (s, n)
         assert not bool(torch.isnan(g[0].view(BF16)).any())
+    b.close()
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_steps_as_modelled(monkeypatch, seed):
+    """Prompts, decode steps, drafts, accepted paths and forks in any order: lengths, tables, counts, the rows
+    that are NaN and the values in every slot are those of the model of test_attention_block_pool_host.py."""
+    from tests import block_model as bm
+
+    r = random.Random(seed)
+    kw = dict(max_seqs=6, max_len=40, page=r.choice([1, 4, 16]))
+    if seed % 3 == 0:
+        kw.update(window=r.randint(1, 20), sinks=r.randint(0, 5))
+    n_pages, count, ops, alive = r.randint(4, 14), 0, [], 0
+    for _ in range(60):
+        op = "prefill" if not alive else r.choice(["decode"] * 4 + ["draft"] * 3 * ("window" not in kw) + ["fork"] * 2 + ["prefill"])
+        if op == "prefill":
+            lens = [r.randint(0, 41) for _ in range(r.randint(1, 6))]
+            if not sum(lens):
+                continue
+            args, n, alive = (lens,), sum(lens), len(lens)
+        elif op == "decode":
+            args, n = (), r.randint(1, alive)
+        elif op == "draft":
+            trees = [[r.randint(-1, j - 1) for j in range(r.randint(0, 7))] for _ in range(r.randint(1, alive))]
+            if not sum(map(len, trees)):
+                continue
+            args, n = (trees,), sum(map(len, trees))
+        else:
+            args, n = ([r.randint(-1, alive) for _ in range(r.randint(1, 6))],), 0
+            alive = len(args[0])
+        ops.append((op, args, count, n))
+        count += n
+        if op == "draft" and r.random() < 0.8:
+            kept = torch.full((r.randint(1, len(trees)), 8), -1, dtype=torch.int32)
+            lens = []
+            for i in range(kept.shape[0]):
+                path, j = [], r.randint(-1, len(trees[i]) - 1)
+                while j >= 0:
+                    path.insert(0, j)
+                    j = trees[i][j]
+                kept[i, : len(path)] = torch.tensor(path, dtype=torch.int32)
+                lens.append(len(path))
+            ops.append(("accept", (kept, torch.tensor(lens, dtype=torch.int32)), count, 0))
+
+    def run(b, rows, dev, after):
+        for op, args, first, n in ops:
+            if op == "fork":
+                args = (torch.tensor(args[0], dtype=torch.int32),)
+            args = [a.to(dev) if isinstance(a, torch.Tensor) else a for a in args]
+            getattr(b, op)(*([rows(first, n)] if n else []), *args)
+            after([t.cpu().clone() for t in (b.lens, b.held, b.pages, b.refs)],
+                  torch.isnan(b.attn[:n].float()).all(1).tolist(), torch.isnan(b.attn[:n].float()).any(1).tolist())
+
+    want = []
+    with bm.modelled(monkeypatch) as (m, calls):
+        b = bm.block(m, n_pages, **kw)
+        run(b, bm.tokens, "cpu", lambda state, nan, some: want.append((state, nan, dict(calls.slots))))
+        b.close()
+    H, G, D, hidden = 2, 1, 64, 128
+    wqkv, wo = normal(1, hidden, (H + 2 * G) * D) / 11, normal(2, H * D, hidden) / 11
+    from chunked_tp_overlap_amd.attention_block import AttentionBlock
+
+    b = AttentionBlock(wqkv, wo, H, G, D, capacity=256, n_pages=n_pages, **kw)
+    x = normal(3, count, hidden)
+    values = x.double().cpu() @ wqkv[:, (H + G) * D:].double().cpu()
+    norms = 4e-3 * x.double().cpu().norm(dim=1)[:, None] * wqkv[:, (H + G) * D:].double().cpu().norm(dim=0)
+    at, lost = 0, 0
+
+    def after(state, nan, some):
+        nonlocal at, lost
+        (lens, held, pages, refs), rows, slots = want[at]
+        what = (at, ops[at][0])
+        assert nan == some == rows, what
+        for g, w, name in zip(state, (lens, held, pages, refs), ("lens", "held", "pages", "refs")):
+            assert torch.equal(g, w), (what, name)
+        v, keys = b.v_cache.double().cpu(), [k for k, t in slots.items() if t is not None]
+        if keys:  # (a matrix product's bound, as for the library's GEMMs)
+            pg, off = torch.tensor(keys).unbind(1)
+            t = torch.tensor([slots[k] for k in keys])
+            assert bool(((v[pg, 0, off] - values[t]).abs() <= norms[t]).all()), what
+        lost += sum(nan)
+        at += 1
+
+    run(b, lambda first, n: x[first: first + n], "cuda", after)
+    assert at == len(want) and lost > 0
     b.close()
